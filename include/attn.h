@@ -327,6 +327,142 @@ int attn_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, const 
                              int out_layout, int mask_planes, int dtype, int num_splits,
                              float *lse, void *stream);
 
+/*
+ * The paged 8-bit KV cache: three calls for one step of a batch of requests
+ * (prompts, chunks of prompts and single new tokens mixed freely), all on
+ * device memory the caller owns, none needing a host round trip:
+ *   attn_cache_assign      cache blocks, block tables and token slots from the
+ *                          requests' lengths
+ *   attn_cache_append_fp8  the step's K / V rows into their slots, as e4m3
+ *   attn_fwd_paged_fp8     attention of the step's rows over the cache
+ * They have no counterpart in the source pages; the attention is attn_fwd's
+ * definition over rows that are e4m3 bytes times a scale.
+ *
+ * Layout.  The cache (one for K, one for V) is num_blocks blocks of
+ * block_size (16, 32, 64 or 128) token slots, [num_blocks, Hkv, block_size, D]
+ * e4m3 bytes (finite to +-448, 0x7f / 0xff NaN), D = 64 or 128, with f32
+ * scales [num_blocks, Hkv]: the value of a byte is e4m3 * scale.  Slot s is
+ * row s % block_size of block s / block_size.  A request's block table maps
+ * its position p to block table[p / block_size]; entries without a block are
+ * negative.  The rows of a step are packed: request b owns rows
+ * [q_starts[b], q_starts[b + 1]) of num_tokens, its newest tokens in order.
+ */
+
+/*
+ * attn_cache_assign -- one step's block tables and token slots.
+ *
+ * For every request b (a row of the tables), with past_b = past_lengths[b], or
+ * 0 when finished[b] is set:
+ *   first, rows with finished[b] set give all their blocks back: pushed onto
+ *   the free stack in row and entry order, the row's entries becoming -1;
+ *   then every negative entry i < ceil((past_b + new_lengths[b]) / block_size)
+ *   takes the block on top of the free stack, in row and entry order;
+ *   q_starts       [B + 1]: exclusive prefix sum of new_lengths
+ *   total_lengths  [B]: past_b + new_lengths[b] (the next step's past_lengths)
+ *   slot_map       [num_tokens]: the slot of each new token, row by row
+ *                  (request b's token i has position past_b + i), then -1
+ * Entries that hold a block are kept, so a repeated call changes nothing and
+ * a request whose length shrank keeps its blocks.
+ * result receives 0, or why the step cannot be done: 1 too few free blocks,
+ * 2 a request needs more than max_blocks entries, 3 more new tokens than
+ * num_tokens, 4 a negative length, 5 free_count or a table entry out of range.
+ * Then the tables, the free stack and its count are left as they were,
+ * q_starts is all 0, total_lengths = past_lengths and every slot is -1: the
+ * step's append and attention do nothing.
+ *
+ * Arguments (device pointers, caller-owned, no two overlapping):
+ *   past_lengths, new_lengths  int32 [B]
+ *   finished       NULL or uint8 [B], nonzero = finished
+ *   block_tables   int32 [B, max_blocks], read and written
+ *   free_blocks    int32 [num_blocks], a stack: entries [0, free_count) are free blocks
+ *   free_count     int32 [1], read and written
+ *   result         int32 [1]
+ *   B              0..8192 (more: ATTN_ERR_UNSUPPORTED)
+ * One launch on `stream`; allocates and synchronises nothing.
+ */
+int attn_cache_assign(const int32_t *past_lengths, const int32_t *new_lengths, const uint8_t *finished,
+                      int32_t *block_tables, int32_t *free_blocks, int32_t *free_count, int32_t *q_starts,
+                      int32_t *total_lengths, int64_t *slot_map, int32_t *result, int B, int max_blocks,
+                      int block_size, int num_blocks, int num_tokens, void *stream);
+
+/*
+ * attn_cache_append_fp8 -- K and V rows into their slots, quantised.
+ *
+ * Tokens whose slots follow one another inside a block are a run.  For a run
+ * and a kv head, over the run's finite values x:
+ *   need  = the smallest power of two s >= 2^-100 with max |x| <= 448 s
+ *   s     = need when the run starts at the block's row 0, else
+ *           max(need, the block's scale), the rows before it being held
+ *   byte  = e4m3(x / s), to nearest even; |x / s| > 448 is cut to 448
+ *           (infinities so), NaN stays NaN
+ * and where s grew, the block's earlier rows are encoded again:
+ * e4m3(byte * old / s).  s becomes the block's scale.  Scales written here
+ * are powers of two; a block to be continued has one of those.  Negative
+ * slots and slots of no block are passed over.
+ *
+ * Arguments (device pointers, caller-owned; the caches and scales overlap nothing):
+ *   k, v          [num_tokens, Hkv, D] dtype, 16-byte aligned; token t begins
+ *                 at element t * token_stride (>= Hkv * D, whole 16 bytes), so
+ *                 slices of a fused projection can be passed
+ *   slot_map      int64 [num_tokens], as attn_cache_assign leaves it.  A block's
+ *                 tokens are adjacent in the map, skipped ones between them
+ *                 aside, and its runs are taken in order; a block whose tokens
+ *                 lie on both sides of another's is left with unspecified contents
+ *   k_cache, v_cache, k_scales, v_scales   see the layout above
+ *   dtype         enum attn_dtype of k and v
+ * One launch on `stream`; allocates and synchronises nothing.
+ */
+int attn_cache_append_fp8(const void *k, const void *v, const int64_t *slot_map, void *k_cache, void *v_cache,
+                          float *k_scales, float *v_scales, int num_tokens, int Hkv, int D,
+                          int64_t k_token_stride, int64_t v_token_stride, int num_blocks, int block_size,
+                          int dtype, void *stream);
+
+/*
+ * attn_fwd_paged_fp8 -- attention of the step's rows over the paged cache.
+ *
+ * Row i of request b (token t = q_starts[b] + i, new_b rows in all) has
+ * position pos = total_lengths[b] - new_b + i.  For every query head h, with
+ * kv_head = h / (Hq / Hkv):
+ *   key j is visible iff 0 <= j < min(total_lengths[b], max_blocks * block_size),
+ *     j > pos - local_window when local_window > 0, and (causal == 0 or j <= pos)
+ *   s_j = scale * <q[t,h,:], k_j>, then softcap * tanh(s_j / softcap) when softcap > 0
+ *   out[t,h,:] = sum_j softmax(s)_j v_j, or 0 when no key is visible
+ *   lse[t,h]   = log sum_j exp(s_j), natural log, -inf when no key is visible
+ * k_j, v_j: the cache's e4m3 bytes times their block's scale.
+ * Rows t >= q_starts[B] belong to no request: out and lse are left as they were there.
+ * Slots at or past a request's total length may hold any bits; they never
+ * reach the output.  A NaN byte in a slot below it may reach every row of
+ * the same request and kv head.
+ *
+ * Arguments (device pointers, caller-owned; out, lse and workspace overlap nothing):
+ *   q             [num_tokens, Hq, D] dtype, 16-byte aligned, token t at element
+ *                 t * q_token_stride (>= Hq * D, whole 16 bytes)
+ *   k_scales, v_scales  finite and >= 0
+ *   block_tables  int32 [B, max_blocks].  An entry below a request's length that
+ *                 names no block of [0, num_blocks) is not followed: its keys
+ *                 count as zeros, and attn_get_device_status then reports
+ *                 ATTN_ERR_INVALID_ARG once
+ *   q_starts      int32 [B + 1], non-decreasing in [0, num_tokens]
+ *   total_lengths int32 [B]
+ *   out           [num_tokens, Hq, D] dtype;  lse NULL or f32 [num_tokens, Hq]
+ *   dtype         ATTN_F16 or ATTN_BF16 (ATTN_F32: ATTN_ERR_UNSUPPORTED)
+ *   B             0..4096 (more: ATTN_ERR_UNSUPPORTED)
+ *   workspace     at least attn_paged_workspace_bytes(...) bytes, 16-byte
+ *                 aligned, for partial rows; nothing in it has to start at zero.
+ *                 Calls that share a workspace must not overlap on the GPU.
+ * Enqueues on `stream`; allocates and synchronises nothing, so it may be captured into a CUDA
+ * graph (make one call on the device before capturing).
+ */
+int attn_fwd_paged_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+                       const float *v_scales, const int32_t *block_tables, const int32_t *q_starts,
+                       const int32_t *total_lengths, void *out, float *lse, int num_tokens, int B, int Hq, int Hkv,
+                       int D, int64_t q_token_stride, int num_blocks, int block_size, int max_blocks, int causal,
+                       int local_window, float scale, float softcap, int dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Workspace bytes attn_fwd_paged_fp8 needs on the current device. */
+size_t attn_paged_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, int D);
+
 /* Human-readable name of a status code; never NULL. */
 const char *attn_status_string(int status);
 
@@ -338,7 +474,8 @@ int attn_last_cuda_error(void);
  * attn_get_device_status -- synchronises `stream`, then reports and clears
  * the device-side status word of the current device: ATTN_ERR_TIMEOUT if any
  * kernel of this library gave up on a bounded wait since the last query,
- * else ATTN_OK (or ATTN_ERR_CUDA if the synchronisation failed).
+ * else ATTN_ERR_INVALID_ARG if attn_fwd_paged_fp8 met a block-table entry that
+ * names no block, else ATTN_OK (or ATTN_ERR_CUDA if the synchronisation failed).
  */
 int attn_get_device_status(void *stream);
 

@@ -52,6 +52,11 @@ SIGNATURES = {
     "dsa_index_select_workspace_bytes": (ctypes.c_size_t, [_i32, _i32, _i32]),
     "attn_splitkv_num_splits": (_i32, [_i32, _i32, _i32, _i32, _i32]),
     "attn_splitkv_workspace_bytes": (ctypes.c_size_t, [_i32, _i32, _i32, _i32, _i32]),
+    "attn_cache_assign": (_i32, [_vp] * 10 + [_i32] * 5 + [_vp]),
+    "attn_cache_append_fp8": (_i32, [_vp] * 7 + [_i32] * 3 + [ctypes.c_int64] * 2 + [_i32] * 3 + [_vp]),
+    "attn_fwd_paged_fp8": (_i32, [_vp] * 10 + [_i32] * 5 + [ctypes.c_int64] + [_i32] * 5 +
+                           [ctypes.c_float, ctypes.c_float, _i32, _vp, ctypes.c_size_t, _vp]),
+    "attn_paged_workspace_bytes": (ctypes.c_size_t, [_i32] * 5),
     "attn_status_string": (ctypes.c_char_p, [_i32]),
     "attn_last_cuda_error": (_i32, []),
     "attn_get_device_status": (_i32, [_vp]),
@@ -446,9 +451,191 @@ def dsa_index_select(query, key, weights, bias, *, top_k, scale, weights_scale=1
     return dev_out
 
 
+# ---------------------------------------------------------------------------
+# The paged 8-bit KV cache.  These calls run once a layer or once a step with
+# little work each, so the checks here are written to cost few microseconds.
+CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+class _NullContext:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NULL = _NullContext()
+
+
+def _on(device):
+    """A context with `device` current: nothing to do when it already is."""
+    return _NULL if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _need(t, name, dtype, shape, device):
+    """Raises unless t is a contiguous tensor of this dtype, shape and device."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}: got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _cache_shape(k_cache, v_cache, k_scales, v_scales, Hkv, D, device):
+    """(num_blocks, block_size) of a cache, after checking its four tensors."""
+    if k_cache.dim() != 4 or k_cache.dtype not in CACHE_DTYPES:
+        raise ValueError("the caches must be [num_blocks, Hkv, block_size, D] of float8_e4m3fn or uint8")
+    num_blocks, heads, block_size, width = k_cache.shape
+    if heads != Hkv or width != D:
+        raise ValueError(f"shape mismatch: rows of {Hkv} kv heads and head dim {D}, cache {tuple(k_cache.shape)}")
+    _need(k_cache, "k_cache", k_cache.dtype, (num_blocks, Hkv, block_size, D), device)
+    _need(v_cache, "v_cache", k_cache.dtype, (num_blocks, Hkv, block_size, D), device)
+    _need(k_scales, "k_scales", torch.float32, (num_blocks, Hkv), device)
+    _need(v_scales, "v_scales", torch.float32, (num_blocks, Hkv), device)
+    return num_blocks, block_size
+
+
+def _token_stride(t, name):
+    """Elements from one token of a [T, H, D] tensor to the next; its heads must be dense."""
+    T, H, D = t.shape
+    if t.stride(2) != 1 and D > 1 or t.stride(1) != D and H > 1:
+        raise ValueError(f"{name}: the heads of a token must be contiguous, strides {t.stride()}")
+    return t.stride(0) if T > 1 else H * D
+
+
+def attn_cache_assign(past_lengths, new_lengths, block_tables, free_blocks, free_count, *, block_size, num_tokens,
+                      finished=None, q_starts=None, total_lengths=None, slot_map=None, result=None):
+    """One step's cache blocks (attn_cache_assign in the C ABI), on the GPU.
+
+    past_lengths, new_lengths int32 [B]; block_tables int32 [B, max_blocks]
+    (negative = no block), free_blocks int32 [num_blocks] (a stack of block
+    numbers) and free_count int32 [1] are read and updated in place; finished
+    None or bool / uint8 [B] marks rows whose blocks go back first and whose
+    past counts as 0.  num_tokens is the length of the slot map, at least the
+    sum of new_lengths.  Returns (q_starts int32 [B + 1], total_lengths int32
+    [B], slot_map int64 [num_tokens], result int32 [1]), allocated with torch
+    when not given; result is 0, or why the step was not done (1 too few free
+    blocks, 2 a table row too short, 3 too many tokens, 4 a negative length, 5
+    a count or entry out of range), in which case nothing was assigned."""
+    dev = past_lengths.device
+    if not past_lengths.is_cuda or past_lengths.dim() != 1 or block_tables.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("attn_cache_assign takes CUDA tensors: lengths [B], block_tables [B, max_blocks], "
+                         "free_blocks [num_blocks]")
+    B, T, i32 = past_lengths.shape[0], int(num_tokens), torch.int32
+    width, num_blocks = block_tables.shape[1], free_blocks.shape[0]
+    _need(past_lengths, "past_lengths", i32, (B,), dev)
+    _need(new_lengths, "new_lengths", i32, (B,), dev)
+    _need(block_tables, "block_tables", i32, (B, width), dev)
+    _need(free_blocks, "free_blocks", i32, (num_blocks,), dev)
+    _need(free_count, "free_count", i32, (1,), dev)
+    if finished is not None:
+        if finished.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("finished must be bool or uint8")
+        _need(finished, "finished", finished.dtype, (B,), dev)
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    made = []
+    for t, name, dtype, n in ((q_starts, "q_starts", i32, B + 1), (total_lengths, "total_lengths", i32, B),
+                              (slot_map, "slot_map", torch.int64, T), (result, "result", i32, 1)):
+        if t is None:
+            t = torch.empty(n, dtype=dtype, device=dev)
+        else:
+            _need(t, name, dtype, (n,), dev)
+        made.append(t)
+    with _on(dev):
+        rc = load_library().attn_cache_assign(
+            past_lengths.data_ptr(), new_lengths.data_ptr(), None if finished is None else finished.data_ptr(),
+            block_tables.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(), made[0].data_ptr(),
+            made[1].data_ptr(), made[2].data_ptr(), made[3].data_ptr(), B, width, int(block_size), num_blocks, T,
+            _stream_handle(dev))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_assign")
+    return tuple(made)
+
+
+def attn_cache_append_fp8(k, v, slot_map, k_cache, v_cache, k_scales, v_scales):
+    """New K / V rows into the paged cache, as e4m3 with one power-of-two scale
+    for each (block, kv head) (attn_cache_append_fp8 in the C ABI).
+
+    k, v [T, Hkv, D] (one dtype among float32 / float16 / bfloat16; a token's
+    heads contiguous, tokens any stride apart); slot_map int64 [T] (negative =
+    skip); k_cache, v_cache [num_blocks, Hkv, block_size, D] float8_e4m3fn (or
+    uint8) and k_scales, v_scales float32 [num_blocks, Hkv], updated in place."""
+    if k.dim() != 3 or not k.is_cuda or v.shape != k.shape or v.device != k.device:
+        raise ValueError("k, v must be CUDA tensors [T, Hkv, D] of one shape and device")
+    if k.dtype not in DTYPE_CODES or v.dtype != k.dtype:
+        raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
+    T, Hkv, D = k.shape
+    dev = k.device
+    num_blocks, block_size = _cache_shape(k_cache, v_cache, k_scales, v_scales, Hkv, D, dev)
+    _need(slot_map, "slot_map", torch.int64, (T,), dev)
+    with _on(dev):
+        rc = load_library().attn_cache_append_fp8(
+            k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), T, Hkv, D, _token_stride(k, "k"), _token_stride(v, "v"),
+            num_blocks, block_size, DTYPE_CODES[k.dtype], _stream_handle(dev))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_append_fp8")
+
+
+def attn_fwd_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_starts, total_lengths, *, causal=True,
+                       local_window=0, scale=None, softcap=0.0, out=None, lse=None, workspace=None):
+    """Attention over the paged 8-bit KV cache (attn_fwd_paged_fp8 in the C ABI).
+
+    q [T, Hq, D] float16 or bfloat16, the packed rows of all requests (a
+    token's heads contiguous, tokens any stride apart); k_cache, v_cache
+    [num_blocks, Hkv, block_size, D] float8_e4m3fn (or uint8) with k_scales,
+    v_scales float32 [num_blocks, Hkv]; block_tables int32 [B, max_blocks];
+    request b owns rows q_starts[b] .. q_starts[b + 1] (int32 [B + 1]), the last
+    of its total_lengths[b] (int32 [B]) tokens.  scale defaults to 1/sqrt(D).
+    Returns out [T, Hq, D] (allocated with torch when not given; rows of no
+    request are not written); lse, when given, float32 [T, Hq], receives the
+    natural-log log-sum-exp of each row.  The workspace
+    (attn_paged_workspace_bytes) is allocated with torch when not given."""
+    if q.dim() != 3 or not q.is_cuda or k_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("attn_fwd_paged_fp8 takes CUDA tensors: q [T, Hq, D], caches "
+                         "[num_blocks, Hkv, block_size, D], block_tables [B, max_blocks]")
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16")
+    T, Hq, D = q.shape
+    dev, Hkv, (B, width) = q.device, k_cache.shape[1], block_tables.shape
+    num_blocks, block_size = _cache_shape(k_cache, v_cache, k_scales, v_scales, Hkv, D, dev)
+    _need(block_tables, "block_tables", torch.int32, (B, width), dev)
+    _need(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+    _need(total_lengths, "total_lengths", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", q.dtype, (T, Hq, D), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, Hq), dev)
+    lib = load_library()
+    with _on(dev):
+        need = lib.attn_paged_workspace_bytes(T, B, Hq, Hkv, D)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        rc = lib.attn_fwd_paged_fp8(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_tables.data_ptr(), q_starts.data_ptr(), total_lengths.data_ptr(), out.data_ptr(),
+            None if lse is None else lse.data_ptr(), T, B, Hq, Hkv, D, _token_stride(q, "q"), num_blocks, block_size,
+            width, int(bool(causal)), int(local_window), 1.0 / math.sqrt(D) if scale is None else float(scale),
+            float(softcap), DTYPE_CODES[q.dtype], None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(dev))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_paged_fp8")
+    return out
+
+
+def attn_paged_workspace_bytes(num_tokens, B, Hq, Hkv, D) -> int:
+    """Workspace bytes attn_fwd_paged_fp8 needs on the current device, for callers that keep their own."""
+    return load_library().attn_paged_workspace_bytes(int(num_tokens), int(B), int(Hq), int(Hkv), int(D))
+
+
 def get_device_status(device=None) -> int:
     """Synchronises the current stream and returns (and clears) the device
-    status word: ATTN_OK or ATTN_ERR_TIMEOUT."""
+    status word: ATTN_OK, ATTN_ERR_TIMEOUT, or ATTN_ERR_INVALID_ARG after an
+    attn_fwd_paged_fp8 whose block tables named no block below a length."""
     dev = device if device is not None else torch.cuda.current_device()
     with torch.cuda.device(dev):
         return load_library().attn_get_device_status(_stream_handle(dev))

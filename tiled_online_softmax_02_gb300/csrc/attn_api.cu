@@ -21,10 +21,12 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/attn.h"
+#include "api_internal.h"
 #include "attn_decode.h"
 #include "attn_internal.h"
 #include "dsa_internal.h"
 #include "device_common.cuh"
+#include "paged_internal.h"
 
 namespace gb300_attn {
 namespace {
@@ -33,6 +35,10 @@ __device__ int g_status_word;  // ORed kStatus* bits from every kernel
 
 thread_local int t_last_cuda_error = 0;
 std::atomic<uint64_t> g_timeout_ns{2000000000ull};
+
+}  // namespace
+
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 
 int cuda_fail(cudaError_t e) {
   t_last_cuda_error = (int)e;
@@ -81,6 +87,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn(int* err) {
   return fn;
 }
 
+namespace {
+
 // 16-bit tensor [planes, rows, D] as a 3-D TMA map with a {64, box_rows, 1}
 // box and the 128-byte swizzle the tcgen05 shared-memory descriptors expect.
 // Rows and planes out of range read as zero.
@@ -99,21 +107,6 @@ int encode_map(CUtensorMap* map, const void* base, bool bf16, int64_t planes, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
   return ATTN_OK;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > (INT64_C(1) << 62) / a) return false;
-  *out = a * b;
-  return true;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
 
 __global__ void selftest_wait_kernel(uint64_t timeout_ns, int* status) {
@@ -773,7 +766,8 @@ extern "C" int attn_get_device_status(void* stream) {
     e = cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  return (word & kStatusTimeout) ? ATTN_ERR_TIMEOUT : ATTN_OK;
+  if (word & kStatusTimeout) return ATTN_ERR_TIMEOUT;
+  return (word & kStatusBadBlock) ? ATTN_ERR_INVALID_ARG : ATTN_OK;
 }
 
 extern "C" int attn_set_wait_timeout_ns(uint64_t timeout_ns) {

@@ -1,0 +1,82 @@
+// paged_internal.h -- parameter blocks and launchers of the paged 8-bit KV
+// cache, shared between the C ABI layer (paged_api.cu) and the kernels.  Not
+// part of the public interface.
+//
+// The cache is num_blocks blocks of block_size token slots; a block holds
+// every kv head: [num_blocks, Hkv, block_size, D] e4m3 bytes, one fp32 scale
+// for each (block, head).  Slot s is row s % block_size of block
+// s / block_size; a request's block table maps position p to block
+// table[p / block_size].
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace gb300_attn {
+
+// Status bit: an attention call met a block-table entry that names no block.
+constexpr int kStatusBadBlock = 2;
+
+// Codes attn_cache_assign leaves in `result`.
+enum AssignResult {
+  kAssignOk = 0,
+  kAssignNoBlocks = 1,   // fewer free blocks than needed
+  kAssignRowShort = 2,   // a request needs more table entries than a row has
+  kAssignTokens = 3,     // more new tokens than the slot map holds
+  kAssignLength = 4,     // a negative length
+  kAssignCorrupt = 5     // free_count, a table entry or a free-list entry out of range
+};
+
+constexpr int kAssignMaxRequests = 8192;
+constexpr int kPagedMaxRequests = 4096;
+
+struct AssignParams {
+  const int32_t* past;      // [B] tokens in the cache
+  const int32_t* added;     // [B] tokens this step adds
+  const uint8_t* finished;  // [B] or nullptr: rows that give their blocks back first
+  int32_t* tables;          // [B, width]
+  int32_t* free_blocks;     // [num_blocks] stack
+  int32_t* free_count;      // [1]
+  int32_t* q_starts;        // [B + 1]
+  int32_t* totals;          // [B]
+  int64_t* slot_map;        // [T]
+  int32_t* result;          // [1]
+  int B, width, block_size, num_blocks, T;
+};
+
+struct AppendParams {
+  const void* x[2];         // k, v: [T, Hkv, D], token t at x + t * stride elements
+  int64_t stride[2];
+  const int64_t* slot_map;  // [T]
+  uint8_t* cache[2];        // [num_blocks, Hkv, block_size, D]
+  float* scales[2];         // [num_blocks, Hkv]
+  int64_t num_slots;        // num_blocks * block_size
+  int T, Hkv, D, block_size;
+  int chunk;                // tokens whose runs one CTA owns
+};
+
+struct PagedParams {
+  const void* q;            // [T, Hq, D], token t at q + t * q_stride elements
+  int64_t q_stride;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* tables;    // [B, width]
+  const int32_t* q_starts;  // [B + 1]
+  const int32_t* totals;    // [B]
+  void* out;                // [T, Hq, D]
+  float* lse;               // [T, Hq] or nullptr
+  int T, B, Hq, Hkv, D, group, num_blocks, block_size, width;
+  int causal, local_window;
+  float scale, softcap;
+  uint64_t timeout_ns;
+  int* status;
+};
+
+cudaError_t launch_cache_assign(const AssignParams& p, cudaStream_t stream);
+cudaError_t launch_cache_append(const AppendParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_paged(const PagedParams& p, bool bf16, cudaStream_t stream);
+
+}  // namespace gb300_attn
