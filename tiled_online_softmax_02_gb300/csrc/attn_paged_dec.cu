@@ -1,0 +1,770 @@
+// attn_paged_dec.cu -- attention over the paged 8-bit KV cache for few query
+// rows per (request, kv head): decode steps, drafted tokens to verify.
+//
+// Bound: HBM.  Every cached byte is read once, and the e4m3 bytes go from the
+// cache to the tensor cores as they are -- TMA into shared memory, tcgen05
+// kind::f8f6f4 from there -- so no lane converts a K or V value.  As few rows
+// would leave a 128-row tile empty, keys stand in M and rows in N:
+//   S^T[key, row] = K_tile Q^T           M = 128 keys, N = pieces * NR, K = D
+//   O^T[d, row]  += V_tile^T P^T         M = 128 (d),  N = 3 * NR, K = 128 keys
+// The 16-bit and fp32 factors are carried as sums of e4m3 pieces, each piece
+// its own rows of N:  x = x0 + x1 / 32 + x2 / 1024, x0 = e4m3(x),
+// x1 = e4m3(32 (x - x0)), ...  A piece's rest is at most 2^-4 of it, so two
+// pieces hold a bf16 Q exactly and three an f16 Q (down to 2^-23 and 2^-28 of
+// the unit's largest element: one power of two scales Q to e4m3's range), and
+// P in three pieces is good to 2^-12, or 2^-25 of its largest value: better
+// than a P rounded to f16.
+//
+// Scales: a key's K scale multiplies its scores (the thread that owns the key
+// holds it).  Its V scale enters the exponent, t = s log2 e + log2 v_scale,
+// so O accumulates 2^(t - m) v8 whatever the scales are, m being the running
+// maximum of t, and the row sum takes 2^(t - m) / v_scale.
+//
+// One CTA walks its share of the line of key tiles (paged_sched.cuh).  Roles
+// (256 threads): warps 0-3 softmax, thread = key; warp 4 K loads, warp 5 V
+// loads (block table lookup by lanes, one TMA box a block), warp 6 MMA issue,
+// warp 7 Q rows of the next unit into pieces.
+#include <atomic>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "paged_sched.cuh"
+
+namespace gb300_attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6, kQWarp = 7;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kStep = 32.0f, kInvStep = 1.0f / 32.0f;  // from one e4m3 piece to the next
+// P is carried as 32 * 2^(t - m); the maximum moves when a key passes it by
+// more than 3 (log2 units), so the first piece stays below 256 < 448.
+constexpr float kRise = 3.0f, kPLog2 = 5.0f;
+constexpr float kNone = -1e30f;       // m of a row that has seen no key
+constexpr float kMinVScale = 7.9e-31f;  // 2^-100: a block of zeros may have scale 0
+
+template <int D, int NR, bool BF16>
+struct Cfg {
+  static constexpr int kQP = BF16 ? 2 : 3;                        // pieces of Q
+  static constexpr int kPP = 3;                                   // pieces of P
+  static constexpr int kNQ = (kQP * NR + 15) / 16 * 16;           // N of S^T
+  static constexpr int kNP = (kPP * NR + 15) / 16 * 16;           // N of O^T
+  static constexpr int kTile = kPagedKeys * D;                    // bytes of a K or V tile
+  static constexpr int kCtas = NR <= 16 ? 2 : 1;                  // CTAs an SM
+  static constexpr int kSK = D == 64 ? 4 : (NR <= 16 ? 3 : 4);    // K stages
+  static constexpr int kSV = D == 64 ? 4 : (NR <= 16 ? 2 : 4);    // V stages
+  static constexpr int kQBytes = (kNQ * D + 1023) / 1024 * 1024;
+  static constexpr int kPBytes = kNP * kPagedKeys;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kSK * kTile;
+  static constexpr int kOffQ = kOffV + kSV * kTile;               // two buffers
+  static constexpr int kOffP = kOffQ + 2 * kQBytes;               // two buffers
+  static constexpr int kOffLim = kOffP + 2 * kPBytes;             // int2 [2][NR]
+  static constexpr int kOffM = kOffLim + 2 * NR * 8;              // float [NR]: running maxima
+  static constexpr int kOffRed = kOffM + NR * 4;                  // float [2][4][NR]
+  static constexpr int kOffFlag = kOffRed + 2 * 4 * NR * 4;       // int [2][4]
+  static constexpr int kOffQs = kOffFlag + 32;                    // float [2]: 1 / scale of Q's pieces
+  static constexpr int kOffBar = kOffQs + 16;
+  // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2], red [2], drain
+  static constexpr int kBars = 2 * kSK + 2 * kSV + 13;
+  static constexpr int kOffSlot = kOffBar + kBars * 8;
+  static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShareSmem) + 1024;  // + alignment slack
+  static constexpr int kColO = 2 * kNQ;                           // TMEM: S^T twice, then O^T
+  static constexpr int kCols = 2 * kNQ + kNP;
+  static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512 && kTmem * kCtas <= 512, "tensor memory");
+  static_assert(kSmem <= (kCtas == 2 ? 115200 : 232448), "shared memory");
+  static_assert(kOffBar % 8 == 0 && kOffQ % 1024 == 0 && kOffP % 1024 == 0, "alignment");
+};
+
+template <int D, int NR, bool BF16>
+struct Lay {
+  using C = Cfg<D, NR, BF16>;
+  uint8_t* base;
+  uint32_t s;
+  __device__ uint32_t k_tile(int i) const { return s + C::kOffK + i * C::kTile; }
+  __device__ uint32_t v_tile(int i) const { return s + C::kOffV + i * C::kTile; }
+  __device__ uint8_t* v_ptr(int i) const { return base + C::kOffV + i * C::kTile; }
+  __device__ uint32_t q(int i) const { return s + C::kOffQ + i * C::kQBytes; }
+  __device__ uint8_t* q_ptr(int i) const { return base + C::kOffQ + i * C::kQBytes; }
+  __device__ uint32_t p(int i) const { return s + C::kOffP + i * C::kPBytes; }
+  __device__ uint8_t* p_ptr(int i) const { return base + C::kOffP + i * C::kPBytes; }
+  __device__ int2* lim(int i) const { return reinterpret_cast<int2*>(base + C::kOffLim) + i * NR; }
+  __device__ float* m() const { return reinterpret_cast<float*>(base + C::kOffM); }
+  __device__ float* red(int i) const { return reinterpret_cast<float*>(base + C::kOffRed) + i * 4 * NR; }
+  __device__ int* flag(int i) const { return reinterpret_cast<int*>(base + C::kOffFlag) + i * 4; }
+  __device__ float* qs() const { return reinterpret_cast<float*>(base + C::kOffQs); }
+  __device__ uint32_t bar(int i) const { return s + C::kOffBar + i * 8; }
+  __device__ uint32_t k_full(int i) const { return bar(i); }
+  __device__ uint32_t k_empty(int i) const { return bar(C::kSK + i); }
+  __device__ uint32_t v_full(int i) const { return bar(2 * C::kSK + i); }
+  __device__ uint32_t v_empty(int i) const { return bar(2 * C::kSK + C::kSV + i); }
+  __device__ uint32_t rest(int i) const { return bar(2 * C::kSK + 2 * C::kSV + i); }
+  __device__ uint32_t s_full(int i) const { return rest(i); }
+  __device__ uint32_t p_full(int i) const { return rest(2 + i); }
+  __device__ uint32_t pv_done(int i) const { return rest(4 + i); }
+  __device__ uint32_t q_full(int i) const { return rest(6 + i); }
+  __device__ uint32_t q_empty(int i) const { return rest(8 + i); }
+  __device__ uint32_t red_bar(int i) const { return rest(10 + i); }
+  __device__ uint32_t drain() const { return rest(12); }
+  __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
+  __device__ PagedShareSmem* share() const { return reinterpret_cast<PagedShareSmem*>(base + C::kOffShare); }
+};
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulator (bits
+// 4-5 = 1), A and B e4m3 (bits 7-9 and 10-12 = 0), major-ness of A / B in bits
+// 15 / 16 (1 = MN-major), N >> 3 in 17-22, M >> 4 in 24-28.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor; layout 2 = 128-byte swizzle, 4 = 64-byte, 0 = none.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)layout << 61;
+}
+
+__device__ __forceinline__ void mma8_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// n consecutive 32-bit columns of this thread's TMEM lane (n = 4, 8, 16 or 32).
+__device__ __forceinline__ void tld(uint32_t a, float (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tld(uint32_t a, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tld(uint32_t a, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tld(uint32_t a, float (&r)[32]) {
+  tmem_ld32(a, reinterpret_cast<uint32_t(&)[32]>(r));
+}
+__device__ __forceinline__ void tst16(uint32_t a, const float (&r)[16]) {
+  tmem_st16(a, reinterpret_cast<const uint32_t(&)[16]>(r));
+}
+
+// e4m3 pieces of two values (lo in bits 0-7): the piece, and what is left of them times 32.
+__device__ __forceinline__ uint32_t piece2(float& lo, float& hi) {
+  uint16_t b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+  lo = (lo - f.x) * kStep;
+  hi = (hi - f.y) * kStep;
+  return b;
+}
+__device__ __forceinline__ uint32_t last2(float lo, float hi) {
+  uint16_t b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
+  return b;
+}
+
+// Reduce-scatter over the warp: on entry each lane holds NR values; on exit
+// lane l holds the max (sum) over all lanes of value row_of_lane<NR>(l).
+template <int NR>
+__device__ __forceinline__ int row_of_lane(int lane) {
+  int r = 0, half = NR / 2;
+#pragma unroll
+  for (int bit = 4; half >= 1; --bit, half >>= 1)
+    if (lane & (1 << bit)) r += half;
+  return r;
+}
+template <int NR, bool MAX>
+__device__ __forceinline__ float reduce_scatter(float (&v)[NR], int lane) {
+#pragma unroll
+  for (int half = NR / 2, bit = 4; half >= 1; half >>= 1, --bit) {
+    const bool upper = (lane >> bit) & 1;
+#pragma unroll
+    for (int k = 0; k < half; ++k) {
+      const float send = upper ? v[k] : v[k + half];
+      const float keep = upper ? v[k + half] : v[k];
+      const float got = __shfl_xor_sync(0xffffffffu, send, 1 << bit);
+      v[k] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int bit = 0; (1 << bit) < 32 / NR; ++bit) {
+    const float got = __shfl_xor_sync(0xffffffffu, x, 1 << bit);
+    x = MAX ? fmaxf(x, got) : x + got;
+  }
+  return x;
+}
+
+struct DecParams {
+  CUtensorMap tmap_k;  // e4m3 [num_blocks * Hkv, block_size, D], box {D, block_size, 1}
+  CUtensorMap tmap_v;
+  PagedParams c;
+  float* ws_o;         // [2 * CTAs][NR][D]: partial rows, sum of 2^(t - m) v8
+  float2* ws_ml;       // [2 * CTAs][NR]: m, sum of 2^(t - m) / v_scale
+  PagedCut* cuts;      // [CTAs]
+  float k1, k2, k3;    // soft-cap in log2 units: k2 / (2^(k1 s) + 1) + k3
+  float scale_log2;
+};
+
+// ------------------------------------------------------------------ loaders
+// One warp; lane i looks up and loads block i of a tile.  Blocks past the
+// request's last key, and entries that name no block, are read out of range,
+// which fills their rows with zeros and touches no memory.
+template <int D, int NR, int NS>
+__device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap* tmap, PagedWalk<NR> w, uint32_t ring,
+                                          uint32_t full0, uint32_t empty0, int lane, bool report) {
+  const PagedParams& p = P.c;
+  constexpr int kTile = kPagedKeys * D;
+  const int per = kPagedKeys / p.block_size, box = p.block_size * D;
+  int g = 0;
+  bool ok = true;
+  for (; ok && !w.done(); w.next(p)) {
+    const int64_t cap = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
+    auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
+      const int64_t i = (int64_t)t * per + lane;
+      if (lane >= per || i * p.block_size >= cap) return -1;
+      const int e = __ldg(table + i);
+      return e >= 0 && e < p.num_blocks ? e : -2;
+    };
+    int next = w.nt > 0 ? lookup(w.t0) : -1;
+    for (int n = 0; n < w.nt; ++n, ++g) {
+      const int st = g % NS, blk = next;
+      if (n + 1 < w.nt) next = lookup(w.t0 + n + 1);
+      if (g >= NS && !mbar_wait_warp(empty0 + st * 8, ((g / NS) - 1) & 1, p.timeout_ns, p.status)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(full0 + st * 8, kTile);
+      __syncwarp();
+      if (lane < per) {
+        if (report && blk == -2) atomicOr(p.status, kStatusBadBlock);
+        tma_load_3d(ring + st * kTile + lane * box, tmap, full0 + st * 8, 0, 0,
+                    blk >= 0 ? blk * p.Hkv + w.u.kvh : p.num_blocks * p.Hkv);
+      }
+    }
+  }
+  // every copy lands before the CTA may exit
+  for (int n = g > NS ? g - NS : 0; n < g; ++n) mbar_wait_warp(full0 + (n % NS) * 8, (n / NS) & 1, p.timeout_ns, p.status);
+}
+
+// ----------------------------------------------------------------- Q pieces
+// One warp: the unit's rows as e4m3 pieces, piece i of row r at row i * NR + r,
+// K-major in the swizzle of the row width; rows past the unit's are zeros.
+template <int D, int NR, bool BF16>
+__device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16>& sm, PagedWalk<NR> w, int lane) {
+  using C = Cfg<D, NR, BF16>;
+  const PagedParams& p = P.c;
+  constexpr int kVec = D / 8;  // 8-value pieces of a row
+  for (; !w.done(); w.next(p)) {
+    const int buf = w.index & 1;
+    if (w.index >= 2 && !mbar_wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;
+    const PagedUnit& u = w.u;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + (int64_t)u.kvh * p.group * D;
+    auto row = [&](int r) {
+      const int x = u.row0 + r;
+      return q + (int64_t)(x / p.group) * p.q_stride + (x % p.group) * D;
+    };
+    auto widen = [&](uint32_t v, float& a, float& b) {
+      if constexpr (BF16) {
+        a = __uint_as_float(v << 16);
+        b = __uint_as_float(v & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        a = f.x;
+        b = f.y;
+      }
+    };
+    float top = 0.0f;
+    for (int c = lane; c < u.rows * kVec; c += 32) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row(c / kVec)) + c % kVec);
+      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        widen(e[i], a, b);
+        a = fabsf(a);
+        b = fabsf(b);
+        if (a < INFINITY) top = fmaxf(top, a);
+        if (b < INFINITY) top = fmaxf(top, b);
+      }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    // the power of two that brings the largest element into [128, 256)
+    int e = (int)(__float_as_uint(top) >> 23) - 127;
+    e = top > 0.0f ? min(max(7 - e, -120), 120) : 0;
+    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+    uint8_t* dst = sm.q_ptr(buf);
+    for (int c = lane; c < C::kNQ * kVec; c += 32) {  // 8 bytes of a row of N: rows of pieces not written stay zero
+      const int n = c / kVec, k = c % kVec, r = n % NR, piece = n / NR;
+      uint32_t lo = 0, hi = 0;
+      if (r < u.rows && piece < C::kQP) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row(r)) + k);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          widen(x[i], a, b);
+          // an element that is not finite makes its row's scores NaN (0x7f in the first piece)
+          const bool fa = fabsf(a) < INFINITY, fb = fabsf(b) < INFINITY;
+          a = fa ? a * up : (piece == 0 ? NAN : 0.0f);
+          b = fb ? b * up : (piece == 0 ? NAN : 0.0f);
+          for (int s = 0; s < piece; ++s) piece2(a, b);
+          const uint32_t two = last2(a, b);
+          if (i < 2) lo |= two << (16 * i); else hi |= two << (16 * (i - 2));
+        }
+      }
+      // 16-byte chunk k / 2 of the row, its index XORed as the swizzle does
+      const int chunk = D == 128 ? ((k >> 1) ^ (n & 7)) : ((k >> 1) ^ ((n >> 1) & 3));
+      *reinterpret_cast<uint2*>(dst + n * D + chunk * 16 + (k & 1) * 8) = make_uint2(lo, hi);
+    }
+    for (int r = lane; r < NR; r += 32)
+      sm.lim(buf)[r] = r < u.rows ? paged_limits(p, u.q, (u.row0 + r) / p.group) : make_int2(0, 0);
+    if (lane == 0) sm.qs()[buf] = 1.0f / up;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.q_full(buf));
+  }
+}
+
+// ---------------------------------------------------------------- MMA issuer
+// Tile i of the CTA's line: S^T(i) into buffer i % 2, then O^T += V^T P^T of
+// tile i - 1.  That buffer is free: P(i - 2), written after S(i - 2) was read,
+// was waited for in the step before.
+template <int D, int NR, bool BF16>
+__device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF16>& sm, PagedWalk<NR> w, uint32_t tmem,
+                                         int lane) {
+  using C = Cfg<D, NR, BF16>;
+  const PagedParams& p = P.c;
+  constexpr uint32_t kIdS = idesc_e4m3(128, C::kNQ, false, false);
+  constexpr uint32_t kIdO = idesc_e4m3(128, C::kNP, true, true);
+  constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;
+  constexpr uint32_t kGroup8 = 8 * D;  // bytes of 8 rows
+  int g = 0;
+  bool pending = false;   // a tile whose P V is still to be issued
+  bool pend_first = false;
+  int64_t pend_key0 = 0, pend_valid = 0;
+  bool ok = true;
+  auto pv = [&](int t) -> bool {
+    if (!mbar_wait_warp(sm.p_full(t & 1), (t >> 1) & 1, p.timeout_ns, p.status)) return false;
+    const int vs = t % C::kSV;
+    if (!mbar_wait_warp(sm.v_full(vs), (t / C::kSV) & 1, p.timeout_ns, p.status)) return false;
+    if (pend_valid < pend_key0 + kPagedKeys) {
+      // slots past the request's last key may hold NaN bytes: P is 0 there but 0 * NaN is not
+      const int r0 = pend_valid > pend_key0 ? (int)(pend_valid - pend_key0) : 0;
+      for (int c = r0 * (D / 16) + lane; c < kPagedKeys * (D / 16); c += 32)
+        *reinterpret_cast<uint4*>(sm.v_ptr(vs) + c * 16) = make_uint4(0u, 0u, 0u, 0u);  // whole rows: the swizzle does not matter
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    tc_fence_after();
+    // A = V^T: M-major, one swizzle atom of 128 (64: repeated, LBO 0) d's by 8 keys, SBO apart
+    const uint64_t a0 = sdesc(sm.v_tile(vs), 0, kGroup8, kSwizzle);
+    // B = P^T: N-major without swizzle, 16 rows of N by 8 keys in 128 bytes; LBO to the next 8 keys, SBO to the next 16 rows
+    const uint64_t b0 = sdesc(sm.p(t & 1), 128, 16 * kPagedKeys, 0);
+#pragma unroll
+    for (int k = 0; k < kPagedKeys / 32; ++k)
+      mma8_elect(tmem + C::kColO, a0 + (uint32_t)((k * 4 * kGroup8) >> 4), b0 + (uint32_t)((k * 512) >> 4), kIdO,
+                 (!pend_first || k > 0) ? 1u : 0u);
+    tc_commit_elect(sm.pv_done(t & 1));
+    tc_commit_elect(sm.v_empty(vs));
+    return true;
+  };
+  for (; ok && !w.done(); w.next(p)) {
+    const int buf = w.index & 1;
+    if (w.nt == 0 && pending) {  // no tile to issue before it: the waiting P V goes now
+      if (!pv(g - 1)) { ok = false; break; }
+      pending = false;
+    }
+    if (!mbar_wait_warp(sm.q_full(buf), (w.index >> 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+    const int64_t valid = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    for (int n = 0; ok && n < w.nt; ++n, ++g) {
+      const int ks = g % C::kSK;
+      if (!mbar_wait_warp(sm.k_full(ks), (g / C::kSK) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t a0 = sdesc(sm.k_tile(ks), 16, kGroup8, kSwizzle);
+      const uint64_t b0 = sdesc(sm.q(buf), 16, kGroup8, kSwizzle);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+        mma8_elect(tmem + (g & 1) * C::kNQ, a0 + (uint32_t)(k * 2), b0 + (uint32_t)(k * 2), kIdS, k > 0 ? 1u : 0u);
+      tc_commit_elect(sm.s_full(g & 1));
+      tc_commit_elect(sm.k_empty(ks));
+      if (pending && !pv(g - 1)) { ok = false; break; }
+      pending = true;
+      pend_first = n == 0;
+      pend_key0 = (int64_t)(w.t0 + n) * kPagedKeys;
+      pend_valid = valid;
+    }
+    // Q and the limits are free once this unit's S^T products are done and its rows' softmax has read
+    // them: the softmax arrives for itself
+    if (ok) tc_commit_elect(sm.q_empty(buf));
+  }
+  if (ok && pending) pv(g - 1);
+  // every MMA done before tensor memory is given back
+  tc_commit_elect(sm.drain());
+  mbar_wait_warp(sm.drain(), 0, p.timeout_ns, p.status);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t to_bits(float x) {
+  if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  else return __half_as_ushort(__float2half_rn(x));
+}
+
+// ------------------------------------------------------------------ softmax
+// Thread tid of warps 0-3 owns key tid of every tile (lane tid of S^T) and, at
+// a unit's end, d = tid of O^T.
+template <int D, int NR, bool BF16>
+__device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR, BF16>& sm, PagedWalk<NR> w,
+                                             const PagedShare& share, uint32_t tmem, int warp, int lane) {
+  using C = Cfg<D, NR, BF16>;
+  const PagedParams& p = P.c;
+  const int tid = warp * 32 + lane;
+  const uint32_t tq = tmem + ((uint32_t)(warp * 32) << 16);
+  float* const m = sm.m();
+  int g = 0, use = 0;  // tiles and exchanges so far
+  // every softmax warp has written its part of exchange `use`
+  auto exchange = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.red_bar(use & 1));
+    const bool r = mbar_wait_warp(sm.red_bar(use & 1), (use >> 1) & 1, p.timeout_ns, p.status);
+    ++use;
+    return r;
+  };
+  for (; !w.done(); w.next(p)) {
+    const PagedUnit& u = w.u;
+    const int buf = w.index & 1;
+    const int64_t valid = min(u.q.total, (int64_t)p.width * p.block_size);
+    const int32_t* table = p.tables + (int64_t)u.b * p.width;
+    // block and scales of this thread's key, a tile ahead of their use
+    auto block_of = [&](int n) {
+      const int64_t j = (int64_t)(w.t0 + n) * kPagedKeys + tid;
+      const int b = n < w.nt && j < valid ? __ldg(table + (int)j / p.block_size) : -1;
+      return b >= 0 && b < p.num_blocks ? b : -1;
+    };
+    float ks_next = 0.0f, vs_next = 1.0f;
+    int blk_next = block_of(0);
+    auto fetch = [&](int n) {  // scales of tile n, block of tile n + 1
+      ks_next = 0.0f;
+      vs_next = 1.0f;
+      if (blk_next >= 0) {
+        const int64_t at = (int64_t)blk_next * p.Hkv + u.kvh;
+        ks_next = __ldg(p.k_scales + at);
+        vs_next = __ldg(p.v_scales + at);
+      }
+      blk_next = block_of(n + 1);
+    };
+    fetch(0);
+    if (!mbar_wait_warp(sm.q_full(buf), (w.index >> 1) & 1, p.timeout_ns, p.status)) return;
+    const int2* lim = sm.lim(buf);
+    const float qs = sm.qs()[buf];
+    const int full_lo = lim[u.rows - 1].x, full_hi = lim[0].y;  // keys every row sees
+    float l[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+    // m starts below everything (its readers of the last unit met at that unit's sum exchange)
+    if (tid < NR) m[tid] = kNone;
+    if (!exchange()) return;
+
+    for (int n = 0; n < w.nt; ++n, ++g) {
+      const int key0 = (w.t0 + n) * kPagedKeys, j = key0 + tid;
+      const float kmul = qs * ks_next;
+      const float vsc = fmaxf(vs_next, kMinVScale);
+      const float lv = __log2f(vsc), iv = 1.0f / vsc;
+      fetch(n + 1);
+      if (!mbar_wait_warp(sm.s_full(g & 1), (g >> 1) & 1, p.timeout_ns, p.status)) return;
+      tc_fence_after();
+      float t[NR];
+      {
+        float x1[NR], x2[C::kQP > 2 ? NR : 1];
+        const uint32_t a = tq + (uint32_t)((g & 1) * C::kNQ);
+        tld(a, t);
+        tld(a + NR, x1);
+        if constexpr (C::kQP > 2) tld(a + 2 * NR, x2);
+        tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          if constexpr (C::kQP > 2) x1[r] = fmaf(x2[r], kInvStep, x1[r]);
+          t[r] = fmaf(x1[r], kInvStep, t[r]);
+        }
+      }
+      if (p.softcap > 0.0f) {
+        const float k1 = P.k1 * kmul, c = P.k3 + lv;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) t[r] = fmaf(P.k2, fast_rcp(fast_exp2(t[r] * k1) + 1.0f), c);
+      } else {
+        const float km = P.scale_log2 * kmul;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) t[r] = fmaf(t[r], km, lv);
+      }
+      if (key0 < full_lo || key0 + kPagedKeys > full_hi) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const int2 e = lim[r];
+          t[r] = (j >= e.x && j < e.y) ? t[r] : -INFINITY;
+        }
+      }
+      // does any key pass its row's maximum by more than kRise?
+      float over = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) over = fmaxf(over, t[r] - m[r]);
+      const bool rise = __any_sync(0xffffffffu, over > kRise);
+      int* flag = sm.flag(use & 1);
+      if (lane == 0) flag[warp] = rise ? 1 : 0;
+      if (!exchange()) return;
+      if (flag[0] | flag[1] | flag[2] | flag[3]) {
+        float x[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) x[r] = t[r];
+        const float wm = reduce_scatter<NR, true>(x, lane);
+        float* red = sm.red(use & 1);
+        if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = wm;
+        if (!exchange()) return;
+        float alpha[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float old = m[r];
+          const float top = fmaxf(fmaxf(red[r], red[NR + r]), fmaxf(red[2 * NR + r], red[3 * NR + r]));
+          const float mn = top > old + kRise ? top : old;
+          alpha[r] = fast_exp2(old - mn);
+          l[r] *= alpha[r];
+          x[r] = mn;
+        }
+        if (n > 0) {  // O^T holds the unit's earlier tiles once their P V is done
+          if (!mbar_wait_warp(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, p.timeout_ns, p.status)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < C::kNP; c += 16) {
+            float o[16];
+            tld(tq + (uint32_t)(C::kColO + c), o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha[(c + i) % NR];
+            tst16(tq + (uint32_t)(C::kColO + c), o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        if (!exchange()) return;  // everyone has read the old maxima
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (tid == r) m[r] = x[r];
+        if (!exchange()) return;
+      }
+      // P buffer g % 2 was last read by the P V of tile g - 2
+      if (g >= 2 && !mbar_wait_warp(sm.pv_done(g & 1), ((g - 2) >> 1) & 1, p.timeout_ns, p.status)) return;
+      uint32_t words[C::kNP / 4];
+#pragma unroll
+      for (int i = 0; i < C::kNP / 4; ++i) words[i] = 0u;
+#pragma unroll
+      for (int r = 0; r < NR; r += 2) {
+        float a = fast_exp2(t[r] - m[r] + kPLog2), b = fast_exp2(t[r + 1] - m[r + 1] + kPLog2);
+        l[r] = fmaf(a, iv, l[r]);
+        l[r + 1] = fmaf(b, iv, l[r + 1]);
+        words[r / 4] |= piece2(a, b) << (16 * ((r >> 1) & 1));
+        words[(NR + r) / 4] |= piece2(a, b) << (16 * ((r >> 1) & 1));
+        words[(2 * NR + r) / 4] |= last2(a, b) << (16 * ((r >> 1) & 1));
+      }
+      uint8_t* pb = sm.p_ptr(g & 1) + tid * 16;
+#pragma unroll
+      for (int c = 0; c < C::kNP / 16; ++c)
+        *reinterpret_cast<uint4*>(pb + c * 16 * kPagedKeys) =
+            make_uint4(words[4 * c], words[4 * c + 1], words[4 * c + 2], words[4 * c + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.p_full(g & 1));
+    }
+
+    // ---- the segment's rows: sums over the threads, O^T, and out (or a partial row)
+    float x[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) x[r] = l[r];
+    const float ws = reduce_scatter<NR, false>(x, lane);
+    float* red = sm.red(use & 1);
+    if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = ws;
+    const float my_m = tid < NR ? m[tid] : 0.0f;
+    if (!exchange()) return;
+    float o[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) o[r] = 0.0f;
+    if (w.nt > 0) {
+      if (!mbar_wait_warp(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, p.timeout_ns, p.status)) return;
+      tc_fence_after();
+      float o1[NR], o2[NR];
+      tld(tq + (uint32_t)C::kColO, o);
+      tld(tq + (uint32_t)(C::kColO + NR), o1);
+      tld(tq + (uint32_t)(C::kColO + 2 * NR), o2);
+      tmem_wait_ld();
+      tc_fence_before();
+#pragma unroll
+      for (int r = 0; r < NR; ++r) o[r] = fmaf(fmaf(o2[r], kInvStep, o1[r]), kInvStep, o[r]);
+    }
+    const int slot = 2 * blockIdx.x + (w.head ? 1 : 0);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (r >= u.rows) break;
+      const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
+      if (w.whole) {
+        const int xr = u.row0 + r;
+        const int64_t row = (int64_t)(u.q.s0 + xr / p.group) * p.Hq + u.kvh * p.group + xr % p.group;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        if (tid < D) static_cast<uint16_t*>(p.out)[row * D + tid] = to_bits<BF16>(o[r] * inv);
+        if (p.lse != nullptr && tid == r)
+          p.lse[row] = L == 0.0f ? -INFINITY : (my_m + (__log2f(L) - kPLog2)) * kLn2;
+      } else {
+        if (tid < D) P.ws_o[((int64_t)slot * NR + r) * D + tid] = o[r];
+        if (tid == r) P.ws_ml[slot * NR + r] = make_float2(my_m, L);
+      }
+    }
+    if (!w.whole && w.head && tid == 0) {
+      PagedCut c;
+      c.parts = paged_parts(w, share);
+      c.token0 = u.q.s0;
+      c.head0 = u.kvh * p.group;
+      c.row0 = u.row0;
+      c.rows = u.rows;
+      P.cuts[blockIdx.x] = c;
+    }
+    // the limits and the Q scale may be replaced once every warp is here
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.q_empty(buf));
+  }
+}
+
+template <int D, int NR, bool BF16>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
+    attn_paged_dec_kernel(const __grid_constant__ DecParams P) {
+  using C = Cfg<D, NR, BF16>;
+  const PagedParams& p = P.c;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Lay<D, NR, BF16> sm;
+  sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  sm.s = smem_u32(sm.base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSK; ++i) {
+      mbar_init(sm.k_full(i), 1);
+      mbar_init(sm.k_empty(i), 1);
+    }
+    for (int i = 0; i < C::kSV; ++i) {
+      mbar_init(sm.v_full(i), 1);
+      mbar_init(sm.v_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sm.s_full(i), 1);
+      mbar_init(sm.p_full(i), 4);
+      mbar_init(sm.pv_done(i), 1);
+      mbar_init(sm.q_full(i), 1);
+      mbar_init(sm.q_empty(i), 5);  // four softmax warps and the MMA warp's commit
+      mbar_init(sm.red_bar(i), 4);
+    }
+    mbar_init(sm.drain(), 1);
+    mbar_init_fence();
+    P.cuts[blockIdx.x].parts = 0;
+  }
+  if (warp == kKWarp && lane == 0) tma_prefetch_desc(&P.tmap_k);
+  if (warp == kVWarp && lane == 0) tma_prefetch_desc(&P.tmap_v);
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(sm.slot()), C::kTmem);
+    tmem_relinquish();
+  }
+  const PagedShare share = paged_share<NR, kThreads>(p, sm.share());
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.slot());
+  PagedWalk<NR> w;
+  w.begin(p, share);
+  if (warp < 4) {
+    softmax_role<D, NR, BF16>(P, sm, w, share, tmem, warp, lane);
+  } else if (warp == kKWarp) {
+    load_role<D, NR, C::kSK>(P, &P.tmap_k, w, sm.k_tile(0), sm.k_full(0), sm.k_empty(0), lane, true);
+  } else if (warp == kVWarp) {
+    load_role<D, NR, C::kSV>(P, &P.tmap_v, w, sm.v_tile(0), sm.v_full(0), sm.v_empty(0), lane, false);
+  } else if (warp == kMmaWarp) {
+    mma_role<D, NR, BF16>(P, sm, w, tmem, lane);
+  } else {
+    q_role<D, NR, BF16>(P, sm, w, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+
+template <int D, int NR, bool BF16>
+cudaError_t launch_dec(const DecParams& P, int grid, cudaStream_t stream) {
+  auto kernel = attn_paged_dec_kernel<D, NR, BF16>;
+  constexpr int smem = Cfg<D, NR, BF16>::kSmem;
+  static std::atomic<bool> ready[128];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128 || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  kernel<<<grid, kThreads, smem, stream>>>(P);
+  return cudaGetLastError();
+}
+
+template <int NR>
+cudaError_t launch_dec_nr(const DecParams& P, bool bf16, int grid, cudaStream_t stream) {
+  if (P.c.D == 128)
+    return bf16 ? launch_dec<128, NR, true>(P, grid, stream) : launch_dec<128, NR, false>(P, grid, stream);
+  return bf16 ? launch_dec<64, NR, true>(P, grid, stream) : launch_dec<64, NR, false>(P, grid, stream);
+}
+
+}  // namespace
+
+int paged_dec_ctas_per_sm(int nr) { return nr <= 16 ? 2 : 1; }
+
+cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream) {
+  DecParams P{};
+  P.tmap_k = L.tmap_k;
+  P.tmap_v = L.tmap_v;
+  P.c = L.c;
+  P.ws_o = L.ws_o;
+  P.ws_ml = L.ws_ml;
+  P.cuts = L.cuts;
+  const double l2e = 1.4426950408889634;
+  P.scale_log2 = (float)((double)L.c.scale * l2e);
+  if (L.c.softcap > 0.0f) {
+    P.k1 = (float)(2.0 * l2e * (double)L.c.scale / (double)L.c.softcap);
+    P.k2 = (float)(-2.0 * (double)L.c.softcap * l2e);
+    P.k3 = (float)((double)L.c.softcap * l2e);
+  }
+  switch (L.rows) {
+    case 4: return launch_dec_nr<4>(P, bf16, L.grid, stream);
+    case 8: return launch_dec_nr<8>(P, bf16, L.grid, stream);
+    case 16: return launch_dec_nr<16>(P, bf16, L.grid, stream);
+    case 32: return launch_dec_nr<32>(P, bf16, L.grid, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gb300_attn

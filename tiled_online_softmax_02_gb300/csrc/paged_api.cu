@@ -2,6 +2,7 @@
 // attn_cache_append_fp8, attn_fwd_paged_fp8 in include/attn.h): argument
 // validation, then one launcher call each.  As for attn_fwd, a request the
 // kernels cannot run is refused with a status before anything is launched.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -114,9 +115,56 @@ extern "C" int attn_cache_append_fp8(const void* k, const void* v, const int64_t
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
+namespace {
+
+// How a call of attn_fwd_paged_fp8 runs: rows of a unit (0: one warp a row), CTAs, and the parts of the workspace.
+struct PagedPlan {
+  int rows, grid;
+  size_t ml_at, cuts_at, bytes;
+};
+
+PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
+  PagedPlan pl{};
+  if (T <= 0 || B <= 0 || Hkv <= 0 || Hq <= 0) return pl;
+  const int group = Hq / Hkv;
+  // rows per (request, kv head) of an even batch; a request with more takes several units
+  const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
+  if (rows > 64) return pl;
+  pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t most = (int64_t)sms * paged_dec_ctas_per_sm(pl.rows);
+  // no more CTAs than there can be tiles
+  const int64_t units = (T * group / pl.rows + B) * Hkv;
+  pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
+  const size_t slots = 2 * (size_t)most * pl.rows;
+  pl.ml_at = slots * D * 4;
+  pl.cuts_at = pl.ml_at + slots * 8;
+  pl.bytes = pl.cuts_at + (size_t)most * sizeof(PagedCut);
+  return pl;
+}
+
+// The cache as a 3-D map of bytes [num_blocks * Hkv, block_size, D]; a box is one block of one head, its rows in
+// the swizzle that the tensor cores read; planes out of range read as zero.
+int encode_cache(CUtensorMap* map, const void* base, int64_t planes, int block_size, int D) {
+  int err = ATTN_OK;
+  auto fn = encode_fn(&err);
+  if (!fn) return err;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)block_size, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)block_size * (cuuint64_t)D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)block_size, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+}  // namespace
+
 extern "C" size_t attn_paged_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, int D) {
-  (void)num_tokens; (void)B; (void)Hq; (void)Hkv; (void)D;
-  return 0;
+  return paged_plan(num_tokens, B, Hq, Hkv, D, 1).bytes;
 }
 
 extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
@@ -138,7 +186,7 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   if ((int64_t)max_blocks * block_size > INT32_MAX) return ATTN_ERR_INVALID_ARG;
   if (num_tokens == 0 || B == 0) return ATTN_OK;  // no row belongs to a request
   if (!q || !out || !q_starts || !total_lengths) return ATTN_ERR_INVALID_ARG;
-  if ((num_blocks > 0 && (!k_cache || !v_cache || !k_scales || !v_scales)) || (max_blocks > 0 && !block_tables))
+  if (num_blocks == 0 || !k_cache || !v_cache || !k_scales || !v_scales || (max_blocks > 0 && !block_tables))
     return ATTN_ERR_INVALID_ARG;
   const size_t need = attn_paged_workspace_bytes(num_tokens, B, Hq, Hkv, D);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
@@ -180,6 +228,27 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   p.softcap = softcap > 0.0f ? softcap : 0.0f;
   p.timeout_ns = wait_timeout_ns();
   p.status = status;
-  const cudaError_t e = launch_attn_paged(p, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream));
+  const bool bf16 = dtype == ATTN_BF16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t max_tiles = std::max<int64_t>(1, ((int64_t)max_blocks * block_size + 127) / 128);
+  const PagedPlan plan = paged_plan(num_tokens, B, Hq, Hkv, D, max_tiles);
+  cudaError_t e;
+  if (plan.rows == 0) {
+    e = launch_attn_paged(p, bf16, st);
+  } else {
+    PagedLaunch L{};
+    L.c = p;
+    int rc = encode_cache(&L.tmap_k, k_cache, (int64_t)num_blocks * Hkv, block_size, D);
+    if (rc == ATTN_OK) rc = encode_cache(&L.tmap_v, v_cache, (int64_t)num_blocks * Hkv, block_size, D);
+    if (rc != ATTN_OK) return rc;
+    L.rows = plan.rows;
+    L.grid = plan.grid;
+    L.ws_o = static_cast<float*>(workspace);
+    L.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ml_at);
+    L.cuts = reinterpret_cast<PagedCut*>(static_cast<char*>(workspace) + plan.cuts_at);
+    L.ml_log2 = 5.0f;
+    e = launch_attn_paged_dec(L, bf16, st);
+    if (e == cudaSuccess && max_tiles > 1) e = launch_attn_paged_join(L, bf16, st);
+  }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

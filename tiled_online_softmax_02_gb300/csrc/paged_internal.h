@@ -77,6 +77,34 @@ struct PagedParams {
 
 cudaError_t launch_cache_assign(const AssignParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const AppendParams& p, int dtype, cudaStream_t stream);
+
+// What the joining kernel is told of a unit that begins in a CTA's share and
+// goes on in the next ones: its partial rows are slot 2 c + 1 of that CTA and
+// slots 2 (c + k) of the CTAs after it.
+struct PagedCut {
+  int parts;      // CTAs that hold a part; 0: no such unit
+  int token0;     // packed row of the request's first token
+  int head0;      // first query head of the kv head
+  int row0, rows; // rows [row0, row0 + rows): token row / group, head row % group
+  int pad[3];
+};
+
+// A launch of one of the attention kernels, and of the kernel that joins the
+// partial rows of units cut between CTAs.
+struct PagedLaunch {
+  PagedParams c;
+  CUtensorMap tmap_k, tmap_v;  // e4m3 [num_blocks * Hkv, block_size, D], box {D, block_size, 1}
+  int rows;                    // query rows of a unit
+  int grid;
+  float* ws_o;                 // [2 * grid][rows][D]: partial rows, sum of 2^(t - m) v8
+  float2* ws_ml;               // [2 * grid][rows]: m, sum of 2^(t - m) / v_scale
+  PagedCut* cuts;              // [grid]
+  float ml_log2;               // the kernel's 2^(t - m) carries this factor (log2)
+};
+
 cudaError_t launch_attn_paged(const PagedParams& p, bool bf16, cudaStream_t stream);
+int paged_dec_ctas_per_sm(int nr);
+cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn_paged_join(const PagedLaunch& L, bool bf16, cudaStream_t stream);
 
 }  // namespace gb300_attn
