@@ -30,20 +30,18 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "paged_mma.cuh"
 #include "paged_sched.cuh"
 
 namespace gb300_attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6, kQWarp = 7;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kStep = 32.0f, kInvStep = 1.0f / 32.0f;  // from one e4m3 piece to the next
+constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6;  // warp 7: Q
+constexpr float kInvStep = 1.0f / kPieceStep;
 // P is carried as 32 * 2^(t - m); the maximum moves when a key passes it by
 // more than 3 (log2 units), so the first piece stays below 256 < 448.
-constexpr float kRise = 3.0f, kPLog2 = 5.0f;
-constexpr float kNone = -1e30f;       // m of a row that has seen no key
-constexpr float kMinVScale = 7.9e-31f;  // 2^-100: a block of zeros may have scale 0
+constexpr float kRise = 3.0f, kPLog2 = kPagedDecLog2;
 
 template <int D, int NR, bool BF16>
 struct Cfg {
@@ -114,20 +112,6 @@ struct Lay {
   __device__ PagedShareSmem* share() const { return reinterpret_cast<PagedShareSmem*>(base + C::kOffShare); }
 };
 
-// Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulator (bits
-// 4-5 = 1), A and B e4m3 (bits 7-9 and 10-12 = 0), major-ness of A / B in bits
-// 15 / 16 (1 = MN-major), N >> 3 in 17-22, M >> 4 in 24-28.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-
-// Shared-memory matrix descriptor; layout 2 = 128-byte swizzle, 4 = 64-byte, 0 = none.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)layout << 61;
-}
-
 __device__ __forceinline__ void mma8_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -161,23 +145,6 @@ __device__ __forceinline__ void tld(uint32_t a, float (&r)[32]) {
 }
 __device__ __forceinline__ void tst16(uint32_t a, const float (&r)[16]) {
   tmem_st16(a, reinterpret_cast<const uint32_t(&)[16]>(r));
-}
-
-// e4m3 pieces of two values (lo in bits 0-7): the piece, and what is left of them times 32.
-__device__ __forceinline__ uint32_t piece2(float& lo, float& hi) {
-  uint16_t b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  lo = (lo - f.x) * kStep;
-  hi = (hi - f.y) * kStep;
-  return b;
-}
-__device__ __forceinline__ uint32_t last2(float lo, float hi) {
-  uint16_t b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
-  return b;
 }
 
 // Reduce-scatter over the warp: on entry each lane holds NR values; on exit
@@ -420,12 +387,6 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
   // every MMA done before tensor memory is given back
   tc_commit_elect(sm.drain());
   mbar_wait_warp(sm.drain(), 0, p.timeout_ns, p.status);
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint16_t to_bits(float x) {
-  if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  else return __half_as_ushort(__float2half_rn(x));
 }
 
 // ------------------------------------------------------------------ softmax

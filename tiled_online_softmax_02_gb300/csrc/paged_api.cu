@@ -117,7 +117,7 @@ extern "C" int attn_cache_append_fp8(const void* k, const void* v, const int64_t
 
 namespace {
 
-// How a call of attn_fwd_paged_fp8 runs: rows of a unit (0: one warp a row), CTAs, and the parts of the workspace.
+// How a call of attn_fwd_paged_fp8 runs: rows of a unit, CTAs, and the parts of the workspace.
 struct PagedPlan {
   int rows, grid;
   size_t ml_at, cuts_at, bytes;
@@ -129,11 +129,10 @@ PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_t
   const int group = Hq / Hkv;
   // rows per (request, kv head) of an even batch; a request with more takes several units
   const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
-  if (rows > 64) return pl;
-  pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTcRows;
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t most = (int64_t)sms * paged_dec_ctas_per_sm(pl.rows);
+  const int64_t most = (int64_t)sms * (pl.rows == kPagedTcRows ? 1 : paged_dec_ctas_per_sm(pl.rows));
   // no more CTAs than there can be tiles
   const int64_t units = (T * group / pl.rows + B) * Hkv;
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
@@ -232,23 +231,24 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t max_tiles = std::max<int64_t>(1, ((int64_t)max_blocks * block_size + 127) / 128);
   const PagedPlan plan = paged_plan(num_tokens, B, Hq, Hkv, D, max_tiles);
+  PagedLaunch L{};
+  L.c = p;
+  int rc = encode_cache(&L.tmap_k, k_cache, (int64_t)num_blocks * Hkv, block_size, D);
+  if (rc == ATTN_OK) rc = encode_cache(&L.tmap_v, v_cache, (int64_t)num_blocks * Hkv, block_size, D);
+  if (rc != ATTN_OK) return rc;
+  L.rows = plan.rows;
+  L.grid = plan.grid;
+  L.ws_o = static_cast<float*>(workspace);
+  L.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ml_at);
+  L.cuts = reinterpret_cast<PagedCut*>(static_cast<char*>(workspace) + plan.cuts_at);
   cudaError_t e;
-  if (plan.rows == 0) {
-    e = launch_attn_paged(p, bf16, st);
+  if (plan.rows == kPagedTcRows) {
+    L.ml_log2 = kPagedTcLog2;
+    e = launch_attn_paged_tc(L, bf16, st);
   } else {
-    PagedLaunch L{};
-    L.c = p;
-    int rc = encode_cache(&L.tmap_k, k_cache, (int64_t)num_blocks * Hkv, block_size, D);
-    if (rc == ATTN_OK) rc = encode_cache(&L.tmap_v, v_cache, (int64_t)num_blocks * Hkv, block_size, D);
-    if (rc != ATTN_OK) return rc;
-    L.rows = plan.rows;
-    L.grid = plan.grid;
-    L.ws_o = static_cast<float*>(workspace);
-    L.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ml_at);
-    L.cuts = reinterpret_cast<PagedCut*>(static_cast<char*>(workspace) + plan.cuts_at);
-    L.ml_log2 = 5.0f;
+    L.ml_log2 = kPagedDecLog2;
     e = launch_attn_paged_dec(L, bf16, st);
-    if (e == cudaSuccess && max_tiles > 1) e = launch_attn_paged_join(L, bf16, st);
   }
+  if (e == cudaSuccess && max_tiles > 1) e = launch_attn_paged_join(L, bf16, st);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

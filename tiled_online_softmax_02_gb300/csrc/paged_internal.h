@@ -91,6 +91,10 @@ struct PagedCut {
 
 // A launch of one of the attention kernels, and of the kernel that joins the
 // partial rows of units cut between CTAs.
+constexpr int kPagedTcRows = 256;
+constexpr float kPagedDecLog2 = 5.0f;  // log2 of the factor that P carries, in each of the kernels
+constexpr float kPagedTcLog2 = 7.0f;
+
 struct PagedLaunch {
   PagedParams c;
   CUtensorMap tmap_k, tmap_v;  // e4m3 [num_blocks * Hkv, block_size, D], box {D, block_size, 1}
@@ -102,9 +106,9 @@ struct PagedLaunch {
   float ml_log2;               // the kernel's 2^(t - m) carries this factor (log2)
 };
 
-cudaError_t launch_attn_paged(const PagedParams& p, bool bf16, cudaStream_t stream);
-int paged_dec_ctas_per_sm(int nr);
-cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream);
+int paged_dec_ctas_per_sm(int rows);
+cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream);  // rows 4, 8, 16 or 32
+cudaError_t launch_attn_paged_tc(const PagedLaunch& L, bool bf16, cudaStream_t stream);   // rows kPagedTcRows
 cudaError_t launch_attn_paged_join(const PagedLaunch& L, bool bf16, cudaStream_t stream);
 
 }  // namespace gb300_attn
