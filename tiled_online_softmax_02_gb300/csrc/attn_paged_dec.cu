@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr int kBars = 2 * kSK + 2 * kSV + 13;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
-  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShareSmem) + 1024;  // + alignment slack
+  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;  // + alignment slack
   static constexpr int kColO = 2 * kNQ;                           // TMEM: S^T twice, then O^T
   static constexpr int kCols = 2 * kNQ + kNP;
   static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -109,7 +109,7 @@ struct Lay {
   __device__ uint32_t red_bar(int i) const { return rest(10 + i); }
   __device__ uint32_t drain() const { return rest(12); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
-  __device__ PagedShareSmem* share() const { return reinterpret_cast<PagedShareSmem*>(base + C::kOffShare); }
+  __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
 
 __device__ __forceinline__ void mma8_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -199,15 +199,15 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
                                           uint32_t full0, uint32_t empty0, int lane, bool report) {
   const PagedParams& p = P.c;
   constexpr int kTile = kPagedKeys * D;
-  const int per = kPagedKeys / p.block_size, box = p.block_size * D;
+  const int per = kPagedKeys >> p.block_shift, box = p.block_size * D;
   int g = 0;
   bool ok = true;
   for (; ok && !w.done(); w.next(p)) {
-    const int64_t cap = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    const int valid = paged_valid(p, w.u.q);
     const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
     auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
-      const int64_t i = (int64_t)t * per + lane;
-      if (lane >= per || i * p.block_size >= cap) return -1;
+      const int i = t * per + lane;
+      if (lane >= per || i >= (valid + p.block_size - 1) >> p.block_shift) return -1;
       const int e = __ldg(table + i);
       return e >= 0 && e < p.num_blocks ? e : -2;
     };
@@ -327,16 +327,15 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
   int g = 0;
   bool pending = false;   // a tile whose P V is still to be issued
   bool pend_first = false;
-  int64_t pend_key0 = 0, pend_valid = 0;
+  int pend_valid = kPagedKeys;  // valid keys from its first one on
   bool ok = true;
   auto pv = [&](int t) -> bool {
     if (!mbar_wait_warp(sm.p_full(t & 1), (t >> 1) & 1, p.timeout_ns, p.status)) return false;
     const int vs = t % C::kSV;
     if (!mbar_wait_warp(sm.v_full(vs), (t / C::kSV) & 1, p.timeout_ns, p.status)) return false;
-    if (pend_valid < pend_key0 + kPagedKeys) {
+    if (pend_valid < kPagedKeys) {
       // slots past the request's last key may hold NaN bytes: P is 0 there but 0 * NaN is not
-      const int r0 = pend_valid > pend_key0 ? (int)(pend_valid - pend_key0) : 0;
-      for (int c = r0 * (D / 16) + lane; c < kPagedKeys * (D / 16); c += 32)
+      for (int c = max(pend_valid, 0) * (D / 16) + lane; c < kPagedKeys * (D / 16); c += 32)
         *reinterpret_cast<uint4*>(sm.v_ptr(vs) + c * 16) = make_uint4(0u, 0u, 0u, 0u);  // whole rows: the swizzle does not matter
       fence_proxy_async_smem();
       __syncwarp();
@@ -361,7 +360,7 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
       pending = false;
     }
     if (!mbar_wait_warp(sm.q_full(buf), (w.index >> 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
-    const int64_t valid = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    const int valid = paged_valid(p, w.u.q);
     for (int n = 0; ok && n < w.nt; ++n, ++g) {
       const int ks = g % C::kSK;
       if (!mbar_wait_warp(sm.k_full(ks), (g / C::kSK) & 1, p.timeout_ns, p.status)) { ok = false; break; }
@@ -376,8 +375,7 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
       if (pending && !pv(g - 1)) { ok = false; break; }
       pending = true;
       pend_first = n == 0;
-      pend_key0 = (int64_t)(w.t0 + n) * kPagedKeys;
-      pend_valid = valid;
+      pend_valid = valid - (w.t0 + n) * kPagedKeys;
     }
     // Q and the limits are free once this unit's S^T products are done and its rows' softmax has read
     // them: the softmax arrives for itself
@@ -394,7 +392,7 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
 // a unit's end, d = tid of O^T.
 template <int D, int NR, bool BF16>
 __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR, BF16>& sm, PagedWalk<NR> w,
-                                             const PagedShare& share, uint32_t tmem, int warp, int lane) {
+                                             uint32_t tmem, int warp, int lane) {
   using C = Cfg<D, NR, BF16>;
   const PagedParams& p = P.c;
   const int tid = warp * 32 + lane;
@@ -412,12 +410,12 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
   for (; !w.done(); w.next(p)) {
     const PagedUnit& u = w.u;
     const int buf = w.index & 1;
-    const int64_t valid = min(u.q.total, (int64_t)p.width * p.block_size);
+    const int valid = paged_valid(p, u.q);
     const int32_t* table = p.tables + (int64_t)u.b * p.width;
     // block and scales of this thread's key, a tile ahead of their use
     auto block_of = [&](int n) {
-      const int64_t j = (int64_t)(w.t0 + n) * kPagedKeys + tid;
-      const int b = n < w.nt && j < valid ? __ldg(table + (int)j / p.block_size) : -1;
+      const uint32_t j = (uint32_t)(w.t0 + n) * kPagedKeys + tid;
+      const int b = n < w.nt && j < (uint32_t)valid ? __ldg(table + (j >> p.block_shift)) : -1;
       return b >= 0 && b < p.num_blocks ? b : -1;
     };
     float ks_next = 0.0f, vs_next = 1.0f;
@@ -597,7 +595,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
     }
     if (!w.whole && w.head && tid == 0) {
       PagedCut c;
-      c.parts = paged_parts(w, share);
+      c.parts = paged_parts(w, sm.share());
       c.token0 = u.q.s0;
       c.head0 = u.kvh * p.group;
       c.row0 = u.row0;
@@ -648,15 +646,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
     tmem_alloc(smem_u32(sm.slot()), C::kTmem);
     tmem_relinquish();
   }
-  const PagedShare share = paged_share<NR, kThreads>(p, sm.share());
+  paged_share<NR, kThreads>(p, sm.share());
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.slot());
   PagedWalk<NR> w;
-  w.begin(p, share);
+  w.begin(p, sm.share());
   if (warp < 4) {
-    softmax_role<D, NR, BF16>(P, sm, w, share, tmem, warp, lane);
+    softmax_role<D, NR, BF16>(P, sm, w, tmem, warp, lane);
   } else if (warp == kKWarp) {
     load_role<D, NR, C::kSK>(P, &P.tmap_k, w, sm.k_tile(0), sm.k_full(0), sm.k_empty(0), lane, true);
   } else if (warp == kVWarp) {

@@ -3,8 +3,9 @@
 // 2^(t - m_k) v8, its maximum m_k and L_k = sum of 2^(t - m_k) / v_scale; with
 // M = max m_k the row is
 //   sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) L_k   (0 when the latter is 0).
-// Bound: latency; the partial rows lie in L2.  One warp a row, lanes over d;
-// the parts' (m, L) are read 32 at a time and their O_k in flight together.
+// Bound: latency; the partial rows lie in L2.  A warp takes a row, lanes over
+// d, with several of its parts in flight; where the parts are few (long work:
+// most units are cut once), four rows and all their parts.
 // A programmatic dependent of the attention kernel: it may be scheduled while
 // that one drains, and waits for all of it before it reads.
 #include <cuda_bf16.h>
@@ -15,54 +16,29 @@
 namespace gb300_attn {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kRowsPerCta = 32;
+constexpr int kFew = 4;  // up to this many parts a warp takes four rows at once
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) attn_paged_join_kernel(const PagedCut* cuts, const float* ws_o,
-                                                                      const float2* ws_ml, int unit_rows, int Hq,
-                                                                      int group, float ml_log2, uint16_t* out,
-                                                                      float* lse) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const PagedCut cut = cuts[c];
-  if (r >= cut.rows || cut.parts == 0) return;
-  auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * unit_rows + r; };
-  float M = -INFINITY;
-  for (int k = lane; k < cut.parts; k += 32) M = fmaxf(M, ws_ml[slot(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  constexpr int V = D / 32;
-  float acc[V], L = 0.0f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  for (int k0 = 0; k0 < cut.parts; k0 += 32) {
-    float w = 0.0f;
-    if (k0 + lane < cut.parts) {
-      const float2 ml = ws_ml[slot(k0 + lane)];
-      w = exp2f(ml.x - M);
-      L = fmaf(w, ml.y, L);
-    }
-    const int n = min(32, cut.parts - k0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* o = ws_o + slot(k0 + k) * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(o);
-        acc[0] = fmaf(wk, x.x, acc[0]);
-        acc[1] = fmaf(wk, x.y, acc[1]);
-        acc[2] = fmaf(wk, x.z, acc[2]);
-        acc[3] = fmaf(wk, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(o);
-        acc[0] = fmaf(wk, x.x, acc[0]);
-        acc[1] = fmaf(wk, x.y, acc[1]);
-      }
+template <int D>
+struct RowVec {
+  static constexpr int V = D / 32;  // values of a lane
+  float x[V];
+  __device__ __forceinline__ void load(const float* row, int lane) {
+    if constexpr (V == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(row + lane * 4);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(row + lane * 2);
+      x[0] = v.x; x[1] = v.y;
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ void store_row(const PagedCut& cut, int r, int Hq, int group, float ml_log2, uint16_t* out,
+                                          float* lse, int lane, const float (&acc)[D / 32], float M, float L) {
+  constexpr int V = D / 32;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   const int x = cut.row0 + r;
   const int64_t row = (int64_t)(cut.token0 + x / group) * Hq + cut.head0 + x % group;
@@ -85,9 +61,92 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_kernel(const Page
 }
 
 template <int D, bool BF16>
+__global__ void __launch_bounds__(kWarps * 32) attn_paged_join_kernel(const PagedCut* cuts, const float* ws_o,
+                                                                      const float2* ws_ml, int unit_rows, int Hq,
+                                                                      int group, float ml_log2, uint16_t* out,
+                                                                      float* lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = D / 32;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PagedCut cut = cuts[c];
+  const int row0 = blockIdx.y * kRowsPerCta;
+  if (cut.parts == 0 || row0 >= cut.rows) return;
+  auto slot = [&](int k, int r) { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * unit_rows + r; };
+  if (cut.parts <= kFew) {
+    // rows row0 + warp + 8 i: lane 4 i + k holds (m, L) of row i, part k; all parts of all four rows in flight
+    const int mi = (lane >> 2) & 3, mk = min(lane & 3, cut.parts - 1);
+    const int mr = min(row0 + warp + kWarps * mi, cut.rows - 1);
+    const float2 ml = ws_ml[slot(mk, mr)];
+    RowVec<D> o[4][kFew];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const int r = row0 + warp + kWarps * i;
+        if (r < cut.rows && k < cut.parts) o[i][k].load(ws_o + slot(k, r) * D, lane);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + warp + kWarps * i;
+      if (r >= cut.rows) break;
+      float m[kFew], M = -INFINITY, L = 0.0f, acc[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        m[k] = __shfl_sync(0xffffffffu, ml.x, 4 * i + k);
+        if (k < cut.parts) M = fmaxf(M, m[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const float l = __shfl_sync(0xffffffffu, ml.y, 4 * i + k);
+        if (k >= cut.parts) continue;
+        const float w = exp2f(m[k] - M);
+        L = fmaf(w, l, L);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[i][k].x[v], acc[v]);
+      }
+      store_row<D, BF16>(cut, r, Hq, group, ml_log2, out, lse, lane, acc, M, L);
+    }
+    return;
+  }
+  for (int r = row0 + warp; r < min(cut.rows, row0 + kRowsPerCta); r += kWarps) {
+    float M = -INFINITY, L = 0.0f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+    for (int k = lane; k < cut.parts; k += 32) M = fmaxf(M, ws_ml[slot(k, r)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int k0 = 0; k0 < cut.parts; k0 += 32) {
+      float w = 0.0f;  // 0 past the last part
+      if (k0 + lane < cut.parts) {
+        const float2 ml = ws_ml[slot(k0 + lane, r)];
+        w = exp2f(ml.x - M);
+        L = fmaf(w, ml.y, L);
+      }
+      const int n = min(32, cut.parts - k0);
+      for (int k = 0; k < n; k += 8) {  // eight parts in flight
+        RowVec<D> o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j].load(ws_o + slot(min(k0 + k + j, cut.parts - 1), r) * D, lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wk = __shfl_sync(0xffffffffu, w, k + j);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = k + j < n ? fmaf(wk, o[j].x[v], acc[v]) : acc[v];
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    store_row<D, BF16>(cut, r, Hq, group, ml_log2, out, lse, lane, acc, M, L);
+  }
+}
+
+template <int D, bool BF16>
 cudaError_t launch_t(const PagedLaunch& L, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)L.grid, (unsigned)((L.rows + kWarps - 1) / kWarps), 1);
+  cfg.gridDim = dim3((unsigned)L.grid, (unsigned)((L.rows + kRowsPerCta - 1) / kRowsPerCta), 1);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -26,9 +26,9 @@
 //
 // One CTA an SM walks its share of the line of key tiles (paged_sched.cuh).
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two lanes, thread =
-// row, which also bring the next unit's Q rows into pieces before they finish
-// the last; warps 8-11 widen V; warp 12 loads (TMA), 13 issues MMAs, 14 looks
-// up scales.  Registers move from the latter eight warps to the softmax.
+// row, which also bring the next unit's Q into pieces before they store the
+// last one's rows; warps 8-11 widen V; warp 12 loads (TMA), 13 issues MMAs, 14
+// looks up scales and prefetches the next unit's Q rows into L2.  Registers move from the latter eight warps to the softmax.
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
 #include <atomic>
 
@@ -62,13 +62,14 @@ struct Cfg {
   static constexpr int kOffV8 = kOffK + kSK * kTile8;
   static constexpr int kOffV = kOffV8 + kSV8 * kTile8;
   static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kSC][kGroups]: k scale, log2 v scale, 1 / v scale
-  static constexpr int kOffBar = kOffSc + kSC * kGroups * 16;
+  static constexpr int kOffQe = kOffSc + kSC * kGroups * 16;  // int8 [256]: log2 of the Q rows' scales
+  static constexpr int kOffBar = kOffQe + kRows;
   // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_full, sc_empty [kSC],
   // q_full, s_full, p_full, o_final [2], drain
   static constexpr int kBars = 2 * (kSK + kSV8 + kSV + kSC) + 9;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
-  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShareSmem) + 1024;
+  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kOffBar % 8 == 0 && kQLane % 1024 == 0, "alignment");
 };
@@ -101,8 +102,9 @@ struct Lay {
   __device__ uint32_t p_full(int t) const { return rest(2 * kSC + 4 + t); }
   __device__ uint32_t o_final(int t) const { return rest(2 * kSC + 6 + t); }
   __device__ uint32_t drain() const { return rest(2 * kSC + 8); }
+  __device__ int8_t* q_exp() const { return reinterpret_cast<int8_t*>(base + C::kOffQe); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
-  __device__ PagedShareSmem* share() const { return reinterpret_cast<PagedShareSmem*>(base + C::kOffShare); }
+  __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
 
 struct PagedTcParams {
@@ -112,8 +114,9 @@ struct PagedTcParams {
   float* ws_o;         // [2 * CTAs][256][D]
   float2* ws_ml;       // [2 * CTAs][256]
   PagedCut* cuts;      // [CTAs]
-  float scale_abs;     // |scale|: its sign goes into Q, so larger raw scores are larger scores
-  float sc_in, sc_out; // soft-cap: sc_out tanh(sc_in s), log2 units
+  float scale_log2;    // |scale| log2 e: its sign goes into Q, so larger raw scores are larger scores
+  bool aligned32;      // out and ws_o begin on 32-byte boundaries
+  float sc_in, sc_out; // soft-cap, from and to log2 units: sc_out tanh(sc_in s)
 };
 
 using Walk = PagedWalk<kRows>;
@@ -129,16 +132,16 @@ template <int D, bool BF16>
 __device__ __forceinline__ void load_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, int lane) {
   using C = Cfg<D, BF16>;
   const PagedParams& p = P.c;
-  const int per = BN / p.block_size, box = p.block_size * D;
+  const int per = BN >> p.block_shift, box = p.block_size * D;
   int g = 0;
   bool ok = true;
   int k_done = 0, v_done = 0;
   for (; ok && !w.done(); w.next(p)) {
-    const int64_t cap = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    const int valid = paged_valid(p, w.u.q);
     const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
     auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
-      const int64_t i = (int64_t)t * per + lane;
-      if (lane >= per || i * p.block_size >= cap) return -1;
+      const int i = t * per + lane;
+      if (lane >= per || i >= (valid + p.block_size - 1) >> p.block_shift) return -1;
       const int e = __ldg(table + i);
       return e >= 0 && e < p.num_blocks ? e : -2;
     };
@@ -175,11 +178,18 @@ __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, 
   const PagedParams& p = P.c;
   int g = 0;
   for (; !w.done(); w.next(p)) {
-    const int64_t valid = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    Walk x = w;
+    x.next(p);
+    if (!x.done()) {  // the next unit's Q: whole tokens of the kv head's query heads
+      const int t0 = x.u.row0 / p.group, t1 = (x.u.row0 + x.u.rows - 1) / p.group;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)x.u.q.s0 * p.q_stride + x.u.kvh * p.group * D;
+      for (int i = t0 + lane; i <= t1; i += 32) bulk_prefetch_l2(q + i * p.q_stride, (uint32_t)(p.group * D * 2));
+    }
+    const int valid = paged_valid(p, w.u.q);
     const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
     auto block_of = [&](int n) {
-      const int64_t j = (int64_t)(w.t0 + n) * BN + lane * 16;
-      const int b = lane < kGroups && n < w.nt && j < valid ? __ldg(table + (int)j / p.block_size) : -1;
+      const uint32_t j = (uint32_t)(w.t0 + n) * BN + lane * 16;
+      const int b = lane < kGroups && n < w.nt && j < (uint32_t)valid ? __ldg(table + (j >> p.block_shift)) : -1;
       return b >= 0 && b < p.num_blocks ? b : -1;
     };
     int blk = block_of(0), blk1 = block_of(1);
@@ -199,7 +209,7 @@ __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, 
       blk1 = block_of(n + 2);
       const int st = g % kSC;
       if (g >= kSC && !mbar_wait_warp(sm.sc_empty(st), ((g / kSC) - 1) & 1, p.timeout_ns, p.status)) return;
-      if (lane < kGroups) sm.scales(st)[lane] = make_float4(k0 * P.scale_abs, __log2f(v0), 1.0f / v0, 0.0f);
+      if (lane < kGroups) sm.scales(st)[lane] = make_float4(k0 * P.scale_log2, __log2f(v0), 1.0f / v0, 0.0f);
       __syncwarp();
       if (lane == 0) mbar_arrive(sm.sc_full(st));
     }
@@ -220,17 +230,16 @@ __device__ __forceinline__ void widen_role(const PagedTcParams& P, const Lay<D, 
   int g = 0;
   const int c = lane & 3, r8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);  // row of a group of 8
   for (; !w.done(); w.next(p)) {
-    const int64_t valid = min(w.u.q.total, (int64_t)p.width * p.block_size);
+    const int valid = paged_valid(p, w.u.q);
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int s8 = g % C::kSV8, sv = g % C::kSV;
       if (!mbar_wait_warp(sm.v8_full(s8), (g / C::kSV8) & 1, p.timeout_ns, p.status)) return;
       if (g >= C::kSV && !mbar_wait_warp(sm.v_empty(sv), ((g / C::kSV) - 1) & 1, p.timeout_ns, p.status)) return;
-      const int64_t left = valid - (int64_t)(w.t0 + n) * BN;
-      const int rows = left < BN ? (int)left : BN;
+      const int rows = min(valid - (w.t0 + n) * BN, BN);
       const uint8_t* src = sm.v8_ptr(s8);
       uint8_t* dst = sm.v_ptr(sv);
       constexpr int kIters = BN / 8 * (D / 64) / 4;
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < kIters; ++i) {
         const int it = i * 4 + warp;
         const int row = (it / (D / 64)) * 8 + r8, half = it % (D / 64);
@@ -319,7 +328,7 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
                     (!first || k > 0) ? 1u : 0u);
   };
   for (; ok && !w.done(); w.next(p)) {
-    if (w.nt == 0) continue;  // no S: the softmax warps take no Q of it either
+    if (w.nt == 0) continue;  // no S, and no Q was brought
     const bool two = lane_on(w.u, 1);
     for (int n = 0; ok && n <= w.nt; ++n) {
       const int sv = (g + n - 1 + C::kSV) % C::kSV, ks = (g + n) % C::kSK;
@@ -359,116 +368,131 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
 }
 
 // ------------------------------------------------------------------ softmax
-// This thread's row of Q as e4m3 pieces into its lane's buffer.  Returns
-// 1 / the row's scale.
+// A lane's rows of Q as e4m3 pieces, K-major in the swizzle of the row width;
+// rows past the unit's are zeros.  Each warp brings its own 32 rows: a row is
+// D / 8 threads wide (16 bytes each), so an instruction loads 2 (D = 64: 4)
+// rows, and half the warp's rows are in flight together.  It stands between
+// two units, where the tensor core waits for it, so it is written for few
+// instructions: the row's largest |x| on packed 16-bit integers (magnitudes
+// order as their bits), the pieces and their rests on packed f16, which holds
+// x scaled below 256 exactly down to 2^-24.  Returns 1 / the scale of this
+// thread's own row.
 template <int D, bool BF16>
-__device__ __forceinline__ float bring_q(const PagedTcParams& P, const Lay<D, BF16>& sm, const PagedUnit& u, int t, int row) {
+__device__ __forceinline__ float bring_q(const PagedTcParams& P, const Lay<D, BF16>& sm, const PagedUnit& u, int t,
+                                         int wq, int lane) {
   using C = Cfg<D, BF16>;
   const PagedParams& p = P.c;
-  const int x = u.row0 + t * BM + row;
-  const bool in = t * BM + row < u.rows;
-  uint4 raw[D / 8];
-  if (in) {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                    (int64_t)(u.q.s0 + x / p.group) * p.q_stride +
-                                                    (u.kvh * p.group + x % p.group) * D);
+  constexpr int kVec = D / 8, kPer = 32 / kVec, kBatch = 16 / kPer;
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on are not finite
+  const int c = lane % kVec, sub = lane / kVec;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + u.kvh * p.group * D + c * 8;
+  uint8_t* dst = sm.q_ptr(t) + (c & 1) * 8;
+  int8_t* exps = sm.q_exp() + t * BM;
+  const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;
+  // this thread's first row as (token, head); the next ones kPer rows on
+  int r = wq * 32 + sub;
+  int tok = (u.row0 + t * BM + r) / p.group, head = (u.row0 + t * BM + r) - tok * p.group;
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    uint4 raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) raw[i] = __ldg(q + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  auto widen = [&](uint32_t v, float& a, float& b) {
-    if constexpr (BF16) {
-      a = __uint_as_float(v << 16);
-      b = __uint_as_float(v & 0xffff0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-      a = f.x;
-      b = f.y;
+    for (int i = 0; i < kBatch; ++i) {
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (t * BM + r + i * kPer < u.rows)
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride + head * D));
+      for (head += kPer; head >= p.group; head -= p.group) ++tok;
     }
-  };
-  float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const uint32_t e[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    for (int i = 0; i < kBatch; ++i, r += kPer) {
+      const uint32_t e[4] = {raw[i].x ^ sign, raw[i].y ^ sign, raw[i].z ^ sign, raw[i].w ^ sign};
+      const uint32_t top2 = __vmaxu2(__vmaxu2(e[0] & 0x7fff7fffu, e[1] & 0x7fff7fffu),
+                                     __vmaxu2(e[2] & 0x7fff7fffu, e[3] & 0x7fff7fffu));
+      uint32_t top = max(top2 & 0xffffu, top2 >> 16);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float a, b;
-      widen(e[k], a, b);
-      a = fabsf(a);
-      b = fabsf(b);
-      top = a < INFINITY ? fmaxf(top, a) : top;
-      top = b < INFINITY ? fmaxf(top, b) : top;
-    }
-  }
-  // the power of two that brings the largest element into [128, 256)
-  int ex = (int)(__float_as_uint(top) >> 23) - 127;
-  ex = top > 0.0f ? min(max(7 - ex, -120), 120) : 0;
-  const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-  const float mul = P.c.scale < 0.0f ? -up : up;
-  uint8_t* dst = sm.q_ptr(t) + row * D;
+      for (int o = 1; o < kVec; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool odd = top >= kInf;  // the row holds an infinity or NaN: its scores become NaN
+      // the power of two that brings the row's largest element into [128, 256)
+      int ex;
+      if constexpr (BF16) ex = (int)(top >> 7) - 127;
+      else ex = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
+      ex = top == 0u || odd ? 0 : min(max(7 - ex, -120), 120);
+      const float mul = __uint_as_float((uint32_t)(ex + 127) << 23);
+      if (c == 0) exps[r] = (int8_t)ex;
+      uint32_t h[4];  // scaled, f16 pairs
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    uint32_t w[3][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 r = raw[2 * c + (k >> 1)];
-      const uint32_t e0 = (k & 1) ? r.z : r.x, e1 = (k & 1) ? r.w : r.y;
-      float v[4];
-      widen(e0, v[0], v[1]);
-      widen(e1, v[2], v[3]);
-      bool odd = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        odd |= !(fabsf(v[i]) < INFINITY);
-        v[i] *= mul;
+      for (int k = 0; k < 4; ++k) {
+        float a, b2;
+        if constexpr (BF16) {
+          a = __uint_as_float(e[k] << 16);
+          b2 = __uint_as_float(e[k] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&e[k]));
+          a = f.x;
+          b2 = f.y;
+        }
+        f2_split(fmul2(f2(a, b2), f2(mul, mul)), a, b2);
+        const __half2 hh = __floats2half2_rn(a, b2);
+        h[k] = *reinterpret_cast<const uint32_t*>(&hh);
       }
+      // 8 bytes of chunk c / 2 of the row, whose index the swizzle XORs
+      const int at = D == 128 ? ((c >> 1) ^ (r & 7)) : ((c >> 1) ^ ((r >> 1) & 3));
+      uint8_t* out = dst + r * D + at * 16;
 #pragma unroll
-      for (int i = 0; i < C::kQP; ++i) {
-        uint32_t two[2];
+      for (int j = 0; j < C::kQP; ++j) {
+        uint32_t w[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint16_t b;
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-          two[j] = b;
-          if (i + 1 < C::kQP) {
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-            v[2 * j] -= f.x;
-            v[2 * j + 1] -= f.y;
+        for (int k = 0; k < 2; ++k) {
+          uint16_t b0, b1;
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(h[2 * k]));
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h[2 * k + 1]));
+          asm("mov.b32 %0, {%1, %2};" : "=r"(w[k]) : "h"(b0), "h"(b1));
+          if (j + 1 < C::kQP) {
+            uint32_t f0, f1;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f0) : "h"(b0));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f1) : "h"(b1));
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * k]) : "r"(h[2 * k]), "r"(f0));
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * k + 1]) : "r"(h[2 * k + 1]), "r"(f1));
           }
         }
-        w[i][k] = two[0] | (two[1] << 16);
+        if (odd) w[0] = w[1] = j == 0 ? 0x7f7f7f7fu : 0u;
+        *reinterpret_cast<uint2*>(out + j * (BM * D)) = make_uint2(w[0], w[1]);
       }
-      if (odd) w[0][k] = 0x7f7f7f7fu;  // an element that is not finite makes its row's scores NaN
     }
-    const int at = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-#pragma unroll
-    for (int i = 0; i < C::kQP; ++i)
-      *reinterpret_cast<uint4*>(dst + i * (BM * D) + at * 16) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
   }
-  return 1.0f / up;
+  __syncwarp();
+  return __uint_as_float((uint32_t)(127 - exps[wq * 32 + lane]) << 23);
+}
+
+// 32 bytes of a row, which lies apart from other threads' rows: one store of
+// a whole sector where the buffer allows it, else two.
+__device__ __forceinline__ void store_32b(void* ptr, const uint32_t* v, bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(ptr)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(ptr)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 template <int D, bool BF16, bool SOFTCAP>
-__device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, const PagedShare& share,
-                                             uint32_t tmem, int warp, int lane) {
+__device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, uint32_t tmem,
+                                             int warp, int lane) {
   const PagedParams& p = P.c;
   const int t = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
   const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + t * 128;
   const uint32_t o_addr = s_addr - t * 128 + kColO + t * 128;
-  int g = 0, sc = 0, oc = 0;  // tiles of the line, S tiles and finished units of this lane
-  float qinv = 0.0f;
-  auto q_ready = [&](const Walk& x) {
+  int g = 0, sc = 0, oc = 0;  // tiles of the line, S tiles and units with tiles of this lane
+  float qinv = 1.0f;          // 1 / the scale of this row's Q pieces
+  auto next_q = [&](const Walk& x) {
     if (x.done() || x.nt == 0 || !lane_on(x.u, t)) return;
-    qinv = bring_q<D, BF16>(P, sm, x.u, t, row);
+    qinv = bring_q<D, BF16>(P, sm, x.u, t, wq, lane);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(sm.q_full(t));
   };
-  q_ready(w);
+  next_q(w);
   while (!w.done()) {
     const PagedUnit u = w.u;
     const int nt = w.nt, t0 = w.t0;
@@ -479,7 +503,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         if (lane == 0) mbar_arrive(sm.sc_empty(g % kSC));
       }
       w.next(p);
-      q_ready(w);
+      next_q(w);
       continue;
     }
     const int x0 = u.row0 + t * BM;
@@ -491,17 +515,9 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     for (int n = 0; n < nt; ++n, ++g, ++sc) {
       const int key0 = (t0 + n) * BN;
       if (!mbar_wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
-      // raw score -> log2 units: x km + lv.  km stays above 0, so that -inf does
-      float km[kGroups], lv[kGroups], iv[kGroups];
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const float4 s = sm.scales(g % kSC)[i];
-        km[i] = fmaxf(s.x * qs, 1.2e-38f);
-        lv[i] = s.y;
-        iv[i] = s.z;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm.sc_empty(g % kSC));
+      // a group's (k scale |scale| log2 e, log2 v scale, 1 / v scale); raw scores times the row's
+      // factor and the first are in log2 units.  The product stays above 0, so that -inf stays -inf
+      const float4* scl = sm.scales(g % kSC);
       if (!mbar_wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
       tc_fence_after();
       float x[BN];
@@ -512,13 +528,13 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         // tanh(scale s / c) as the raw value, c log2 e the factor.  The hardware tanh: its error, 2^-11 of c, is
         // below what a 16-bit output holds of scores that c caps
 #pragma unroll
-        for (int i = 0; i < BN; ++i) x[i] = fast_tanh(x[i] * (km[i / 16] * P.sc_in));
+        for (int i = 0; i < kGroups; ++i) {
+          const float in = scl[i].x * qs * P.sc_in;
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) km[i] = P.sc_out;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) km[i] = fmaxf(km[i] * 1.4426950408889634f, 1.2e-38f);
+          for (int k = 0; k < 16; ++k) x[16 * i + k] = fast_tanh(x[16 * i + k] * in);
+        }
       }
+      auto factor = [&](float k) { return SOFTCAP ? P.sc_out : fmaxf(k * qs, 1.2e-38f); };
       if (key0 < full_lo || key0 + BN > full_hi) {
         const int lo = min(max(lim.x - key0, 0), BN), hi = min(max(lim.y - key0, 0), BN);
         const uint32_t span = hi > lo ? (uint32_t)(hi - lo) : 0u;
@@ -534,7 +550,8 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
           a = fmax3(a, x[16 * i + k], x[16 * i + k + 1]);
           b = fmax3(b, x[16 * i + k + 2], x[16 * i + k + 3]);
         }
-        m_tile = fmaxf(m_tile, fmaf(fmaxf(a, b), km[i], lv[i]));
+        const float2 kl = *reinterpret_cast<const float2*>(scl + i);
+        m_tile = fmaxf(m_tile, fmaf(fmaxf(a, b), factor(kl.x), kl.y));
       }
       float alpha = 1.0f;
       const bool rise = m_tile > m_run + kRise;
@@ -551,7 +568,9 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int i = ch * 2 + h;
-          const uint64_t mul = f2(km[i], km[i]), add = f2(lv[i] + off, lv[i] + off);
+          const float4 s4 = scl[i];
+          const float kf = factor(s4.x);
+          const uint64_t mul = f2(kf, kf), add = f2(s4.y + off, s4.y + off);
           uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -563,7 +582,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
             const __half2 hh = __floats2half2_rn(a, b);
             pk[8 * h + k] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          sum = ffma2(fadd2(part[0], part[1]), f2(iv[i], iv[i]), sum);
+          sum = ffma2(fadd2(part[0], part[1]), f2(s4.z, s4.z), sum);
         }
         tmem_st16(s_addr + ch * 16, pk);
       }
@@ -584,21 +603,26 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sm.p_full(t));
+      if (lane == 0) {
+        mbar_arrive(sm.sc_empty(g % kSC));
+        mbar_arrive(sm.p_full(t));
+      }
     }
-    // ---- the next unit's Q (this lane's S of the last tile has been read, so its Q is free), then this unit's rows
-    const bool whole = w.whole, head = w.head;
-    if (!whole && head && threadIdx.x == 0) {
+    // ---- the segment's rows
+    if (!w.whole && w.head && threadIdx.x == 0) {
       PagedCut c;
-      c.parts = paged_parts(w, share);
+      c.parts = paged_parts(w, sm.share());
       c.token0 = u.q.s0;
       c.head0 = u.kvh * p.group;
       c.row0 = u.row0;
       c.rows = u.rows;
       P.cuts[blockIdx.x] = c;
     }
+    const bool whole = w.whole, head = w.head;
+    // the next unit's Q first: this lane's last S has been read, so its Q is free, and the
+    // tensor core can begin the next unit while this one's rows are stored
     w.next(p);
-    q_ready(w);
+    next_q(w);
     if (nt > 0) {
       if (!mbar_wait_warp(sm.o_final(t), oc & 1, p.timeout_ns, p.status)) return;
       ++oc;
@@ -624,13 +648,13 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         for (int i = 0; i < 16; ++i)
           v[i] = (uint32_t)to_bits<BF16>(__uint_as_float(o[2 * i]) * inv) |
                  (uint32_t)to_bits<BF16>(__uint_as_float(o[2 * i + 1]) * inv) << 16;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * D + k * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + out_row * D + k * 32;
+        store_32b(dst, &v[0], P.aligned32);
+        store_32b(dst + 16, &v[8], P.aligned32);
       } else if (mine) {
-        uint4* dst = reinterpret_cast<uint4*>(P.ws_o + ws_row * D + k * 32);
+        float* dst = P.ws_o + ws_row * D + k * 32;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) store_32b(dst + 8 * i, &o[8 * i], P.aligned32);
       }
     }
     if (mine && whole && p.lse != nullptr)
@@ -685,21 +709,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     tmem_alloc(smem_u32(sm.slot()), 512);
     tmem_relinquish();
   }
-  const PagedShare share = paged_share<kRows, kThreads>(p, sm.share());
+  paged_share<kRows, kThreads>(p, sm.share());
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.slot());
-  // 512 threads of 128 registers at launch: 256 x 200 + 256 x 56 = 512 x 128
+  // 512 threads of 128 registers at launch: 256 x 192 + 256 x 64 = 512 x 128
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     Walk w;
-    w.begin(p, share);
-    softmax_role<D, BF16, SOFTCAP>(P, sm, w, share, tmem, warp, lane);
+    w.begin(p, sm.share());
+    softmax_role<D, BF16, SOFTCAP>(P, sm, w, tmem, warp, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     Walk w;
-    w.begin(p, share);
+    w.begin(p, sm.share());
     if (warp < kTmaWarp) widen_role<D, BF16>(P, sm, w, warp - kVWarp0, lane);
     else if (warp == kTmaWarp) load_role<D, BF16>(P, sm, w, lane);
     else if (warp == kMmaWarp) mma_role<D, BF16>(P, sm, w, tmem, lane);
@@ -745,9 +769,10 @@ cudaError_t launch_attn_paged_tc(const PagedLaunch& L, bool bf16, cudaStream_t s
   P.ws_o = L.ws_o;
   P.ws_ml = L.ws_ml;
   P.cuts = L.cuts;
-  P.scale_abs = fabsf(L.c.scale);
+  P.aligned32 = ((reinterpret_cast<uintptr_t>(L.c.out) | reinterpret_cast<uintptr_t>(L.ws_o)) & 31) == 0;
+  P.scale_log2 = (float)(fabs((double)L.c.scale) * 1.4426950408889634);
   if (L.c.softcap > 0.0f) {
-    P.sc_in = 1.0f / L.c.softcap;
+    P.sc_in = (float)(0.6931471805599453 / (double)L.c.softcap);
     P.sc_out = (float)((double)L.c.softcap * 1.4426950408889634);
   }
   if (L.c.D == 128) return bf16 ? launch_tc_d<128, true>(P, L.grid, stream) : launch_tc_d<128, false>(P, L.grid, stream);

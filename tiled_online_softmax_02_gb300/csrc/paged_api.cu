@@ -180,7 +180,8 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   int64_t cbytes, qspan, rows, out_elems, table_bytes;
   if (!cache_bytes(num_blocks, Hkv, block_size, D, &cbytes)) return ATTN_ERR_INVALID_ARG;
   if (!strided_span(num_tokens, q_token_stride, (int64_t)Hq * D, &qspan)) return ATTN_ERR_INVALID_ARG;
-  if (!mul_ok(num_tokens, Hq, &rows) || rows > INT32_MAX || !mul_ok(rows, D, &out_elems)) return ATTN_ERR_INVALID_ARG;
+  if (!mul_ok(num_tokens, Hq, &rows) || rows > INT32_MAX - 1024 || !mul_ok(rows, D, &out_elems))
+    return ATTN_ERR_INVALID_ARG;
   if (!mul_ok((int64_t)B * 4, max_blocks, &table_bytes)) return ATTN_ERR_INVALID_ARG;
   if ((int64_t)max_blocks * block_size > INT32_MAX) return ATTN_ERR_INVALID_ARG;
   if (num_tokens == 0 || B == 0) return ATTN_OK;  // no row belongs to a request
@@ -221,6 +222,8 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   p.lse = lse;
   p.T = num_tokens; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.group = Hq / Hkv;
   p.num_blocks = num_blocks; p.block_size = block_size; p.width = max_blocks;
+  p.block_shift = block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
+  p.cap = max_blocks * block_size;
   p.causal = causal;
   p.local_window = local_window > 0 ? local_window : 0;
   p.scale = scale;

@@ -68,7 +68,8 @@ struct PagedParams {
   const int32_t* totals;    // [B]
   void* out;                // [T, Hq, D]
   float* lse;               // [T, Hq] or nullptr
-  int T, B, Hq, Hkv, D, group, num_blocks, block_size, width;
+  int T, B, Hq, Hkv, D, group, num_blocks, block_size, block_shift, width;
+  int cap;                  // width * block_size: keys a block table can name
   int causal, local_window;
   float scale, softcap;
   uint64_t timeout_ns;

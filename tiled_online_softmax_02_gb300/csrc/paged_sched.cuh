@@ -22,26 +22,28 @@ constexpr int kPagedKeys = 128;  // keys of a tile
 
 // A request's packed rows and lengths.
 struct PagedReq {
-  int s0, n;        // first row, rows
-  int64_t total;    // cached tokens, these rows' among them
+  int s0, n;   // first row, rows
+  int total;   // cached tokens, these rows' among them (at least 0: below it nothing is visible either)
 };
 
 __device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int b) {
   PagedReq r;
   r.s0 = min(max(__ldg(p.q_starts + b), 0), p.T);
   r.n = min(max(__ldg(p.q_starts + b + 1), r.s0), p.T) - r.s0;
-  r.total = __ldg(p.totals + b);
+  r.total = max(__ldg(p.totals + b), 0);
   return r;
 }
+
+// Keys that have a slot.
+__device__ __forceinline__ int paged_valid(const PagedParams& p, const PagedReq& q) { return min(q.total, p.cap); }
 
 // Visible keys [x, y) of the request's row qi; none where y <= x.  Both ends
 // rise with qi.
 __device__ __forceinline__ int2 paged_limits(const PagedParams& p, const PagedReq& q, int qi) {
-  const int64_t pos = q.total - q.n + qi, cap = (int64_t)p.width * p.block_size;
-  int64_t lo = p.local_window > 0 ? pos + 1 - p.local_window : 0;
-  int64_t hi = q.total < cap ? q.total : cap;
-  if (p.causal && pos + 1 < hi) hi = pos + 1;
-  return make_int2((int)max(lo, (int64_t)0), (int)max(hi, (int64_t)0));
+  const int pos = q.total - q.n + qi;  // from -2^31 + 2
+  const int lo = p.local_window > 0 && pos >= p.local_window ? pos - p.local_window + 1 : 0;
+  const int valid = paged_valid(p, q);
+  return make_int2(lo, p.causal && pos < valid ? max(pos + 1, 0) : valid);
 }
 
 struct PagedUnit {
@@ -70,32 +72,30 @@ template <int NR>
 __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, int b) {
   PagedUnit u;
   u.q = paged_req(p, b);
-  const int64_t rows = (int64_t)u.q.n * p.group;
+  const int rows = u.q.n * p.group;
   long long c = 0;
-  for (u.rt = 0; (int64_t)u.rt * NR < rows; ++u.rt) {
+  for (u.rt = 0; u.rt * NR < rows; ++u.rt) {
     paged_unit_tiles<NR>(p, u);
     c += paged_cost(u);
   }
   return c;
 }
 
-// A CTA's piece of the line.
+// A CTA's piece of the line, in shared memory.
 struct PagedShare {
-  long long total;    // tiles of all units
-  long long w0, w1;   // this CTA's
-  int ctas;           // CTAs that have a piece
+  long long total;      // tiles of all units
+  long long w0;         // where this CTA's piece begins
+  int len;              // its tiles
+  int ctas;             // CTAs that have a piece
   int b, kvh, rt, off;  // the unit w0 lies in, and how many of its tiles lie before
+  long long warp_sum[32];
 };
 
 __device__ __forceinline__ long long paged_cut(long long total, int ctas, int c) { return total * c / ctas; }
 
-// Called by every thread of the CTA (NT threads); sh is shared memory.
-struct PagedShareSmem {
-  long long warp_sum[32];
-  int b, kvh, rt, off;
-};
+// Called by every thread of the CTA (NT threads) before a __syncthreads().
 template <int NR, int NT>
-__device__ __forceinline__ PagedShare paged_share(const PagedParams& p, PagedShareSmem* sh) {
+__device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -109,22 +109,23 @@ __device__ __forceinline__ PagedShare paged_share(const PagedParams& p, PagedSha
   }
   if (lane == 31) sh->warp_sum[warp] = inc;
   __syncthreads();
-  PagedShare s;
-  s.total = 0;
-  long long before = inc - mine;
+  long long total = 0, before = inc - mine;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += sh->warp_sum[w];
-    s.total += sh->warp_sum[w];
+    total += sh->warp_sum[w];
   }
-  s.ctas = (int)min((long long)gridDim.x, s.total);
-  s.w0 = s.w1 = 0;
-  s.b = s.kvh = s.rt = s.off = 0;
-  if ((int)blockIdx.x >= s.ctas) return s;
-  s.w0 = paged_cut(s.total, s.ctas, blockIdx.x);
-  s.w1 = paged_cut(s.total, s.ctas, blockIdx.x + 1);
-  if (mine > 0 && s.w0 >= before && s.w0 < before + mine) {
-    long long rest = s.w0 - before, c;
+  const int ctas = (int)min((long long)gridDim.x, total);
+  const bool in = (int)blockIdx.x < ctas;
+  const long long w0 = in ? paged_cut(total, ctas, blockIdx.x) : 0;
+  if (tid == 0) {
+    sh->total = total;
+    sh->w0 = w0;
+    sh->len = in ? (int)(paged_cut(total, ctas, blockIdx.x + 1) - w0) : 0;
+    sh->ctas = ctas;
+  }
+  if (in && mine > 0 && w0 >= before && w0 < before + mine) {  // one thread's requests hold w0
+    long long rest = w0 - before, c;
     PagedUnit u;
     for (u.b = b0;; ++u.b) {
       c = paged_head_cost<NR>(p, u.b);
@@ -143,53 +144,43 @@ __device__ __forceinline__ PagedShare paged_share(const PagedParams& p, PagedSha
     sh->rt = u.rt;
     sh->off = (int)rest;
   }
-  __syncthreads();
-  s.b = sh->b;
-  s.kvh = sh->kvh;
-  s.rt = sh->rt;
-  s.off = sh->off;
-  return s;
 }
 
 // Walks a CTA's piece, segment by segment: a unit's tiles [t0, t0 + nt).
 template <int NR>
 struct PagedWalk {
   PagedUnit u;
-  long long pos, pos_next, end;  // the segment's ends on the line; the piece's end
-  int off;               // tiles of the unit before pos
+  int left, off;         // tiles of the piece from this segment on; tiles of the unit before it
   int t0, nt;            // key tiles of this segment (nt = 0: a unit without visible keys)
   bool head, whole;      // begins at the unit's first tile; holds all of it
   int index;             // segments walked before this one
 
-  __device__ __forceinline__ void begin(const PagedParams& p, const PagedShare& s) {
-    pos = s.w0;
-    end = s.w1;
+  __device__ __forceinline__ void begin(const PagedParams& p, const PagedShare* s) {
+    left = s->len;
     index = 0;
-    if (pos >= end) return;
-    u.b = s.b;
-    u.kvh = s.kvh;
-    u.rt = s.rt;
+    if (left <= 0) return;
+    u.b = s->b;
+    u.kvh = s->kvh;
+    u.rt = s->rt;
     u.q = paged_req(p, u.b);
     paged_unit_tiles<NR>(p, u);
-    off = s.off;
+    off = s->off;
     segment();
   }
-  __device__ __forceinline__ bool done() const { return pos >= end; }
+  __device__ __forceinline__ bool done() const { return left <= 0; }
+  __device__ __forceinline__ int len() const { return min(paged_cost(u) - off, left); }
   __device__ __forceinline__ void segment() {
-    const int cost = paged_cost(u);
-    const int len = (int)min((long long)(cost - off), end - pos);
     head = off == 0;
-    whole = head && len == cost;
+    whole = head && len() == paged_cost(u);
     t0 = u.tb + off;
-    nt = u.te > u.tb ? len : 0;
-    pos_next = pos + len;
+    nt = u.te > u.tb ? len() : 0;
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
-    pos = pos_next;
+    left -= len();
     ++index;
-    if (pos >= end) return;
+    if (left <= 0) return;
     off = 0;
-    if ((int64_t)(++u.rt) * NR >= (int64_t)u.q.n * p.group) {
+    if ((++u.rt) * NR >= u.q.n * p.group) {
       u.rt = 0;
       if (++u.kvh == p.Hkv) {
         u.kvh = 0;
@@ -201,12 +192,12 @@ struct PagedWalk {
   }
 };
 
-// CTAs from this one on that hold a part of the unit at the walk's position.
+// CTAs from this one on that hold a part of the walk's unit.
 template <int NR>
-__device__ __forceinline__ int paged_parts(const PagedWalk<NR>& w, const PagedShare& s) {
-  const long long last = w.pos - w.off + paged_cost(w.u) - 1;
+__device__ __forceinline__ int paged_parts(const PagedWalk<NR>& w, const PagedShare* s) {
+  const long long last = s->w0 + s->len - w.left - w.off + paged_cost(w.u) - 1;
   int c = blockIdx.x;
-  while (c + 1 < s.ctas && paged_cut(s.total, s.ctas, c + 1) <= last) ++c;
+  while (c + 1 < s->ctas && paged_cut(s->total, s->ctas, c + 1) <= last) ++c;
   return c - (int)blockIdx.x + 1;
 }
 
