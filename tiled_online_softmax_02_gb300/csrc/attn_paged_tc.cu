@@ -28,7 +28,7 @@
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two lanes, thread =
 // row, which also bring the next unit's Q into pieces before they store the
 // last one's rows; warps 8-11 widen V; warp 12 loads (TMA), 13 issues MMAs, 14
-// looks up scales and prefetches the next unit's Q rows into L2.  Registers move from the latter eight warps to the softmax.
+// looks up scales and prefetches the next unit's Q rows into L2.
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
 #include <atomic>
 
@@ -47,6 +47,7 @@ constexpr float kRise = 8.0f;          // the maximum moves when a key passes it
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
 constexpr int kSC = 4;                 // stages of the scale ring
+constexpr int kMaxUnroll = 1, kExpUnroll = 1;
 
 template <int D, bool BF16>
 struct Cfg {
@@ -520,62 +521,71 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       const float4* scl = sm.scales(g % kSC);
       if (!mbar_wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
       tc_fence_after();
-      float x[BN];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(s_addr + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[k * 32]));
-      tmem_wait_ld();
-      if constexpr (SOFTCAP) {
-        // tanh(scale s / c) as the raw value, c log2 e the factor.  The hardware tanh: its error, 2^-11 of c, is
-        // below what a 16-bit output holds of scores that c caps
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          const float in = scl[i].x * qs * P.sc_in;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[16 * i + k] = fast_tanh(x[16 * i + k] * in);
-        }
-      }
+      const bool edge = key0 < full_lo || key0 + BN > full_hi;  // some key is hidden from some row
+      const int lo = min(max(lim.x - key0, 0), BN), span = max(min(max(lim.y - key0, 0), BN) - lo, 0);
       auto factor = [&](float k) { return SOFTCAP ? P.sc_out : fmaxf(k * qs, 1.2e-38f); };
-      if (key0 < full_lo || key0 + BN > full_hi) {
-        const int lo = min(max(lim.x - key0, 0), BN), hi = min(max(lim.y - key0, 0), BN);
-        const uint32_t span = hi > lo ? (uint32_t)(hi - lo) : 0u;
-#pragma unroll
-        for (int i = 0; i < BN; ++i) x[i] = (uint32_t)(i - lo) < span ? x[i] : -INFINITY;
-      }
+      // The row's largest score, 32 keys at a time: the loops stay rolled and S is read a second
+      // time below, which costs less than the instruction fetches of code four times the size
       float m_tile = -INFINITY;
+#pragma unroll kMaxUnroll
+      for (int ch = 0; ch < 4; ++ch) {
+        float x[32];
+        tmem_ld32(s_addr + ch * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+        tmem_wait_ld();
+        if (edge) {
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        float a = fmaxf(x[16 * i], x[16 * i + 1]), b = fmaxf(x[16 * i + 2], x[16 * i + 3]);
-#pragma unroll
-        for (int k = 4; k < 16; k += 4) {
-          a = fmax3(a, x[16 * i + k], x[16 * i + k + 1]);
-          b = fmax3(b, x[16 * i + k + 2], x[16 * i + k + 3]);
+          for (int i = 0; i < 32; ++i) x[i] = (uint32_t)(ch * 32 + i - lo) < (uint32_t)span ? x[i] : -INFINITY;
         }
-        const float2 kl = *reinterpret_cast<const float2*>(scl + i);
-        m_tile = fmaxf(m_tile, fmaf(fmaxf(a, b), factor(kl.x), kl.y));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 kl = *reinterpret_cast<const float2*>(scl + 2 * ch + h);
+          float a = fmaxf(x[16 * h], x[16 * h + 1]), b = fmaxf(x[16 * h + 2], x[16 * h + 3]);
+#pragma unroll
+          for (int k = 4; k < 16; k += 4) {
+            a = fmax3(a, x[16 * h + k], x[16 * h + k + 1]);
+            b = fmax3(b, x[16 * h + k + 2], x[16 * h + k + 3]);
+          }
+          a = fmaxf(a, b);
+          if constexpr (SOFTCAP) a = a == -INFINITY ? a : fast_tanh(a * (kl.x * qs * P.sc_in));
+          m_tile = fmaxf(m_tile, fmaf(a, factor(kl.x), kl.y));
+        }
       }
-      float alpha = 1.0f;
       const bool rise = m_tile > m_run + kRise;
-      if (rise) {
-        alpha = fast_exp2(m_run - m_tile);
-        m_run = m_tile;
-        l_run *= alpha;
-      }
+      const float m_new = rise ? m_tile : m_run;
+      const float alpha = fast_exp2(m_run - m_new);  // 1 where the maximum stays
+      m_run = m_new;
       const float off = kPLog2 - m_run;
       uint64_t sum = 0ull;
-#pragma unroll
+#pragma unroll kExpUnroll
       for (int ch = 0; ch < 4; ++ch) {
+        float x[32];
+        tmem_ld32(s_addr + ch * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+        tmem_wait_ld();
+        if constexpr (SOFTCAP) {
+          // tanh(scale s / c) as the raw value, c log2 e the factor.  The hardware tanh: its error, 2^-11 of c, is
+          // below what a 16-bit output holds of scores that c caps
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float in = scl[2 * ch + h].x * qs * P.sc_in;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[16 * h + k] = fast_tanh(x[16 * h + k] * in);
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = (uint32_t)(ch * 32 + i - lo) < (uint32_t)span ? x[i] : -INFINITY;
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int i = ch * 2 + h;
-          const float4 s4 = scl[i];
+          const float4 s4 = scl[2 * ch + h];
           const float kf = factor(s4.x);
           const uint64_t mul = f2(kf, kf), add = f2(s4.y + off, s4.y + off);
           uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float a, b;
-            f2_split(ffma2(f2(x[16 * i + 2 * k], x[16 * i + 2 * k + 1]), mul, add), a, b);
+            f2_split(ffma2(f2(x[16 * h + 2 * k], x[16 * h + 2 * k + 1]), mul, add), a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
             part[k & 1] = fadd2(part[k & 1], f2(a, b));
@@ -584,11 +594,11 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
           }
           sum = ffma2(fadd2(part[0], part[1]), f2(s4.z, s4.z), sum);
         }
-        tmem_st16(s_addr + ch * 16, pk);
+        tmem_st16(s_addr + ch * 16, pk);  // over columns of S that have been read
       }
       float sa, sb;
       f2_split(sum, sa, sb);
-      l_run += sa + sb;
+      l_run = fmaf(l_run, alpha, sa + sb);
       if (n > 0 && __any_sync(0xffffffffu, rise)) {  // O holds every earlier tile
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
@@ -714,21 +724,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.slot());
-  // 512 threads of 128 registers at launch: 256 x 192 + 256 x 64 = 512 x 128
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    Walk w;
-    w.begin(p, sm.share());
-    softmax_role<D, BF16, SOFTCAP>(P, sm, w, tmem, warp, lane);
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    Walk w;
-    w.begin(p, sm.share());
-    if (warp < kTmaWarp) widen_role<D, BF16>(P, sm, w, warp - kVWarp0, lane);
-    else if (warp == kTmaWarp) load_role<D, BF16>(P, sm, w, lane);
-    else if (warp == kMmaWarp) mma_role<D, BF16>(P, sm, w, tmem, lane);
-    else if (warp == kScaleWarp) scale_role<D, BF16>(P, sm, w, lane);
-  }
+  Walk w;
+  w.begin(p, sm.share());
+  if (warp < kVWarp0) softmax_role<D, BF16, SOFTCAP>(P, sm, w, tmem, warp, lane);
+  else if (warp < kTmaWarp) widen_role<D, BF16>(P, sm, w, warp - kVWarp0, lane);
+  else if (warp == kTmaWarp) load_role<D, BF16>(P, sm, w, lane);
+  else if (warp == kMmaWarp) mma_role<D, BF16>(P, sm, w, tmem, lane);
+  else if (warp == kScaleWarp) scale_role<D, BF16>(P, sm, w, lane);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {

@@ -65,7 +65,12 @@ __device__ __forceinline__ void paged_unit_tiles(const PagedParams& p, PagedUnit
   u.te = hi > lo ? (hi + kPagedKeys - 1) / kPagedKeys : 0;
 }
 
-__device__ __forceinline__ int paged_cost(const PagedUnit& u) { return max(u.te - u.tb, 1); }
+// What a unit costs besides its tiles, in tiles.
+template <int NR>
+constexpr int kOver = NR == kPagedTcRows ? 3 : 1;
+
+template <int NR>
+__device__ __forceinline__ int paged_cost(const PagedUnit& u) { return max(u.te - u.tb, 1) + kOver<NR>; }
 
 // Tiles of one kv head of request b: the sum over its row tiles.
 template <int NR>
@@ -76,18 +81,17 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, int b
   long long c = 0;
   for (u.rt = 0; u.rt * NR < rows; ++u.rt) {
     paged_unit_tiles<NR>(p, u);
-    c += paged_cost(u);
+    c += paged_cost<NR>(u);
   }
   return c;
 }
 
 // A CTA's piece of the line, in shared memory.
 struct PagedShare {
-  long long total;      // tiles of all units
-  long long w0;         // where this CTA's piece begins
-  int len;              // its tiles
+  long long total;      // length of the line
+  long long w0, w1;     // this CTA's piece
   int ctas;             // CTAs that have a piece
-  int b, kvh, rt, off;  // the unit w0 lies in, and how many of its tiles lie before
+  int b, kvh, rt, off;  // the unit w0 lies in, and how far into it: 0, or more than kOver
   long long warp_sum[32];
 };
 
@@ -118,31 +122,42 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
   const int ctas = (int)min((long long)gridDim.x, total);
   const bool in = (int)blockIdx.x < ctas;
   const long long w0 = in ? paged_cut(total, ctas, blockIdx.x) : 0;
+  const long long w1 = in ? paged_cut(total, ctas, blockIdx.x + 1) : 0;
   if (tid == 0) {
     sh->total = total;
-    sh->w0 = w0;
-    sh->len = in ? (int)(paged_cut(total, ctas, blockIdx.x + 1) - w0) : 0;
     sh->ctas = ctas;
+    if (!in) sh->w0 = 0;
+    if (!in || w1 == total) sh->w1 = w1;
   }
-  if (in && mine > 0 && w0 >= before && w0 < before + mine) {  // one thread's requests hold w0
-    long long rest = w0 - before, c;
+  // the thread whose requests hold a border finds its unit
+  for (int end = 0; end < 2; ++end) {
+    const long long at = end ? w1 : w0;
+    if (!in || at < before || at >= before + mine) continue;
+    long long rest = at - before, c;
     PagedUnit u;
     for (u.b = b0;; ++u.b) {
       c = paged_head_cost<NR>(p, u.b);
       if (rest < c * p.Hkv) break;
       rest -= c * p.Hkv;
     }
-    sh->b = u.b;
-    sh->kvh = (int)(rest / c);
-    rest -= c * sh->kvh;
+    u.kvh = (int)(rest / c);
+    rest -= c * u.kvh;
     u.q = paged_req(p, u.b);
     for (u.rt = 0;; ++u.rt) {
       paged_unit_tiles<NR>(p, u);
-      if (rest < paged_cost(u)) break;
-      rest -= paged_cost(u);
+      if (rest < paged_cost<NR>(u)) break;
+      rest -= paged_cost<NR>(u);
     }
-    sh->rt = u.rt;
-    sh->off = (int)rest;
+    const int off = rest > kOver<NR> ? (int)rest : 0;
+    if (end) {
+      sh->w1 = at - (rest - off);
+    } else {
+      sh->w0 = at - (rest - off);
+      sh->b = u.b;
+      sh->kvh = u.kvh;
+      sh->rt = u.rt;
+      sh->off = off;
+    }
   }
 }
 
@@ -150,13 +165,13 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
 template <int NR>
 struct PagedWalk {
   PagedUnit u;
-  int left, off;         // tiles of the piece from this segment on; tiles of the unit before it
+  int left, off;         // what is left of the piece; how far into the unit this segment begins
   int t0, nt;            // key tiles of this segment (nt = 0: a unit without visible keys)
   bool head, whole;      // begins at the unit's first tile; holds all of it
   int index;             // segments walked before this one
 
   __device__ __forceinline__ void begin(const PagedParams& p, const PagedShare* s) {
-    left = s->len;
+    left = (int)(s->w1 - s->w0);
     index = 0;
     if (left <= 0) return;
     u.b = s->b;
@@ -168,12 +183,13 @@ struct PagedWalk {
     segment();
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
-  __device__ __forceinline__ int len() const { return min(paged_cost(u) - off, left); }
+  __device__ __forceinline__ int len() const { return min(paged_cost<NR>(u) - off, left); }
   __device__ __forceinline__ void segment() {
     head = off == 0;
-    whole = head && len() == paged_cost(u);
-    t0 = u.tb + off;
-    nt = u.te > u.tb ? len() : 0;
+    whole = head && len() == paged_cost<NR>(u);
+    const int before = head ? 0 : off - kOver<NR>;
+    t0 = u.tb + before;
+    nt = u.te > u.tb ? off + len() - kOver<NR> - before : 0;
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
     left -= len();
@@ -195,7 +211,7 @@ struct PagedWalk {
 // CTAs from this one on that hold a part of the walk's unit.
 template <int NR>
 __device__ __forceinline__ int paged_parts(const PagedWalk<NR>& w, const PagedShare* s) {
-  const long long last = s->w0 + s->len - w.left - w.off + paged_cost(w.u) - 1;
+  const long long last = s->w1 - w.left - w.off + paged_cost<NR>(w.u) - 1;
   int c = blockIdx.x;
   while (c + 1 < s->ctas && paged_cut(s->total, s->ctas, c + 1) <= last) ++c;
   return c - (int)blockIdx.x + 1;
