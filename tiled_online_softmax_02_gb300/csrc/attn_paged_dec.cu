@@ -61,12 +61,11 @@ struct Cfg {
   static constexpr int kOffP = kOffQ + 2 * kQBytes;               // two buffers
   static constexpr int kOffLim = kOffP + 2 * kPBytes;             // int2 [2][NR]
   static constexpr int kOffM = kOffLim + 2 * NR * 8;              // float [NR]: running maxima
-  static constexpr int kOffRed = kOffM + NR * 4;                  // float [2][4][NR]
-  static constexpr int kOffFlag = kOffRed + 2 * 4 * NR * 4;       // int [2][4]
-  static constexpr int kOffQs = kOffFlag + 32;                    // float [2]: 1 / scale of Q's pieces
+  static constexpr int kOffRed = kOffM + NR * 4;                  // float [4][NR]
+  static constexpr int kOffQs = kOffRed + 4 * NR * 4;             // float [2]: 1 / scale of Q's pieces
   static constexpr int kOffBar = kOffQs + 16;
-  // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2], red [2], drain
-  static constexpr int kBars = 2 * kSK + 2 * kSV + 13;
+  // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2], drain
+  static constexpr int kBars = 2 * kSK + 2 * kSV + 11;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;  // + alignment slack
@@ -92,8 +91,7 @@ struct Lay {
   __device__ uint8_t* p_ptr(int i) const { return base + C::kOffP + i * C::kPBytes; }
   __device__ int2* lim(int i) const { return reinterpret_cast<int2*>(base + C::kOffLim) + i * NR; }
   __device__ float* m() const { return reinterpret_cast<float*>(base + C::kOffM); }
-  __device__ float* red(int i) const { return reinterpret_cast<float*>(base + C::kOffRed) + i * 4 * NR; }
-  __device__ int* flag(int i) const { return reinterpret_cast<int*>(base + C::kOffFlag) + i * 4; }
+  __device__ float* red() const { return reinterpret_cast<float*>(base + C::kOffRed); }
   __device__ float* qs() const { return reinterpret_cast<float*>(base + C::kOffQs); }
   __device__ uint32_t bar(int i) const { return s + C::kOffBar + i * 8; }
   __device__ uint32_t k_full(int i) const { return bar(i); }
@@ -106,8 +104,7 @@ struct Lay {
   __device__ uint32_t pv_done(int i) const { return rest(4 + i); }
   __device__ uint32_t q_full(int i) const { return rest(6 + i); }
   __device__ uint32_t q_empty(int i) const { return rest(8 + i); }
-  __device__ uint32_t red_bar(int i) const { return rest(10 + i); }
-  __device__ uint32_t drain() const { return rest(12); }
+  __device__ uint32_t drain() const { return rest(10); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
@@ -215,7 +212,7 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int st = g % NS, blk = next;
       if (n + 1 < w.nt) next = lookup(w.t0 + n + 1);
-      if (g >= NS && !mbar_wait_warp(empty0 + st * 8, ((g / NS) - 1) & 1, p.timeout_ns, p.status)) {
+      if (g >= NS && !wait_warp(empty0 + st * 8, ((g / NS) - 1) & 1, p.timeout_ns, p.status)) {
         ok = false;
         break;
       }
@@ -229,7 +226,7 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
     }
   }
   // every copy lands before the CTA may exit
-  for (int n = g > NS ? g - NS : 0; n < g; ++n) mbar_wait_warp(full0 + (n % NS) * 8, (n / NS) & 1, p.timeout_ns, p.status);
+  for (int n = g > NS ? g - NS : 0; n < g; ++n) wait_warp(full0 + (n % NS) * 8, (n / NS) & 1, p.timeout_ns, p.status);
 }
 
 // ----------------------------------------------------------------- Q pieces
@@ -242,7 +239,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
   constexpr int kVec = D / 8;  // 8-value pieces of a row
   for (; !w.done(); w.next(p)) {
     const int buf = w.index & 1;
-    if (w.index >= 2 && !mbar_wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;
+    if (w.index >= 2 && !wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;
     const PagedUnit& u = w.u;
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + (int64_t)u.kvh * p.group * D;
     auto row = [&](int r) {
@@ -330,9 +327,9 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
   int pend_valid = kPagedKeys;  // valid keys from its first one on
   bool ok = true;
   auto pv = [&](int t) -> bool {
-    if (!mbar_wait_warp(sm.p_full(t & 1), (t >> 1) & 1, p.timeout_ns, p.status)) return false;
+    if (!wait_warp(sm.p_full(t & 1), (t >> 1) & 1, p.timeout_ns, p.status)) return false;
     const int vs = t % C::kSV;
-    if (!mbar_wait_warp(sm.v_full(vs), (t / C::kSV) & 1, p.timeout_ns, p.status)) return false;
+    if (!wait_warp(sm.v_full(vs), (t / C::kSV) & 1, p.timeout_ns, p.status)) return false;
     if (pend_valid < kPagedKeys) {
       // slots past the request's last key may hold NaN bytes: P is 0 there but 0 * NaN is not
       for (int c = max(pend_valid, 0) * (D / 16) + lane; c < kPagedKeys * (D / 16); c += 32)
@@ -359,11 +356,11 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
       if (!pv(g - 1)) { ok = false; break; }
       pending = false;
     }
-    if (!mbar_wait_warp(sm.q_full(buf), (w.index >> 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+    if (!wait_warp(sm.q_full(buf), (w.index >> 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
     const int valid = paged_valid(p, w.u.q);
     for (int n = 0; ok && n < w.nt; ++n, ++g) {
       const int ks = g % C::kSK;
-      if (!mbar_wait_warp(sm.k_full(ks), (g / C::kSK) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+      if (!wait_warp(sm.k_full(ks), (g / C::kSK) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       tc_fence_after();
       const uint64_t a0 = sdesc(sm.k_tile(ks), 16, kGroup8, kSwizzle);
       const uint64_t b0 = sdesc(sm.q(buf), 16, kGroup8, kSwizzle);
@@ -384,7 +381,7 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
   if (ok && pending) pv(g - 1);
   // every MMA done before tensor memory is given back
   tc_commit_elect(sm.drain());
-  mbar_wait_warp(sm.drain(), 0, p.timeout_ns, p.status);
+  wait_warp(sm.drain(), 0, p.timeout_ns, p.status);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -398,14 +395,21 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
   const int tid = warp * 32 + lane;
   const uint32_t tq = tmem + ((uint32_t)(warp * 32) << 16);
   float* const m = sm.m();
-  int g = 0, use = 0;  // tiles and exchanges so far
-  // every softmax warp has written its part of exchange `use`
-  auto exchange = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(sm.red_bar(use & 1));
-    const bool r = mbar_wait_warp(sm.red_bar(use & 1), (use >> 1) & 1, p.timeout_ns, p.status);
-    ++use;
-    return r;
+  int g = 0;  // tiles so far
+  // The four warps meet at a hardware barrier, so none of them may leave early: one whose bounded
+  // wait has run out goes on without waiting (the status word has the timeout; the rows are not valid).
+  bool dead = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (!dead) dead = !wait_warp(bar, parity, p.timeout_ns, p.status);
+  };
+  auto meet = [] { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); };
+  auto meet_any = [](bool x) {  // ... and learn whether x holds for some thread
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, 1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"((uint32_t)x) : "memory");
+    return r != 0;
   };
   for (; !w.done(); w.next(p)) {
     const PagedUnit& u = w.u;
@@ -431,7 +435,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       blk_next = block_of(n + 1);
     };
     fetch(0);
-    if (!mbar_wait_warp(sm.q_full(buf), (w.index >> 1) & 1, p.timeout_ns, p.status)) return;
+    wait(sm.q_full(buf), (w.index >> 1) & 1);
     const int2* lim = sm.lim(buf);
     const float qs = sm.qs()[buf];
     const int full_lo = lim[u.rows - 1].x, full_hi = lim[0].y;  // keys every row sees
@@ -440,7 +444,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
     for (int r = 0; r < NR; ++r) l[r] = 0.0f;
     // m starts below everything (its readers of the last unit met at that unit's sum exchange)
     if (tid < NR) m[tid] = kNone;
-    if (!exchange()) return;
+    meet();
 
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int key0 = (w.t0 + n) * kPagedKeys, j = key0 + tid;
@@ -448,7 +452,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       const float vsc = fmaxf(vs_next, kMinVScale);
       const float lv = __log2f(vsc), iv = 1.0f / vsc;
       fetch(n + 1);
-      if (!mbar_wait_warp(sm.s_full(g & 1), (g >> 1) & 1, p.timeout_ns, p.status)) return;
+      wait(sm.s_full(g & 1), (g >> 1) & 1);
       tc_fence_after();
       float t[NR];
       {
@@ -484,18 +488,14 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       float over = -INFINITY;
 #pragma unroll
       for (int r = 0; r < NR; ++r) over = fmaxf(over, t[r] - m[r]);
-      const bool rise = __any_sync(0xffffffffu, over > kRise);
-      int* flag = sm.flag(use & 1);
-      if (lane == 0) flag[warp] = rise ? 1 : 0;
-      if (!exchange()) return;
-      if (flag[0] | flag[1] | flag[2] | flag[3]) {
+      if (meet_any(over > kRise)) {
         float x[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) x[r] = t[r];
         const float wm = reduce_scatter<NR, true>(x, lane);
-        float* red = sm.red(use & 1);
+        float* red = sm.red();
         if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = wm;
-        if (!exchange()) return;
+        meet();
         float alpha[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -507,7 +507,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           x[r] = mn;
         }
         if (n > 0) {  // O^T holds the unit's earlier tiles once their P V is done
-          if (!mbar_wait_warp(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, p.timeout_ns, p.status)) return;
+          wait(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1);
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < C::kNP; c += 16) {
@@ -521,14 +521,14 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           tmem_wait_st();
           tc_fence_before();
         }
-        if (!exchange()) return;  // everyone has read the old maxima
+        meet();  // everyone has read the old maxima
 #pragma unroll
         for (int r = 0; r < NR; ++r)
           if (tid == r) m[r] = x[r];
-        if (!exchange()) return;
+        meet();
       }
       // P buffer g % 2 was last read by the P V of tile g - 2
-      if (g >= 2 && !mbar_wait_warp(sm.pv_done(g & 1), ((g - 2) >> 1) & 1, p.timeout_ns, p.status)) return;
+      if (g >= 2) wait(sm.pv_done(g & 1), ((g - 2) >> 1) & 1);
       uint32_t words[C::kNP / 4];
 #pragma unroll
       for (int i = 0; i < C::kNP / 4; ++i) words[i] = 0u;
@@ -557,15 +557,15 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
 #pragma unroll
     for (int r = 0; r < NR; ++r) x[r] = l[r];
     const float ws = reduce_scatter<NR, false>(x, lane);
-    float* red = sm.red(use & 1);
+    float* red = sm.red();
     if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = ws;
     const float my_m = tid < NR ? m[tid] : 0.0f;
-    if (!exchange()) return;
+    meet();
     float o[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) o[r] = 0.0f;
     if (w.nt > 0) {
-      if (!mbar_wait_warp(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, p.timeout_ns, p.status)) return;
+      wait(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1);
       tc_fence_after();
       float o1[NR], o2[NR];
       tld(tq + (uint32_t)C::kColO, o);
@@ -634,7 +634,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
       mbar_init(sm.pv_done(i), 1);
       mbar_init(sm.q_full(i), 1);
       mbar_init(sm.q_empty(i), 5);  // four softmax warps and the MMA warp's commit
-      mbar_init(sm.red_bar(i), 4);
     }
     mbar_init(sm.drain(), 1);
     mbar_init_fence();

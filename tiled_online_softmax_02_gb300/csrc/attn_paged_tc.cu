@@ -153,12 +153,12 @@ __device__ __forceinline__ void load_role(const PagedTcParams& P, const Lay<D, B
       if (blk == -2) atomicOr(p.status, kStatusBadBlock);
       const int plane = blk >= 0 ? blk * p.Hkv + w.u.kvh : p.num_blocks * p.Hkv;
       const int sk = g % C::kSK, sv = g % C::kSV8;
-      if (g >= C::kSK && !mbar_wait_warp(sm.k_empty(sk), ((g / C::kSK) - 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+      if (g >= C::kSK && !wait_warp(sm.k_empty(sk), ((g / C::kSK) - 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       if (lane == 0) mbar_arrive_expect_tx(sm.k_full(sk), C::kTile8);
       __syncwarp();
       if (lane < per) tma_load_3d(sm.k_tile(sk) + lane * box, &P.tmap_k, sm.k_full(sk), 0, 0, plane);
       ++k_done;
-      if (g >= C::kSV8 && !mbar_wait_warp(sm.v8_empty(sv), ((g / C::kSV8) - 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+      if (g >= C::kSV8 && !wait_warp(sm.v8_empty(sv), ((g / C::kSV8) - 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       if (lane == 0) mbar_arrive_expect_tx(sm.v8_full(sv), C::kTile8);
       __syncwarp();
       if (lane < per) tma_load_3d(sm.v8_tile(sv) + lane * box, &P.tmap_v, sm.v8_full(sv), 0, 0, plane);
@@ -167,9 +167,9 @@ __device__ __forceinline__ void load_role(const PagedTcParams& P, const Lay<D, B
   }
   // every copy lands before the CTA may exit
   for (int n = max(0, k_done - C::kSK); n < k_done; ++n)
-    mbar_wait_warp(sm.k_full(n % C::kSK), (n / C::kSK) & 1, p.timeout_ns, p.status);
+    wait_warp(sm.k_full(n % C::kSK), (n / C::kSK) & 1, p.timeout_ns, p.status);
   for (int n = max(0, v_done - C::kSV8); n < v_done; ++n)
-    mbar_wait_warp(sm.v8_full(n % C::kSV8), (n / C::kSV8) & 1, p.timeout_ns, p.status);
+    wait_warp(sm.v8_full(n % C::kSV8), (n / C::kSV8) & 1, p.timeout_ns, p.status);
 }
 
 // ------------------------------------------------------------------ scales
@@ -209,7 +209,7 @@ __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, 
       fetch(blk1);
       blk1 = block_of(n + 2);
       const int st = g % kSC;
-      if (g >= kSC && !mbar_wait_warp(sm.sc_empty(st), ((g / kSC) - 1) & 1, p.timeout_ns, p.status)) return;
+      if (g >= kSC && !wait_warp(sm.sc_empty(st), ((g / kSC) - 1) & 1, p.timeout_ns, p.status)) return;
       if (lane < kGroups) sm.scales(st)[lane] = make_float4(k0 * P.scale_log2, __log2f(v0), 1.0f / v0, 0.0f);
       __syncwarp();
       if (lane == 0) mbar_arrive(sm.sc_full(st));
@@ -234,13 +234,13 @@ __device__ __forceinline__ void widen_role(const PagedTcParams& P, const Lay<D, 
     const int valid = paged_valid(p, w.u.q);
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int s8 = g % C::kSV8, sv = g % C::kSV;
-      if (!mbar_wait_warp(sm.v8_full(s8), (g / C::kSV8) & 1, p.timeout_ns, p.status)) return;
-      if (g >= C::kSV && !mbar_wait_warp(sm.v_empty(sv), ((g / C::kSV) - 1) & 1, p.timeout_ns, p.status)) return;
+      if (!wait_warp(sm.v8_full(s8), (g / C::kSV8) & 1, p.timeout_ns, p.status)) return;
+      if (g >= C::kSV && !wait_warp(sm.v_empty(sv), ((g / C::kSV) - 1) & 1, p.timeout_ns, p.status)) return;
       const int rows = min(valid - (w.t0 + n) * BN, BN);
       const uint8_t* src = sm.v8_ptr(s8);
       uint8_t* dst = sm.v_ptr(sv);
       constexpr int kIters = BN / 8 * (D / 64) / 4;
-#pragma unroll 2
+#pragma unroll 1
       for (int i = 0; i < kIters; ++i) {
         const int it = i * 4 + warp;
         const int row = (it / (D / 64)) * 8 + r8, half = it % (D / 64);
@@ -334,10 +334,10 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
     for (int n = 0; ok && n <= w.nt; ++n) {
       const int sv = (g + n - 1 + C::kSV) % C::kSV, ks = (g + n) % C::kSK;
       bool k_ready = false;
-      if (n >= 1 && !mbar_wait_warp(sm.v_full(sv), ((g + n - 1) / C::kSV) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+      if (n >= 1 && !wait_warp(sm.v_full(sv), ((g + n - 1) / C::kSV) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         if (n >= 1) {
-          if (!mbar_wait_warp(sm.p_full(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
+          if (!wait_warp(sm.p_full(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
           issue_pv(t, sv, n == 1);
           if (n == w.nt) tc_commit_elect(sm.o_final(t));
@@ -345,11 +345,11 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
         }
         if (n < w.nt) {
           if (n == 0) {
-            if (!mbar_wait_warp(sm.q_full(t), units[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
+            if (!wait_warp(sm.q_full(t), units[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
             ++units[t];
           }
           if (!k_ready) {
-            if (!mbar_wait_warp(sm.k_full(ks), ((g + n) / C::kSK) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+            if (!wait_warp(sm.k_full(ks), ((g + n) / C::kSK) & 1, p.timeout_ns, p.status)) { ok = false; break; }
             k_ready = true;
           }
           tc_fence_after();
@@ -365,14 +365,14 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
     g += w.nt;
   }
   tc_commit_elect(sm.drain());
-  mbar_wait_warp(sm.drain(), 0, p.timeout_ns, p.status);
+  wait_warp(sm.drain(), 0, p.timeout_ns, p.status);
 }
 
 // ------------------------------------------------------------------ softmax
 // A lane's rows of Q as e4m3 pieces, K-major in the swizzle of the row width;
 // rows past the unit's are zeros.  Each warp brings its own 32 rows: a row is
 // D / 8 threads wide (16 bytes each), so an instruction loads 2 (D = 64: 4)
-// rows, and half the warp's rows are in flight together.  It stands between
+// rows, and a quarter of the warp's rows are in flight together.  It stands between
 // two units, where the tensor core waits for it, so it is written for few
 // instructions: the row's largest |x| on packed 16-bit integers (magnitudes
 // order as their bits), the pieces and their rests on packed f16, which holds
@@ -383,7 +383,7 @@ __device__ __forceinline__ float bring_q(const PagedTcParams& P, const Lay<D, BF
                                          int wq, int lane) {
   using C = Cfg<D, BF16>;
   const PagedParams& p = P.c;
-  constexpr int kVec = D / 8, kPer = 32 / kVec, kBatch = 16 / kPer;
+  constexpr int kVec = D / 8, kPer = 32 / kVec, kBatch = 8 / kPer;
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on are not finite
   const int c = lane % kVec, sub = lane / kVec;
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + u.kvh * p.group * D + c * 8;
@@ -394,7 +394,7 @@ __device__ __forceinline__ float bring_q(const PagedTcParams& P, const Lay<D, BF
   int r = wq * 32 + sub;
   int tok = (u.row0 + t * BM + r) / p.group, head = (u.row0 + t * BM + r) - tok * p.group;
 #pragma unroll 1
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < 4; ++b) {
     uint4 raw[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -485,44 +485,100 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
   const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + t * 128;
   const uint32_t o_addr = s_addr - t * 128 + kColO + t * 128;
   int g = 0, sc = 0, oc = 0;  // tiles of the line, S tiles and units with tiles of this lane
-  float qinv = 1.0f;          // 1 / the scale of this row's Q pieces
-  auto next_q = [&](const Walk& x) {
-    if (x.done() || x.nt == 0 || !lane_on(x.u, t)) return;
-    qinv = bring_q<D, BF16>(P, sm, x.u, t, wq, lane);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(sm.q_full(t));
-  };
-  next_q(w);
-  while (!w.done()) {
-    const PagedUnit u = w.u;
+  // of the unit whose rows are still to be stored
+  bool stored = true, whole = false, head = false, mine = false;
+  int prev_nt = 0;
+  int64_t out_row = 0;
+  float m_run = kNone, l_run = 0.0f;
+  for (;;) {
+    // ---- a unit's Q: this lane's last S has been read, so its Q is free, and the tensor core can
+    // begin the unit while the last one's rows are stored
+    float qs = 1.0f;  // 1 / the scale of this row's Q pieces
+    if (!w.done() && w.nt > 0 && lane_on(w.u, t)) {
+      qs = bring_q<D, BF16>(P, sm, w.u, t, wq, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.q_full(t));
+    }
+    if (!stored) {
+      // ---- the last unit's rows
+      stored = true;
+      if (prev_nt > 0) {
+        if (!wait_warp(sm.o_final(t), oc & 1, p.timeout_ns, p.status)) return;
+        ++oc;
+        tc_fence_after();
+      }
+      const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+      const int64_t ws_row = (int64_t)(2 * blockIdx.x + (head ? 1 : 0)) * kRows + t * BM + row;
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        if (prev_nt > 0) {
+          tmem_ld32(o_addr + k * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (mine && whole) {
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = (uint32_t)to_bits<BF16>(__uint_as_float(o[2 * i]) * inv) |
+                   (uint32_t)to_bits<BF16>(__uint_as_float(o[2 * i + 1]) * inv) << 16;
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + out_row * D + k * 32;
+          store_32b(dst, &v[0], P.aligned32);
+          store_32b(dst + 16, &v[8], P.aligned32);
+        } else if (mine) {
+          float* dst = P.ws_o + ws_row * D + k * 32;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store_32b(dst + 8 * i, &o[8 * i], P.aligned32);
+        }
+      }
+      if (mine && whole && p.lse != nullptr)
+        p.lse[out_row] = l_run == 0.0f ? -INFINITY : (m_run + (__log2f(l_run) - kPLog2)) * kLn2;
+      if (mine && !whole) P.ws_ml[ws_row] = make_float2(m_run, l_run);
+      tc_fence_before();  // these reads before this lane's next P arrival, which the next P V waits for
+    }
+    if (w.done()) return;
+    const PagedUnit& u = w.u;
     const int nt = w.nt, t0 = w.t0;
-    const bool on = lane_on(u, t), mine = t * BM + row < u.rows;
-    if (!on) {  // the other lane's tiles pass by; their scales too
+    if (!lane_on(u, t)) {  // the other lane's tiles pass by; their scales too
       for (int n = 0; n < nt; ++n, ++g) {
-        if (!mbar_wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
+        if (!wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
         if (lane == 0) mbar_arrive(sm.sc_empty(g % kSC));
       }
       w.next(p);
-      next_q(w);
       continue;
     }
+    mine = t * BM + row < u.rows;
     const int x0 = u.row0 + t * BM;
     const int last = min(x0 + BM, u.row0 + u.rows) - 1;
     const int2 lim = mine ? paged_limits(p, u.q, (x0 + row) / p.group) : make_int2(0, 0);
     const int full_lo = paged_limits(p, u.q, last / p.group).x, full_hi = paged_limits(p, u.q, x0 / p.group).y;
-    const float qs = qinv;
-    float m_run = kNone, l_run = 0.0f;
+    m_run = kNone;
+    l_run = 0.0f;
     for (int n = 0; n < nt; ++n, ++g, ++sc) {
       const int key0 = (t0 + n) * BN;
-      if (!mbar_wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
+      if (!wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
       // a group's (k scale |scale| log2 e, log2 v scale, 1 / v scale); raw scores times the row's
       // factor and the first are in log2 units.  The product stays above 0, so that -inf stays -inf
       const float4* scl = sm.scales(g % kSC);
-      if (!mbar_wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
+      if (!wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
       tc_fence_after();
-      const bool edge = key0 < full_lo || key0 + BN > full_hi;  // some key is hidden from some row
-      const int lo = min(max(lim.x - key0, 0), BN), span = max(min(max(lim.y - key0, 0), BN) - lo, 0);
+      if (key0 < full_lo || key0 + BN > full_hi) {  // some key is hidden from some row: -inf over its score
+        const int lo = min(max(lim.x - key0, 0), BN), span = max(min(max(lim.y - key0, 0), BN) - lo, 0);
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t x[32];
+          tmem_ld32(s_addr + ch * 32, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = (uint32_t)(ch * 32 + i - lo) < (uint32_t)span ? x[i] : 0xff800000u;
+          tmem_st32(s_addr + ch * 32, x);
+        }
+        tmem_wait_st();
+      }
       auto factor = [&](float k) { return SOFTCAP ? P.sc_out : fmaxf(k * qs, 1.2e-38f); };
       // The row's largest score, 32 keys at a time: the loops stay rolled and S is read a second
       // time below, which costs less than the instruction fetches of code four times the size
@@ -532,10 +588,6 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         float x[32];
         tmem_ld32(s_addr + ch * 32, reinterpret_cast<uint32_t(&)[32]>(x));
         tmem_wait_ld();
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (uint32_t)(ch * 32 + i - lo) < (uint32_t)span ? x[i] : -INFINITY;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float2 kl = *reinterpret_cast<const float2*>(scl + 2 * ch + h);
@@ -568,12 +620,11 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
           for (int h = 0; h < 2; ++h) {
             const float in = scl[2 * ch + h].x * qs * P.sc_in;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[16 * h + k] = fast_tanh(x[16 * h + k] * in);
+            for (int k = 0; k < 16; ++k) {
+              const float raw = x[16 * h + k];
+              x[16 * h + k] = raw == -INFINITY ? raw : fast_tanh(raw * in);
+            }
           }
-        }
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (uint32_t)(ch * 32 + i - lo) < (uint32_t)span ? x[i] : -INFINITY;
         }
         uint32_t pk[16];
 #pragma unroll
@@ -600,7 +651,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       f2_split(sum, sa, sb);
       l_run = fmaf(l_run, alpha, sa + sb);
       if (n > 0 && __any_sync(0xffffffffu, rise)) {  // O holds every earlier tile
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
           tmem_ld32(o_addr + k * 32, o);
@@ -618,8 +669,13 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         mbar_arrive(sm.p_full(t));
       }
     }
-    // ---- the segment's rows
-    if (!w.whole && w.head && threadIdx.x == 0) {
+    stored = false;
+    whole = w.whole;
+    head = w.head;
+    prev_nt = nt;
+    const int xr = x0 + row;
+    out_row = (int64_t)(u.q.s0 + xr / p.group) * p.Hq + u.kvh * p.group + xr % p.group;
+    if (!whole && head && threadIdx.x == 0) {
       PagedCut c;
       c.parts = paged_parts(w, sm.share());
       c.token0 = u.q.s0;
@@ -628,49 +684,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       c.rows = u.rows;
       P.cuts[blockIdx.x] = c;
     }
-    const bool whole = w.whole, head = w.head;
-    // the next unit's Q first: this lane's last S has been read, so its Q is free, and the
-    // tensor core can begin the next unit while this one's rows are stored
     w.next(p);
-    next_q(w);
-    if (nt > 0) {
-      if (!mbar_wait_warp(sm.o_final(t), oc & 1, p.timeout_ns, p.status)) return;
-      ++oc;
-      tc_fence_after();
-    }
-    const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-    const int xr = x0 + row;
-    const int64_t out_row = (int64_t)(u.q.s0 + xr / p.group) * p.Hq + u.kvh * p.group + xr % p.group;
-    const int64_t ws_row = (int64_t)(2 * blockIdx.x + (head ? 1 : 0)) * kRows + t * BM + row;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-      uint32_t o[32];
-      if (nt > 0) {
-        tmem_ld32(o_addr + k * 32, o);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0u;
-      }
-      if (mine && whole) {
-        uint32_t v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = (uint32_t)to_bits<BF16>(__uint_as_float(o[2 * i]) * inv) |
-                 (uint32_t)to_bits<BF16>(__uint_as_float(o[2 * i + 1]) * inv) << 16;
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + out_row * D + k * 32;
-        store_32b(dst, &v[0], P.aligned32);
-        store_32b(dst + 16, &v[8], P.aligned32);
-      } else if (mine) {
-        float* dst = P.ws_o + ws_row * D + k * 32;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) store_32b(dst + 8 * i, &o[8 * i], P.aligned32);
-      }
-    }
-    if (mine && whole && p.lse != nullptr)
-      p.lse[out_row] = l_run == 0.0f ? -INFINITY : (m_run + (__log2f(l_run) - kPLog2)) * kLn2;
-    if (mine && !whole) P.ws_ml[ws_row] = make_float2(m_run, l_run);
-    tc_fence_before();  // these reads before this lane's next P arrival, which the next P V waits for
   }
 }
 
