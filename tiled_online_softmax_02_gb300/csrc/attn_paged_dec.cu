@@ -23,7 +23,7 @@
 // One CTA walks its share of the line of key tiles (paged_sched.cuh).  Roles
 // (256 threads): warps 0-3 softmax, thread = key; warp 4 K loads, warp 5 V
 // loads (block table lookup by lanes, one TMA box a block), warp 6 MMA issue,
-// warp 7 Q rows of the next unit into pieces.
+// warp 7 the next unit's Q into pieces, and the scales of its tiles.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -63,9 +63,11 @@ struct Cfg {
   static constexpr int kOffM = kOffLim + 2 * NR * 8;              // float [NR]: running maxima
   static constexpr int kOffRed = kOffM + NR * 4;                  // float [4][NR]
   static constexpr int kOffQs = kOffRed + 4 * NR * 4;             // float [2]: 1 / scale of Q's pieces
-  static constexpr int kOffBar = kOffQs + 16;
-  // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2], drain
-  static constexpr int kBars = 2 * kSK + 2 * kSV + 11;
+  static constexpr int kOffSc = kOffQs + 16;                      // float4 [kScaleStages][kScaleGroups]
+  static constexpr int kOffBar = kOffSc + kScaleStages * kScaleGroups * 16;
+  // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2],
+  // sc_full, sc_empty [kScaleStages], drain
+  static constexpr int kBars = 2 * kSK + 2 * kSV + 11 + 2 * kScaleStages;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;  // + alignment slack
@@ -104,7 +106,10 @@ struct Lay {
   __device__ uint32_t pv_done(int i) const { return rest(4 + i); }
   __device__ uint32_t q_full(int i) const { return rest(6 + i); }
   __device__ uint32_t q_empty(int i) const { return rest(8 + i); }
-  __device__ uint32_t drain() const { return rest(10); }
+  __device__ uint32_t sc_full(int i) const { return rest(10 + i); }
+  __device__ uint32_t sc_empty(int i) const { return rest(10 + kScaleStages + i); }
+  __device__ uint32_t drain() const { return rest(10 + 2 * kScaleStages); }
+  __device__ float4* scales(int i) const { return reinterpret_cast<float4*>(base + C::kOffSc) + i * kScaleGroups; }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
@@ -199,19 +204,20 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
   const int per = kPagedKeys >> p.block_shift, box = p.block_size * D;
   int g = 0;
   bool ok = true;
-  for (; ok && !w.done(); w.next(p)) {
-    const int valid = paged_valid(p, w.u.q);
-    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
-    auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
-      const int i = t * per + lane;
-      if (lane >= per || i >= (valid + p.block_size - 1) >> p.block_shift) return -1;
-      const int e = __ldg(table + i);
-      return e >= 0 && e < p.num_blocks ? e : -2;
-    };
-    int next = w.nt > 0 ? lookup(w.t0) : -1;
+  auto lookup = [&](const PagedWalk<NR>& x, int n) {  // tile n of x's segment.  -1: past the last key; -2: names no block
+    const int i = (x.t0 + n) * per + lane;
+    if (lane >= per || i >= (paged_valid(p, x.u.q) + p.block_size - 1) >> p.block_shift) return -1;
+    const int e = __ldg(p.tables + (int64_t)x.u.b * p.width + i);
+    return e >= 0 && e < p.num_blocks ? e : -2;
+  };
+  int next = w.done() ? -1 : lookup(w, 0);
+  while (ok && !w.done()) {
+    PagedWalk<NR> y = w;  // the next unit, its first blocks looked up while this one's stream
+    y.next(p);
+    const int first = y.done() ? -1 : lookup(y, 0);
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int st = g % NS, blk = next;
-      if (n + 1 < w.nt) next = lookup(w.t0 + n + 1);
+      if (n + 1 < w.nt) next = lookup(w, n + 1);
       if (g >= NS && !wait_warp(empty0 + st * 8, ((g / NS) - 1) & 1, p.timeout_ns, p.status)) {
         ok = false;
         break;
@@ -224,87 +230,116 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
                     blk >= 0 ? blk * p.Hkv + w.u.kvh : p.num_blocks * p.Hkv);
       }
     }
+    w = y;
+    next = first;
   }
   // every copy lands before the CTA may exit
   for (int n = g > NS ? g - NS : 0; n < g; ++n) wait_warp(full0 + (n % NS) * 8, (n / NS) & 1, p.timeout_ns, p.status);
 }
 
-// ----------------------------------------------------------------- Q pieces
+// ------------------------------------------------------- Q pieces and scales
 // One warp: the unit's rows as e4m3 pieces, piece i of row r at row i * NR + r,
-// K-major in the swizzle of the row width; rows past the unit's are zeros.
+// K-major in the swizzle of the row width; rows past the unit's are zeros (the
+// rows of N past the pieces were zeroed once).  Then the scales of the unit's
+// tiles.  A row is D / 8 lanes wide (16 bytes each), all rows in flight
+// together; the next unit waits for this, so it is written for few
+// instructions: the largest |x| on packed 16-bit integers (magnitudes order as
+// their bits), pieces and rests on packed f16, which holds x scaled below 256
+// exactly down to 2^-24.
 template <int D, int NR, bool BF16>
 __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16>& sm, PagedWalk<NR> w, int lane) {
   using C = Cfg<D, NR, BF16>;
   const PagedParams& p = P.c;
-  constexpr int kVec = D / 8;  // 8-value pieces of a row
+  constexpr int kVec = D / 8, kPer = 32 / kVec;  // rows an instruction
+  constexpr int kLoads = NR / kPer > 0 ? NR / kPer : 1;
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on are not finite
+  const int c = lane % kVec, sub = lane / kVec;
+  ScaleFeed feed;
   for (; !w.done(); w.next(p)) {
     const int buf = w.index & 1;
     if (w.index >= 2 && !wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;
     const PagedUnit& u = w.u;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + (int64_t)u.kvh * p.group * D;
-    auto row = [&](int r) {
-      const int x = u.row0 + r;
-      return q + (int64_t)(x / p.group) * p.q_stride + (x % p.group) * D;
-    };
-    auto widen = [&](uint32_t v, float& a, float& b) {
-      if constexpr (BF16) {
-        a = __uint_as_float(v << 16);
-        b = __uint_as_float(v & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-        a = f.x;
-        b = f.y;
-      }
-    };
-    float top = 0.0f;
-    for (int c = lane; c < u.rows * kVec; c += 32) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row(c / kVec)) + c % kVec);
-      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + u.kvh * p.group * D + c * 8;
+    const int tok0 = (u.row0 + sub) / p.group;
+    int tok = tok0, head = u.row0 + sub - tok0 * p.group;
+    uint4 raw[kLoads];
+    uint32_t top2 = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float a, b;
-        widen(e[i], a, b);
-        a = fabsf(a);
-        b = fabsf(b);
-        if (a < INFINITY) top = fmaxf(top, a);
-        if (b < INFINITY) top = fmaxf(top, b);
-      }
+    for (int i = 0; i < kLoads; ++i) {
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (i * kPer + sub < u.rows)
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride + head * D));
+      for (head += kPer; head >= p.group; head -= p.group) ++tok;
     }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    // the power of two that brings the largest element into [128, 256)
-    int e = (int)(__float_as_uint(top) >> 23) - 127;
-    e = top > 0.0f ? min(max(7 - e, -120), 120) : 0;
-    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-    uint8_t* dst = sm.q_ptr(buf);
-    for (int c = lane; c < C::kNQ * kVec; c += 32) {  // 8 bytes of a row of N: rows of pieces not written stay zero
-      const int n = c / kVec, k = c % kVec, r = n % NR, piece = n / NR;
-      uint32_t lo = 0, hi = 0;
-      if (r < u.rows && piece < C::kQP) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row(r)) + k);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    // one power of two for the unit, by its largest finite element
+    bool odd[kLoads];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a, b;
-          widen(x[i], a, b);
-          // an element that is not finite makes its row's scores NaN (0x7f in the first piece)
-          const bool fa = fabsf(a) < INFINITY, fb = fabsf(b) < INFINITY;
-          a = fa ? a * up : (piece == 0 ? NAN : 0.0f);
-          b = fb ? b * up : (piece == 0 ? NAN : 0.0f);
-          for (int s = 0; s < piece; ++s) piece2(a, b);
-          const uint32_t two = last2(a, b);
-          if (i < 2) lo |= two << (16 * i); else hi |= two << (16 * (i - 2));
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t t2 = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                   __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+      odd[i] = max(t2 & 0xffffu, t2 >> 16) >= kInf;  // an infinity or NaN: its row's scores become NaN
+      if (!odd[i]) top2 = __vmaxu2(top2, t2);
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+    int ex;  // brings it into [128, 256)
+    if constexpr (BF16) ex = (int)(top >> 7) - 127;
+    else ex = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
+    ex = top == 0u ? 0 : min(max(7 - ex, -120), 120);
+    const float mul = __uint_as_float((uint32_t)(ex + 127) << 23);
+    uint8_t* dst = sm.q_ptr(buf) + (c & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = i * kPer + sub;
+      const uint32_t e[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t h[4];  // scaled, f16 pairs
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x, y;
+        if constexpr (BF16) {
+          x = __uint_as_float(e[k] << 16);
+          y = __uint_as_float(e[k] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&e[k]));
+          x = f.x;
+          y = f.y;
         }
+        f2_split(fmul2(f2(x, y), f2(mul, mul)), x, y);
+        const __half2 hh = __floats2half2_rn(x, y);
+        h[k] = *reinterpret_cast<const uint32_t*>(&hh);
       }
-      // 16-byte chunk k / 2 of the row, its index XORed as the swizzle does
-      const int chunk = D == 128 ? ((k >> 1) ^ (n & 7)) : ((k >> 1) ^ ((n >> 1) & 3));
-      *reinterpret_cast<uint2*>(dst + n * D + chunk * 16 + (k & 1) * 8) = make_uint2(lo, hi);
+#pragma unroll
+      for (int j = 0; j < C::kQP; ++j) {
+        uint32_t w2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint16_t b0, b1;
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(h[2 * k]));
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h[2 * k + 1]));
+          asm("mov.b32 %0, {%1, %2};" : "=r"(w2[k]) : "h"(b0), "h"(b1));
+          if (j + 1 < C::kQP) {  // the rest, times 32
+            uint32_t f0, f1;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f0) : "h"(b0));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f1) : "h"(b1));
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k]) : "r"(f0));
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k + 1]) : "r"(f1));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k]) : "r"(0x50005000u));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k + 1]) : "r"(0x50005000u));
+          }
+        }
+        if (odd[i]) w2[0] = w2[1] = j == 0 ? 0x7f7f7f7fu : 0u;
+        // 8 bytes of chunk c / 2 of row n, the chunk's index XORed as the swizzle does
+        const int n = j * NR + r;
+        const int at = D == 128 ? ((c >> 1) ^ (n & 7)) : ((c >> 1) ^ ((n >> 1) & 3));
+        if (NR >= kPer || r < NR) *reinterpret_cast<uint2*>(dst + n * D + at * 16) = make_uint2(w2[0], w2[1]);
+      }
     }
     for (int r = lane; r < NR; r += 32)
       sm.lim(buf)[r] = r < u.rows ? paged_limits(p, u.q, (u.row0 + r) / p.group) : make_int2(0, 0);
-    if (lane == 0) sm.qs()[buf] = 1.0f / up;
+    if (lane == 0) sm.qs()[buf] = __uint_as_float((uint32_t)(127 - ex) << 23);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(sm.q_full(buf));
+    if (!feed.unit(p, w, 1.0f, sm.scales(0), sm.sc_full(0), sm.sc_empty(0), lane)) return;
   }
 }
 
@@ -414,27 +449,6 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
   for (; !w.done(); w.next(p)) {
     const PagedUnit& u = w.u;
     const int buf = w.index & 1;
-    const int valid = paged_valid(p, u.q);
-    const int32_t* table = p.tables + (int64_t)u.b * p.width;
-    // block and scales of this thread's key, a tile ahead of their use
-    auto block_of = [&](int n) {
-      const uint32_t j = (uint32_t)(w.t0 + n) * kPagedKeys + tid;
-      const int b = n < w.nt && j < (uint32_t)valid ? __ldg(table + (j >> p.block_shift)) : -1;
-      return b >= 0 && b < p.num_blocks ? b : -1;
-    };
-    float ks_next = 0.0f, vs_next = 1.0f;
-    int blk_next = block_of(0);
-    auto fetch = [&](int n) {  // scales of tile n, block of tile n + 1
-      ks_next = 0.0f;
-      vs_next = 1.0f;
-      if (blk_next >= 0) {
-        const int64_t at = (int64_t)blk_next * p.Hkv + u.kvh;
-        ks_next = __ldg(p.k_scales + at);
-        vs_next = __ldg(p.v_scales + at);
-      }
-      blk_next = block_of(n + 1);
-    };
-    fetch(0);
     wait(sm.q_full(buf), (w.index >> 1) & 1);
     const int2* lim = sm.lim(buf);
     const float qs = sm.qs()[buf];
@@ -448,10 +462,12 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
 
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int key0 = (w.t0 + n) * kPagedKeys, j = key0 + tid;
-      const float kmul = qs * ks_next;
-      const float vsc = fmaxf(vs_next, kMinVScale);
-      const float lv = __log2f(vsc), iv = 1.0f / vsc;
-      fetch(n + 1);
+      const int st = g % kScaleStages;
+      wait(sm.sc_full(st), (g / kScaleStages) & 1);
+      const float4 scl = sm.scales(st)[tid >> 4];  // of this thread's key
+      const float kmul = qs * scl.x, lv = scl.y, iv = scl.z;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.sc_empty(st));
       wait(sm.s_full(g & 1), (g >> 1) & 1);
       tc_fence_after();
       float t[NR];
@@ -635,9 +651,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
       mbar_init(sm.q_full(i), 1);
       mbar_init(sm.q_empty(i), 5);  // four softmax warps and the MMA warp's commit
     }
+    for (int i = 0; i < kScaleStages; ++i) {
+      mbar_init(sm.sc_full(i), 1);
+      mbar_init(sm.sc_empty(i), 4);
+    }
     mbar_init(sm.drain(), 1);
     mbar_init_fence();
     P.cuts[blockIdx.x].parts = 0;
+  }
+  if constexpr (C::kQP * NR < C::kNQ) {  // rows of N that no piece fills
+    for (int i = threadIdx.x; i < 2 * C::kQBytes / 16; i += kThreads)
+      *reinterpret_cast<uint4*>(sm.q_ptr(0) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
   }
   if (warp == kKWarp && lane == 0) tma_prefetch_desc(&P.tmap_k);
   if (warp == kVWarp && lane == 0) tma_prefetch_desc(&P.tmap_v);

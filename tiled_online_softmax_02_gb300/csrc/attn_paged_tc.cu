@@ -42,11 +42,9 @@ constexpr int BM = 128, BN = kPagedKeys;
 constexpr int kRows = kPagedTcRows;    // rows of a unit: two lanes of 128
 constexpr int kThreads = 512;
 constexpr int kVWarp0 = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
-constexpr int kGroups = BN / 16;       // scale groups of a tile
 constexpr float kRise = 8.0f;          // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
-constexpr int kSC = 4;                 // stages of the scale ring
 constexpr int kMaxUnroll = 1, kExpUnroll = 1;
 
 template <int D, bool BF16>
@@ -62,12 +60,12 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + 2 * kQLane;
   static constexpr int kOffV8 = kOffK + kSK * kTile8;
   static constexpr int kOffV = kOffV8 + kSV8 * kTile8;
-  static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kSC][kGroups]: k scale, log2 v scale, 1 / v scale
-  static constexpr int kOffQe = kOffSc + kSC * kGroups * 16;  // int8 [256]: log2 of the Q rows' scales
+  static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kScaleStages][kScaleGroups]: k scale, log2 v scale, 1 / v scale
+  static constexpr int kOffQe = kOffSc + kScaleStages * kScaleGroups * 16;  // int8 [256]: log2 of the Q rows' scales
   static constexpr int kOffBar = kOffQe + kRows;
-  // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_full, sc_empty [kSC],
+  // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_full, sc_empty [kScaleStages],
   // q_full, s_full, p_full, o_final [2], drain
-  static constexpr int kBars = 2 * (kSK + kSV8 + kSV + kSC) + 9;
+  static constexpr int kBars = 2 * (kSK + kSV8 + kSV + kScaleStages) + 9;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;
@@ -87,7 +85,7 @@ struct Lay {
   __device__ const uint8_t* v8_ptr(int i) const { return base + C::kOffV8 + i * C::kTile8; }
   __device__ uint32_t v_tile(int i) const { return s + C::kOffV + i * C::kTile16; }
   __device__ uint8_t* v_ptr(int i) const { return base + C::kOffV + i * C::kTile16; }
-  __device__ float4* scales(int i) const { return reinterpret_cast<float4*>(base + C::kOffSc) + i * kGroups; }
+  __device__ float4* scales(int i) const { return reinterpret_cast<float4*>(base + C::kOffSc) + i * kScaleGroups; }
   __device__ uint32_t bar(int i) const { return s + C::kOffBar + i * 8; }
   __device__ uint32_t k_full(int i) const { return bar(i); }
   __device__ uint32_t k_empty(int i) const { return bar(C::kSK + i); }
@@ -97,12 +95,12 @@ struct Lay {
   __device__ uint32_t v_empty(int i) const { return bar(2 * C::kSK + 2 * C::kSV8 + C::kSV + i); }
   __device__ uint32_t rest(int i) const { return bar(2 * (C::kSK + C::kSV8 + C::kSV) + i); }
   __device__ uint32_t sc_full(int i) const { return rest(i); }
-  __device__ uint32_t sc_empty(int i) const { return rest(kSC + i); }
-  __device__ uint32_t q_full(int t) const { return rest(2 * kSC + t); }
-  __device__ uint32_t s_full(int t) const { return rest(2 * kSC + 2 + t); }
-  __device__ uint32_t p_full(int t) const { return rest(2 * kSC + 4 + t); }
-  __device__ uint32_t o_final(int t) const { return rest(2 * kSC + 6 + t); }
-  __device__ uint32_t drain() const { return rest(2 * kSC + 8); }
+  __device__ uint32_t sc_empty(int i) const { return rest(kScaleStages + i); }
+  __device__ uint32_t q_full(int t) const { return rest(2 * kScaleStages + t); }
+  __device__ uint32_t s_full(int t) const { return rest(2 * kScaleStages + 2 + t); }
+  __device__ uint32_t p_full(int t) const { return rest(2 * kScaleStages + 4 + t); }
+  __device__ uint32_t o_final(int t) const { return rest(2 * kScaleStages + 6 + t); }
+  __device__ uint32_t drain() const { return rest(2 * kScaleStages + 8); }
   __device__ int8_t* q_exp() const { return reinterpret_cast<int8_t*>(base + C::kOffQe); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
@@ -173,47 +171,20 @@ __device__ __forceinline__ void load_role(const PagedTcParams& P, const Lay<D, B
 }
 
 // ------------------------------------------------------------------ scales
-// One warp: lane i < 8 holds the scales of keys 16 i .. of a tile.
+// One warp: the scales of every tile, and the next unit's Q rows into L2.
 template <int D, bool BF16>
 __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, int lane) {
   const PagedParams& p = P.c;
-  int g = 0;
+  ScaleFeed feed;
   for (; !w.done(); w.next(p)) {
     Walk x = w;
     x.next(p);
-    if (!x.done()) {  // the next unit's Q: whole tokens of the kv head's query heads
+    if (!x.done()) {  // whole tokens of the kv head's query heads
       const int t0 = x.u.row0 / p.group, t1 = (x.u.row0 + x.u.rows - 1) / p.group;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)x.u.q.s0 * p.q_stride + x.u.kvh * p.group * D;
       for (int i = t0 + lane; i <= t1; i += 32) bulk_prefetch_l2(q + i * p.q_stride, (uint32_t)(p.group * D * 2));
     }
-    const int valid = paged_valid(p, w.u.q);
-    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
-    auto block_of = [&](int n) {
-      const uint32_t j = (uint32_t)(w.t0 + n) * BN + lane * 16;
-      const int b = lane < kGroups && n < w.nt && j < (uint32_t)valid ? __ldg(table + (j >> p.block_shift)) : -1;
-      return b >= 0 && b < p.num_blocks ? b : -1;
-    };
-    int blk = block_of(0), blk1 = block_of(1);
-    float ks = 0.0f, vs = 1.0f;
-    auto fetch = [&](int b) {
-      ks = 0.0f;
-      vs = 1.0f;
-      if (b >= 0) {
-        ks = __ldg(p.k_scales + (int64_t)b * p.Hkv + w.u.kvh);
-        vs = __ldg(p.v_scales + (int64_t)b * p.Hkv + w.u.kvh);
-      }
-    };
-    fetch(blk);
-    for (int n = 0; n < w.nt; ++n, ++g) {
-      const float k0 = ks, v0 = fmaxf(vs, kMinVScale);
-      fetch(blk1);
-      blk1 = block_of(n + 2);
-      const int st = g % kSC;
-      if (g >= kSC && !wait_warp(sm.sc_empty(st), ((g / kSC) - 1) & 1, p.timeout_ns, p.status)) return;
-      if (lane < kGroups) sm.scales(st)[lane] = make_float4(k0 * P.scale_log2, __log2f(v0), 1.0f / v0, 0.0f);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm.sc_full(st));
-    }
+    if (!feed.unit(p, w, P.scale_log2, sm.scales(0), sm.sc_full(0), sm.sc_empty(0), lane)) return;
   }
 }
 
@@ -545,8 +516,8 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     const int nt = w.nt, t0 = w.t0;
     if (!lane_on(u, t)) {  // the other lane's tiles pass by; their scales too
       for (int n = 0; n < nt; ++n, ++g) {
-        if (!wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
-        if (lane == 0) mbar_arrive(sm.sc_empty(g % kSC));
+        if (!wait_warp(sm.sc_full(g % kScaleStages), (g / kScaleStages) & 1, p.timeout_ns, p.status)) return;
+        if (lane == 0) mbar_arrive(sm.sc_empty(g % kScaleStages));
       }
       w.next(p);
       continue;
@@ -560,10 +531,10 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     l_run = 0.0f;
     for (int n = 0; n < nt; ++n, ++g, ++sc) {
       const int key0 = (t0 + n) * BN;
-      if (!wait_warp(sm.sc_full(g % kSC), (g / kSC) & 1, p.timeout_ns, p.status)) return;
+      if (!wait_warp(sm.sc_full(g % kScaleStages), (g / kScaleStages) & 1, p.timeout_ns, p.status)) return;
       // a group's (k scale |scale| log2 e, log2 v scale, 1 / v scale); raw scores times the row's
       // factor and the first are in log2 units.  The product stays above 0, so that -inf stays -inf
-      const float4* scl = sm.scales(g % kSC);
+      const float4* scl = sm.scales(g % kScaleStages);
       if (!wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
       tc_fence_after();
       if (key0 < full_lo || key0 + BN > full_hi) {  // some key is hidden from some row: -inf over its score
@@ -665,7 +636,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(sm.sc_empty(g % kSC));
+        mbar_arrive(sm.sc_empty(g % kScaleStages));
         mbar_arrive(sm.p_full(t));
       }
     }
@@ -711,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       mbar_init(sm.v_full(i), 4);
       mbar_init(sm.v_empty(i), 1);
     }
-    for (int i = 0; i < kSC; ++i) {
+    for (int i = 0; i < kScaleStages; ++i) {
       mbar_init(sm.sc_full(i), 1);
       mbar_init(sm.sc_empty(i), 8);
     }

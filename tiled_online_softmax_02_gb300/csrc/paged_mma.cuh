@@ -13,26 +13,7 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;         // running maximum of a row that has seen no key
-constexpr float kMinVScale = 7.9e-31f;  // 2^-100: a block of zeros may have scale 0
 constexpr float kPieceStep = 32.0f;     // from one e4m3 piece to the next
-
-// mbar_wait_warp in fewer instructions: these kernels have many waits in many
-// roles, and are bound by their instruction fetches before anything else.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t timeout_ns, int* status) {
-  uint64_t t0 = 0;
-  bool ok = true;
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if ((it & 15u) != 0u) continue;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > timeout_ns) {
-      atomicOr(status, kStatusTimeout);
-      ok = false;
-      break;
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulator (bits
 // 4-5 = 1), A and B e4m3 (bits 7-9 and 10-12 = 0), major-ness of A / B in bits

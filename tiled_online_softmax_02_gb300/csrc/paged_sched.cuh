@@ -20,6 +20,24 @@ namespace gb300_attn {
 
 constexpr int kPagedKeys = 128;  // keys of a tile
 
+// mbar_wait_warp in fewer instructions: these kernels have many waits in many
+// roles, and are bound by their instruction fetches before anything else.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t timeout_ns, int* status) {
+  uint64_t t0 = 0;
+  bool ok = true;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 15u) != 0u) continue;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > timeout_ns) {
+      atomicOr(status, kStatusTimeout);
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // A request's packed rows and lengths.
 struct PagedReq {
   int s0, n;   // first row, rows
@@ -67,16 +85,16 @@ __device__ __forceinline__ void paged_unit_tiles(const PagedParams& p, PagedUnit
 
 // What a unit costs besides its tiles, in tiles.
 template <int NR>
-constexpr int kOver = NR == kPagedTcRows ? 3 : 1;
+constexpr int kOver = 3;
 
 template <int NR>
 __device__ __forceinline__ int paged_cost(const PagedUnit& u) { return max(u.te - u.tb, 1) + kOver<NR>; }
 
-// Tiles of one kv head of request b: the sum over its row tiles.
+// Length on the line of one kv head of a request: the sum over its row tiles.
 template <int NR>
-__device__ __forceinline__ long long paged_head_cost(const PagedParams& p, int b) {
+__device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedReq& q) {
   PagedUnit u;
-  u.q = paged_req(p, b);
+  u.q = q;
   const int rows = u.q.n * p.group;
   long long c = 0;
   for (u.rt = 0; u.rt * NR < rows; ++u.rt) {
@@ -86,25 +104,38 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, int b
   return c;
 }
 
+// a / b for 0 <= a, 0 < b, in 32 bits where they fit.
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A CTA's piece of the line, in shared memory.
 struct PagedShare {
-  long long total;      // length of the line
+  long long per, more;  // length of a piece; the first `more` ones are longer by one
   long long w0, w1;     // this CTA's piece
   int ctas;             // CTAs that have a piece
   int b, kvh, rt, off;  // the unit w0 lies in, and how far into it: 0, or more than kOver
+  PagedReq q;           // its request
   long long warp_sum[32];
 };
 
-__device__ __forceinline__ long long paged_cut(long long total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ long long paged_cut(long long per, long long more, int c) {
+  return per * c + min((long long)c, more);
+}
 
 // Called by every thread of the CTA (NT threads) before a __syncthreads().
 template <int NR, int NT>
 __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + NT - 1) / NT;
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += paged_head_cost<NR>(p, b) * p.Hkv;
+  const int n = (p.B + NT - 1) / NT;  // requests of a thread
+  const int b0 = min(tid * n, p.B), b1 = min(b0 + n, p.B);
+  PagedReq q{0, 0, 0};
+  long long c = 0, mine = 0;  // of the thread's last request; of all of them
+  for (int b = b0; b < b1; ++b) {
+    q = paged_req(p, b);
+    c = paged_head_cost<NR>(p, q);
+    mine += c * p.Hkv;
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -121,10 +152,16 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
   }
   const int ctas = (int)min((long long)gridDim.x, total);
   const bool in = (int)blockIdx.x < ctas;
-  const long long w0 = in ? paged_cut(total, ctas, blockIdx.x) : 0;
-  const long long w1 = in ? paged_cut(total, ctas, blockIdx.x + 1) : 0;
+  long long per = 0, more = 0, w0 = 0, w1 = 0;
+  if (in) {
+    per = paged_div(total, ctas);
+    more = total - per * ctas;
+    w0 = paged_cut(per, more, blockIdx.x);
+    w1 = paged_cut(per, more, blockIdx.x + 1);
+  }
   if (tid == 0) {
-    sh->total = total;
+    sh->per = per;
+    sh->more = more;
     sh->ctas = ctas;
     if (!in) sh->w0 = 0;
     if (!in || w1 == total) sh->w1 = w1;
@@ -133,16 +170,20 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
   for (int end = 0; end < 2; ++end) {
     const long long at = end ? w1 : w0;
     if (!in || at < before || at >= before + mine) continue;
-    long long rest = at - before, c;
+    long long rest = at - before;
     PagedUnit u;
-    for (u.b = b0;; ++u.b) {
-      c = paged_head_cost<NR>(p, u.b);
-      if (rest < c * p.Hkv) break;
-      rest -= c * p.Hkv;
+    u.b = b1 - 1;
+    u.q = q;
+    if (n > 1) {  // not the thread's only request
+      for (u.b = b0;; ++u.b) {
+        u.q = paged_req(p, u.b);
+        c = paged_head_cost<NR>(p, u.q);
+        if (rest < c * p.Hkv) break;
+        rest -= c * p.Hkv;
+      }
     }
-    u.kvh = (int)(rest / c);
+    u.kvh = (int)paged_div(rest, c);
     rest -= c * u.kvh;
-    u.q = paged_req(p, u.b);
     for (u.rt = 0;; ++u.rt) {
       paged_unit_tiles<NR>(p, u);
       if (rest < paged_cost<NR>(u)) break;
@@ -157,6 +198,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
       sh->kvh = u.kvh;
       sh->rt = u.rt;
       sh->off = off;
+      sh->q = u.q;
     }
   }
 }
@@ -165,6 +207,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
 template <int NR>
 struct PagedWalk {
   PagedUnit u;
+  PagedReq ahead;        // of request u.b + 1, read a unit or more before it is needed
   int left, off;         // what is left of the piece; how far into the unit this segment begins
   int t0, nt;            // key tiles of this segment (nt = 0: a unit without visible keys)
   bool head, whole;      // begins at the unit's first tile; holds all of it
@@ -177,7 +220,8 @@ struct PagedWalk {
     u.b = s->b;
     u.kvh = s->kvh;
     u.rt = s->rt;
-    u.q = paged_req(p, u.b);
+    u.q = s->q;
+    ahead = paged_req(p, min(u.b + 1, p.B - 1));
     paged_unit_tiles<NR>(p, u);
     off = s->off;
     segment();
@@ -200,7 +244,11 @@ struct PagedWalk {
       u.rt = 0;
       if (++u.kvh == p.Hkv) {
         u.kvh = 0;
-        do u.q = paged_req(p, ++u.b); while (u.q.n == 0);
+        do {  // the piece goes on, so some later request has rows
+          ++u.b;
+          u.q = ahead;
+          ahead = paged_req(p, min(u.b + 1, p.B - 1));
+        } while (u.q.n == 0);
       }
     }
     paged_unit_tiles<NR>(p, u);
@@ -213,8 +261,56 @@ template <int NR>
 __device__ __forceinline__ int paged_parts(const PagedWalk<NR>& w, const PagedShare* s) {
   const long long last = s->w1 - w.left - w.off + paged_cost<NR>(w.u) - 1;
   int c = blockIdx.x;
-  while (c + 1 < s->ctas && paged_cut(s->total, s->ctas, c + 1) <= last) ++c;
+  while (c + 1 < s->ctas && paged_cut(s->per, s->more, c + 1) <= last) ++c;
   return c - (int)blockIdx.x + 1;
 }
+
+// The scales of a unit's tiles, from block tables and scale arrays into a ring
+// in shared memory, by one warp: lane i < 8 has keys 16 i .. of a tile (a block
+// holds 16 or more).  An entry is (k scale * mul, log2 v scale, 1 / v scale).
+constexpr int kScaleGroups = kPagedKeys / 16;
+constexpr int kScaleStages = 4;
+constexpr float kMinVScale = 7.9e-31f;  // 2^-100: a block of zeros may have scale 0
+
+struct ScaleFeed {
+  int g = 0;  // tiles so far
+  template <int NR>
+  __device__ __forceinline__ bool unit(const PagedParams& p, const PagedWalk<NR>& w, float mul, float4* ring,
+                                       uint32_t full0, uint32_t empty0, int lane) {
+    const int valid = paged_valid(p, w.u.q);
+    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
+    auto block_of = [&](int n) {
+      const uint32_t j = (uint32_t)(w.t0 + n) * kPagedKeys + lane * 16;
+      const int b = lane < kScaleGroups && n < w.nt && j < (uint32_t)valid ? __ldg(table + (j >> p.block_shift)) : -1;
+      return b >= 0 && b < p.num_blocks ? b : -1;
+    };
+    float ks, vs;
+    auto fetch = [&](int b) {  // a block that is none has key scale 0
+      ks = 0.0f;
+      vs = 1.0f;
+      if (b >= 0) {
+        ks = __ldg(p.k_scales + (int64_t)b * p.Hkv + w.u.kvh);
+        vs = __ldg(p.v_scales + (int64_t)b * p.Hkv + w.u.kvh);
+      }
+    };
+    const int first = block_of(0);
+    int next = block_of(1);
+    fetch(first);
+    for (int n = 0; n < w.nt; ++n, ++g) {  // scales a tile ahead, blocks two
+      const float k0 = ks, v0 = fmaxf(vs, kMinVScale);
+      fetch(next);
+      next = block_of(n + 2);
+      const int st = g % kScaleStages;
+      if (g >= kScaleStages &&
+          !wait_warp(empty0 + st * 8, ((g / kScaleStages) - 1) & 1, p.timeout_ns, p.status))
+        return false;
+      if (lane < kScaleGroups)
+        ring[st * kScaleGroups + lane] = make_float4(k0 * mul, __log2f(v0), 1.0f / v0, 0.0f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + st * 8);
+    }
+    return true;
+  }
+};
 
 }  // namespace gb300_attn
