@@ -9,6 +9,7 @@ library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -84,6 +85,8 @@ def library_path() -> str:
 def load_library():
     """Load libattn.so; raises if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -453,8 +456,10 @@ def dsa_index_select(query, key, weights, bias, *, top_k, scale, weights_scale=1
 
 # ---------------------------------------------------------------------------
 # The paged 8-bit KV cache.  These calls run once a layer or once a step with
-# little work each, so the checks here are written to cost few microseconds.
+# little work each (a decode step's kernels take about ten microseconds), so
+# the checks are written to cost few microseconds.
 CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 class _NullContext:
@@ -468,38 +473,45 @@ class _NullContext:
 _NULL = _NullContext()
 
 
-def _on(device):
-    """A context with `device` current: nothing to do when it already is."""
-    return _NULL if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _on(index):
+    """A context with device `index` current: nothing to do when it already is."""
+    return _NULL if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _need(t, name, dtype, shape, device):
-    """Raises unless t is a contiguous tensor of this dtype, shape and device."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}: got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _need(t, name, dtype, shape, index):
+    """Raises unless t is a contiguous tensor of this dtype and shape on CUDA device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}: got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
-def _cache_shape(k_cache, v_cache, k_scales, v_scales, Hkv, D, device):
-    """(num_blocks, block_size) of a cache, after checking its four tensors."""
-    if k_cache.dim() != 4 or k_cache.dtype not in CACHE_DTYPES:
-        raise ValueError("the caches must be [num_blocks, Hkv, block_size, D] of float8_e4m3fn or uint8")
-    num_blocks, heads, block_size, width = k_cache.shape
-    if heads != Hkv or width != D:
-        raise ValueError(f"shape mismatch: rows of {Hkv} kv heads and head dim {D}, cache {tuple(k_cache.shape)}")
-    _need(k_cache, "k_cache", k_cache.dtype, (num_blocks, Hkv, block_size, D), device)
-    _need(v_cache, "v_cache", k_cache.dtype, (num_blocks, Hkv, block_size, D), device)
-    _need(k_scales, "k_scales", torch.float32, (num_blocks, Hkv), device)
-    _need(v_scales, "v_scales", torch.float32, (num_blocks, Hkv), device)
-    return num_blocks, block_size
+def _cache_shape(k_cache, v_cache, k_scales, v_scales, D, index):
+    """(num_blocks, Hkv, block_size) of a cache, after checking its four tensors."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != D or k_cache.dtype not in CACHE_DTYPES:
+        raise ValueError(f"the caches must be [num_blocks, Hkv, block_size, {D}] of float8_e4m3fn or uint8: got "
+                         f"{k_cache.dtype} {tuple(shape)}")
+    dtype, blocks = k_cache.dtype, shape[:2]
+    _need(k_cache, "k_cache", dtype, shape, index)
+    _need(v_cache, "v_cache", dtype, shape, index)
+    _need(k_scales, "k_scales", _F32, blocks, index)
+    _need(v_scales, "v_scales", _F32, blocks, index)
+    return shape[0], shape[1], shape[2]
 
 
 def _token_stride(t, name):
     """Elements from one token of a [T, H, D] tensor to the next; its heads must be dense."""
     T, H, D = t.shape
-    if t.stride(2) != 1 and D > 1 or t.stride(1) != D and H > 1:
-        raise ValueError(f"{name}: the heads of a token must be contiguous, strides {t.stride()}")
-    return t.stride(0) if T > 1 else H * D
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, strides {(st, sh, sd)}")
+    return st if T > 1 else H * D
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace(num_tokens, B, Hq, Hkv, D, index):
+    with _on(index):
+        return load_library().attn_paged_workspace_bytes(num_tokens, B, Hq, Hkv, D)
 
 
 def attn_cache_assign(past_lengths, new_lengths, block_tables, free_blocks, free_count, *, block_size, num_tokens,
@@ -516,40 +528,43 @@ def attn_cache_assign(past_lengths, new_lengths, block_tables, free_blocks, free
     when not given; result is 0, or why the step was not done (1 too few free
     blocks, 2 a table row too short, 3 too many tokens, 4 a negative length, 5
     a count or entry out of range), in which case nothing was assigned."""
-    dev = past_lengths.device
-    if not past_lengths.is_cuda or past_lengths.dim() != 1 or block_tables.dim() != 2 or free_blocks.dim() != 1:
+    index = past_lengths.get_device()
+    if index < 0 or past_lengths.dim() != 1 or block_tables.dim() != 2 or free_blocks.dim() != 1:
         raise ValueError("attn_cache_assign takes CUDA tensors: lengths [B], block_tables [B, max_blocks], "
                          "free_blocks [num_blocks]")
-    B, T, i32 = past_lengths.shape[0], int(num_tokens), torch.int32
-    width, num_blocks = block_tables.shape[1], free_blocks.shape[0]
-    _need(past_lengths, "past_lengths", i32, (B,), dev)
-    _need(new_lengths, "new_lengths", i32, (B,), dev)
-    _need(block_tables, "block_tables", i32, (B, width), dev)
-    _need(free_blocks, "free_blocks", i32, (num_blocks,), dev)
-    _need(free_count, "free_count", i32, (1,), dev)
+    B, width = block_tables.shape
+    T, num_blocks = int(num_tokens), free_blocks.shape[0]
+    _need(past_lengths, "past_lengths", _I32, (B,), index)
+    _need(new_lengths, "new_lengths", _I32, (B,), index)
+    _need(block_tables, "block_tables", _I32, (B, width), index)
+    _need(free_blocks, "free_blocks", _I32, (num_blocks,), index)
+    _need(free_count, "free_count", _I32, (1,), index)
     if finished is not None:
         if finished.dtype not in (torch.bool, torch.uint8):
             raise ValueError("finished must be bool or uint8")
-        _need(finished, "finished", finished.dtype, (B,), dev)
+        _need(finished, "finished", finished.dtype, (B,), index)
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    made = []
-    for t, name, dtype, n in ((q_starts, "q_starts", i32, B + 1), (total_lengths, "total_lengths", i32, B),
-                              (slot_map, "slot_map", torch.int64, T), (result, "result", i32, 1)):
+
+    def made(t, name, dtype, n):
         if t is None:
-            t = torch.empty(n, dtype=dtype, device=dev)
-        else:
-            _need(t, name, dtype, (n,), dev)
-        made.append(t)
-    with _on(dev):
+            return torch.empty(n, dtype=dtype, device=past_lengths.device)
+        _need(t, name, dtype, (n,), index)
+        return t
+
+    q_starts = made(q_starts, "q_starts", _I32, B + 1)
+    total_lengths = made(total_lengths, "total_lengths", _I32, B)
+    slot_map = made(slot_map, "slot_map", _I64, T)
+    result = made(result, "result", _I32, 1)
+    with _on(index):
         rc = load_library().attn_cache_assign(
             past_lengths.data_ptr(), new_lengths.data_ptr(), None if finished is None else finished.data_ptr(),
-            block_tables.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(), made[0].data_ptr(),
-            made[1].data_ptr(), made[2].data_ptr(), made[3].data_ptr(), B, width, int(block_size), num_blocks, T,
-            _stream_handle(dev))
+            block_tables.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(), q_starts.data_ptr(),
+            total_lengths.data_ptr(), slot_map.data_ptr(), result.data_ptr(), B, width, int(block_size), num_blocks, T,
+            torch._C._cuda_getCurrentRawStream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_assign")
-    return tuple(made)
+    return q_starts, total_lengths, slot_map, result
 
 
 def attn_cache_append_fp8(k, v, slot_map, k_cache, v_cache, k_scales, v_scales):
@@ -560,19 +575,21 @@ def attn_cache_append_fp8(k, v, slot_map, k_cache, v_cache, k_scales, v_scales):
     heads contiguous, tokens any stride apart); slot_map int64 [T] (negative =
     skip); k_cache, v_cache [num_blocks, Hkv, block_size, D] float8_e4m3fn (or
     uint8) and k_scales, v_scales float32 [num_blocks, Hkv], updated in place."""
-    if k.dim() != 3 or not k.is_cuda or v.shape != k.shape or v.device != k.device:
+    index, dtype = k.get_device(), k.dtype
+    if k.dim() != 3 or index < 0 or v.shape != k.shape or v.get_device() != index:
         raise ValueError("k, v must be CUDA tensors [T, Hkv, D] of one shape and device")
-    if k.dtype not in DTYPE_CODES or v.dtype != k.dtype:
+    if dtype not in DTYPE_CODES or v.dtype is not dtype:
         raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
     T, Hkv, D = k.shape
-    dev = k.device
-    num_blocks, block_size = _cache_shape(k_cache, v_cache, k_scales, v_scales, Hkv, D, dev)
-    _need(slot_map, "slot_map", torch.int64, (T,), dev)
-    with _on(dev):
+    num_blocks, heads, block_size = _cache_shape(k_cache, v_cache, k_scales, v_scales, D, index)
+    if heads != Hkv:
+        raise ValueError(f"shape mismatch: rows of {Hkv} kv heads, a cache of {heads}")
+    _need(slot_map, "slot_map", _I64, (T,), index)
+    with _on(index):
         rc = load_library().attn_cache_append_fp8(
             k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scales.data_ptr(), v_scales.data_ptr(), T, Hkv, D, _token_stride(k, "k"), _token_stride(v, "v"),
-            num_blocks, block_size, DTYPE_CODES[k.dtype], _stream_handle(dev))
+            num_blocks, block_size, DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_append_fp8")
 
@@ -591,37 +608,39 @@ def attn_fwd_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_
     request are not written); lse, when given, float32 [T, Hq], receives the
     natural-log log-sum-exp of each row.  The workspace
     (attn_paged_workspace_bytes) is allocated with torch when not given."""
-    if q.dim() != 3 or not q.is_cuda or k_cache.dim() != 4 or block_tables.dim() != 2:
+    index, dtype = q.get_device(), q.dtype
+    if q.dim() != 3 or index < 0 or block_tables.dim() != 2:
         raise ValueError("attn_fwd_paged_fp8 takes CUDA tensors: q [T, Hq, D], caches "
                          "[num_blocks, Hkv, block_size, D], block_tables [B, max_blocks]")
-    if q.dtype not in (torch.float16, torch.bfloat16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError("q must be float16 or bfloat16")
-    T, Hq, D = q.shape
-    dev, Hkv, (B, width) = q.device, k_cache.shape[1], block_tables.shape
-    num_blocks, block_size = _cache_shape(k_cache, v_cache, k_scales, v_scales, Hkv, D, dev)
-    _need(block_tables, "block_tables", torch.int32, (B, width), dev)
-    _need(q_starts, "q_starts", torch.int32, (B + 1,), dev)
-    _need(total_lengths, "total_lengths", torch.int32, (B,), dev)
+    shape = q.shape
+    T, Hq, D = shape
+    B, width = block_tables.shape
+    num_blocks, Hkv, block_size = _cache_shape(k_cache, v_cache, k_scales, v_scales, D, index)
+    _need(block_tables, "block_tables", _I32, (B, width), index)
+    _need(q_starts, "q_starts", _I32, (B + 1,), index)
+    _need(total_lengths, "total_lengths", _I32, (B,), index)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
     else:
-        _need(out, "out", q.dtype, (T, Hq, D), dev)
+        _need(out, "out", dtype, shape, index)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (T, Hq), dev)
-    lib = load_library()
-    with _on(dev):
-        need = lib.attn_paged_workspace_bytes(T, B, Hq, Hkv, D)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        rc = lib.attn_fwd_paged_fp8(
+        _need(lse, "lse", _F32, (T, Hq), index)
+    ws_bytes = _paged_workspace(T, B, Hq, Hkv, D, index)
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    with _on(index):
+        rc = load_library().attn_fwd_paged_fp8(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             block_tables.data_ptr(), q_starts.data_ptr(), total_lengths.data_ptr(), out.data_ptr(),
             None if lse is None else lse.data_ptr(), T, B, Hq, Hkv, D, _token_stride(q, "q"), num_blocks, block_size,
-            width, int(bool(causal)), int(local_window), 1.0 / math.sqrt(D) if scale is None else float(scale),
-            float(softcap), DTYPE_CODES[q.dtype], None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(dev))
+            width, 1 if causal else 0, int(local_window), 1.0 / math.sqrt(D) if scale is None else scale, softcap,
+            DTYPE_CODES[dtype], workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_paged_fp8")
     return out

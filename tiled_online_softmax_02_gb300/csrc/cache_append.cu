@@ -14,8 +14,11 @@
 // Bound: HBM for prompts (2 or 4 bytes in and 1 out per value), the latency
 // of one load -> maximum -> store chain for a decode step.  One CTA owns the
 // runs that begin in its chunk of tokens, for one head of K or of V: short
-// runs (a decode step's) take a warp each, long ones the whole CTA, and a
-// run's second reading comes out of L1.
+// runs (a decode step's) take a warp each, long ones the whole CTA.  The slots
+// that can matter are read once into shared memory, and a thread keeps its
+// first values in registers between finding the maximum and encoding them.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -29,37 +32,82 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxChunk = 16;
-constexpr int kShortRun = 4;  // tokens: up to this many a warp takes alone
+constexpr int kMaxChunk = 64;
+constexpr int kWindow = 1 + kMaxChunk + 128;  // slots kept: one before the chunk, and a block after it
+constexpr int kWarpPieces = 128;  // up to this many 16-value pieces a warp takes a run alone
 
-// 16 values at src as fp32.
-__device__ __forceinline__ void load16(const float* src, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(src) + i);
-    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-  }
-}
-__device__ __forceinline__ float2 widen(uint32_t w, __half) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-__device__ __forceinline__ float2 widen(uint32_t w, __nv_bfloat16) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-}
+// 16 values of a row as they lie in memory: what a thread takes at a time.
 template <typename T>
-__device__ __forceinline__ void load16(const T* src, float (&x)[16]) {
+struct Piece {
+  static constexpr int kVecs = sizeof(T);  // 16-byte loads
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < kVecs; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+  }
+  __device__ __forceinline__ void widen(float (&x)[16]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = widen(w[j], T{});
-      x[8 * i + 2 * j] = f.x;
-      x[8 * i + 2 * j + 1] = f.y;
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          x[4 * i + j] = __uint_as_float(w[j]);
+        } else {
+          const float2 f = pair(w[j], T{});
+          x[8 * i + 2 * j] = f.x;
+          x[8 * i + 2 * j + 1] = f.y;
+        }
+      }
     }
   }
-}
+  static __device__ __forceinline__ float2 pair(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ float2 pair(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ float2 pair(uint32_t, float) { return make_float2(0.0f, 0.0f); }
+  // The largest finite |x|, as fp32 bits: magnitudes order as their bits, and
+  // 16-bit ones are compared two at a time.
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a = w[j] & 0x7fffffffu;
+          m = a < 0x7f800000u ? max(m, a) : m;
+        }
+      }
+      return m;
+    } else {
+      constexpr uint32_t inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                 __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+      uint32_t t = max(m & 0xffffu, m >> 16);
+      if (t >= inf) {  // infinities and NaN set no scale
+        t = 0;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+            t = lo < inf ? max(t, lo) : t;
+            t = hi < inf ? max(t, hi) : t;
+          }
+        }
+      }
+      return __float_as_uint(pair(t, T{}).x);
+    }
+  }
+};
 
 // 16 e4m3 bytes of x * mul.
 __device__ __forceinline__ uint4 encode16(const float (&x)[16], float mul) {
@@ -98,34 +146,51 @@ __device__ __forceinline__ float scale_for(float amax) {
 // threads tid, tid + NT, ... of one warp (NT = 32) or of the CTA.
 template <typename T, int D, int NT>
 __device__ __forceinline__ void append_run(const T* x, int64_t stride, uint8_t* tile, float* scale, int off0,
-                                           int len, int tid, float* red) {
+                                           int len, int tid, uint32_t* red) {
   constexpr int kVec = D / 16;  // 16-value pieces of a row
   const float old = off0 > 0 ? *scale : 0.0f;
-  float amax = 0.0f;
-  for (int c = tid; c < len * kVec; c += NT) {
-    float v[16];
-    load16(x + (int64_t)(c / kVec) * stride + (c % kVec) * 16, v);
+  const T* x0 = x + (tid % kVec) * 16;  // NT is a multiple of kVec: a thread keeps its column
+  constexpr int kKeep = 2;              // pieces kept in registers
+  Piece<T> keep[kKeep];
+  const int pieces = len * kVec;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = fabsf(v[i]);
-      amax = a <= 3.4028235e38f ? fmaxf(amax, a) : amax;  // infinities and NaN set no scale
-    }
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + k * NT < pieces) keep[k].load(x0 + (int64_t)((tid + k * NT) / kVec) * stride);
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + k * NT < pieces) top = max(top, keep[k].top());
+#pragma unroll 2
+  for (int c = tid + kKeep * NT; c < pieces; c += NT) {
+    Piece<T> v;
+    v.load(x0 + (int64_t)(c / kVec) * stride);
+    top = max(top, v.top());
   }
-  // non-negative floats order as their bits
-  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+  top = __reduce_max_sync(0xffffffffu, top);
   if constexpr (NT > 32) {
     __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = __uint_as_float(top);
+    if ((tid & 31) == 0) red[tid >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) top = max(top, __float_as_uint(red[w]));
+    for (int w = 0; w < NT / 32; ++w) top = max(top, red[w]);
   }
   const float s = fmaxf(scale_for(__uint_as_float(top)), old);
   const float inv = 1.0f / s;
-  for (int c = tid; c < len * kVec; c += NT) {
+  uint8_t* out = tile + off0 * D + (tid % kVec) * 16;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + k * NT < pieces) {
+      float v[16];
+      keep[k].widen(v);
+      *reinterpret_cast<uint4*>(out + (tid + k * NT) / kVec * D) = encode16(v, inv);
+    }
+#pragma unroll 2
+  for (int c = tid + kKeep * NT; c < pieces; c += NT) {
+    Piece<T> w;
+    w.load(x0 + (int64_t)(c / kVec) * stride);
     float v[16];
-    load16(x + (int64_t)(c / kVec) * stride + (c % kVec) * 16, v);
-    *reinterpret_cast<uint4*>(tile + (off0 + c / kVec) * D + (c % kVec) * 16) = encode16(v, inv);
+    w.widen(v);
+    *reinterpret_cast<uint4*>(out + c / kVec * D) = encode16(v, inv);
   }
   if (off0 > 0 && s > old) {
     const float again = old * inv;
@@ -141,39 +206,48 @@ __device__ __forceinline__ void append_run(const T* x, int64_t stride, uint8_t* 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ int64_t slots[kMaxChunk + 1];  // of tokens first - 1 ..
-  __shared__ int begin[kMaxChunk];          // 1 where a run begins
-  __shared__ float red[kWarps];
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_append_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ int64_t window[kWindow];  // slots of tokens first - 1 ..
+  __shared__ uint32_t begin[kMaxChunk / 32];  // a bit where a block's tokens begin
+  __shared__ uint32_t red[kWarps];
   const int first = blockIdx.x * p.chunk, h = blockIdx.y, which = blockIdx.z;
   const int n = min(p.chunk, p.T - first);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x <= n)
-    slots[threadIdx.x] = first + (int)threadIdx.x == 0 ? -1 : __ldg(p.slot_map + first + threadIdx.x - 1);
+  const int bs = p.block_size, shift = p.block_shift;
+  const int held = 1 + p.chunk + bs;
+  for (int i = threadIdx.x; i < held; i += kThreads) {
+    const int t = first + i - 1;
+    window[i] = t >= 0 && t < p.T ? __ldg(p.slot_map + t) : -1;
+  }
   __syncthreads();
-  const int bs = p.block_size;
+  auto slot_of = [&](int t) -> int64_t {  // -1 past the map
+    const int i = t - first + 1;
+    return i < held ? window[i] : t < p.T ? __ldg(p.slot_map + t) : -1;
+  };
   auto valid = [&](int64_t s) { return s >= 0 && s < p.num_slots; };
-  if (warp == 0) {
+  for (int i0 = warp * 32; i0 < n; i0 += kThreads) {
     // a token begins its block's tokens unless the nearest token before it
     // that has a slot is of the same block (that one is almost always the
     // one before; past skipped tokens the warp looks 32 back at a time)
-    const int64_t s = lane < n ? slots[lane + 1] : -1, prev = lane < n ? slots[lane] : -1;
-    int b = valid(s) && !(valid(prev) && prev / bs == s / bs);
-    unsigned look = __ballot_sync(0xffffffffu, b && !valid(prev) && first + lane > 0);
+    const int i = i0 + lane;
+    const int64_t s = i < n ? window[i + 1] : -1, prev = i < n ? window[i] : -1;
+    int b = valid(s) && !(valid(prev) && prev >> shift == s >> shift);
+    unsigned look = __ballot_sync(0xffffffffu, b && !valid(prev) && first + i > 0);
     while (look) {
-      const int i = __ffs(look) - 1;
+      const int l = __ffs(look) - 1;
       look &= look - 1;
-      const int64_t mine = slots[i + 1] / bs;
-      for (int back = first + i - 1; back >= 0; back -= 32) {
+      const int64_t mine = window[i0 + l + 1] >> shift;
+      for (int back = first + i0 + l - 1; back >= 0; back -= 32) {
         const int64_t t = back - lane >= 0 ? __ldg(p.slot_map + back - lane) : -1;
         const unsigned m = __ballot_sync(0xffffffffu, valid(t));
         if (m) {
-          if (__shfl_sync(0xffffffffu, t, __ffs(m) - 1) / bs == mine && lane == i) b = 0;
+          if (__shfl_sync(0xffffffffu, t, __ffs(m) - 1) >> shift == mine && lane == l) b = 0;
           break;
         }
       }
     }
-    if (lane < n) begin[lane] = b;
+    const unsigned m = __ballot_sync(0xffffffffu, b);
+    if (lane == 0) begin[i0 >> 5] = m;
   }
   __syncthreads();
   const T* x0 = static_cast<const T*>(which ? p.x[1] : p.x[0]);
@@ -183,21 +257,22 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 
   for (int pass = 0; pass < 2; ++pass) {  // blocks with a short first run by warps, then the others by the CTA
     int mine = 0;
-    for (int i = 0; i < n; ++i) {
-      if (!begin[i]) continue;
+    for (int j = 0; j < n; j += 32)
+    for (uint32_t todo = begin[j >> 5]; todo != 0; todo &= todo - 1) {
       if (pass == 0 && (mine++ % kWarps) != warp) continue;
+      const int i = j + __ffs(todo) - 1;
       // the block's runs, one after the other (more than one only where skipped tokens lie between them)
       int t = first + i;
-      int64_t s = slots[i + 1];
-      const int64_t blk = s / bs;
+      int64_t s = window[i + 1];
+      const int64_t blk = s >> shift;
       bool later = false;
       for (;;) {
-        const int off = (int)(s - blk * bs);
+        const int off = (int)s & (bs - 1);
         // length: tokens t + 1 .. whose slots rise by one inside the block, 32 looked at a time
         int len = 1;
         int64_t next;  // the slot after the run; -1 where it names no row
         for (;;) {
-          const int64_t y = t + len + lane < p.T ? __ldg(p.slot_map + t + len + lane) : -1;
+          const int64_t y = slot_of(t + len + lane);
           const unsigned m = __ballot_sync(0xffffffffu, off + len + lane < bs && y == s + len + lane);
           const int more = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
           len += more;
@@ -206,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
             break;
           }
         }
-        if (!later && (len <= kShortRun) != (pass == 0)) break;
+        if (!later && (len * (D / 16) <= kWarpPieces) != (pass == 0)) break;
         const T* x = x0 + (int64_t)t * stride + h * D;
         const int64_t tile = blk * p.Hkv + h;
         if (pass == 0)
@@ -215,13 +290,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
           append_run<T, D, kThreads>(x, stride, cache + tile * bs * D, scales + tile, off, len, threadIdx.x, red);
         t += len;
         while (!valid(next) && t < p.T) {  // over skipped tokens
-          const int64_t y = t + lane < p.T ? __ldg(p.slot_map + t + lane) : -1;
+          const int64_t y = slot_of(t + lane);
           const unsigned m = __ballot_sync(0xffffffffu, valid(y));
           const int skip = m ? __ffs(m) - 1 : 32;
           t += skip;
           if (m) next = __shfl_sync(0xffffffffu, y, skip);
         }
-        if (!valid(next) || next / bs != blk) break;
+        if (!valid(next) || next >> shift != blk) break;
         s = next;
         later = true;
         if (pass == 0) __syncwarp(); else __syncthreads();  // the block's rows and scale are written
@@ -242,7 +317,7 @@ cudaError_t launch_t(const AppendParams& p, cudaStream_t stream) {
 
 cudaError_t launch_cache_append(const AppendParams& in, int dtype, cudaStream_t stream) {
   AppendParams p = in;
-  // few tokens: one run a warp and CTA; many: a CTA looks at 16 tokens, a quarter of a usual block
+  // few tokens: a CTA for every four, to spread single-token runs; many: one for every 64, which a run or two begin in
   p.chunk = p.T <= 1024 ? 4 : kMaxChunk;
   if (dtype == ATTN_BF16) return launch_t<__nv_bfloat16>(p, stream);
   if (dtype == ATTN_F16) return launch_t<__half>(p, stream);

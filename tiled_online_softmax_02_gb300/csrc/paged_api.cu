@@ -3,6 +3,7 @@
 // validation, then one launcher call each.  As for attn_fwd, a request the
 // kernels cannot run is refused with a status before anything is launched.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -16,6 +17,8 @@ using namespace gb300_attn;
 namespace {
 
 bool block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+
+int block_shift(int bs) { return bs == 16 ? 4 : bs == 32 ? 5 : bs == 64 ? 6 : 7; }
 
 struct Span {
   const void* p;
@@ -111,11 +114,24 @@ extern "C" int attn_cache_append_fp8(const void* k, const void* v, const int64_t
   p.scales[0] = k_scales; p.scales[1] = v_scales;
   p.num_slots = (int64_t)num_blocks * block_size;
   p.T = num_tokens; p.Hkv = Hkv; p.D = D; p.block_size = block_size;
+  p.block_shift = block_shift(block_size);
   const cudaError_t e = launch_cache_append(p, dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
 namespace {
+
+// SMs of the current device, looked up once for each.
+int sm_count() {
+  static std::atomic<int> cache[128];
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return sms;
+  const int known = cache[dev].load(std::memory_order_relaxed);
+  if (known > 0) return known;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  cache[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
 
 // How a call of attn_fwd_paged_fp8 runs: rows of a unit, CTAs, and the parts of the workspace.
 struct PagedPlan {
@@ -130,9 +146,7 @@ PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_t
   // rows per (request, kv head) of an even batch; a request with more takes several units
   const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
   pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTcRows;
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t most = (int64_t)sms * (pl.rows == kPagedTcRows ? 1 : paged_dec_ctas_per_sm(pl.rows));
+  const int64_t most = (int64_t)sm_count() * (pl.rows == kPagedTcRows ? 1 : paged_dec_ctas_per_sm(pl.rows));
   // no more CTAs than there can be tiles
   const int64_t units = (T * group / pl.rows + B) * Hkv;
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
@@ -222,7 +236,7 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   p.lse = lse;
   p.T = num_tokens; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.group = Hq / Hkv;
   p.num_blocks = num_blocks; p.block_size = block_size; p.width = max_blocks;
-  p.block_shift = block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
+  p.block_shift = block_shift(block_size);
   p.cap = max_blocks * block_size;
   p.causal = causal;
   p.local_window = local_window > 0 ? local_window : 0;

@@ -52,7 +52,7 @@ struct AppendParams {
   uint8_t* cache[2];        // [num_blocks, Hkv, block_size, D]
   float* scales[2];         // [num_blocks, Hkv]
   int64_t num_slots;        // num_blocks * block_size
-  int T, Hkv, D, block_size;
+  int T, Hkv, D, block_size, block_shift;
   int chunk;                // tokens whose runs one CTA owns
 };
 
