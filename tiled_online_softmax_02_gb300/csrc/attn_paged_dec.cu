@@ -37,6 +37,7 @@ namespace gb300_attn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kScaleStages = 4;
 constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6;  // warp 7: Q
 constexpr float kInvStep = 1.0f / kPieceStep;
 // P is carried as 32 * 2^(t - m); the maximum moves when a key passes it by
@@ -254,7 +255,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
   constexpr int kLoads = NR / kPer > 0 ? NR / kPer : 1;
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on are not finite
   const int c = lane % kVec, sub = lane / kVec;
-  ScaleFeed feed;
+  ScaleFeed<kScaleStages> feed;
   for (; !w.done(); w.next(p)) {
     const int buf = w.index & 1;
     if (w.index >= 2 && !wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;

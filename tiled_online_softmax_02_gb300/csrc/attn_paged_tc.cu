@@ -45,7 +45,7 @@ constexpr int kVWarp0 = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
 constexpr float kRise = 8.0f;          // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
-constexpr int kMaxUnroll = 1, kExpUnroll = 1;
+constexpr int kMaxUnroll = 4, kExpUnroll = 1;
 
 template <int D, bool BF16>
 struct Cfg {
@@ -60,12 +60,12 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + 2 * kQLane;
   static constexpr int kOffV8 = kOffK + kSK * kTile8;
   static constexpr int kOffV = kOffV8 + kSV8 * kTile8;
-  static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kScaleStages][kScaleGroups]: k scale, log2 v scale, 1 / v scale
-  static constexpr int kOffQe = kOffSc + kScaleStages * kScaleGroups * 16;  // int8 [256]: log2 of the Q rows' scales
+  static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kSK][kScaleGroups]: k scale, log2 v scale, 1 / v scale
+  static constexpr int kOffQe = kOffSc + kSK * kScaleGroups * 16;  // int8 [256]: log2 of the Q rows' scales
   static constexpr int kOffBar = kOffQe + kRows;
-  // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_full, sc_empty [kScaleStages],
+  // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_empty [kSK],
   // q_full, s_full, p_full, o_final [2], drain
-  static constexpr int kBars = 2 * (kSK + kSV8 + kSV + kScaleStages) + 9;
+  static constexpr int kBars = 2 * (kSK + kSV8 + kSV) + kSK + 9;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;
@@ -94,13 +94,12 @@ struct Lay {
   __device__ uint32_t v_full(int i) const { return bar(2 * C::kSK + 2 * C::kSV8 + i); }
   __device__ uint32_t v_empty(int i) const { return bar(2 * C::kSK + 2 * C::kSV8 + C::kSV + i); }
   __device__ uint32_t rest(int i) const { return bar(2 * (C::kSK + C::kSV8 + C::kSV) + i); }
-  __device__ uint32_t sc_full(int i) const { return rest(i); }
-  __device__ uint32_t sc_empty(int i) const { return rest(kScaleStages + i); }
-  __device__ uint32_t q_full(int t) const { return rest(2 * kScaleStages + t); }
-  __device__ uint32_t s_full(int t) const { return rest(2 * kScaleStages + 2 + t); }
-  __device__ uint32_t p_full(int t) const { return rest(2 * kScaleStages + 4 + t); }
-  __device__ uint32_t o_final(int t) const { return rest(2 * kScaleStages + 6 + t); }
-  __device__ uint32_t drain() const { return rest(2 * kScaleStages + 8); }
+  __device__ uint32_t sc_empty(int i) const { return rest(i); }
+  __device__ uint32_t q_full(int t) const { return rest(C::kSK + t); }
+  __device__ uint32_t s_full(int t) const { return rest(C::kSK + 2 + t); }
+  __device__ uint32_t p_full(int t) const { return rest(C::kSK + 4 + t); }
+  __device__ uint32_t o_final(int t) const { return rest(C::kSK + 6 + t); }
+  __device__ uint32_t drain() const { return rest(C::kSK + 8); }
   __device__ int8_t* q_exp() const { return reinterpret_cast<int8_t*>(base + C::kOffQe); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
@@ -175,7 +174,7 @@ __device__ __forceinline__ void load_role(const PagedTcParams& P, const Lay<D, B
 template <int D, bool BF16>
 __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, int lane) {
   const PagedParams& p = P.c;
-  ScaleFeed feed;
+  ScaleFeed<Cfg<D, BF16>::kSK> feed;
   for (; !w.done(); w.next(p)) {
     Walk x = w;
     x.next(p);
@@ -184,7 +183,7 @@ __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, 
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)x.u.q.s0 * p.q_stride + x.u.kvh * p.group * D;
       for (int i = t0 + lane; i <= t1; i += 32) bulk_prefetch_l2(q + i * p.q_stride, (uint32_t)(p.group * D * 2));
     }
-    if (!feed.unit(p, w, P.scale_log2, sm.scales(0), sm.sc_full(0), sm.sc_empty(0), lane)) return;
+    if (!feed.unit(p, w, P.scale_log2, sm.scales(0), sm.k_full(0), sm.sc_empty(0), lane)) return;
   }
 }
 
@@ -192,15 +191,18 @@ __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, 
 // Four warps: V tile rows, e4m3 to f16, rows past the last key as zeros (their
 // slots may hold NaN bytes; P is 0 there but 0 * NaN is not).  In: rows of D
 // bytes in the swizzle of that width.  Out: 64-value blocks of [128 keys][128
-// bytes] in the 128-byte swizzle.  A quarter-warp takes the four 16-byte pieces
-// of 64 values of rows k and k ^ 5: the in-swizzle puts those in disjoint banks
-// (bit 2 differs), and so does the out-swizzle (bit 0 differs).
+// bytes] in the 128-byte swizzle.  Eight lanes read 128 bytes that lie together
+// (a row, or two of 64) and write each 16-byte piece as two: at D = 128 the
+// upper four lanes, whose block lies a multiple of 128 bytes further, write
+// theirs in the other order, so that the eight never share a bank.
 template <int D, bool BF16>
 __device__ __forceinline__ void widen_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, int warp, int lane) {
   using C = Cfg<D, BF16>;
   const PagedParams& p = P.c;
   int g = 0;
-  const int c = lane & 3, r8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);  // row of a group of 8
+  constexpr int kVec = D / 16;  // 16-byte pieces of a row
+  const int c = lane % kVec, r0 = lane / kVec;
+  const bool swap = c >= 4;
   for (; !w.done(); w.next(p)) {
     const int valid = paged_valid(p, w.u.q);
     for (int n = 0; n < w.nt; ++n, ++g) {
@@ -210,13 +212,11 @@ __device__ __forceinline__ void widen_role(const PagedTcParams& P, const Lay<D, 
       const int rows = min(valid - (w.t0 + n) * BN, BN);
       const uint8_t* src = sm.v8_ptr(s8);
       uint8_t* dst = sm.v_ptr(sv);
-      constexpr int kIters = BN / 8 * (D / 64) / 4;
+      constexpr int kIters = BN * kVec / 32 / 4;
 #pragma unroll 1
       for (int i = 0; i < kIters; ++i) {
-        const int it = i * 4 + warp;
-        const int row = (it / (D / 64)) * 8 + r8, half = it % (D / 64);
-        const int piece = half * 4 + c;
-        const int at = D == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3);
+        const int row = (i * 4 + warp) * (32 / kVec) + r0;
+        const int at = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
         uint4 v = *reinterpret_cast<const uint4*>(src + row * D + at * 16);
         if (row >= rows) v = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t e[4] = {v.x, v.y, v.z, v.w};
@@ -226,9 +226,11 @@ __device__ __forceinline__ void widen_role(const PagedTcParams& P, const Lay<D, 
           asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
               : "=r"(h[2 * k]), "=r"(h[2 * k + 1]) : "r"(e[k]));
         }
-        uint8_t* out = dst + half * (BN * 128) + row * 128;
-        *reinterpret_cast<uint4*>(out + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(out + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        uint8_t* out = dst + (c >> 2) * (BN * 128) + row * 128;
+        const int lo = (2 * (c & 3)) ^ (row & 7), hi = lo ^ 1;
+        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4*>(out + ((swap ? hi : lo) << 4)) = swap ? b : a;
+        *reinterpret_cast<uint4*>(out + ((swap ? lo : hi) << 4)) = swap ? a : b;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -451,6 +453,7 @@ __device__ __forceinline__ void store_32b(void* ptr, const uint32_t* v, bool ali
 template <int D, bool BF16, bool SOFTCAP>
 __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D, BF16>& sm, Walk w, uint32_t tmem,
                                              int warp, int lane) {
+  using C = Cfg<D, BF16>;
   const PagedParams& p = P.c;
   const int t = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
   const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + t * 128;
@@ -516,8 +519,8 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     const int nt = w.nt, t0 = w.t0;
     if (!lane_on(u, t)) {  // the other lane's tiles pass by; their scales too
       for (int n = 0; n < nt; ++n, ++g) {
-        if (!wait_warp(sm.sc_full(g % kScaleStages), (g / kScaleStages) & 1, p.timeout_ns, p.status)) return;
-        if (lane == 0) mbar_arrive(sm.sc_empty(g % kScaleStages));
+        if (!wait_warp(sm.k_full(g % C::kSK), (g / C::kSK) & 1, p.timeout_ns, p.status)) return;
+        if (lane == 0) mbar_arrive(sm.sc_empty(g % C::kSK));
       }
       w.next(p);
       continue;
@@ -531,10 +534,10 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     l_run = 0.0f;
     for (int n = 0; n < nt; ++n, ++g, ++sc) {
       const int key0 = (t0 + n) * BN;
-      if (!wait_warp(sm.sc_full(g % kScaleStages), (g / kScaleStages) & 1, p.timeout_ns, p.status)) return;
       // a group's (k scale |scale| log2 e, log2 v scale, 1 / v scale); raw scores times the row's
       // factor and the first are in log2 units.  The product stays above 0, so that -inf stays -inf
-      const float4* scl = sm.scales(g % kScaleStages);
+      // (they lie there once S does: K's barrier, which S waited for, takes the scale warp's arrival too)
+      const float4* scl = sm.scales(g % C::kSK);
       if (!wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
       tc_fence_after();
       if (key0 < full_lo || key0 + BN > full_hi) {  // some key is hidden from some row: -inf over its score
@@ -636,7 +639,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(sm.sc_empty(g % kScaleStages));
+        mbar_arrive(sm.sc_empty(g % C::kSK));
         mbar_arrive(sm.p_full(t));
       }
     }
@@ -671,8 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSK; ++i) {
-      mbar_init(sm.k_full(i), 1);
+      mbar_init(sm.k_full(i), 2);  // the TMA's, and the scale warp's
       mbar_init(sm.k_empty(i), 1);
+      mbar_init(sm.sc_empty(i), 8);
     }
     for (int i = 0; i < C::kSV8; ++i) {
       mbar_init(sm.v8_full(i), 1);
@@ -681,10 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     for (int i = 0; i < C::kSV; ++i) {
       mbar_init(sm.v_full(i), 4);
       mbar_init(sm.v_empty(i), 1);
-    }
-    for (int i = 0; i < kScaleStages; ++i) {
-      mbar_init(sm.sc_full(i), 1);
-      mbar_init(sm.sc_empty(i), 8);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(sm.q_full(t), 4);

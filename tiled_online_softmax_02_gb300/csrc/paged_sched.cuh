@@ -269,9 +269,9 @@ __device__ __forceinline__ int paged_parts(const PagedWalk<NR>& w, const PagedSh
 // in shared memory, by one warp: lane i < 8 has keys 16 i .. of a tile (a block
 // holds 16 or more).  An entry is (k scale * mul, log2 v scale, 1 / v scale).
 constexpr int kScaleGroups = kPagedKeys / 16;
-constexpr int kScaleStages = 4;
 constexpr float kMinVScale = 7.9e-31f;  // 2^-100: a block of zeros may have scale 0
 
+template <int kStages>
 struct ScaleFeed {
   int g = 0;  // tiles so far
   template <int NR>
@@ -300,9 +300,9 @@ struct ScaleFeed {
       const float k0 = ks, v0 = fmaxf(vs, kMinVScale);
       fetch(next);
       next = block_of(n + 2);
-      const int st = g % kScaleStages;
-      if (g >= kScaleStages &&
-          !wait_warp(empty0 + st * 8, ((g / kScaleStages) - 1) & 1, p.timeout_ns, p.status))
+      const int st = g % kStages;
+      if (g >= kStages &&
+          !wait_warp(empty0 + st * 8, ((g / kStages) - 1) & 1, p.timeout_ns, p.status))
         return false;
       if (lane < kScaleGroups)
         ring[st * kScaleGroups + lane] = make_float4(k0 * mul, __log2f(v0), 1.0f / v0, 0.0f);
