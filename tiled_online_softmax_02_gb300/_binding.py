@@ -508,6 +508,24 @@ def _token_stride(t, name):
     return st if T > 1 else H * D
 
 
+_workspaces = threading.local()  # .by_device: this thread's workspace on each device, for the default stream
+
+
+def _workspace(nbytes, index, stream, device):
+    """A workspace for one call.  Allocating it costs half as much as all else the call does on the host, so
+    calls on the default stream share one for each device and thread: their kernels run one after the other.
+    Calls on other streams, the only ones that can be captured into graphs, get their own."""
+    if stream != 0:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    held = getattr(_workspaces, "by_device", None)
+    if held is None:
+        held = _workspaces.by_device = {}
+    ws = held.get(index)
+    if ws is None or ws.shape[0] < nbytes:
+        ws = held[index] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws
+
+
 @functools.lru_cache(maxsize=4096)
 def _paged_workspace(num_tokens, B, Hq, Hkv, D, index):
     with _on(index):
@@ -607,7 +625,8 @@ def attn_fwd_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_
     Returns out [T, Hq, D] (allocated with torch when not given; rows of no
     request are not written); lse, when given, float32 [T, Hq], receives the
     natural-log log-sum-exp of each row.  The workspace
-    (attn_paged_workspace_bytes) is allocated with torch when not given."""
+    (attn_paged_workspace_bytes) is provided when not given: calls on the
+    default stream keep one for each device and thread, others allocate it."""
     index, dtype = q.get_device(), q.dtype
     if q.dim() != 3 or index < 0 or block_tables.dim() != 2:
         raise ValueError("attn_fwd_paged_fp8 takes CUDA tensors: q [T, Hq, D], caches "
@@ -627,20 +646,18 @@ def attn_fwd_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_
         _need(out, "out", dtype, shape, index)
     if lse is not None:
         _need(lse, "lse", _F32, (T, Hq), index)
-    ws_bytes = _paged_workspace(T, B, Hq, Hkv, D, index)
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    else:
-        if workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-        ws_bytes = workspace.numel() * workspace.element_size()
+        workspace = _workspace(_paged_workspace(T, B, Hq, Hkv, D, index), index, stream, q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     with _on(index):
         rc = load_library().attn_fwd_paged_fp8(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             block_tables.data_ptr(), q_starts.data_ptr(), total_lengths.data_ptr(), out.data_ptr(),
             None if lse is None else lse.data_ptr(), T, B, Hq, Hkv, D, _token_stride(q, "q"), num_blocks, block_size,
             width, 1 if causal else 0, int(local_window), 1.0 / math.sqrt(D) if scale is None else scale, softcap,
-            DTYPE_CODES[dtype], workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(index))
+            DTYPE_CODES[dtype], workspace.data_ptr(), workspace.nbytes, stream)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_paged_fp8")
     return out
