@@ -61,9 +61,8 @@ struct Cfg {
   static constexpr int kOffQ = kOffV + kSV * kTile;               // two buffers
   static constexpr int kOffP = kOffQ + 2 * kQBytes;               // two buffers
   static constexpr int kOffLim = kOffP + 2 * kPBytes;             // int2 [2][NR]
-  static constexpr int kOffM = kOffLim + 2 * NR * 8;              // float [NR]: running maxima
-  static constexpr int kOffRed = kOffM + NR * 4;                  // float [4][NR]
-  static constexpr int kOffQs = kOffRed + 4 * NR * 4;             // float [2]: 1 / scale of Q's pieces
+  static constexpr int kOffRed = kOffLim + 2 * NR * 8;            // float [2][4][NR]: maxima, sums
+  static constexpr int kOffQs = kOffRed + 2 * 4 * NR * 4;             // float [2]: 1 / scale of Q's pieces
   static constexpr int kOffSc = kOffQs + 16;                      // float4 [kScaleStages][kScaleGroups]
   static constexpr int kOffBar = kOffSc + kScaleStages * kScaleGroups * 16;
   // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2],
@@ -93,8 +92,7 @@ struct Lay {
   __device__ uint32_t p(int i) const { return s + C::kOffP + i * C::kPBytes; }
   __device__ uint8_t* p_ptr(int i) const { return base + C::kOffP + i * C::kPBytes; }
   __device__ int2* lim(int i) const { return reinterpret_cast<int2*>(base + C::kOffLim) + i * NR; }
-  __device__ float* m() const { return reinterpret_cast<float*>(base + C::kOffM); }
-  __device__ float* red() const { return reinterpret_cast<float*>(base + C::kOffRed); }
+  __device__ float* red(int i) const { return reinterpret_cast<float*>(base + C::kOffRed) + i * 4 * NR; }
   __device__ float* qs() const { return reinterpret_cast<float*>(base + C::kOffQs); }
   __device__ uint32_t bar(int i) const { return s + C::kOffBar + i * 8; }
   __device__ uint32_t k_full(int i) const { return bar(i); }
@@ -261,7 +259,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
     if (w.index >= 2 && !wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;
     const PagedUnit& u = w.u;
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + u.kvh * p.group * D + c * 8;
-    const int tok0 = (u.row0 + sub) / p.group;
+    const int tok0 = paged_token(p, u.row0 + sub);
     int tok = tok0, head = u.row0 + sub - tok0 * p.group;
     uint4 raw[kLoads];
     uint32_t top2 = 0;
@@ -335,7 +333,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
       }
     }
     for (int r = lane; r < NR; r += 32)
-      sm.lim(buf)[r] = r < u.rows ? paged_limits(p, u.q, (u.row0 + r) / p.group) : make_int2(0, 0);
+      sm.lim(buf)[r] = r < u.rows ? paged_limits(p, u.q, paged_token(p, u.row0 + r)) : make_int2(0, 0);
     if (lane == 0) sm.qs()[buf] = __uint_as_float((uint32_t)(127 - ex) << 23);
     fence_proxy_async_smem();
     __syncwarp();
@@ -430,7 +428,6 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
   const PagedParams& p = P.c;
   const int tid = warp * 32 + lane;
   const uint32_t tq = tmem + ((uint32_t)(warp * 32) << 16);
-  float* const m = sm.m();
   int g = 0;  // tiles so far
   // The four warps meet at a hardware barrier, so none of them may leave early: one whose bounded
   // wait has run out goes on without waiting (the status word has the timeout; the rows are not valid).
@@ -457,9 +454,10 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
     float l[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-    // m starts below everything (its readers of the last unit met at that unit's sum exchange)
-    if (tid < NR) m[tid] = kNone;
-    meet();
+    float m[NR];  // the running maxima, the same in every thread
+#pragma unroll
+    for (int r = 0; r < NR; ++r) m[r] = kNone;
+    if (w.nt == 0) meet();  // a unit without a tile has no other meeting before its sums
 
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int key0 = (w.t0 + n) * kPagedKeys, j = key0 + tid;
@@ -505,15 +503,15 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       float over = -INFINITY;
 #pragma unroll
       for (int r = 0; r < NR; ++r) over = fmaxf(over, t[r] - m[r]);
-      if (meet_any(over > kRise)) {
+      if (n == 0 || meet_any(over > kRise)) {
         float x[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) x[r] = t[r];
         const float wm = reduce_scatter<NR, true>(x, lane);
-        float* red = sm.red();
+        float* red = sm.red(0);
         if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = wm;
         meet();
-        float alpha[NR];
+        float* alpha = x;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float old = m[r];
@@ -521,7 +519,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           const float mn = top > old + kRise ? top : old;
           alpha[r] = fast_exp2(old - mn);
           l[r] *= alpha[r];
-          x[r] = mn;
+          m[r] = mn;
         }
         if (n > 0) {  // O^T holds the unit's earlier tiles once their P V is done
           wait(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1);
@@ -538,11 +536,6 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           tmem_wait_st();
           tc_fence_before();
         }
-        meet();  // everyone has read the old maxima
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-          if (tid == r) m[r] = x[r];
-        meet();
       }
       // P buffer g % 2 was last read by the P V of tile g - 2
       if (g >= 2) wait(sm.pv_done(g & 1), ((g - 2) >> 1) & 1);
@@ -574,9 +567,8 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
 #pragma unroll
     for (int r = 0; r < NR; ++r) x[r] = l[r];
     const float ws = reduce_scatter<NR, false>(x, lane);
-    float* red = sm.red();
+    float* red = sm.red(1);  // not the maxima's, which a slower warp may still read
     if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = ws;
-    const float my_m = tid < NR ? m[tid] : 0.0f;
     meet();
     float o[NR];
 #pragma unroll
@@ -600,14 +592,15 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       const float L = red[r] + red[NR + r] + red[2 * NR + r] + red[3 * NR + r];
       if (w.whole) {
         const int xr = u.row0 + r;
-        const int64_t row = (int64_t)(u.q.s0 + xr / p.group) * p.Hq + u.kvh * p.group + xr % p.group;
+        const int tok = paged_token(p, xr);
+        const int64_t row = (int64_t)(u.q.s0 + tok) * p.Hq + u.kvh * p.group + xr - tok * p.group;
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         if (tid < D) static_cast<uint16_t*>(p.out)[row * D + tid] = to_bits<BF16>(o[r] * inv);
         if (p.lse != nullptr && tid == r)
-          p.lse[row] = L == 0.0f ? -INFINITY : (my_m + (__log2f(L) - kPLog2)) * kLn2;
+          p.lse[row] = L == 0.0f ? -INFINITY : (m[r] + (__log2f(L) - kPLog2)) * kLn2;
       } else {
         if (tid < D) P.ws_o[((int64_t)slot * NR + r) * D + tid] = o[r];
-        if (tid == r) P.ws_ml[slot * NR + r] = make_float2(my_m, L);
+        if (tid == r) P.ws_ml[slot * NR + r] = make_float2(m[r], L);
       }
     }
     if (!w.whole && w.head && tid == 0) {

@@ -143,10 +143,78 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_kernel(const Page
   }
 }
 
+// Few rows and often many parts (decode): one CTA a row, its warps over the
+// parts, whose (m, L) and O_k are read at the same time.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kWarps * 32) attn_paged_join_rows_kernel(const PagedCut* cuts, const float* ws_o,
+                                                                           const float2* ws_ml, int unit_rows, int Hq,
+                                                                           int group, float ml_log2, uint16_t* out,
+                                                                           float* lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = D / 32;
+  __shared__ float sum_o[kWarps][D];
+  __shared__ float2 sum_ml[kWarps];
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+  const PagedCut cut = cuts[c];
+  if (r >= cut.rows || cut.parts == 0) return;
+  auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * unit_rows + r; };
+  // this warp's parts: warp, warp + 8, ..., four at a time, under its own maximum
+  float M = -INFINITY, L = 0.0f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  for (int k0 = warp; k0 < cut.parts; k0 += 4 * kWarps) {
+    RowVec<D> o[4];
+    float2 ml[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * kWarps;
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      if (k < cut.parts) {
+        ml[i] = ws_ml[slot(k)];
+        o[i].load(ws_o + slot(k) * D, lane);
+      }
+    }
+    const float Mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+    const float keep = exp2f(M - Mn);  // Mn is finite: part k0 is there
+    L *= keep;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= keep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + i * kWarps >= cut.parts) continue;
+      const float w = exp2f(ml[i].x - Mn);
+      L = fmaf(w, ml[i].y, L);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[i].x[v], acc[v]);
+    }
+    M = Mn;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum_o[warp][lane * V + v] = acc[v];
+  if (lane == 0) sum_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  if (warp != 0) return;
+  float Ma = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) Ma = fmaxf(Ma, sum_ml[k].x);  // warps without a part hold -inf
+  L = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    const float w = exp2f(sum_ml[k].x - Ma);
+    L = fmaf(w, sum_ml[k].y, L);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, sum_o[k][lane * V + v], acc[v]);
+  }
+  store_row<D, BF16>(cut, r, Hq, group, ml_log2, out, lse, lane, acc, Ma, L);
+}
+
 template <int D, bool BF16>
 cudaError_t launch_t(const PagedLaunch& L, cudaStream_t stream) {
+  const bool few_rows = L.rows < kRowsPerCta;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)L.grid, (unsigned)((L.rows + kRowsPerCta - 1) / kRowsPerCta), 1);
+  cfg.gridDim = dim3((unsigned)L.grid, (unsigned)(few_rows ? L.rows : (L.rows + kRowsPerCta - 1) / kRowsPerCta), 1);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -154,9 +222,9 @@ cudaError_t launch_t(const PagedLaunch& L, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, BF16>, (const PagedCut*)L.cuts, (const float*)L.ws_o,
-                            (const float2*)L.ws_ml, L.rows, L.c.Hq, L.c.group, L.ml_log2,
-                            static_cast<uint16_t*>(L.c.out), L.c.lse);
+  return cudaLaunchKernelEx(&cfg, few_rows ? attn_paged_join_rows_kernel<D, BF16> : attn_paged_join_kernel<D, BF16>,
+                            (const PagedCut*)L.cuts, (const float*)L.ws_o, (const float2*)L.ws_ml, L.rows, L.c.Hq,
+                            L.c.group, L.ml_log2, static_cast<uint16_t*>(L.c.out), L.c.lse);
 }
 
 }  // namespace

@@ -179,7 +179,7 @@ __device__ __forceinline__ void scale_role(const PagedTcParams& P, const Lay<D, 
     Walk x = w;
     x.next(p);
     if (!x.done()) {  // whole tokens of the kv head's query heads
-      const int t0 = x.u.row0 / p.group, t1 = (x.u.row0 + x.u.rows - 1) / p.group;
+      const int t0 = paged_token(p, x.u.row0), t1 = paged_token(p, x.u.row0 + x.u.rows - 1);
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)x.u.q.s0 * p.q_stride + x.u.kvh * p.group * D;
       for (int i = t0 + lane; i <= t1; i += 32) bulk_prefetch_l2(q + i * p.q_stride, (uint32_t)(p.group * D * 2));
     }
@@ -365,7 +365,7 @@ __device__ __forceinline__ float bring_q(const PagedTcParams& P, const Lay<D, BF
   const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;
   // this thread's first row as (token, head); the next ones kPer rows on
   int r = wq * 32 + sub;
-  int tok = (u.row0 + t * BM + r) / p.group, head = (u.row0 + t * BM + r) - tok * p.group;
+  int tok = paged_token(p, u.row0 + t * BM + r), head = (u.row0 + t * BM + r) - tok * p.group;
 #pragma unroll 1
   for (int b = 0; b < 4; ++b) {
     uint4 raw[kBatch];
@@ -528,8 +528,8 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     mine = t * BM + row < u.rows;
     const int x0 = u.row0 + t * BM;
     const int last = min(x0 + BM, u.row0 + u.rows) - 1;
-    const int2 lim = mine ? paged_limits(p, u.q, (x0 + row) / p.group) : make_int2(0, 0);
-    const int full_lo = paged_limits(p, u.q, last / p.group).x, full_hi = paged_limits(p, u.q, x0 / p.group).y;
+    const int2 lim = mine ? paged_limits(p, u.q, paged_token(p, x0 + row)) : make_int2(0, 0);
+    const int full_lo = paged_limits(p, u.q, paged_token(p, last)).x, full_hi = paged_limits(p, u.q, paged_token(p, x0)).y;
     m_run = kNone;
     l_run = 0.0f;
     for (int n = 0; n < nt; ++n, ++g, ++sc) {
@@ -648,7 +648,8 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     head = w.head;
     prev_nt = nt;
     const int xr = x0 + row;
-    out_row = (int64_t)(u.q.s0 + xr / p.group) * p.Hq + u.kvh * p.group + xr % p.group;
+    const int tok = paged_token(p, xr);
+    out_row = (int64_t)(u.q.s0 + tok) * p.Hq + u.kvh * p.group + xr - tok * p.group;
     if (!whole && head && threadIdx.x == 0) {
       PagedCut c;
       c.parts = paged_parts(w, sm.share());

@@ -238,6 +238,9 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   p.num_blocks = num_blocks; p.block_size = block_size; p.width = max_blocks;
   p.block_shift = block_shift(block_size);
   p.cap = max_blocks * block_size;
+  p.group_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (p.group == 1 << i) p.group_shift = i;
   p.causal = causal;
   p.local_window = local_window > 0 ? local_window : 0;
   p.scale = scale;

@@ -70,6 +70,7 @@ struct PagedParams {
   float* lse;               // [T, Hq] or nullptr
   int T, B, Hq, Hkv, D, group, num_blocks, block_size, block_shift, width;
   int cap;                  // width * block_size: keys a block table can name
+  int group_shift;          // log2 of group, -1 where it is no power of two
   int causal, local_window;
   float scale, softcap;
   uint64_t timeout_ns;

@@ -38,6 +38,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_
   return __all_sync(0xffffffffu, ok);
 }
 
+// Token of a kv head's row x (x / group; the head is the rest).
+__device__ __forceinline__ int paged_token(const PagedParams& p, int x) {
+  return p.group_shift >= 0 ? x >> p.group_shift : x / p.group;
+}
+
 // A request's packed rows and lengths.
 struct PagedReq {
   int s0, n;   // first row, rows
@@ -77,8 +82,8 @@ template <int NR>
 __device__ __forceinline__ void paged_unit_tiles(const PagedParams& p, PagedUnit& u) {
   u.row0 = u.rt * NR;
   u.rows = min(NR, u.q.n * p.group - u.row0);
-  const int lo = paged_limits(p, u.q, u.row0 / p.group).x;
-  const int hi = paged_limits(p, u.q, (u.row0 + u.rows - 1) / p.group).y;
+  const int lo = paged_limits(p, u.q, paged_token(p, u.row0)).x;
+  const int hi = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).y;
   u.tb = hi > lo ? lo / kPagedKeys : 0;
   u.te = hi > lo ? (hi + kPagedKeys - 1) / kPagedKeys : 0;
 }
