@@ -113,33 +113,52 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
 
   // ---- what every row of this CTA needs and gives
   auto need_of = [&](int b) {
-    return ((long long)past[b] + max(__ldg(p.added + b), 0) + p.block_size - 1) / p.block_size;
+    return ((long long)past[b] + max(__ldg(p.added + b), 0) + p.block_size - 1) >> p.block_shift;
   };
-  for (int r = warp; r < rows; r += kWarps) {
-    const int b = row0 + r;
-    const bool fin = finished(b);
-    const long long want = need_of(b);
-    int flags = 0;
-    if (want > p.width || (long long)past[b] + max(__ldg(p.added + b), 0) > INT32_MAX) flags = 1 << kAssignRowShort;
-    const int need = (int)min(want, (long long)p.width);
-    const int32_t* row = p.tables + (int64_t)b * p.width;
-    int n_lack = 0, n_given = 0;
-    const int upto = fin ? p.width : need;
-#pragma unroll 4
-    for (int c = lane; c < upto; c += 32) {
-      const int e = __ldcg(row + c);
-      flags |= e >= p.num_blocks ? 1 << kAssignCorrupt : 0;
-      n_given += fin && e >= 0;
-      n_lack += fin ? c < need : e < 0;
+  // (128 entries of two rows in flight at a time: a row's loads do not wait for one another)
+  for (int r0 = warp; r0 < rows; r0 += 2 * kWarps) {
+    int need[2], upto[2], n_lack[2] = {0, 0}, n_given[2] = {0, 0}, flags = 0;
+    bool fin[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + i * kWarps, b = row0 + min(r, rows - 1);
+      const long long want = need_of(b);
+      if (r < rows && (want > p.width || (long long)past[b] + max(__ldg(p.added + b), 0) > INT32_MAX))
+        flags = 1 << kAssignRowShort;
+      fin[i] = finished(b);
+      need[i] = (int)min(want, (long long)p.width);
+      upto[i] = r < rows ? (fin[i] ? p.width : need[i]) : 0;
     }
-    n_lack = __reduce_add_sync(0xffffffffu, n_lack);
-    n_given = __reduce_add_sync(0xffffffffu, n_given);
+    for (int c0 = 0; c0 < max(upto[0], upto[1]); c0 += 128) {
+      int e[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + 32 * k + lane;
+          e[i][k] = c < upto[i] ? __ldcg(p.tables + (int64_t)(row0 + r0 + i * kWarps) * p.width + c) : 0;
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + 32 * k + lane;
+          if (c >= upto[i]) continue;
+          flags |= e[i][k] >= p.num_blocks ? 1 << kAssignCorrupt : 0;
+          n_given[i] += fin[i] && e[i][k] >= 0;
+          n_lack[i] += fin[i] ? c < need[i] : e[i][k] < 0;
+        }
+    }
     flags = __reduce_or_sync(0xffffffffu, flags);
-    if (lane == 0) {
-      lacks[r] = n_lack;
-      given[r] = n_given;
-      if (flags) atomicOr(&sums.flags, flags);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int l = __reduce_add_sync(0xffffffffu, n_lack[i]), g = __reduce_add_sync(0xffffffffu, n_given[i]);
+      if (lane == 0 && r0 + i * kWarps < rows) {
+        lacks[r0 + i * kWarps] = l;
+        given[r0 + i * kWarps] = g;
+      }
     }
+    if (lane == 0 && flags) atomicOr(&sums.flags, flags);
   }
   __syncthreads();
 
@@ -208,13 +227,17 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
       if (!finished(b)) continue;
       int32_t* row = p.tables + (int64_t)b * p.width;
       long long at = (long long)count0 + given_base + given[r];
-      for (int c0 = 0; c0 < p.width; c0 += 32) {
-        const int c = c0 + lane;
-        const int e = c < p.width ? __ldcg(row + c) : -1;
-        const unsigned held = __ballot_sync(0xffffffffu, e >= 0);
-        if (e >= 0) p.free_blocks[at + __popc(held & ((1u << lane) - 1u))] = e;
-        if (c < p.width) row[c] = -1;
-        at += __popc(held);
+      for (int c0 = 0; c0 < p.width; c0 += 128) {
+        int e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = c0 + 32 * k + lane < p.width ? __ldcg(row + c0 + 32 * k + lane) : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned held = __ballot_sync(0xffffffffu, e[k] >= 0);
+          if (e[k] >= 0) p.free_blocks[at + __popc(held & ((1u << lane) - 1u))] = e[k];
+          if (c0 + 32 * k + lane < p.width) row[c0 + 32 * k + lane] = -1;
+          at += __popc(held);
+        }
       }
     }
   }
@@ -228,12 +251,21 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
       int32_t* row = p.tables + (int64_t)b * p.width;
       long long nth = (long long)lack_base + lacks[r];
       if ((r + 1 < rows ? lacks[r + 1] : sums.lacks) == lacks[r]) continue;  // it lacks none
-      for (int c0 = 0; c0 < need; c0 += 32) {
-        const int c = c0 + lane;
-        const bool lack = c < need && __ldcg(row + c) < 0;
-        const unsigned m = __ballot_sync(0xffffffffu, lack);
-        if (lack) row[c] = __ldcg(p.free_blocks + (count1 - 1 - nth - __popc(m & ((1u << lane) - 1u))));
-        nth += __popc(m);
+      for (int c0 = 0; c0 < need; c0 += 128) {
+        int e[4];
+        bool lack[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = c0 + 32 * k + lane < need ? __ldcg(row + c0 + 32 * k + lane) : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          lack[k] = e[k] < 0;
+          const unsigned m = __ballot_sync(0xffffffffu, lack[k]);
+          if (lack[k]) e[k] = __ldcg(p.free_blocks + (count1 - 1 - nth - __popc(m & ((1u << lane) - 1u))));
+          nth += __popc(m);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (lack[k]) row[c0 + 32 * k + lane] = e[k];
       }
     }
     if (rank == 0 && tid == 0) *p.free_count = (int)(count1 - lack_all);
@@ -256,8 +288,8 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
         if (starts[mid] <= t) lo = mid; else hi = mid - 1;
       }
       const int pos = past[lo] + (int)t - starts[lo];
-      const int blk = __ldcg(p.tables + (int64_t)lo * p.width + pos / p.block_size);
-      slot[i] = (int64_t)blk * p.block_size + pos % p.block_size;
+      const int blk = __ldcg(p.tables + (int64_t)lo * p.width + (pos >> p.block_shift));
+      slot[i] = ((int64_t)blk << p.block_shift) + (pos & (p.block_size - 1));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -78,7 +78,7 @@ extern "C" int attn_cache_assign(const int32_t* past_lengths, const int32_t* new
     if (!aligned(s.p, s.p == slot_map ? 8 : 4)) return ATTN_ERR_UNSUPPORTED;
   if (!aligned(past_lengths, 4) || !aligned(new_lengths, 4)) return ATTN_ERR_UNSUPPORTED;
   AssignParams p{past_lengths, new_lengths, finished, block_tables, free_blocks, free_count, q_starts, total_lengths,
-                 slot_map, result, B, max_blocks, block_size, num_blocks, num_tokens};
+                 slot_map, result, B, max_blocks, block_size, block_shift(block_size), num_blocks, num_tokens};
   const cudaError_t e = launch_cache_assign(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

@@ -42,7 +42,7 @@ struct AssignParams {
   int32_t* totals;          // [B]
   int64_t* slot_map;        // [T]
   int32_t* result;          // [1]
-  int B, width, block_size, num_blocks, T;
+  int B, width, block_size, block_shift, num_blocks, T;
 };
 
 struct AppendParams {
