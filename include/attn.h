@@ -446,7 +446,7 @@ int attn_cache_append_fp8(const void *k, const void *v, const int64_t *slot_map,
  *   total_lengths int32 [B]
  *   out           [num_tokens, Hq, D] dtype;  lse NULL or f32 [num_tokens, Hq]
  *   dtype         ATTN_F16 or ATTN_BF16 (ATTN_F32: ATTN_ERR_UNSUPPORTED)
- *   B             0..4096 (more: ATTN_ERR_UNSUPPORTED)
+ *   B             0..8192 (more: ATTN_ERR_UNSUPPORTED);  Hq up to 65535 (more: ATTN_ERR_UNSUPPORTED)
  *   workspace     at least attn_paged_workspace_bytes(...) bytes, 16-byte
  *                 aligned, for partial rows; nothing in it has to start at zero.
  *                 Calls that share a workspace must not overlap on the GPU.

@@ -363,6 +363,83 @@ def test_repeats_and_streams_give_the_same_bits(new):
     assert torch.equal(other, out)
 
 
+@pytest.mark.parametrize("new", [(1, 1), (3, 2), (90, 30)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_of_very_different_size(new, dtype):
+    """One head of one token 2^12 times the others: each row keeps its own accuracy."""
+    w = BASE.replace(new=new, total=(300, 200), dtype=dtype, q_std=0.5)
+    x = ref.make(w)
+    x["q"][0, 1] *= 4096.0
+    x["q"][-5, 2] *= 2.0 ** -9
+    g = _gpu(x)
+    out = torch.full(x["q"].shape, -7.0, dtype=x["q"].dtype, device="cuda")
+    lse = torch.full(x["q"].shape[:2], -7.0, device="cuda")
+    _attend(w, g, out, lse)
+    _check_out(w, x, out, lse)
+
+
+@pytest.mark.parametrize("new", [(2, 1), (80, 40)])
+def test_a_row_that_is_not_finite_reaches_no_other(new):
+    w = BASE.replace(new=new, total=(300, 200), Hq=8, Hkv=2)
+    x = ref.make(w)
+    whole = _attend(w, _gpu(x))
+    x["q"][1, 2, 5] = float("nan")
+    x["q"][1, 5, 100] = float("inf")
+    got = _attend(w, _gpu(x))
+    torch.cuda.synchronize()
+    n = sum(new)
+    assert got[1, 2].isnan().all() and got[1, 5].isnan().all()
+    keep = torch.ones(n, 8, dtype=torch.bool, device="cuda")
+    keep[1, 2] = keep[1, 5] = False
+    assert torch.equal(got[:n][keep], whole[:n][keep])
+
+
+def test_many_requests():
+    rng = np.random.Generator(np.random.PCG64(4))
+    total = tuple(int(t) for t in rng.integers(0, 40, 2500))
+    new = tuple(min(t, int(n)) for t, n in zip(total, rng.integers(0, 3, 2500)))
+    _check(Problem(new=new, total=total, Hq=2, Hkv=1, D=64, block=16))
+
+
+def test_negative_totals_see_nothing():
+    w = BASE.replace(new=(1, 2, 40), total=(-5, 100, -1))
+    _check(w)
+
+
+def test_calls_from_two_threads():
+    """Each thread's calls on the default stream have a workspace of their own."""
+    import threading
+    w = [BASE.replace(new=(1,) * 8, total=tuple(range(900, 1700, 100)), seed=s) for s in (1, 2)]
+    g = [_gpu(ref.make(v)) for v in w]
+    want = [_attend(v, x).clone() for v, x in zip(w, g)]
+    torch.cuda.synchronize()
+    good = [0, 0]
+
+    def work(i):
+        for _ in range(200):
+            good[i] += torch.equal(_attend(w[i], g[i])[:8], want[i][:8])
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert good == [200, 200]
+
+
+def test_caller_workspace():
+    w = BASE.replace(new=(1, 3), total=(3000, 500))
+    g, out = _check(w)
+    T, Hq, D = out.shape
+    need = attn.attn_paged_workspace_bytes(T, 2, Hq, w.Hkv, D)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # nothing in it has to start at zero
+    again = torch.full_like(out, -7.0)
+    _attend(w, g, again, workspace=ws)
+    assert torch.equal(again, out)
+    with pytest.raises(attn.AttnError):
+        _attend(w, g, again, workspace=ws[:need - 16])
+
+
 def test_float8_and_uint8_caches_are_the_same():
     w = BASE
     g, out = _check(w)

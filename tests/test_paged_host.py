@@ -63,9 +63,9 @@ CASES = [
         dict(block=0), dict(width=-1), dict(causal=2), dict(scale=math.nan), dict(softcap=math.inf), dict(qst=255),
         dict(q=None), dict(kc=None), dict(vs=None), dict(tables=None), dict(starts=None), dict(totals=None),
         dict(out=None), dict(out=A[0]), dict(out=A[1] + 16), dict(lse=A[8]), dict(lse=A[6]), dict(width=2 ** 30),
-        dict(T=2 ** 30)]),
+        dict(T=2 ** 30), dict(Hq=65536, Hkv=65536, qst=65536 * 64)]),  # the last: caches of 27 GB overlap here
     (attend, attn.ATTN_ERR_UNSUPPORTED, [
-        dict(dtype=attn.ATTN_F32), dict(D=96, qst=384), dict(D=256, qst=1024), dict(block=24), dict(B=4097),
+        dict(dtype=attn.ATTN_F32), dict(D=96, qst=384), dict(D=256, qst=1024), dict(block=24), dict(B=8193), dict(Hq=65536, Hkv=1, qst=65536 * 64),
         dict(q=A[0] + 8), dict(qst=257), dict(out=A[8] + 2), dict(kc=A[1] + 8), dict(lse=A[10] + 1),
         dict(tables=A[5] + 2)]),
 ]

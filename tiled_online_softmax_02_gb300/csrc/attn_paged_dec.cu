@@ -11,7 +11,7 @@
 // its own rows of N:  x = x0 + x1 / 32 + x2 / 1024, x0 = e4m3(x),
 // x1 = e4m3(32 (x - x0)), ...  A piece's rest is at most 2^-4 of it, so two
 // pieces hold a bf16 Q exactly and three an f16 Q (down to 2^-23 and 2^-28 of
-// the unit's largest element: one power of two scales Q to e4m3's range), and
+// the row's largest element, which a power of two brings into e4m3's range), and
 // P in three pieces is good to 2^-12, or 2^-25 of its largest value: better
 // than a P rounded to f16.
 //
@@ -62,8 +62,8 @@ struct Cfg {
   static constexpr int kOffP = kOffQ + 2 * kQBytes;               // two buffers
   static constexpr int kOffLim = kOffP + 2 * kPBytes;             // int2 [2][NR]
   static constexpr int kOffRed = kOffLim + 2 * NR * 8;            // float [2][4][NR]: maxima, sums
-  static constexpr int kOffQs = kOffRed + 2 * 4 * NR * 4;             // float [2]: 1 / scale of Q's pieces
-  static constexpr int kOffSc = kOffQs + 16;                      // float4 [kScaleStages][kScaleGroups]
+  static constexpr int kOffQs = kOffRed + 2 * 4 * NR * 4;         // float [2][NR]: 1 / scale of a row's Q pieces
+  static constexpr int kOffSc = kOffQs + 2 * NR * 4;                      // float4 [kScaleStages][kScaleGroups]
   static constexpr int kOffBar = kOffSc + kScaleStages * kScaleGroups * 16;
   // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2],
   // sc_full, sc_empty [kScaleStages], drain
@@ -93,7 +93,7 @@ struct Lay {
   __device__ uint8_t* p_ptr(int i) const { return base + C::kOffP + i * C::kPBytes; }
   __device__ int2* lim(int i) const { return reinterpret_cast<int2*>(base + C::kOffLim) + i * NR; }
   __device__ float* red(int i) const { return reinterpret_cast<float*>(base + C::kOffRed) + i * 4 * NR; }
-  __device__ float* qs() const { return reinterpret_cast<float*>(base + C::kOffQs); }
+  __device__ float* qs(int i) const { return reinterpret_cast<float*>(base + C::kOffQs) + i * NR; }
   __device__ uint32_t bar(int i) const { return s + C::kOffBar + i * 8; }
   __device__ uint32_t k_full(int i) const { return bar(i); }
   __device__ uint32_t k_empty(int i) const { return bar(C::kSK + i); }
@@ -242,7 +242,7 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
 // rows of N past the pieces were zeroed once).  Then the scales of the unit's
 // tiles.  A row is D / 8 lanes wide (16 bytes each), all rows in flight
 // together; the next unit waits for this, so it is written for few
-// instructions: the largest |x| on packed 16-bit integers (magnitudes order as
+// instructions: a row's largest |x| on packed 16-bit integers (magnitudes order as
 // their bits), pieces and rests on packed f16, which holds x scaled below 256
 // exactly down to 2^-24.
 template <int D, int NR, bool BF16>
@@ -262,7 +262,6 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
     const int tok0 = paged_token(p, u.row0 + sub);
     int tok = tok0, head = u.row0 + sub - tok0 * p.group;
     uint4 raw[kLoads];
-    uint32_t top2 = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -270,26 +269,24 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
         raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride + head * D));
       for (head += kPer; head >= p.group; head -= p.group) ++tok;
     }
-    // one power of two for the unit, by its largest finite element
-    bool odd[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t t2 = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                                   __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
-      odd[i] = max(t2 & 0xffffu, t2 >> 16) >= kInf;  // an infinity or NaN: its row's scores become NaN
-      if (!odd[i]) top2 = __vmaxu2(top2, t2);
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
-    int ex;  // brings it into [128, 256)
-    if constexpr (BF16) ex = (int)(top >> 7) - 127;
-    else ex = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
-    ex = top == 0u ? 0 : min(max(7 - ex, -120), 120);
-    const float mul = __uint_as_float((uint32_t)(ex + 127) << 23);
     uint8_t* dst = sm.q_ptr(buf) + (c & 1) * 8;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int r = i * kPer + sub;
       const uint32_t e[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      const uint32_t top2 = __vmaxu2(__vmaxu2(e[0] & 0x7fff7fffu, e[1] & 0x7fff7fffu),
+                                     __vmaxu2(e[2] & 0x7fff7fffu, e[3] & 0x7fff7fffu));
+      uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+#pragma unroll
+      for (int o = 1; o < kVec; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool odd = top >= kInf;  // the row holds an infinity or NaN: its scores become NaN
+      // the power of two that brings the row's largest element into [128, 256)
+      int ex;
+      if constexpr (BF16) ex = (int)(top >> 7) - 127;
+      else ex = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
+      ex = top == 0u || odd ? 0 : min(max(7 - ex, -120), 120);
+      const float mul = __uint_as_float((uint32_t)(ex + 127) << 23);
+      if (c == 0 && r < NR) sm.qs(buf)[r] = __uint_as_float((uint32_t)(127 - ex) << 23);
       uint32_t h[4];  // scaled, f16 pairs
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -325,7 +322,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
             asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k + 1]) : "r"(0x50005000u));
           }
         }
-        if (odd[i]) w2[0] = w2[1] = j == 0 ? 0x7f7f7f7fu : 0u;
+        if (odd) w2[0] = w2[1] = j == 0 ? 0x7f7f7f7fu : 0u;
         // 8 bytes of chunk c / 2 of row n, the chunk's index XORed as the swizzle does
         const int n = j * NR + r;
         const int at = D == 128 ? ((c >> 1) ^ (n & 7)) : ((c >> 1) ^ ((n >> 1) & 3));
@@ -334,7 +331,6 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
     }
     for (int r = lane; r < NR; r += 32)
       sm.lim(buf)[r] = r < u.rows ? paged_limits(p, u.q, paged_token(p, u.row0 + r)) : make_int2(0, 0);
-    if (lane == 0) sm.qs()[buf] = __uint_as_float((uint32_t)(127 - ex) << 23);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(sm.q_full(buf));
@@ -449,7 +445,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
     const int buf = w.index & 1;
     wait(sm.q_full(buf), (w.index >> 1) & 1);
     const int2* lim = sm.lim(buf);
-    const float qs = sm.qs()[buf];
+    const float4* qs4 = reinterpret_cast<const float4*>(sm.qs(buf));
     const int full_lo = lim[u.rows - 1].x, full_hi = lim[0].y;  // keys every row sees
     float l[NR];
 #pragma unroll
@@ -464,7 +460,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       const int st = g % kScaleStages;
       wait(sm.sc_full(st), (g / kScaleStages) & 1);
       const float4 scl = sm.scales(st)[tid >> 4];  // of this thread's key
-      const float kmul = qs * scl.x, lv = scl.y, iv = scl.z;
+      const float lv = scl.y, iv = scl.z;
       __syncwarp();
       if (lane == 0) mbar_arrive(sm.sc_empty(st));
       wait(sm.s_full(g & 1), (g >> 1) & 1);
@@ -483,12 +479,20 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           t[r] = fmaf(x1[r], kInvStep, t[r]);
         }
       }
-      if (p.softcap > 0.0f) {
-        const float k1 = P.k1 * kmul, c = P.k3 + lv;
+      const float km = (p.softcap > 0.0f ? P.k1 : P.scale_log2) * scl.x;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) t[r] = fmaf(P.k2, fast_rcp(fast_exp2(t[r] * k1) + 1.0f), c);
+      for (int r = 0; r < NR; r += 4) {
+        const float4 q4 = qs4[r / 4];
+        t[r] *= q4.x;
+        t[r + 1] *= q4.y;
+        t[r + 2] *= q4.z;
+        t[r + 3] *= q4.w;
+      }
+      if (p.softcap > 0.0f) {
+        const float c = P.k3 + lv;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) t[r] = fmaf(P.k2, fast_rcp(fast_exp2(t[r] * km) + 1.0f), c);
       } else {
-        const float km = P.scale_log2 * kmul;
 #pragma unroll
         for (int r = 0; r < NR; ++r) t[r] = fmaf(t[r], km, lv);
       }

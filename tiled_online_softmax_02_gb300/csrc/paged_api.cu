@@ -167,11 +167,18 @@ int encode_cache(CUtensorMap* map, const void* base, int64_t planes, int block_s
   const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)block_size * (cuuint64_t)D};
   const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)block_size, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? ATTN_OK : cuda_fail(cudaErrorInvalidValue);
+  auto encode = [&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  if (encode() == CUDA_SUCCESS) return ATTN_OK;
+  // a host thread that has made no runtime call yet has no context current, which the driver call needs
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return encode() == CUDA_SUCCESS ? ATTN_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
 }  // namespace
@@ -210,7 +217,7 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
                     {block_tables, table_bytes}, {q_starts, n + 4}, {total_lengths, n}};
   if (clash(w, r)) return ATTN_ERR_INVALID_ARG;
   if (dtype == ATTN_F32 || (D != 64 && D != 128) || !block_size_ok(block_size) || B > kPagedMaxRequests ||
-      Hkv > 65535)
+      Hq > 65535)
     return ATTN_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || (q_token_stride * 2) % 16 != 0 || !aligned(out, 16) || !aligned(k_cache, 16) ||
       !aligned(v_cache, 16) || (need > 0 && !aligned(workspace, 16)))

@@ -29,7 +29,7 @@ enum AssignResult {
 };
 
 constexpr int kAssignMaxRequests = 8192;
-constexpr int kPagedMaxRequests = 4096;
+constexpr int kPagedMaxRequests = 8192;
 
 struct AssignParams {
   const int32_t* past;      // [B] tokens in the cache
