@@ -3,9 +3,8 @@
 // 2^(t - m_k) v8, its maximum m_k and L_k = sum of 2^(t - m_k) / v_scale; with
 // M = max m_k the row is
 //   sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) L_k   (0 when the latter is 0).
-// Bound: latency; the partial rows lie in L2.  A warp takes a row, lanes over
-// d, with several of its parts in flight; where the parts are few (long work:
-// most units are cut once), four rows and all their parts.
+// Bound: latency; the partial rows lie in L2.  Lanes go over d, and a warp has
+// several parts of a row, or several rows, in flight.
 // A programmatic dependent of the attention kernel: it may be scheduled while
 // that one drains, and waits for all of it before it reads.
 #include <cuda_bf16.h>
@@ -17,8 +16,7 @@ namespace gb300_attn {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRowsPerCta = 32;
-constexpr int kFew = 4;  // up to this many parts a warp takes four rows at once
+constexpr int kUnitRows = 32;  // rows of a CTA where units have many
 
 template <int D>
 struct RowVec {
@@ -60,86 +58,60 @@ __device__ __forceinline__ void store_row(const PagedCut& cut, int r, int Hq, in
     lse[row] = L == 0.0f ? -INFINITY : (M + (log2f(L) - ml_log2)) * 0.6931471805599453f;
 }
 
+// Many rows, mostly of two parts (long work: a unit is cut once or twice): a
+// warp takes two rows and two parts at a time.  (Four rows at a time: 2 us more
+// on 152 cut units of 256 rows, the registers leaving fewer warps.)
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_kernel(const PagedCut* cuts, const float* ws_o,
-                                                                      const float2* ws_ml, int unit_rows, int Hq,
-                                                                      int group, float ml_log2, uint16_t* out,
-                                                                      float* lse) {
+                                                                             const float2* ws_ml, int unit_rows,
+                                                                             int Hq, int group, float ml_log2,
+                                                                             uint16_t* out, float* lse) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int V = D / 32;
+  constexpr int V = D / 32, kRows = 2, kParts = 2;
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedCut cut = cuts[c];
-  const int row0 = blockIdx.y * kRowsPerCta;
-  if (cut.parts == 0 || row0 >= cut.rows) return;
+  const int end = min(cut.rows, ((int)blockIdx.y + 1) * kUnitRows);
+  if (cut.parts == 0) return;
   auto slot = [&](int k, int r) { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * unit_rows + r; };
-  if (cut.parts <= kFew) {
-    // rows row0 + warp + 8 i: lane 4 i + k holds (m, L) of row i, part k; all parts of all four rows in flight
-    const int mi = (lane >> 2) & 3, mk = min(lane & 3, cut.parts - 1);
-    const int mr = min(row0 + warp + kWarps * mi, cut.rows - 1);
-    const float2 ml = ws_ml[slot(mk, mr)];
-    RowVec<D> o[4][kFew];
+  for (int r0 = blockIdx.y * kUnitRows + warp * kRows; r0 < end; r0 += kWarps * kRows) {
+    float M[kRows], L[kRows], acc[kRows][V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kRows; ++i) {
+      M[i] = -INFINITY;
+      L[i] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kFew; ++k) {
-        const int r = row0 + warp + kWarps * i;
-        if (r < cut.rows && k < cut.parts) o[i][k].load(ws_o + slot(k, r) * D, lane);
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = row0 + warp + kWarps * i;
-      if (r >= cut.rows) break;
-      float m[kFew], M = -INFINITY, L = 0.0f, acc[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kFew; ++k) {
-        m[k] = __shfl_sync(0xffffffffu, ml.x, 4 * i + k);
-        if (k < cut.parts) M = fmaxf(M, m[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kFew; ++k) {
-        const float l = __shfl_sync(0xffffffffu, ml.y, 4 * i + k);
-        if (k >= cut.parts) continue;
-        const float w = exp2f(m[k] - M);
-        L = fmaf(w, l, L);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[i][k].x[v], acc[v]);
-      }
-      store_row<D, BF16>(cut, r, Hq, group, ml_log2, out, lse, lane, acc, M, L);
+      for (int v = 0; v < V; ++v) acc[i][v] = 0.0f;
     }
-    return;
-  }
-  for (int r = row0 + warp; r < min(cut.rows, row0 + kRowsPerCta); r += kWarps) {
-    float M = -INFINITY, L = 0.0f, acc[V];
+    for (int k0 = 0; k0 < cut.parts; k0 += kParts) {
+      // lane 2 i + j holds (m, L) of row i, part j
+      const int mr = min(r0 + ((lane >> 1) & 1), cut.rows - 1), mk = k0 + (lane & 1);
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (mk < cut.parts) ml = ws_ml[slot(mk, mr)];
+      RowVec<D> o[kRows][kParts];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    for (int k = lane; k < cut.parts; k += 32) M = fmaxf(M, ws_ml[slot(k, r)].x);
+      for (int i = 0; i < kRows; ++i)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int k0 = 0; k0 < cut.parts; k0 += 32) {
-      float w = 0.0f;  // 0 past the last part
-      if (k0 + lane < cut.parts) {
-        const float2 ml = ws_ml[slot(k0 + lane, r)];
-        w = exp2f(ml.x - M);
-        L = fmaf(w, ml.y, L);
-      }
-      const int n = min(32, cut.parts - k0);
-      for (int k = 0; k < n; k += 8) {  // eight parts in flight
-        RowVec<D> o[8];
+        for (int j = 0; j < kParts; ++j)
+          if (r0 + i < end && k0 + j < cut.parts) o[i][j].load(ws_o + slot(k0 + j, r0 + i) * D, lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j].load(ws_o + slot(min(k0 + k + j, cut.parts - 1), r) * D, lane);
+      for (int i = 0; i < kRows; ++i) {
+        const float m0 = __shfl_sync(0xffffffffu, ml.x, 2 * i), m1 = __shfl_sync(0xffffffffu, ml.x, 2 * i + 1);
+        const float l0 = __shfl_sync(0xffffffffu, ml.y, 2 * i), l1 = __shfl_sync(0xffffffffu, ml.y, 2 * i + 1);
+        const float Mn = fmaxf(fmaxf(M[i], m0), m1);  // finite: part k0 is there
+        const float keep = exp2f(M[i] - Mn), w0 = exp2f(m0 - Mn), w1 = exp2f(m1 - Mn);
+        M[i] = Mn;
+        L[i] = fmaf(w1, l1, fmaf(w0, l0, L[i] * keep));
+        const bool two = k0 + 1 < cut.parts;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float wk = __shfl_sync(0xffffffffu, w, k + j);
-#pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] = k + j < n ? fmaf(wk, o[j].x[v], acc[v]) : acc[v];
+        for (int v = 0; v < V; ++v) {
+          acc[i][v] = fmaf(w0, o[i][0].x[v], acc[i][v] * keep);
+          if (two) acc[i][v] = fmaf(w1, o[i][1].x[v], acc[i][v]);
         }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    store_row<D, BF16>(cut, r, Hq, group, ml_log2, out, lse, lane, acc, M, L);
+    for (int i = 0; i < kRows; ++i)
+      if (r0 + i < end) store_row<D, BF16>(cut, r0 + i, Hq, group, ml_log2, out, lse, lane, acc[i], M[i], L[i]);
   }
 }
 
@@ -212,9 +184,9 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_rows_kernel(const
 
 template <int D, bool BF16>
 cudaError_t launch_t(const PagedLaunch& L, cudaStream_t stream) {
-  const bool few_rows = L.rows < kRowsPerCta;
+  const bool by_row = L.rows <= 32;  // the decode kernel's units
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)L.grid, (unsigned)(few_rows ? L.rows : (L.rows + kRowsPerCta - 1) / kRowsPerCta), 1);
+  cfg.gridDim = dim3((unsigned)L.grid, (unsigned)(by_row ? L.rows : (L.rows + kUnitRows - 1) / kUnitRows), 1);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -222,7 +194,7 @@ cudaError_t launch_t(const PagedLaunch& L, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_rows ? attn_paged_join_rows_kernel<D, BF16> : attn_paged_join_kernel<D, BF16>,
+  return cudaLaunchKernelEx(&cfg, by_row ? attn_paged_join_rows_kernel<D, BF16> : attn_paged_join_kernel<D, BF16>,
                             (const PagedCut*)L.cuts, (const float*)L.ws_o, (const float2*)L.ws_ml, L.rows, L.c.Hq,
                             L.c.group, L.ml_log2, static_cast<uint16_t*>(L.c.out), L.c.lse);
 }
