@@ -148,6 +148,30 @@ __device__ __forceinline__ void tst16(uint32_t a, const float (&r)[16]) {
   tmem_st16(a, reinterpret_cast<const uint32_t(&)[16]>(r));
 }
 
+// e4m3 pieces of four values in two packed f16 pairs: the piece's bytes, and
+// the pairs become what is left of them times 32 (exact).
+__device__ __forceinline__ uint32_t last4(uint32_t h0, uint32_t h1) {
+  uint16_t b0, b1;
+  uint32_t w;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(h0));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h1));
+  asm("mov.b32 %0, {%1, %2};" : "=r"(w) : "h"(b0), "h"(b1));
+  return w;
+}
+__device__ __forceinline__ uint32_t piece4(uint32_t& h0, uint32_t& h1) {
+  const uint32_t w = last4(h0, h1);
+  uint32_t f0, f1;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+      : "=r"(f0), "=r"(f1) : "r"(w));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h0) : "r"(f0));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h1) : "r"(f1));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h0) : "r"(0x50005000u));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h1) : "r"(0x50005000u));
+  return w;
+}
+
+__device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) { return ffma2(b, f2(-1.0f, -1.0f), a); }
+
 // Reduce-scatter over the warp: on entry each lane holds NR values; on exit
 // lane l holds the max (sum) over all lanes of value row_of_lane<NR>(l).
 template <int NR>
@@ -307,21 +331,8 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
       for (int j = 0; j < C::kQP; ++j) {
         uint32_t w2[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint16_t b0, b1;
-          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(h[2 * k]));
-          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h[2 * k + 1]));
-          asm("mov.b32 %0, {%1, %2};" : "=r"(w2[k]) : "h"(b0), "h"(b1));
-          if (j + 1 < C::kQP) {  // the rest, times 32
-            uint32_t f0, f1;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f0) : "h"(b0));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f1) : "h"(b1));
-            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k]) : "r"(f0));
-            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k + 1]) : "r"(f1));
-            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k]) : "r"(0x50005000u));
-            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[2 * k + 1]) : "r"(0x50005000u));
-          }
-        }
+        for (int k = 0; k < 2; ++k)
+          w2[k] = j + 1 < C::kQP ? piece4(h[2 * k], h[2 * k + 1]) : last4(h[2 * k], h[2 * k + 1]);
         if (odd) w2[0] = w2[1] = j == 0 ? 0x7f7f7f7fu : 0u;
         // 8 bytes of chunk c / 2 of row n, the chunk's index XORed as the swizzle does
         const int n = j * NR + r;
@@ -445,14 +456,15 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
     const int buf = w.index & 1;
     wait(sm.q_full(buf), (w.index >> 1) & 1);
     const int2* lim = sm.lim(buf);
-    const float4* qs4 = reinterpret_cast<const float4*>(sm.qs(buf));
+    const uint64_t* qs2 = reinterpret_cast<const uint64_t*>(sm.qs(buf));  // two rows each
     const int full_lo = lim[u.rows - 1].x, full_hi = lim[0].y;  // keys every row sees
-    float l[NR];
+    // rows two by two (packed fp32): row sums, and the running maxima less kPLog2, the same in every thread
+    uint64_t l2[NR / 2], m2[NR / 2];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-    float m[NR];  // the running maxima, the same in every thread
-#pragma unroll
-    for (int r = 0; r < NR; ++r) m[r] = kNone;
+    for (int r = 0; r < NR / 2; ++r) {
+      l2[r] = 0ull;
+      m2[r] = f2(kNone, kNone);
+    }
     if (w.nt == 0) meet();  // a unit without a tile has no other meeting before its sums
 
     for (int n = 0; n < w.nt; ++n, ++g) {
@@ -465,6 +477,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       if (lane == 0) mbar_arrive(sm.sc_empty(st));
       wait(sm.s_full(g & 1), (g >> 1) & 1);
       tc_fence_after();
+      // scores in log2 units plus log2 v_scale, then less the maxima: t - m + 5
       float t[NR];
       {
         float x1[NR], x2[C::kQP > 2 ? NR : 1];
@@ -473,28 +486,24 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
         tld(a + NR, x1);
         if constexpr (C::kQP > 2) tld(a + 2 * NR, x2);
         tmem_wait_ld();
+        const uint64_t step = f2(kInvStep, kInvStep);
+        const float km = (p.softcap > 0.0f ? P.k1 : P.scale_log2) * scl.x;
+        const uint64_t km2 = f2(km, km), lv2 = f2(lv, lv);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          if constexpr (C::kQP > 2) x1[r] = fmaf(x2[r], kInvStep, x1[r]);
-          t[r] = fmaf(x1[r], kInvStep, t[r]);
+        for (int r = 0; r < NR; r += 2) {
+          uint64_t s = f2(x1[r], x1[r + 1]);
+          if constexpr (C::kQP > 2) s = ffma2(f2(x2[r], x2[r + 1]), step, s);
+          s = ffma2(s, step, f2(t[r], t[r + 1]));
+          s = fmul2(s, qs2[r / 2]);
+          if (p.softcap > 0.0f) {
+            float a0, a1;
+            f2_split(fmul2(s, km2), a0, a1);
+            t[r] = fmaf(P.k2, fast_rcp(fast_exp2(a0) + 1.0f), P.k3 + lv);
+            t[r + 1] = fmaf(P.k2, fast_rcp(fast_exp2(a1) + 1.0f), P.k3 + lv);
+          } else {
+            f2_split(ffma2(s, km2, lv2), t[r], t[r + 1]);
+          }
         }
-      }
-      const float km = (p.softcap > 0.0f ? P.k1 : P.scale_log2) * scl.x;
-#pragma unroll
-      for (int r = 0; r < NR; r += 4) {
-        const float4 q4 = qs4[r / 4];
-        t[r] *= q4.x;
-        t[r + 1] *= q4.y;
-        t[r + 2] *= q4.z;
-        t[r + 3] *= q4.w;
-      }
-      if (p.softcap > 0.0f) {
-        const float c = P.k3 + lv;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) t[r] = fmaf(P.k2, fast_rcp(fast_exp2(t[r] * km) + 1.0f), c);
-      } else {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) t[r] = fmaf(t[r], km, lv);
       }
       if (key0 < full_lo || key0 + kPagedKeys > full_hi) {
 #pragma unroll
@@ -506,8 +515,12 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       // does any key pass its row's maximum by more than kRise?
       float over = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) over = fmaxf(over, t[r] - m[r]);
-      if (n == 0 || meet_any(over > kRise)) {
+      for (int r = 0; r < NR; r += 2) {
+        float a, b;
+        f2_split(fsub2(f2(t[r], t[r + 1]), m2[r / 2]), a, b);
+        over = fmax3(over, a, b);
+      }
+      if (n == 0 || meet_any(over > kRise + kPLog2)) {
         float x[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) x[r] = t[r];
@@ -517,13 +530,18 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
         meet();
         float* alpha = x;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float old = m[r];
-          const float top = fmaxf(fmaxf(red[r], red[NR + r]), fmaxf(red[2 * NR + r], red[3 * NR + r]));
-          const float mn = top > old + kRise ? top : old;
-          alpha[r] = fast_exp2(old - mn);
-          l[r] *= alpha[r];
-          m[r] = mn;
+        for (int r = 0; r < NR; r += 2) {
+          float old[2];
+          f2_split(m2[r / 2], old[0], old[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float top = fmaxf(fmaxf(red[r + i], red[NR + r + i]), fmaxf(red[2 * NR + r + i], red[3 * NR + r + i])) - kPLog2;
+            const float mn = top > old[i] + kRise ? top : old[i];
+            alpha[r + i] = fast_exp2(old[i] - mn);
+            old[i] = mn;
+          }
+          m2[r / 2] = f2(old[0], old[1]);
+          l2[r / 2] = fmul2(l2[r / 2], f2(alpha[r], alpha[r + 1]));
         }
         if (n > 0) {  // O^T holds the unit's earlier tiles once their P V is done
           wait(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1);
@@ -543,17 +561,27 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       }
       // P buffer g % 2 was last read by the P V of tile g - 2
       if (g >= 2) wait(sm.pv_done(g & 1), ((g - 2) >> 1) & 1);
+      // weights, rounded to f16 (11 bits) and carried on as three e4m3 pieces
       uint32_t words[C::kNP / 4];
 #pragma unroll
       for (int i = 0; i < C::kNP / 4; ++i) words[i] = 0u;
+      const uint64_t iv2 = f2(iv, iv);
 #pragma unroll
-      for (int r = 0; r < NR; r += 2) {
-        float a = fast_exp2(t[r] - m[r] + kPLog2), b = fast_exp2(t[r + 1] - m[r + 1] + kPLog2);
-        l[r] = fmaf(a, iv, l[r]);
-        l[r + 1] = fmaf(b, iv, l[r + 1]);
-        words[r / 4] |= piece2(a, b) << (16 * ((r >> 1) & 1));
-        words[(NR + r) / 4] |= piece2(a, b) << (16 * ((r >> 1) & 1));
-        words[(2 * NR + r) / 4] |= last2(a, b) << (16 * ((r >> 1) & 1));
+      for (int r = 0; r < NR; r += 4) {
+        uint32_t h[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float a, b;
+          f2_split(fsub2(f2(t[r + 2 * i], t[r + 2 * i + 1]), m2[r / 2 + i]), a, b);
+          a = fast_exp2(a);
+          b = fast_exp2(b);
+          l2[r / 2 + i] = ffma2(f2(a, b), iv2, l2[r / 2 + i]);
+          const __half2 hh = __floats2half2_rn(a, b);
+          h[i] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        words[r / 4] = piece4(h[0], h[1]);
+        words[(NR + r) / 4] = piece4(h[0], h[1]);
+        words[(2 * NR + r) / 4] = last4(h[0], h[1]);
       }
       uint8_t* pb = sm.p_ptr(g & 1) + tid * 16;
 #pragma unroll
@@ -567,9 +595,12 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
     }
 
     // ---- the segment's rows: sums over the threads, O^T, and out (or a partial row)
-    float x[NR];
+    float x[NR], m[NR];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) x[r] = l[r];
+    for (int r = 0; r < NR; r += 2) {
+      f2_split(l2[r / 2], x[r], x[r + 1]);
+      f2_split(m2[r / 2], m[r], m[r + 1]);
+    }
     const float ws = reduce_scatter<NR, false>(x, lane);
     float* red = sm.red(1);  // not the maxima's, which a slower warp may still read
     if ((lane & (32 / NR - 1)) == 0) red[warp * NR + row_of_lane<NR>(lane)] = ws;
@@ -601,7 +632,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         if (tid < D) static_cast<uint16_t*>(p.out)[row * D + tid] = to_bits<BF16>(o[r] * inv);
         if (p.lse != nullptr && tid == r)
-          p.lse[row] = L == 0.0f ? -INFINITY : (m[r] + (__log2f(L) - kPLog2)) * kLn2;
+          p.lse[row] = L == 0.0f ? -INFINITY : (m[r] + __log2f(L)) * kLn2;
       } else {
         if (tid < D) P.ws_o[((int64_t)slot * NR + r) * D + tid] = o[r];
         if (tid == r) P.ws_ml[slot * NR + r] = make_float2(m[r], L);

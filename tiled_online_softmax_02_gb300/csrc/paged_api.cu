@@ -273,7 +273,7 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
     L.ml_log2 = kPagedTcLog2;
     e = launch_attn_paged_tc(L, bf16, st);
   } else {
-    L.ml_log2 = kPagedDecLog2;
+    L.ml_log2 = 0.0f;  // its maxima already hold the factor
     e = launch_attn_paged_dec(L, bf16, st);
   }
   if (e == cudaSuccess && max_tiles > 1) e = launch_attn_paged_join(L, bf16, st);

@@ -29,23 +29,6 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
          (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)layout << 61;
 }
 
-// e4m3 pieces of two values (lo in bits 0-7): the piece, and what is left of them times 32.
-__device__ __forceinline__ uint32_t piece2(float& lo, float& hi) {
-  uint16_t b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  lo = (lo - f.x) * kPieceStep;
-  hi = (hi - f.y) * kPieceStep;
-  return b;
-}
-__device__ __forceinline__ uint32_t last2(float lo, float hi) {
-  uint16_t b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
-  return b;
-}
-
 template <bool BF16>
 __device__ __forceinline__ uint16_t to_bits(float x) {
   if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
