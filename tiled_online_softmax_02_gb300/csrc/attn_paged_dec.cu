@@ -37,7 +37,6 @@ namespace gb300_attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kScaleStages = 4;
 constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6;  // warp 7: Q
 constexpr float kInvStep = 1.0f / kPieceStep;
 // P is carried as 32 * 2^(t - m); the maximum moves when a key passes it by
@@ -51,9 +50,8 @@ struct Cfg {
   static constexpr int kNQ = (kQP * NR + 15) / 16 * 16;           // N of S^T
   static constexpr int kNP = (kPP * NR + 15) / 16 * 16;           // N of O^T
   static constexpr int kTile = kPagedKeys * D;                    // bytes of a K or V tile
-  static constexpr int kCtas = NR <= 16 ? 2 : 1;                  // CTAs an SM
-  static constexpr int kSK = D == 64 ? 4 : (NR <= 16 ? 3 : 4);    // K stages
-  static constexpr int kSV = D == 64 ? 4 : (NR <= 16 ? 2 : 4);    // V stages
+  static constexpr int kSK = D == 64 ? 4 : 3;                     // K stages
+  static constexpr int kSV = D == 64 ? 4 : 2;                     // V stages
   static constexpr int kQBytes = (kNQ * D + 1023) / 1024 * 1024;
   static constexpr int kPBytes = kNP * kPagedKeys;
   static constexpr int kOffK = 0;
@@ -63,19 +61,19 @@ struct Cfg {
   static constexpr int kOffLim = kOffP + 2 * kPBytes;             // int2 [2][NR]
   static constexpr int kOffRed = kOffLim + 2 * NR * 8;            // float [2][4][NR]: maxima, sums
   static constexpr int kOffQs = kOffRed + 2 * 4 * NR * 4;         // float [2][NR]: 1 / scale of a row's Q pieces
-  static constexpr int kOffSc = kOffQs + 2 * NR * 4;                      // float4 [kScaleStages][kScaleGroups]
-  static constexpr int kOffBar = kOffSc + kScaleStages * kScaleGroups * 16;
+  static constexpr int kOffSc = kOffQs + 2 * NR * 4;                      // float4 [kSK][kScaleGroups]
+  static constexpr int kOffBar = kOffSc + kSK * kScaleGroups * 16;
   // k_full, k_empty [kSK], v_full, v_empty [kSV], s_full, p_full, pv_done, q_full, q_empty [2],
-  // sc_full, sc_empty [kScaleStages], drain
-  static constexpr int kBars = 2 * kSK + 2 * kSV + 11 + 2 * kScaleStages;
+  // sc_empty [kSK], drain
+  static constexpr int kBars = 2 * kSK + 2 * kSV + 11 + kSK;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;  // + alignment slack
   static constexpr int kColO = 2 * kNQ;                           // TMEM: S^T twice, then O^T
   static constexpr int kCols = 2 * kNQ + kNP;
   static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kTmem * kCtas <= 512, "tensor memory");
-  static_assert(kSmem <= (kCtas == 2 ? 115200 : 232448), "shared memory");
+  static_assert(kTmem * kPagedDecCtas <= 512, "tensor memory");
+  static_assert(kSmem <= 115200, "shared memory of two CTAs on an SM");
   static_assert(kOffBar % 8 == 0 && kOffQ % 1024 == 0 && kOffP % 1024 == 0, "alignment");
 };
 
@@ -105,9 +103,8 @@ struct Lay {
   __device__ uint32_t pv_done(int i) const { return rest(4 + i); }
   __device__ uint32_t q_full(int i) const { return rest(6 + i); }
   __device__ uint32_t q_empty(int i) const { return rest(8 + i); }
-  __device__ uint32_t sc_full(int i) const { return rest(10 + i); }
-  __device__ uint32_t sc_empty(int i) const { return rest(10 + kScaleStages + i); }
-  __device__ uint32_t drain() const { return rest(10 + 2 * kScaleStages); }
+  __device__ uint32_t sc_empty(int i) const { return rest(10 + i); }
+  __device__ uint32_t drain() const { return rest(10 + C::kSK); }
   __device__ float4* scales(int i) const { return reinterpret_cast<float4*>(base + C::kOffSc) + i * kScaleGroups; }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
@@ -123,7 +120,7 @@ __device__ __forceinline__ void mma8_elect(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
-// n consecutive 32-bit columns of this thread's TMEM lane (n = 4, 8, 16 or 32).
+// n consecutive 32-bit columns of this thread's TMEM lane (n = 4, 8 or 16).
 __device__ __forceinline__ void tld(uint32_t a, float (&r)[4]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]) : "r"(a) : "memory");
@@ -140,9 +137,6 @@ __device__ __forceinline__ void tld(uint32_t a, float (&r)[16]) {
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
         "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(a) : "memory");
-}
-__device__ __forceinline__ void tld(uint32_t a, float (&r)[32]) {
-  tmem_ld32(a, reinterpret_cast<uint32_t(&)[32]>(r));
 }
 __device__ __forceinline__ void tst16(uint32_t a, const float (&r)[16]) {
   tmem_st16(a, reinterpret_cast<const uint32_t(&)[16]>(r));
@@ -264,9 +258,10 @@ __device__ __forceinline__ void load_role(const DecParams& P, const CUtensorMap*
 // One warp: the unit's rows as e4m3 pieces, piece i of row r at row i * NR + r,
 // K-major in the swizzle of the row width; rows past the unit's are zeros (the
 // rows of N past the pieces were zeroed once).  Then the scales of the unit's
-// tiles.  A row is D / 8 lanes wide (16 bytes each), all rows in flight
-// together; the next unit waits for this, so it is written for few
-// instructions: a row's largest |x| on packed 16-bit integers (magnitudes order as
+// tiles.  A row is D / 8 lanes wide (16 bytes each).  The next unit waits for
+// this, and at the kernel's start every instruction comes from L2 first, so it
+// is a loop of at most four steps' code, the next rows on their way: a row's
+// largest |x| on packed 16-bit integers (magnitudes order as
 // their bits), pieces and rests on packed f16, which holds x scaled below 256
 // exactly down to 2^-24.
 template <int D, int NR, bool BF16>
@@ -277,7 +272,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
   constexpr int kLoads = NR / kPer > 0 ? NR / kPer : 1;
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on are not finite
   const int c = lane % kVec, sub = lane / kVec;
-  ScaleFeed<kScaleStages> feed;
+  ScaleFeed<C::kSK> feed;
   for (; !w.done(); w.next(p)) {
     const int buf = w.index & 1;
     if (w.index >= 2 && !wait_warp(sm.q_empty(buf), ((w.index >> 1) - 1) & 1, p.timeout_ns, p.status)) return;
@@ -285,19 +280,19 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + u.kvh * p.group * D + c * 8;
     const int tok0 = paged_token(p, u.row0 + sub);
     int tok = tok0, head = u.row0 + sub - tok0 * p.group;
-    uint4 raw[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (i * kPer + sub < u.rows)
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride + head * D));
+    auto load = [&](int i) {  // rows i * kPer ..; called in order
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (i * kPer + sub < u.rows) v = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride + head * D));
       for (head += kPer; head >= p.group; head -= p.group) ++tok;
-    }
+      return v;
+    };
     uint8_t* dst = sm.q_ptr(buf) + (c & 1) * 8;
-#pragma unroll
+    uint4 next = load(0);
+#pragma unroll 4
     for (int i = 0; i < kLoads; ++i) {
       const int r = i * kPer + sub;
-      const uint32_t e[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      const uint32_t e[4] = {next.x, next.y, next.z, next.w};
+      next = load(i + 1);
       const uint32_t top2 = __vmaxu2(__vmaxu2(e[0] & 0x7fff7fffu, e[1] & 0x7fff7fffu),
                                      __vmaxu2(e[2] & 0x7fff7fffu, e[3] & 0x7fff7fffu));
       uint32_t top = max(top2 & 0xffffu, top2 >> 16);
@@ -345,7 +340,7 @@ __device__ __forceinline__ void q_role(const DecParams& P, const Lay<D, NR, BF16
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(sm.q_full(buf));
-    if (!feed.unit(p, w, 1.0f, sm.scales(0), sm.sc_full(0), sm.sc_empty(0), lane)) return;
+    if (!feed.unit(p, w, 1.0f, sm.scales(0), sm.k_full(0), sm.sc_empty(0), lane)) return;
   }
 }
 
@@ -393,7 +388,7 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
   };
   for (; ok && !w.done(); w.next(p)) {
     const int buf = w.index & 1;
-    if (w.nt == 0 && pending) {  // no tile to issue before it: the waiting P V goes now
+    if (pending) {  // a unit's last P V does not wait for the next one's Q
       if (!pv(g - 1)) { ok = false; break; }
       pending = false;
     }
@@ -469,14 +464,11 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
 
     for (int n = 0; n < w.nt; ++n, ++g) {
       const int key0 = (w.t0 + n) * kPagedKeys, j = key0 + tid;
-      const int st = g % kScaleStages;
-      wait(sm.sc_full(st), (g / kScaleStages) & 1);
-      const float4 scl = sm.scales(st)[tid >> 4];  // of this thread's key
-      const float lv = scl.y, iv = scl.z;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm.sc_empty(st));
       wait(sm.s_full(g & 1), (g >> 1) & 1);
       tc_fence_after();
+      // the scales of this thread's key lie there once S^T does: K's barrier takes the scale warp's arrival too
+      const float4 scl = sm.scales(g % C::kSK)[tid >> 4];
+      const float lv = scl.y, iv = scl.z;
       // scores in log2 units plus log2 v_scale, then less the maxima: t - m + 5
       float t[NR];
       {
@@ -559,8 +551,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           tc_fence_before();
         }
       }
-      // P buffer g % 2 was last read by the P V of tile g - 2
-      if (g >= 2) wait(sm.pv_done(g & 1), ((g - 2) >> 1) & 1);
+      // P buffer g % 2 was last read by the P V of tile g - 2, issued before S^T(g): S^T(g) ready says it is done
       // weights, rounded to f16 (11 bits) and carried on as three e4m3 pieces
       uint32_t words[C::kNP / 4];
 #pragma unroll
@@ -591,7 +582,10 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sm.p_full(g & 1));
+      if (lane == 0) {
+        mbar_arrive(sm.p_full(g & 1));
+        mbar_arrive(sm.sc_empty(g % C::kSK));
+      }
     }
 
     // ---- the segment's rows: sums over the threads, O^T, and out (or a partial row)
@@ -654,7 +648,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
 }
 
 template <int D, int NR, bool BF16>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
+__global__ void __launch_bounds__(kThreads, kPagedDecCtas)
     attn_paged_dec_kernel(const __grid_constant__ DecParams P) {
   using C = Cfg<D, NR, BF16>;
   const PagedParams& p = P.c;
@@ -666,8 +660,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSK; ++i) {
-      mbar_init(sm.k_full(i), 1);
+      mbar_init(sm.k_full(i), 2);  // the TMA's, and the scale warp's
       mbar_init(sm.k_empty(i), 1);
+      mbar_init(sm.sc_empty(i), 4);
     }
     for (int i = 0; i < C::kSV; ++i) {
       mbar_init(sm.v_full(i), 1);
@@ -679,10 +674,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NR, BF16>::kCtas)
       mbar_init(sm.pv_done(i), 1);
       mbar_init(sm.q_full(i), 1);
       mbar_init(sm.q_empty(i), 5);  // four softmax warps and the MMA warp's commit
-    }
-    for (int i = 0; i < kScaleStages; ++i) {
-      mbar_init(sm.sc_full(i), 1);
-      mbar_init(sm.sc_empty(i), 4);
     }
     mbar_init(sm.drain(), 1);
     mbar_init_fence();
@@ -753,8 +744,6 @@ cudaError_t launch_dec_nr(const DecParams& P, bool bf16, int grid, cudaStream_t 
 
 }  // namespace
 
-int paged_dec_ctas_per_sm(int nr) { return nr <= 16 ? 2 : 1; }
-
 cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream) {
   DecParams P{};
   P.tmap_k = L.tmap_k;
@@ -774,7 +763,6 @@ cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t 
     case 4: return launch_dec_nr<4>(P, bf16, L.grid, stream);
     case 8: return launch_dec_nr<8>(P, bf16, L.grid, stream);
     case 16: return launch_dec_nr<16>(P, bf16, L.grid, stream);
-    case 32: return launch_dec_nr<32>(P, bf16, L.grid, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_rows_kernel(const
 
 template <int D, bool BF16>
 cudaError_t launch_t(const PagedLaunch& L, cudaStream_t stream) {
-  const bool by_row = L.rows <= 32;  // the decode kernel's units
+  const bool by_row = L.rows != kPagedTcRows;  // the decode kernel's units
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)L.grid, (unsigned)(by_row ? L.rows : (L.rows + kUnitRows - 1) / kUnitRows), 1);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);

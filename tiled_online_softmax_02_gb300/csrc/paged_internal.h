@@ -93,6 +93,7 @@ struct PagedCut {
 
 // A launch of one of the attention kernels, and of the kernel that joins the
 // partial rows of units cut between CTAs.
+constexpr int kPagedDecCtas = 2;     // CTAs of the few-rows kernel on an SM
 constexpr int kPagedTcRows = 256;
 constexpr float kPagedDecLog2 = 5.0f;  // log2 of the factor that P carries, in each of the kernels
 constexpr float kPagedTcLog2 = 7.0f;
@@ -108,8 +109,7 @@ struct PagedLaunch {
   float ml_log2;               // the kernel's 2^(t - m) carries this factor (log2)
 };
 
-int paged_dec_ctas_per_sm(int rows);
-cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream);  // rows 4, 8, 16 or 32
+cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream);  // rows 4, 8 or 16
 cudaError_t launch_attn_paged_tc(const PagedLaunch& L, bool bf16, cudaStream_t stream);   // rows kPagedTcRows
 cudaError_t launch_attn_paged_join(const PagedLaunch& L, bool bf16, cudaStream_t stream);
 

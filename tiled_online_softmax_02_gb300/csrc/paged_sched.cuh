@@ -102,6 +102,7 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const
   u.q = q;
   const int rows = u.q.n * p.group;
   long long c = 0;
+#pragma unroll 1
   for (u.rt = 0; u.rt * NR < rows; ++u.rt) {
     paged_unit_tiles<NR>(p, u);
     c += paged_cost<NR>(u);
@@ -136,6 +137,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
   const int b0 = min(tid * n, p.B), b1 = min(b0 + n, p.B);
   PagedReq q{0, 0, 0};
   long long c = 0, mine = 0;  // of the thread's last request; of all of them
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     q = paged_req(p, b);
     c = paged_head_cost<NR>(p, q);
@@ -172,6 +174,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
     if (!in || w1 == total) sh->w1 = w1;
   }
   // the thread whose requests hold a border finds its unit
+#pragma unroll 1
   for (int end = 0; end < 2; ++end) {
     const long long at = end ? w1 : w0;
     if (!in || at < before || at >= before + mine) continue;
@@ -189,6 +192,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
     }
     u.kvh = (int)paged_div(rest, c);
     rest -= c * u.kvh;
+#pragma unroll 1
     for (u.rt = 0;; ++u.rt) {
       paged_unit_tiles<NR>(p, u);
       if (rest < paged_cost<NR>(u)) break;
