@@ -532,3 +532,45 @@ def test_captured_steps_of_a_batch():
         s.enqueue()
     for new, fin in STEPS[1:]:
         s.step(new, fin, graph.replay)
+
+
+# ------------------------------------------------------------ wide tables
+@pytest.fixture
+def wide(monkeypatch):
+    """Tables for 2^21 keys a request: units of 16 and 256 rows instead of 8, whatever the lengths."""
+    make = ref.make
+
+    def widened(w):
+        x = make(w)
+        more = torch.full((len(w.new), 2 ** 21 // w.block), -3, dtype=torch.int32)
+        x["tables"] = torch.cat([x["tables"], more], 1)
+        return x
+    monkeypatch.setattr(ref, "make", widened)
+
+
+@pytest.mark.parametrize("feature", list(FEATURES))
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_wide_tables(shape, feature, wide):
+    _check(Problem(**SHAPES[shape]).replace(**FEATURES[feature]))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("Hq,Hkv", [(9, 1), (12, 1), (16, 1), (17, 1), (32, 2), (40, 1)])
+def test_wide_tables_heads(Hq, Hkv, dtype, D, wide):
+    _check(BASE.replace(Hq=Hq, Hkv=Hkv, dtype=dtype, D=D, total=(1, 130, 300, 64)))
+
+
+@pytest.mark.parametrize("new", [3, 60])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_wide_tables_extremes(new, dtype, wide):
+    test_one_key_far_above_the_others(new, dtype)
+    test_rows_of_very_different_size((new, 9), dtype)
+    test_a_row_that_is_not_finite_reaches_no_other((new, 3))
+    test_tables_that_name_no_block_are_reported((new, 3))
+    test_growing_maximum()
+    test_zero_scales()
+
+
+@pytest.mark.parametrize("new", [(3, 4, 3), (200, 1, 33)])
+def test_wide_tables_repeats_and_streams(new, wide):
+    test_repeats_and_streams_give_the_same_bits(new)
