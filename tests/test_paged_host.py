@@ -84,6 +84,13 @@ def test_empty_problems_touch_nothing(lib):
     assert attend(lib, B=0, tables=None, starts=None, totals=None) == attn.ATTN_OK
 
 
+@pytest.mark.parametrize("sizes", [(0, 4, 8, 2, 128), (5, 0, 8, 2, 128), (-1, 4, 8, 2, 128), (5, 4, 0, 2, 128),
+                                   (5, 4, 1, 2, 128), (5, 4, 8, 0, 128), (5, 4, 8, 2, 0), (5, 4, 8, 2, -64)])
+def test_sizes_of_no_call_need_no_workspace(lib, sizes):
+    assert attn.attn_paged_workspace_bytes(*sizes) == 0
+    assert attn.attn_paged_workspace_bytes(5, 4, 8, 2, 128) > 0
+
+
 def test_binding_rejects_bad_tensors():
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError):  # CPU tensors

@@ -141,7 +141,7 @@ struct PagedPlan {
 
 PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
   PagedPlan pl{};
-  if (T <= 0 || B <= 0 || Hkv <= 0 || Hq <= 0) return pl;
+  if (T <= 0 || B <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0) return pl;
   const int group = Hq / Hkv;
   // Rows per (request, kv head) of an even batch; a request with more takes several units.  The few-rows kernel's
   // time a tile grows with the rows it holds, the many-rows kernel's does not.  48 requests of up to 8K tokens, 4 kv
