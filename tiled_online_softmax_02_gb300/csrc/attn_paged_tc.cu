@@ -30,6 +30,14 @@
 // last one's rows; warps 8-11 widen V; warp 12 loads (TMA), 13 issues MMAs, 14
 // looks up scales and prefetches the next unit's Q rows into L2.
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
+//
+// Measured (one GB300, device time with the join, bf16, 32 query and 8 kv heads,
+// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 583 us, 1230
+// TFLOP/s, 66% of a 16-bit library product's rate; two whole prompts of 3.5K to
+// 4K tokens 262 us, 900 TFLOP/s.  The tensor pipe is busy 52% of the first's
+// time: a lane's S, softmax and P V follow one another, as P takes S's place
+// (two of each and two O of 128 columns fill tensor memory), and two lanes do
+// not cover that entirely.  A unit costs about three tiles more than its tiles.
 #include <atomic>
 
 #include "paged_mma.cuh"

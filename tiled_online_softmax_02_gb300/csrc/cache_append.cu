@@ -17,6 +17,12 @@
 // runs (a decode step's) take a warp each, long ones the whole CTA.  The slots
 // that can matter are read once into shared memory, and a thread keeps its
 // first values in registers between finding the maximum and encoding them.
+//
+// Measured (one GB300, device time): 64 new tokens of 8 kv heads 4.7 us; 16K
+// tokens of 8 kv heads, D = 128, bf16, 27 us, 3.8 TB/s.  The latter issues an
+// instruction in 58% of its cycles and its loads wait for the slots' and the
+// maximum's chain; 256 threads a CTA (31 us), twice the values in registers
+// (30 us: fewer CTAs fit), several heads a CTA (31 to 48 us) were all slower.
 #include <type_traits>
 
 #include <cuda_bf16.h>
