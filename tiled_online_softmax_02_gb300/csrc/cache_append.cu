@@ -19,10 +19,12 @@
 // first values in registers between finding the maximum and encoding them.
 //
 // Measured (one GB300, device time): 64 new tokens of 8 kv heads 4.7 us; 16K
-// tokens of 8 kv heads, D = 128, bf16, 27 us, 3.8 TB/s.  The latter issues an
-// instruction in 58% of its cycles and its loads wait for the slots' and the
-// maximum's chain; 256 threads a CTA (31 us), twice the values in registers
-// (30 us: fewer CTAs fit), several heads a CTA (31 to 48 us) were all slower.
+// tokens of 8 kv heads, D = 128, bf16, 24.7 us, 4.1 TB/s (26.9 without the
+// prefetch).  The latter waits for its chain of slots, rows, maximum and stores
+// (leaving out the maximum's or the encoding's arithmetic changes nothing);
+// 256 threads a CTA (31 us), twice the values in registers (28 us: fewer CTAs
+// fit), several heads a CTA (31 to 48 us), 8 or 12 CTAs an SM instead of 10 (26
+// and 27 us), 32 or 128 tokens a CTA (26 and 29 us) were all slower.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -220,6 +222,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
   const int n = min(p.chunk, p.T - first);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bs = p.block_size, shift = p.block_shift;
+  const T* x0 = static_cast<const T*>(which ? p.x[1] : p.x[0]);
+  const int64_t stride = which ? p.stride[1] : p.stride[0];
+  // Most rows that this CTA will read are its own tokens': their lines come to L2 while the slots are looked up.
+  if (p.chunk == kMaxChunk) {
+    constexpr int kLines = D * sizeof(T) / 128;
+    for (int i = threadIdx.x; i < n * kLines; i += kThreads) {
+      const T* line = x0 + (int64_t)(first + i / kLines) * stride + h * D + i % kLines * (D / kLines);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+    }
+  }
   const int held = 1 + p.chunk + bs;
   for (int i = threadIdx.x; i < held; i += kThreads) {
     const int t = first + i - 1;
@@ -256,8 +268,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
     if (lane == 0) begin[i0 >> 5] = m;
   }
   __syncthreads();
-  const T* x0 = static_cast<const T*>(which ? p.x[1] : p.x[0]);
-  const int64_t stride = which ? p.stride[1] : p.stride[0];
   uint8_t* cache = which ? p.cache[1] : p.cache[0];
   float* scales = which ? p.scales[1] : p.scales[0];
 
