@@ -32,12 +32,16 @@
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
 //
 // Measured (one GB300, device time with the join, bf16, 32 query and 8 kv heads,
-// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 583 us, 1230
+// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 581 us, 1240
 // TFLOP/s, 66% of a 16-bit library product's rate; two whole prompts of 3.5K to
-// 4K tokens 262 us, 900 TFLOP/s.  The tensor pipe is busy 52% of the first's
+// 4K tokens 252 us, 937 TFLOP/s.  The tensor pipe is busy half of the first's
 // time: a lane's S, softmax and P V follow one another, as P takes S's place
 // (two of each and two O of 128 columns fill tensor memory), and two lanes do
-// not cover that entirely.  A unit costs about three tiles more than its tiles.
+// not cover that entirely; P V of a tile's first 64 keys at least runs beside
+// the exponentials of the others.  A lane's tile is 1200 cycles of waiting for S,
+// 700 for the maximum and 1550 for the exponentials.  A unit costs about three
+// tiles more than its tiles: 6000 cycles to bring Q, most of them conversions
+// to e4m3 and back, and 4000 to store the rows.
 #include <atomic>
 
 #include "paged_mma.cuh"
@@ -53,7 +57,7 @@ constexpr int kVWarp0 = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
 constexpr float kRise = 8.0f;          // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
-constexpr int kMaxUnroll = 4, kExpUnroll = 1;
+constexpr int kMaxUnroll = 2, kExpUnroll = 1;
 
 template <int D, bool BF16>
 struct Cfg {
@@ -69,11 +73,11 @@ struct Cfg {
   static constexpr int kOffV8 = kOffK + kSK * kTile8;
   static constexpr int kOffV = kOffV8 + kSV8 * kTile8;
   static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kSK][kScaleGroups]: k scale, log2 v scale, 1 / v scale
-  static constexpr int kOffQe = kOffSc + kSK * kScaleGroups * 16;  // int8 [256]: log2 of the Q rows' scales
-  static constexpr int kOffBar = kOffQe + kRows;
+  static constexpr int kOffQe = kOffSc + kSK * kScaleGroups * 16;  // uint32 [256]: the Q rows' scales, as f32 (bf16 Q) or two f16 factors
+  static constexpr int kOffBar = kOffQe + kRows * 4;
   // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_empty [kSK],
-  // q_full, s_full, p_full, o_final [2], drain
-  static constexpr int kBars = 2 * (kSK + kSV8 + kSV) + kSK + 9;
+  // q_full, s_full, p_half, p_full, o_final [2], drain
+  static constexpr int kBars = 2 * (kSK + kSV8 + kSV) + kSK + 11;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;
@@ -105,10 +109,11 @@ struct Lay {
   __device__ uint32_t sc_empty(int i) const { return rest(i); }
   __device__ uint32_t q_full(int t) const { return rest(C::kSK + t); }
   __device__ uint32_t s_full(int t) const { return rest(C::kSK + 2 + t); }
-  __device__ uint32_t p_full(int t) const { return rest(C::kSK + 4 + t); }
-  __device__ uint32_t o_final(int t) const { return rest(C::kSK + 6 + t); }
-  __device__ uint32_t drain() const { return rest(C::kSK + 8); }
-  __device__ int8_t* q_exp() const { return reinterpret_cast<int8_t*>(base + C::kOffQe); }
+  __device__ uint32_t p_half(int t) const { return rest(C::kSK + 4 + t); }
+  __device__ uint32_t p_full(int t) const { return rest(C::kSK + 6 + t); }
+  __device__ uint32_t o_final(int t) const { return rest(C::kSK + 8 + t); }
+  __device__ uint32_t drain() const { return rest(C::kSK + 10); }
+  __device__ uint32_t* q_mul() const { return reinterpret_cast<uint32_t*>(base + C::kOffQe); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
@@ -300,14 +305,10 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
     }
     tc_commit_elect(sm.s_full(t));
   };
-  auto issue_pv = [&](int t, int vs, bool first) {
-    const uint64_t b = make_sdesc_sw128(sm.v_tile(vs), BN * 128, 1024);
-    const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
-#pragma unroll
-    for (int k = 0; k < BN / 16; k += 4)
-      mma_ts4_elect(d, a + k * 8, b + (uint32_t)(k * 128), a + (k + 1) * 8, b + (uint32_t)((k + 1) * 128),
-                    a + (k + 2) * 8, b + (uint32_t)((k + 2) * 128), a + (k + 3) * 8, b + (uint32_t)((k + 3) * 128), kIdO,
-                    (!first || k > 0) ? 1u : 0u);
+  auto issue_pv = [&](int t, int vs, int half, bool first) {  // keys 64 half .. of the tile
+    const uint64_t b = make_sdesc_sw128(sm.v_tile(vs), BN * 128, 1024) + (uint32_t)(half * 512);
+    const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128 + half * 32;
+    mma_ts4_elect(d, a, b, a + 8, b + 128u, a + 16, b + 256u, a + 24, b + 384u, kIdO, first ? 0u : 1u);
   };
   for (; ok && !w.done(); w.next(p)) {
     if (w.nt == 0) continue;  // no S, and no Q was brought
@@ -318,9 +319,12 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
       if (n >= 1 && !wait_warp(sm.v_full(sv), ((g + n - 1) / C::kSV) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         if (n >= 1) {
+          if (!wait_warp(sm.p_half(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(t, sv, 0, n == 1);
           if (!wait_warp(sm.p_full(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
-          issue_pv(t, sv, n == 1);
+          issue_pv(t, sv, 1, false);
           if (n == w.nt) tc_commit_elect(sm.o_final(t));
           ++pc[t];
         }
@@ -351,98 +355,116 @@ __device__ __forceinline__ void mma_role(const PagedTcParams& P, const Lay<D, BF
 
 // ------------------------------------------------------------------ softmax
 // A lane's rows of Q as e4m3 pieces, K-major in the swizzle of the row width;
-// rows past the unit's are zeros.  Each warp brings its own 32 rows: a row is
-// D / 8 threads wide (16 bytes each), so an instruction loads 2 (D = 64: 4)
-// rows, and a quarter of the warp's rows are in flight together.  It stands between
-// two units, where the tensor core waits for it, so it is written for few
-// instructions: the row's largest |x| on packed 16-bit integers (magnitudes
-// order as their bits), the pieces and their rests on packed f16, which holds
-// x scaled below 256 exactly down to 2^-24.  Returns 1 / the scale of this
-// thread's own row.
+// rows past the unit's are zeros.  Each warp brings its own 32 rows.  The
+// tensor core waits for this between two units, and most of the code comes
+// from L2 each time, so it is three small loops:
+//   all rows into shared memory as they are, in flight together: a row's first
+//   and second half where its first two pieces will lie;
+//   thread = row: its largest |x|, on packed 16-bit integers (magnitudes order as
+//   their bits), and the power of two that brings it into [128, 256);
+//   D / 8 threads a row: 8 values of the row each into pieces, in place, on
+//   packed f16, which holds x scaled below 256 exactly down to 2^-24.
+// Returns 1 / the scale of this thread's own row.
 template <int D, bool BF16>
 __device__ __forceinline__ float bring_q(const PagedTcParams& P, const Lay<D, BF16>& sm, const PagedUnit& u, int t,
                                          int wq, int lane) {
   using C = Cfg<D, BF16>;
   const PagedParams& p = P.c;
-  constexpr int kVec = D / 8, kPer = 32 / kVec, kBatch = 8 / kPer;
+  constexpr int kVec = D / 8, kPer = 32 / kVec, kHalf = kVec / 2;  // 16-byte pieces of a row; rows an instruction
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on are not finite
-  const int c = lane % kVec, sub = lane / kVec;
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)u.q.s0 * p.q_stride + u.kvh * p.group * D + c * 8;
-  uint8_t* dst = sm.q_ptr(t) + (c & 1) * 8;
-  int8_t* exps = sm.q_exp() + t * BM;
-  const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;
-  // this thread's first row as (token, head); the next ones kPer rows on
-  int r = wq * 32 + sub;
-  int tok = paged_token(p, u.row0 + t * BM + r), head = (u.row0 + t * BM + r) - tok * p.group;
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    uint4 raw[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (t * BM + r + i * kPer < u.rows)
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride + head * D));
-      for (head += kPer; head >= p.group; head -= p.group) ++tok;
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i, r += kPer) {
-      const uint32_t e[4] = {raw[i].x ^ sign, raw[i].y ^ sign, raw[i].z ^ sign, raw[i].w ^ sign};
-      const uint32_t top2 = __vmaxu2(__vmaxu2(e[0] & 0x7fff7fffu, e[1] & 0x7fff7fffu),
-                                     __vmaxu2(e[2] & 0x7fff7fffu, e[3] & 0x7fff7fffu));
-      uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-#pragma unroll
-      for (int o = 1; o < kVec; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool odd = top >= kInf;  // the row holds an infinity or NaN: its scores become NaN
-      // the power of two that brings the row's largest element into [128, 256)
-      int ex;
-      if constexpr (BF16) ex = (int)(top >> 7) - 127;
-      else ex = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
-      ex = top == 0u || odd ? 0 : min(max(7 - ex, -120), 120);
-      const float mul = __uint_as_float((uint32_t)(ex + 127) << 23);
-      if (c == 0) exps[r] = (int8_t)ex;
-      uint32_t h[4];  // scaled, f16 pairs
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a, b2;
-        if constexpr (BF16) {
-          a = __uint_as_float(e[k] << 16);
-          b2 = __uint_as_float(e[k] & 0xffff0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&e[k]));
-          a = f.x;
-          b2 = f.y;
-        }
-        f2_split(fmul2(f2(a, b2), f2(mul, mul)), a, b2);
-        const __half2 hh = __floats2half2_rn(a, b2);
-        h[k] = *reinterpret_cast<const uint32_t*>(&hh);
-      }
-      // 8 bytes of chunk c / 2 of the row, whose index the swizzle XORs
-      const int at = D == 128 ? ((c >> 1) ^ (r & 7)) : ((c >> 1) ^ ((r >> 1) & 3));
-      uint8_t* out = dst + r * D + at * 16;
-#pragma unroll
-      for (int j = 0; j < C::kQP; ++j) {
-        uint32_t w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint16_t b0, b1;
-          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(h[2 * k]));
-          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h[2 * k + 1]));
-          asm("mov.b32 %0, {%1, %2};" : "=r"(w[k]) : "h"(b0), "h"(b1));
-          if (j + 1 < C::kQP) {
-            uint32_t f0, f1;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f0) : "h"(b0));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f1) : "h"(b1));
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * k]) : "r"(h[2 * k]), "r"(f0));
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * k + 1]) : "r"(h[2 * k + 1]), "r"(f1));
-          }
-        }
-        if (odd) w[0] = w[1] = j == 0 ? 0x7f7f7f7fu : 0u;
-        *reinterpret_cast<uint2*>(out + j * (BM * D)) = make_uint2(w[0], w[1]);
-      }
+  static_assert(C::kQP >= 2, "a row lies in the room of two pieces");
+  const int c = lane % kVec, sub = lane / kVec, row0 = wq * 32;
+  const uint32_t raw0 = (uint32_t)((c / kHalf) * (BM * D) + (row0 + sub) * D + (c % kHalf) * 16);  // + i kPer D
+  {
+    const int row = t * BM + row0 + lane;  // this thread's own; where it lies goes to the threads that load it
+    const int tok = paged_token(p, u.row0 + row);
+    const int64_t at = row < u.rows ? (int64_t)(u.q.s0 + tok) * p.q_stride +
+                                          (u.kvh * p.group + u.row0 + row - tok * p.group) * D : -1;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + c * 8;
+    const uint32_t to = sm.q(t) + raw0;
+#pragma unroll 2
+    for (int i = 0; i < kVec; ++i) {
+      const int64_t from = __shfl_sync(0xffffffffu, at, i * kPer + sub);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * (kPer * D)),
+                   "l"(q + max(from, (int64_t)0)), "r"(from >= 0 ? 16 : 0) : "memory");
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
-  return __uint_as_float((uint32_t)(127 - exps[wq * 32 + lane]) << 23);
+  float inv;
+  {
+    const uint8_t* mine = sm.q_ptr(t) + (row0 + lane) * D;
+    const int turn = D == 128 ? lane : lane >> 1;  // eight rows' pieces in eight banks' groups
+    uint32_t top2 = 0;
+#pragma unroll 4
+    for (int i = 0; i < kVec; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + i / kHalf * (BM * D) + ((i + turn) % kHalf) * 16);
+      top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    int ex;
+    if constexpr (BF16) ex = (int)(top >> 7) - 127;
+    else ex = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;
+    const bool odd = top >= kInf;  // the row holds an infinity or NaN: its scores become NaN
+    ex = top == 0u || odd ? 0 : min(max(7 - ex, -120), BF16 ? 120 : 30);
+    if constexpr (BF16) {
+      sm.q_mul()[t * BM + row0 + lane] = odd ? 0x7fc00000u : (uint32_t)(ex + 127) << 23;
+    } else {
+      const int e0 = min(ex, 15), e1 = ex - e0;  // ex is -8 .. 30
+      sm.q_mul()[t * BM + row0 + lane] = (uint32_t)(odd ? 0x7e00 : (e0 + 15) << 10) | (uint32_t)(e1 + 15) << 26;
+    }
+    inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+  }
+  __syncwarp();
+  const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;
+  uint8_t* base = sm.q_ptr(t);
+#pragma unroll 1
+  for (int i = 0; i < kVec; ++i) {
+    const int r = row0 + i * kPer + sub;
+    const uint4 v = *reinterpret_cast<const uint4*>(base + raw0 + i * (kPer * D));
+    const uint32_t mbits = sm.q_mul()[t * BM + r];
+    const float mul = __uint_as_float(mbits);                                 // bf16: the scale
+    const uint32_t m0 = __byte_perm(mbits, 0, 0x1010), m1 = __byte_perm(mbits, 0, 0x3232);  // f16: its two factors
+    __syncwarp();  // the row has been read
+    const uint32_t e[4] = {v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
+    uint32_t h[4];  // scaled, f16 pairs
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (BF16) {
+        float a, b2;
+        f2_split(fmul2(f2(__uint_as_float(e[k] << 16), __uint_as_float(e[k] & 0xffff0000u)), f2(mul, mul)), a, b2);
+        const __half2 hh = __floats2half2_rn(a, b2);
+        h[k] = *reinterpret_cast<const uint32_t*>(&hh);
+      } else {  // two powers of two that f16 holds
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[k]) : "r"(e[k]), "r"(m0));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[k]) : "r"(m1));
+      }
+    }
+    // 8 bytes of chunk c / 2 of the row, whose index the swizzle XORs
+    const int at = D == 128 ? ((c >> 1) ^ (r & 7)) : ((c >> 1) ^ ((r >> 1) & 3));
+    uint8_t* out = base + r * D + at * 16 + (c & 1) * 8;
+#pragma unroll
+    for (int j = 0; j < C::kQP; ++j) {
+      uint32_t w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint16_t b0, b1;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b0) : "r"(h[2 * k]));
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h[2 * k + 1]));
+        asm("mov.b32 %0, {%1, %2};" : "=r"(w[k]) : "h"(b0), "h"(b1));
+        if (j + 1 < C::kQP) {
+          uint32_t f0, f1;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f0) : "h"(b0));
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f1) : "h"(b1));
+          asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * k]) : "r"(h[2 * k]), "r"(f0));
+          asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * k + 1]) : "r"(h[2 * k + 1]), "r"(f1));
+        }
+      }
+      *reinterpret_cast<uint2*>(out + j * (BM * D)) = make_uint2(w[0], w[1]);
+    }
+  }
+  return inv;
 }
 
 // 32 bytes of a row, which lies apart from other threads' rows: one store of
@@ -588,6 +610,17 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       const float m_new = rise ? m_tile : m_run;
       const float alpha = fast_exp2(m_run - m_new);  // 1 where the maximum stays
       m_run = m_new;
+      if (n > 0 && __any_sync(0xffffffffu, rise)) {  // O holds every earlier tile
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + k * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(o_addr + k * 32, o);
+        }
+      }
       const float off = kPLog2 - m_run;
       uint64_t sum = 0ull;
 #pragma unroll kExpUnroll
@@ -628,21 +661,16 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
           sum = ffma2(fadd2(part[0], part[1]), f2(s4.z, s4.z), sum);
         }
         tmem_st16(s_addr + ch * 16, pk);  // over columns of S that have been read
+        if (ch == 1) {  // P V of the first 64 keys runs during the others' exponentials
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sm.p_half(t));
+        }
       }
       float sa, sb;
       f2_split(sum, sa, sb);
       l_run = fmaf(l_run, alpha, sa + sb);
-      if (n > 0 && __any_sync(0xffffffffu, rise)) {  // O holds every earlier tile
-#pragma unroll 1
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + k * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(o_addr + k * 32, o);
-        }
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -698,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     for (int t = 0; t < 2; ++t) {
       mbar_init(sm.q_full(t), 4);
       mbar_init(sm.s_full(t), 1);
+      mbar_init(sm.p_half(t), 4);
       mbar_init(sm.p_full(t), 4);
       mbar_init(sm.o_final(t), 1);
     }
