@@ -574,3 +574,44 @@ def test_wide_tables_extremes(new, dtype, wide):
 @pytest.mark.parametrize("new", [(3, 4, 3), (200, 1, 33)])
 def test_wide_tables_repeats_and_streams(new, wide):
     test_repeats_and_streams_give_the_same_bits(new)
+
+
+# ------------------------------------------------- queries at their type's ends
+def _extreme_queries(dtype, new):
+    """Rows of the smallest and (float16) the largest magnitudes, zeros, and one that is not finite."""
+    w = BASE.replace(new=new, total=(300, 250), dtype=dtype, Hq=8, Hkv=2)
+    x = ref.make(w)
+    n = sum(new)
+    sign = torch.sign(x["q"].float())
+    x["q"][0, 0] = (sign[0, 0] * 2.0 ** (-24 if dtype == "f16" else -110)).to(x["q"].dtype)
+    x["q"][0, 1] = 0.0
+    if dtype == "f16":
+        x["q"][n - 1, 6] = (sign[n - 1, 6] * 65504.0).to(x["q"].dtype)
+    x["q"][n - 1, 7, 3:] = 0.0
+    bad = x["q"].clone()
+    bad[1, 3, 9] = float("-inf")
+    bad[1, 6, 0] = float("nan")
+    return w, x, dict(x, q=bad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [(2, 1), (3, 2), (150, 40)])
+def test_queries_at_their_types_ends(new, dtype):
+    w, x, odd = _extreme_queries(dtype, new)
+    g = _gpu(x)
+    out = torch.full(x["q"].shape, -7.0, dtype=x["q"].dtype, device="cuda")
+    lse = torch.full(x["q"].shape[:2], -7.0, device="cuda")
+    _attend(w, g, out, lse)
+    _check_out(w, x, out, lse)
+    got = torch.full_like(out, -7.0)
+    _attend(w, _gpu(odd), got)
+    assert got[1, 3].isnan().all() and got[1, 6].isnan().all()
+    keep = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    keep[1, 3] = keep[1, 6] = False
+    assert torch.equal(got[keep], out[keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [(2, 1), (3, 2), (150, 40)])
+def test_wide_tables_queries_at_their_types_ends(new, dtype, wide):
+    test_queries_at_their_types_ends(new, dtype)
