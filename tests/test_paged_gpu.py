@@ -615,3 +615,60 @@ def test_queries_at_their_types_ends(new, dtype):
 @pytest.mark.parametrize("new", [(2, 1), (3, 2), (150, 40)])
 def test_wide_tables_queries_at_their_types_ends(new, dtype, wide):
     test_queries_at_their_types_ends(new, dtype)
+
+
+# ------------------------------------------------ large caches, concurrent graphs
+@pytest.mark.parametrize("new", [(1, 2, 1), (150, 1, 20)])
+def test_blocks_past_four_gigabytes(new):
+    """The same step over a small cache and over one whose blocks in use lie past 2^32 bytes: equal bits."""
+    w = BASE.replace(new=new, total=(300, 200, 129), Hq=16, Hkv=8)
+    x = ref.make(w)
+    small = _gpu(x)
+    N = x["k_cache"].shape[0]
+    more = 2 ** 32 // (w.Hkv * w.block * w.D) + 5
+    big = dict(small, tables=torch.where((small["tables"] >= 0) & (small["tables"] < N), small["tables"] + more, -1))
+    for name in ("k_cache", "v_cache", "k_scales", "v_scales"):
+        big[name] = torch.zeros((N + more, *small[name].shape[1:]), dtype=small[name].dtype, device="cuda")
+        big[name][more:] = small[name]
+    kv = [torch.randn(sum(new), w.Hkv, w.D, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    slots, tables = [], x["tables"].numpy()
+    for b, n in enumerate(new):
+        for pos in range(w.total[b] - n, w.total[b]):
+            slots.append(int(tables[b, pos // w.block]) * w.block + pos % w.block)
+    slots = torch.tensor(slots, device="cuda")
+    outs = []
+    for g, at in ((small, slots), (big, slots + more * w.block)):
+        attn.attn_cache_append_fp8(*kv, at, g["k_cache"], g["v_cache"], g["k_scales"], g["v_scales"])
+        out = torch.full(x["q"].shape, -7.0, dtype=x["q"].dtype, device="cuda")
+        _attend(w, g, out)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert attn.get_device_status() == attn.ATTN_OK
+    assert torch.equal(outs[0], outs[1])
+    for name in ("k_cache", "v_cache", "k_scales", "v_scales"):
+        assert torch.equal(big[name][more:], small[name])
+
+
+def test_two_graphs_replayed_at_once():
+    """Two captured calls, each with the workspace its capture gave it, on two streams at the same time."""
+    made = []
+    for new, total, seed in (((1,) * 6, (900, 1700, 300, 2500, 40, 1100), 3), ((90, 200, 1), (1500, 700, 2000), 4)):
+        w = BASE.replace(new=new, total=total, seed=seed)
+        x = ref.make(w)
+        g = _gpu(x)
+        want = torch.full(x["q"].shape, -7.0, dtype=x["q"].dtype, device="cuda")
+        _attend(w, g, want)
+        out = torch.full_like(want, -7.0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            _attend(w, g, out)
+        made.append((graph, out, want, torch.cuda.Stream(), g))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, _, _, stream, _ in made:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in made:
+        assert torch.equal(out, want)
+    assert attn.get_device_status() == attn.ATTN_OK
