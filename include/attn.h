@@ -437,7 +437,10 @@ int attn_cache_append_fp8(const void *k, const void *v, const int64_t *slot_map,
  * Arguments (device pointers, caller-owned; out, lse and workspace overlap nothing):
  *   q             [num_tokens, Hq, D] dtype, 16-byte aligned, token t at element
  *                 t * q_token_stride (>= Hq * D, whole 16 bytes)
- *   k_scales, v_scales  finite and >= 0
+ *   k_scales, v_scales  finite and >= 0; up to 2^120, the largest that the append
+ *                 writes.  A key's weight times its V scale is held to 11 bits, or to
+ *                 2^-24 of the row's largest such product, V scales below 2^-100
+ *                 counting as that; the row sum has every key's weight
  *   block_tables  int32 [B, max_blocks].  An entry below a request's length that
  *                 names no block of [0, num_blocks) is not followed: its keys
  *                 count as zeros, and attn_get_device_status then reports

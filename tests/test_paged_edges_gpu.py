@@ -1,0 +1,155 @@
+"""The paged 8-bit KV cache at the ends of what its calls accept, on a GPU.
+Attention is compared with 64 bits, within the kernels' own error bounds and
+with nothing added for a hardware tanh."""
+import numpy as np
+import pytest
+import torch
+
+import paged_reference as ref
+import tiled_online_softmax_02_gb300 as attn
+from paged_reference import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tiled_online_softmax_02_gb300 import build
+    build.build()
+    attn.load_library()
+    torch.cuda.set_device(0)
+
+
+# Rows of a (request, kv head) and the table's width choose the kernel: 2^21 keys of width rule out units of 8 rows.
+KINDS = {
+    "rows4": dict(new=(1, 1), wide=False), "rows8": dict(new=(2, 2), wide=False), "rows16": dict(new=(4, 3), wide=True),
+    "rows256": dict(new=(70, 9), wide=True),
+}
+
+
+def _problem(kind, **kw):
+    """(problem, its tensors): four query heads a kv head, lengths that leave units cut between CTAs and a ragged last block."""
+    w = Problem(new=KINDS[kind]["new"], total=(3001, 420), pad=0, **kw)
+    x = ref.make(w)
+    if KINDS[kind]["wide"]:
+        x["tables"] = torch.cat([x["tables"], torch.full((2, 2 ** 21 // w.block), -3, dtype=torch.int32)], 1)
+    return w, x
+
+
+def _run(w, x):
+    g = {k: v.cuda() for k, v in x.items()}
+    out = torch.full(x["q"].shape, -7.0, dtype=x["q"].dtype, device="cuda")
+    lse = torch.full(x["q"].shape[:2], -7.0, device="cuda")
+    attn.attn_fwd_paged_fp8(g["q"], g["k_cache"], g["v_cache"], g["k_scales"], g["v_scales"], g["tables"], g["starts"],
+                            g["totals"], causal=w.causal, local_window=w.window, scale=w.scale, softcap=w.softcap,
+                            out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert attn.get_device_status() == attn.ATTN_OK
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def _check(w, x, exact=False):
+    """Every row against 64 bits.  With A = sum_j p_j |v_j|, p_j = exp(s_j - max s), l = sum_j p_j, u_j the V scale or
+    2^-100 where that is larger:
+      half a step of the output type on the result;
+      weights of at least 11 bits: A 2^-11; below 2^-13 of the largest p_j u_j, which is what they are carried relative
+      to, an absolute 2^-24 of it: 2^-24 max_j(p_j u_j) sum_j |v8_j| / l;
+      scores off by at most e: 2 e A.  e has fp32's sums over the row, scale 2^-16 sum_d |q_d k_d|, Q's pieces, whose rest
+      is at most 2^-17 of the row's largest element, scale 2^-17 max|q| sum_d |k_d|, and the score and log2 of the V
+      scale as one fp32 number of up to 2^8, rounded three times: 2^-15.  Where `exact`, q and the key bytes are small
+      whole numbers, so that pieces and sums are exact: 2^-21 |s| for the two scales in place of those two;
+      a soft-cap c: 1 - 2 / (e^2y + 1) has ex2's 2^-22 and the reciprocal's 2^-23, each at most doubled, so 2^-20 c; the
+      cap's derivative is at most 1, so e of the score itself does not grow.  A cap of more than 512 adds 2^-17 of the
+      score instead: a series takes over below 1/8 of the cap, where the difference cancels.
+    lse: e, and fp32's rounding of the result."""
+    out, lse = _run(w, x)
+    q = x["q"].double().numpy()
+    starts, totals, tables = x["starts"].numpy(), x["totals"].numpy(), x["tables"].numpy()
+    kc, vc = ref.E4M3[x["k_cache"].numpy()], ref.E4M3[x["v_cache"].numpy()]
+    ks, vs = x["k_scales"].double().numpy(), x["v_scales"].double().numpy()
+    T, Hq, D = q.shape
+    Hkv, bs = kc.shape[1:3]
+    scale = w.scale if w.scale is not None else D ** -0.5
+    half = ref.HALF_STEP[w.dtype]
+    for b, L in enumerate(totals):
+        n = int(starts[b + 1] - starts[b])
+        blk = tables[b, np.arange(L) // bs]
+        k, v8, u = (kc[blk, :, np.arange(L) % bs] * ks[blk][..., None], vc[blk, :, np.arange(L) % bs], vs[blk])
+        for t in range(starts[b], starts[b] + n):
+            hi = int(L) - n + t - int(starts[b]) + 1
+            for h in range(Hq):
+                g = h * Hkv // Hq
+                kk, vv8, uu = k[:hi, g], v8[:hi, g], u[:hi, g]
+                vv = vv8 * uu[:, None]
+                s = scale * (kk @ q[t, h])
+                e = 2.0 ** -15 + (2.0 ** -21 * np.abs(s).max() if exact else
+                                  abs(scale) * (2.0 ** -16 * (np.abs(kk) @ np.abs(q[t, h])).max()
+                                                + 2.0 ** -17 * np.abs(q[t, h]).max() * np.abs(kk).sum(1).max()))
+                if w.softcap > 0:
+                    s = w.softcap * np.tanh(s / w.softcap)
+                    e += 2.0 ** -20 * w.softcap if w.softcap <= 512 else 2.0 ** -17 * np.abs(s).max()
+                m = s.max()
+                p = np.exp(s - m)
+                l = p.sum()
+                want, want_lse = p @ vv / l, m + np.log(l)
+                tol = (half * np.abs(want) + (2.0 ** -11 + 2 * e) * (p @ np.abs(vv)) / l
+                       + 2.0 ** -24 * (p * np.maximum(uu, 2.0 ** -100)).max() * np.abs(vv8).sum(0) / l)
+                err = np.abs(out[t, h] - want)
+                assert (err <= tol).all(), f"row {t} head {h}: worst {np.nanmax(err / np.maximum(tol, 1e-300)):.3g} tolerances"
+                assert abs(lse[t, h] - want_lse) <= e + 2.0 ** -21 * (1 + abs(want_lse) + abs(m)), \
+                    f"lse of row {t} head {h}: {lse[t, h]} instead of {want_lse}"
+
+
+# ---------------------------------------------------------------- V scales
+def _set_v(w, x, name):
+    """Scales in the order of each request's blocks, and zero bytes where the block is one of zeros."""
+    tables, scales, cache = x["tables"].numpy(), x["v_scales"].numpy(), x["v_cache"].numpy()
+    for b, total in enumerate(w.total):
+        n = -(-total // w.block)
+        for i, blk in enumerate(tables[b, :n]):
+            zero = False
+            if name == "zeros_next_to_huge":  # a block of zeros as the append writes it
+                zero, s = i % 3 == 1, 2.0 ** 40
+            elif name == "zeros_first":
+                zero, s = i < 2, 2.0 ** 36
+            elif name == "all_zeros":
+                zero, s = True, 0.0
+            elif name == "no_scale":
+                s = 0.0
+            elif name == "some_no_scale":
+                s = 0.0 if i % 2 else 1.0
+            elif name == "tiny":
+                s = 1e-35 * (1 + i / n)
+            elif name == "huge":
+                s = 2.0 ** 105
+            elif name == "rising":
+                s = 2.0 ** (-100 + 190 * i // n)
+            else:  # falling
+                s = 2.0 ** (90 - 190 * i // n)
+            if zero:
+                s = 2.0 ** -100
+                cache[blk][(cache[blk] & 127) != 127] = 0  # slots of no token stay NaN
+            scales[blk] = s
+
+
+V_SCALES = ["zeros_next_to_huge", "zeros_first", "all_zeros", "no_scale", "some_no_scale", "tiny", "huge", "rising",
+            "falling"]
+
+
+@pytest.mark.parametrize("name", V_SCALES)
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_v_scales_of_any_size(kind, name):
+    """Blocks whose V is 2^100 times smaller or larger than their neighbours' weigh by their scores alone."""
+    w, x = _problem(kind, Hq=4, Hkv=1) if kind != "rows8" else _problem(kind, Hq=8, Hkv=2, D=64, block=32)
+    _set_v(w, x, name)
+    _check(w, x)
+
+
+@pytest.mark.parametrize("name", ["all_zeros", "no_scale"])
+@pytest.mark.parametrize("kind", ["rows4", "rows256"])
+def test_no_values_for_half_queries(kind, name):
+    w, x = _problem(kind, Hq=4, Hkv=1, dtype="f16", D=64)
+    _set_v(w, x, name)
+    _check(w, x)

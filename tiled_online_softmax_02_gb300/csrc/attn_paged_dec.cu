@@ -18,7 +18,8 @@
 // Scales: a key's K scale multiplies its scores (the thread that owns the key
 // holds it).  Its V scale enters the exponent, t = s log2 e + log2 v_scale,
 // so O accumulates 2^(t - m) v8 whatever the scales are, m being the running
-// maximum of t, and the row sum takes 2^(t - m) / v_scale.
+// maximum of t, and the row sum takes 2^(t - m) / v_scale (paged_sched.cuh: in
+// far tiles, without the detour by 2^(t - m)).
 //
 // One CTA walks its share of the line of key tiles (paged_sched.cuh).  Roles
 // (256 threads): warps 0-3 softmax, thread = key; warp 4 K loads, warp 5 V
@@ -212,7 +213,7 @@ struct DecParams {
   CUtensorMap tmap_v;
   PagedParams c;
   float* ws_o;         // [2 * CTAs][NR][D]: partial rows, sum of 2^(t - m) v8
-  float2* ws_ml;       // [2 * CTAs][NR]: m, sum of 2^(t - m) / v_scale
+  float2* ws_ml;       // [2 * CTAs][NR]: m, 2^-8 sum of 2^(t - m) / v_scale
   PagedCut* cuts;      // [CTAs]
   float k1, k2, k3;    // soft-cap in log2 units: k2 / (2^(k1 s) + 1) + k3
   float scale_log2;
@@ -477,7 +478,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       tc_fence_after();
       // the scales of this thread's key lie there once S^T does: K's barrier takes the scale warp's arrival too
       const float4 scl = sm.scales(g % C::kSK)[tid >> 4];
-      const float lv = scl.y, iv = scl.z;
+      const float lv = scl.y;
       // scores in log2 units plus log2 v_scale, then less the maxima: t - m + 5
       float t[NR];
       {
@@ -538,11 +539,15 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           for (int i = 0; i < 2; ++i) {
             const float top = fmaxf(fmaxf(red[r + i], red[NR + r + i]), fmaxf(red[2 * NR + r + i], red[3 * NR + r + i])) - kPLog2;
             const float mn = top > old[i] + kRise ? top : old[i];
-            alpha[r + i] = fast_exp2(old[i] - mn);
+            alpha[r + i] = fast_exp2(0.5f * (old[i] - mn));
             old[i] = mn;
           }
           m2[r / 2] = f2(old[0], old[1]);
-          l2[r / 2] = fmul2(l2[r / 2], f2(alpha[r], alpha[r + 1]));
+          // in two steps: the sum of earlier keys may be as large as the factor is small, where V scales differ
+          const uint64_t half = f2(alpha[r], alpha[r + 1]);
+          l2[r / 2] = fmul2(fmul2(l2[r / 2], half), half);
+          alpha[r] *= alpha[r];
+          alpha[r + 1] *= alpha[r + 1];
         }
         if (n > 0) {  // O^T holds the unit's earlier tiles once their P V is done
           wait(sm.pv_done((g - 1) & 1), ((g - 1) >> 1) & 1);
@@ -565,6 +570,18 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
       uint32_t words[C::kNP / 4];
 #pragma unroll
       for (int i = 0; i < C::kNP / 4; ++i) words[i] = 0u;
+      const float iv = scl.z;
+      if (__builtin_expect(iv == 0.0f, 0)) {  // a far tile
+        const float rest = scl.w - lv;  // not 0 for scales below 2^-100 only
+#pragma unroll
+        for (int r = 0; r < NR; r += 2) {
+          float a, b;
+          f2_split(fsub2(f2(t[r], t[r + 1]), m2[r / 2]), a, b);
+          l2[r / 2] = ffma2(f2(fast_exp2(a - lv), fast_exp2(b - lv)), f2(kPagedSumFactor, kPagedSumFactor), l2[r / 2]);
+          t[r] += rest;
+          t[r + 1] += rest;
+        }
+      }
       const uint64_t iv2 = f2(iv, iv);
 #pragma unroll
       for (int r = 0; r < NR; r += 4) {
@@ -632,10 +649,10 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
         const int xr = u.row0 + r;
         const int tok = paged_token(p, xr);
         const int64_t row = (int64_t)(u.q.s0 + tok) * p.Hq + u.kvh * p.group + xr - tok * p.group;
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const float inv = L == 0.0f ? 0.0f : kPagedSumFactor * (1.0f / L);
         if (tid < D) static_cast<uint16_t*>(p.out)[row * D + tid] = to_bits<BF16>(o[r] * inv);
         if (p.lse != nullptr && tid == r)
-          p.lse[row] = L == 0.0f ? -INFINITY : (m[r] + __log2f(L)) * kLn2;
+          p.lse[row] = L == 0.0f ? -INFINITY : (m[r] + (__log2f(L) + kPagedSumLog2)) * kLn2;
       } else {
         if (tid < D) P.ws_o[((int64_t)slot * NR + r) * D + tid] = o[r];
         if (tid == r) P.ws_ml[slot * NR + r] = make_float2(m[r], L);

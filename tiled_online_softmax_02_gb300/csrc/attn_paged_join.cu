@@ -1,8 +1,10 @@
 // attn_paged_join.cu -- joins the partial rows of units that the borders
 // between CTAs cut (paged_sched.cuh).  Part k of a row holds O_k = sum of
-// 2^(t - m_k) v8, its maximum m_k and L_k = sum of 2^(t - m_k) / v_scale; with
+// 2^(t - m_k) v8, its maximum m_k and L_k = 2^-8 sum of 2^(t - m_k) / v_scale; with
 // M = max m_k the row is
-//   sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) L_k   (0 when the latter is 0).
+//   sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) 2^8 L_k   (0 when the latter is 0).
+// L_k takes its factor as two halves: it may be as large as the factor is small,
+// where the parts' V scales differ.
 // Bound: latency; the partial rows lie in L2.  Lanes go over d, and a warp has
 // several parts of a row, or several rows, in flight.
 // Measured under the profiler (caches flushed): 8 us for 2 MB of partial rows,
@@ -39,7 +41,7 @@ template <int D, bool BF16>
 __device__ __forceinline__ void store_row(const PagedCut& cut, int r, int Hq, int group, float ml_log2, uint16_t* out,
                                           float* lse, int lane, const float (&acc)[D / 32], float M, float L) {
   constexpr int V = D / 32;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const float inv = L == 0.0f ? 0.0f : kPagedSumFactor * (1.0f / L);
   const int x = cut.row0 + r;
   const int64_t row = (int64_t)(cut.token0 + x / group) * Hq + cut.head0 + x % group;
   uint32_t packed[V / 2];
@@ -100,9 +102,10 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_kernel(const Page
         const float m0 = __shfl_sync(0xffffffffu, ml.x, 2 * i), m1 = __shfl_sync(0xffffffffu, ml.x, 2 * i + 1);
         const float l0 = __shfl_sync(0xffffffffu, ml.y, 2 * i), l1 = __shfl_sync(0xffffffffu, ml.y, 2 * i + 1);
         const float Mn = fmaxf(fmaxf(M[i], m0), m1);  // finite: part k0 is there
-        const float keep = exp2f(M[i] - Mn), w0 = exp2f(m0 - Mn), w1 = exp2f(m1 - Mn);
+        const float hk = exp2f(0.5f * (M[i] - Mn)), h0 = exp2f(0.5f * (m0 - Mn)), h1 = exp2f(0.5f * (m1 - Mn));
+        const float keep = hk * hk, w0 = h0 * h0, w1 = h1 * h1;
         M[i] = Mn;
-        L[i] = fmaf(w1, l1, fmaf(w0, l0, L[i] * keep));
+        L[i] = fmaf(h1, l1 * h1, fmaf(h0, l0 * h0, L[i] * hk * hk));
         const bool two = k0 + 1 < cut.parts;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -149,15 +152,15 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_rows_kernel(const
       }
     }
     const float Mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-    const float keep = exp2f(M - Mn);  // Mn is finite: part k0 is there
-    L *= keep;
+    const float hk = exp2f(0.5f * (M - Mn)), keep = hk * hk;  // Mn is finite: part k0 is there
+    L = L * hk * hk;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= keep;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (k0 + i * kWarps >= cut.parts) continue;
-      const float w = exp2f(ml[i].x - Mn);
-      L = fmaf(w, ml[i].y, L);
+      const float hw = exp2f(0.5f * (ml[i].x - Mn)), w = hw * hw;
+      L = fmaf(hw, ml[i].y * hw, L);
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[i].x[v], acc[v]);
     }
@@ -176,8 +179,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_join_rows_kernel(const
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
 #pragma unroll
   for (int k = 0; k < kWarps; ++k) {
-    const float w = exp2f(sum_ml[k].x - Ma);
-    L = fmaf(w, sum_ml[k].y, L);
+    const float hw = exp2f(0.5f * (sum_ml[k].x - Ma)), w = hw * hw;
+    L = fmaf(hw, sum_ml[k].y * hw, L);
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = fmaf(w, sum_o[k][lane * V + v], acc[v]);
   }

@@ -22,7 +22,8 @@
 // Scales are constant over 16 keys or more (the smallest block).  Per group of
 // 16 keys: the largest raw score is found first and scaled once, and
 // 2^(s k_scale + log2 v_scale - m) is one FMA and one ex2 a value; the row sum
-// takes each group's sum times 1 / v_scale.
+// takes each group's sum times 1 / v_scale (paged_sched.cuh: in far tiles,
+// the sum of 2^(s k_scale - m) itself, in a pass of its own).
 //
 // One CTA an SM walks its share of the line of key tiles (paged_sched.cuh).
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two lanes, thread =
@@ -74,7 +75,7 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + 2 * kQLane;
   static constexpr int kOffV8 = kOffK + kSK * kTile8;
   static constexpr int kOffV = kOffV8 + kSV8 * kTile8;
-  static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kSK][kScaleGroups]: k scale, log2 v scale, 1 / v scale
+  static constexpr int kOffSc = kOffV + kSV * kTile16;  // float4 [kSK][kScaleGroups]: as the scale warp leaves them
   static constexpr int kOffQe = kOffSc + kSK * kScaleGroups * 16;  // uint32 [256]: the Q rows' scales, as f32 (bf16 Q) or two f16 factors
   static constexpr int kOffBar = kOffQe + kRows * 4;
   // k_full, k_empty [kSK], v8_full, v8_empty [kSV8], v_full, v_empty [kSV], sc_empty [kSK],
@@ -514,7 +515,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         ++oc;
         tc_fence_after();
       }
-      const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+      const float inv = l_run == 0.0f ? 0.0f : kPagedSumFactor * (1.0f / l_run);
       const int64_t ws_row = (int64_t)(2 * blockIdx.x + (head ? 1 : 0)) * kRows + t * BM + row;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
@@ -542,7 +543,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         }
       }
       if (mine && whole && p.lse != nullptr)
-        p.lse[out_row] = l_run == 0.0f ? -INFINITY : (m_run + (__log2f(l_run) - kPLog2)) * kLn2;
+        p.lse[out_row] = l_run == 0.0f ? -INFINITY : (m_run + (__log2f(l_run) + (kPagedSumLog2 - kPLog2))) * kLn2;
       if (mine && !whole) P.ws_ml[ws_row] = make_float2(m_run, l_run);
       tc_fence_before();  // these reads before this lane's next P arrival, which the next P V waits for
     }
@@ -566,11 +567,12 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
     l_run = 0.0f;
     for (int n = 0; n < nt; ++n, ++g, ++sc) {
       const int key0 = (t0 + n) * BN;
-      // a group's (k scale |scale| log2 e, log2 v scale, 1 / v scale); raw scores times the row's
+      // a group's k scale |scale| log2 e and what follows of its V scale; raw scores times the row's
       // factor and the first are in log2 units.  The product stays above 0, so that -inf stays -inf
       // (they lie there once S does: K's barrier, which S waited for, takes the scale warp's arrival too)
       const float4* scl = sm.scales(g % C::kSK);
       if (!wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
+      const bool far_tile = scl[0].z == 0.0f;
       tc_fence_after();
       if (key0 < full_lo || key0 + BN > full_hi) {  // some key is hidden from some row: -inf over its score
         const int lo = min(max(lim.x - key0, 0), BN), span = max(min(max(lim.y - key0, 0), BN) - lo, 0);
@@ -585,6 +587,12 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         }
         tmem_wait_st();
       }
+      // tanh(scale s / c) of a raw score, c log2 e being the factor.  The hardware tanh: its error, 2^-11 of c, is
+      // below what a 16-bit output holds of scores that c caps
+      auto capped = [&](float x, float k) {
+        if constexpr (SOFTCAP) return x == -INFINITY ? x : fast_tanh(x * (k * qs * P.sc_in));
+        return x;
+      };
       auto factor = [&](float k) { return SOFTCAP ? P.sc_out : fmaxf(k * qs, 1.2e-38f); };
       // The row's largest score, 32 keys at a time: the loops stay rolled and S is read a second
       // time below, which costs less than the instruction fetches of code four times the size
@@ -604,15 +612,15 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
             b = fmax3(b, x[16 * h + k + 2], x[16 * h + k + 3]);
           }
           a = fmaxf(a, b);
-          if constexpr (SOFTCAP) a = a == -INFINITY ? a : fast_tanh(a * (kl.x * qs * P.sc_in));
-          m_tile = fmaxf(m_tile, fmaf(a, factor(kl.x), kl.y));
+          m_tile = fmaxf(m_tile, fmaf(capped(a, kl.x), factor(kl.x), kl.y));
         }
       }
       const bool rise = m_tile > m_run + kRise;
       const float m_new = rise ? m_tile : m_run;
-      const float alpha = fast_exp2(m_run - m_new);  // 1 where the maximum stays
-      m_run = m_new;
       if (n > 0 && __any_sync(0xffffffffu, rise)) {  // O holds every earlier tile
+        // the sum takes the factor in two steps: it may be as large as that is small, where V scales differ
+        const float half = fast_exp2(0.5f * (m_run - m_new)), alpha = half * half;
+        l_run = l_run * half * half;
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
@@ -623,37 +631,39 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
           tmem_st32(o_addr + k * 32, o);
         }
       }
+      m_run = m_new;
       const float off = kPLog2 - m_run;
       uint64_t sum = 0ull;
+      if (__builtin_expect(far_tile, 0)) {  // a far tile
+        float own = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 4) {
+          float x[4];
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(s_addr + c) : "memory");
+          tmem_wait_ld();
+          const float kx = scl[c >> 4].x, kf = factor(kx);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) own += fast_exp2(fmaf(capped(x[k], kx), kf, off));
+        }
+        sum = f2(own * kPagedSumFactor, 0.0f);
+      }
 #pragma unroll kExpUnroll
       for (int ch = 0; ch < 4; ++ch) {
         float x[32];
         tmem_ld32(s_addr + ch * 32, reinterpret_cast<uint32_t(&)[32]>(x));
         tmem_wait_ld();
-        if constexpr (SOFTCAP) {
-          // tanh(scale s / c) as the raw value, c log2 e the factor.  The hardware tanh: its error, 2^-11 of c, is
-          // below what a 16-bit output holds of scores that c caps
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float in = scl[2 * ch + h].x * qs * P.sc_in;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float raw = x[16 * h + k];
-              x[16 * h + k] = raw == -INFINITY ? raw : fast_tanh(raw * in);
-            }
-          }
-        }
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float4 s4 = scl[2 * ch + h];
           const float kf = factor(s4.x);
-          const uint64_t mul = f2(kf, kf), add = f2(s4.y + off, s4.y + off);
+          const uint64_t mul = f2(kf, kf), add = f2(s4.w + off, s4.w + off);
           uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float a, b;
-            f2_split(ffma2(f2(x[16 * h + 2 * k], x[16 * h + 2 * k + 1]), mul, add), a, b);
+            f2_split(ffma2(f2(capped(x[16 * h + 2 * k], s4.x), capped(x[16 * h + 2 * k + 1], s4.x)), mul, add), a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
             part[k & 1] = fadd2(part[k & 1], f2(a, b));
@@ -672,7 +682,7 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
       }
       float sa, sb;
       f2_split(sum, sa, sb);
-      l_run = fmaf(l_run, alpha, sa + sb);
+      l_run += sa + sb;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -284,10 +284,10 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   L.cuts = reinterpret_cast<PagedCut*>(static_cast<char*>(workspace) + plan.cuts_at);
   cudaError_t e;
   if (plan.rows == kPagedTcRows) {
-    L.ml_log2 = kPagedTcLog2;
+    L.ml_log2 = kPagedTcLog2 - kPagedSumLog2;
     e = launch_attn_paged_tc(L, bf16, st);
   } else {
-    L.ml_log2 = 0.0f;  // its maxima already hold the factor
+    L.ml_log2 = -kPagedSumLog2;  // its maxima already hold P's factor
     e = launch_attn_paged_dec(L, bf16, st);
   }
   if (e == cudaSuccess && max_tiles > 1) e = launch_attn_paged_join(L, bf16, st);

@@ -97,6 +97,8 @@ constexpr int kPagedDecCtas = 2;     // CTAs of the few-rows kernel on an SM
 constexpr int kPagedTcRows = 256;
 constexpr float kPagedDecLog2 = 5.0f;  // log2 of the factor that P carries, in each of the kernels
 constexpr float kPagedTcLog2 = 7.0f;
+// Row sums are carried as 2^-8 of themselves: 2^31 keys of scale 2^-100 stay below fp32's range, keys of scale 2^105 above it.
+constexpr float kPagedSumLog2 = 8.0f, kPagedSumFactor = 0x1p-8f;
 
 struct PagedLaunch {
   PagedParams c;
@@ -104,9 +106,9 @@ struct PagedLaunch {
   int rows;                    // query rows of a unit
   int grid;
   float* ws_o;                 // [2 * grid][rows][D]: partial rows, sum of 2^(t - m) v8
-  float2* ws_ml;               // [2 * grid][rows]: m, sum of 2^(t - m) / v_scale
+  float2* ws_ml;               // [2 * grid][rows]: m, 2^-8 sum of 2^(t - m) / v_scale
   PagedCut* cuts;              // [grid]
-  float ml_log2;               // the kernel's 2^(t - m) carries this factor (log2)
+  float ml_log2;               // the kernel's sums carry this factor (log2)
 };
 
 cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t stream);  // rows 4, 8 or 16

@@ -276,9 +276,20 @@ __device__ __forceinline__ int paged_parts(const PagedWalk<NR>& w, const PagedSh
 
 // The scales of a unit's tiles, from block tables and scale arrays into a ring
 // in shared memory, by one warp: lane i < 8 has keys 16 i .. of a tile (a block
-// holds 16 or more).  An entry is (k scale * mul, log2 v scale, 1 / v scale).
+// holds 16 or more).  With u = log2 of the V scale, of 2^-100 where that is
+// larger, a key's weight is 2^(t - m), t = s log2 e + u, and what it adds to the
+// row sum is 2^(t - m) / v_scale.  That holds while 2^(t - m) does not fall below
+// fp32's range although 2^(s log2 e) is among the row's largest: while u lies
+// at most 90 below the largest one of the unit's tiles so far, m being at most
+// that much above t.  Where a tile has a key for which it does not (a block of
+// zeros, say, whose scale is 2^-100), or whose scale has no inverse in fp32's
+// range, the tile is "far": its keys add 2^(s log2 e - m)
+// itself to the sum, and that times the scale is their weight.  It is told by
+// borders, not by the largest scale itself, as all tiles pay for that: scales of
+// 2^-80 to 2^10, or once there has been one above, of 2^10 to 2^100, are near.
+// An entry is (k scale * mul, u, 2^-8 / v scale, u), of far tiles (.., u, 0, log2 v scale).
 constexpr int kScaleGroups = kPagedKeys / 16;
-constexpr float kMinVScale = 7.9e-31f;  // 2^-100: a block of zeros may have scale 0
+constexpr float kMinVLog2 = -100.0f, kNearMin = 0x1p-80f, kNearMax = 0x1p10f, kBigMax = 0x1p100f;
 
 template <int kStages>
 struct ScaleFeed {
@@ -294,6 +305,7 @@ struct ScaleFeed {
       return b >= 0 && b < p.num_blocks ? b : -1;
     };
     float ks, vs;
+    bool big = false;  // a scale above kNearMax so far
     auto fetch = [&](int b) {  // a block that is none has key scale 0
       ks = 0.0f;
       vs = 1.0f;
@@ -306,15 +318,22 @@ struct ScaleFeed {
     int next = block_of(1);
     fetch(first);
     for (int n = 0; n < w.nt; ++n, ++g) {  // scales a tile ahead, blocks two
-      const float k0 = ks, v0 = fmaxf(vs, kMinVScale);
+      const float k0 = ks, v0 = vs;
       fetch(next);
       next = block_of(n + 2);
       const int st = g % kStages;
       if (g >= kStages &&
           !wait_warp(empty0 + st * 8, ((g / kStages) - 1) & 1, p.timeout_ns, p.status))
         return false;
-      if (lane < kScaleGroups)
-        ring[st * kScaleGroups + lane] = make_float4(k0 * mul, __log2f(v0), 1.0f / v0, 0.0f);
+      bool far = false;
+      if (__any_sync(0xffffffffu, big || v0 < kNearMin || v0 > kNearMax)) {
+        big = __any_sync(0xffffffffu, big || v0 > kNearMax);
+        far = __any_sync(0xffffffffu, lane < kScaleGroups && (v0 < (big ? kNearMax : kNearMin) || v0 > kBigMax));
+      }
+      if (lane < kScaleGroups) {
+        const float u = __log2f(v0);
+        ring[st * kScaleGroups + lane] = make_float4(k0 * mul, fmaxf(u, kMinVLog2), far ? 0.0f : kPagedSumFactor * (1.0f / v0), u);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(full0 + st * 8);
     }
