@@ -426,6 +426,7 @@ int attn_cache_append_fp8(const void *k, const void *v, const int64_t *slot_map,
  *   key j is visible iff 0 <= j < min(total_lengths[b], max_blocks * block_size),
  *     j > pos - local_window when local_window > 0, and (causal == 0 or j <= pos)
  *   s_j = scale * <q[t,h,:], k_j>, then softcap * tanh(s_j / softcap) when softcap > 0
+ *     (to 2^-16 of the capped score)
  *   out[t,h,:] = sum_j softmax(s)_j v_j, or 0 when no key is visible
  *   lse[t,h]   = log sum_j exp(s_j), natural log, -inf when no key is visible
  * k_j, v_j: the cache's e4m3 bytes times their block's scale.

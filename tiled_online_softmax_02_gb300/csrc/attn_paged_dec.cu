@@ -34,6 +34,7 @@
 // 80 KB (64 KB at D = 64), keep about 24 MB on their way; a warp's
 // instructions, not registers or shared memory, are what these roles run out
 // of, so loops stay rolled where they can.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -215,7 +216,7 @@ struct DecParams {
   float* ws_o;         // [2 * CTAs][NR][D]: partial rows, sum of 2^(t - m) v8
   float2* ws_ml;       // [2 * CTAs][NR]: m, 2^-8 sum of 2^(t - m) / v_scale
   PagedCut* cuts;      // [CTAs]
-  float k1, k2, k3;    // soft-cap in log2 units: k2 / (2^(k1 s) + 1) + k3
+  float k1, k2, k3;    // soft-cap in log2 units: k2 / (2^(k1 s) + 1) + k3; k3 tanh(k1 s) where k2 is 0
   float scale_log2;
 };
 
@@ -433,7 +434,7 @@ __device__ __forceinline__ void mma_role(const DecParams& P, const Lay<D, NR, BF
 // ------------------------------------------------------------------ softmax
 // Thread tid of warps 0-3 owns key tid of every tile (lane tid of S^T) and, at
 // a unit's end, d = tid of O^T.
-template <int D, int NR, bool BF16>
+template <int D, int NR, bool BF16, bool SOFTCAP>
 __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR, BF16>& sm, PagedWalk<NR> w,
                                              uint32_t tmem, int warp, int lane) {
   using C = Cfg<D, NR, BF16>;
@@ -489,7 +490,8 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
         if constexpr (C::kQP > 2) tld(a + 2 * NR, x2);
         tmem_wait_ld();
         const uint64_t step = f2(kInvStep, kInvStep);
-        const float km = (p.softcap > 0.0f ? P.k1 : P.scale_log2) * scl.x;
+        float km = P.scale_log2 * scl.x;
+        if constexpr (SOFTCAP) km = fminf(fmaxf(P.k1 * scl.x, -3e38f), 3e38f);  // times a score of 0 is 0
         const uint64_t km2 = f2(km, km), lv2 = f2(lv, lv);
 #pragma unroll
         for (int r = 0; r < NR; r += 2) {
@@ -497,11 +499,16 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
           if constexpr (C::kQP > 2) s = ffma2(f2(x2[r], x2[r + 1]), step, s);
           s = ffma2(s, step, f2(t[r], t[r + 1]));
           s = fmul2(s, qs2[r / 2]);
-          if (p.softcap > 0.0f) {
+          if constexpr (SOFTCAP) {
             float a0, a1;
             f2_split(fmul2(s, km2), a0, a1);
-            t[r] = fmaf(P.k2, fast_rcp(fast_exp2(a0) + 1.0f), P.k3 + lv);
-            t[r + 1] = fmaf(P.k2, fast_rcp(fast_exp2(a1) + 1.0f), P.k3 + lv);
+            if (P.k2 != 0.0f) {
+              t[r] = fmaf(P.k2, fast_rcp(fast_exp2(a0) + 1.0f), P.k3 + lv);
+              t[r + 1] = fmaf(P.k2, fast_rcp(fast_exp2(a1) + 1.0f), P.k3 + lv);
+            } else {
+              t[r] = fmaf(P.k3, fast_tanh(a0), lv);
+              t[r + 1] = fmaf(P.k3, fast_tanh(a1), lv);
+            }
           } else {
             f2_split(ffma2(s, km2, lv2), t[r], t[r + 1]);
           }
@@ -673,7 +680,7 @@ __device__ __forceinline__ void softmax_role(const DecParams& P, const Lay<D, NR
   }
 }
 
-template <int D, int NR, bool BF16>
+template <int D, int NR, bool BF16, bool SOFTCAP>
 __global__ void __launch_bounds__(kThreads, kPagedDecCtas)
     attn_paged_dec_kernel(const __grid_constant__ DecParams P) {
   using C = Cfg<D, NR, BF16>;
@@ -724,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, kPagedDecCtas)
   PagedWalk<NR> w;
   w.begin(p, sm.share());
   if (warp < 4) {
-    softmax_role<D, NR, BF16>(P, sm, w, tmem, warp, lane);
+    softmax_role<D, NR, BF16, SOFTCAP>(P, sm, w, tmem, warp, lane);
   } else if (warp == kKWarp) {
     load_role<D, NR, C::kSK>(P, &P.tmap_k, w, sm.k_tile(0), sm.k_full(0), sm.k_empty(0), lane, true);
   } else if (warp == kVWarp) {
@@ -743,9 +750,9 @@ __global__ void __launch_bounds__(kThreads, kPagedDecCtas)
 }
 
 
-template <int D, int NR, bool BF16>
+template <int D, int NR, bool BF16, bool SOFTCAP>
 cudaError_t launch_dec(const DecParams& P, int grid, cudaStream_t stream) {
-  auto kernel = attn_paged_dec_kernel<D, NR, BF16>;
+  auto kernel = attn_paged_dec_kernel<D, NR, BF16, SOFTCAP>;
   constexpr int smem = Cfg<D, NR, BF16>::kSmem;
   static std::atomic<bool> ready[128];
   int dev = 0;
@@ -761,11 +768,16 @@ cudaError_t launch_dec(const DecParams& P, int grid, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D, int NR>
+cudaError_t launch_dec_d(const DecParams& P, bool bf16, int grid, cudaStream_t stream) {
+  if (P.c.softcap > 0.0f)
+    return bf16 ? launch_dec<D, NR, true, true>(P, grid, stream) : launch_dec<D, NR, false, true>(P, grid, stream);
+  return bf16 ? launch_dec<D, NR, true, false>(P, grid, stream) : launch_dec<D, NR, false, false>(P, grid, stream);
+}
+
 template <int NR>
 cudaError_t launch_dec_nr(const DecParams& P, bool bf16, int grid, cudaStream_t stream) {
-  if (P.c.D == 128)
-    return bf16 ? launch_dec<128, NR, true>(P, grid, stream) : launch_dec<128, NR, false>(P, grid, stream);
-  return bf16 ? launch_dec<64, NR, true>(P, grid, stream) : launch_dec<64, NR, false>(P, grid, stream);
+  return P.c.D == 128 ? launch_dec_d<128, NR>(P, bf16, grid, stream) : launch_dec_d<64, NR>(P, bf16, grid, stream);
 }
 
 }  // namespace
@@ -781,8 +793,11 @@ cudaError_t launch_attn_paged_dec(const PagedLaunch& L, bool bf16, cudaStream_t 
   const double l2e = 1.4426950408889634;
   P.scale_log2 = (float)((double)L.c.scale * l2e);
   if (L.c.softcap > 0.0f) {
-    P.k1 = (float)(2.0 * l2e * (double)L.c.scale / (double)L.c.softcap);
-    P.k2 = (float)(-2.0 * (double)L.c.softcap * l2e);
+    // The quotient's error is 2^-21 of the cap, as it is the difference of two numbers of the cap's size; the hardware
+    // tanh's is 2^-16 of the score.  Caps in use, 20 to 50, are better off with the first, large ones with the second.
+    const bool quotient = L.c.softcap <= 512.0f;
+    P.k1 = (float)std::max(-3e38, std::min(3e38, (quotient ? 2.0 * l2e : 1.0) * (double)L.c.scale / (double)L.c.softcap));
+    P.k2 = quotient ? (float)(-2.0 * (double)L.c.softcap * l2e) : 0.0f;
     P.k3 = (float)((double)L.c.softcap * l2e);
   }
   switch (L.rows) {

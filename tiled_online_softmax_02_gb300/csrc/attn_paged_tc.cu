@@ -43,6 +43,7 @@
 // 700 for the maximum and 1550 for the exponentials.  A unit costs about three
 // tiles more than its tiles: 6000 cycles to bring Q, most of them conversions
 // to e4m3 and back, and 4000 to store the rows.
+#include <algorithm>
 #include <atomic>
 
 #include "paged_mma.cuh"
@@ -587,10 +588,11 @@ __device__ __forceinline__ void softmax_role(const PagedTcParams& P, const Lay<D
         }
         tmem_wait_st();
       }
-      // tanh(scale s / c) of a raw score, c log2 e being the factor.  The hardware tanh: its error, 2^-11 of c, is
-      // below what a 16-bit output holds of scores that c caps
+      // tanh(scale s / c) of a raw score, c log2 e being the factor.  The hardware tanh: measured on the GB300 its error
+      // is at most 1.02e-5 of the value, 2^-16.6 (its specification allows 2^-11): at scores of 50 a weight is off by less
+      // than half a step of f16.  As 1 - 2 / (e^2y + 1), two prompts with a cap take 433 us instead of 353.
       auto capped = [&](float x, float k) {
-        if constexpr (SOFTCAP) return x == -INFINITY ? x : fast_tanh(x * (k * qs * P.sc_in));
+        if constexpr (SOFTCAP) return x == -INFINITY ? x : fast_tanh(x * fminf(k * qs * P.sc_in, 3e38f));
         return x;
       };
       auto factor = [&](float k) { return SOFTCAP ? P.sc_out : fmaxf(k * qs, 1.2e-38f); };
@@ -809,7 +811,7 @@ cudaError_t launch_attn_paged_tc(const PagedLaunch& L, bool bf16, cudaStream_t s
   P.aligned32 = ((reinterpret_cast<uintptr_t>(L.c.out) | reinterpret_cast<uintptr_t>(L.ws_o)) & 31) == 0;
   P.scale_log2 = (float)(fabs((double)L.c.scale) * 1.4426950408889634);
   if (L.c.softcap > 0.0f) {
-    P.sc_in = (float)(0.6931471805599453 / (double)L.c.softcap);
+    P.sc_in = (float)std::min(3e38, 0.6931471805599453 / (double)L.c.softcap);
     P.sc_out = (float)((double)L.c.softcap * 1.4426950408889634);
   }
   if (L.c.D == 128) return bf16 ? launch_tc_d<128, true>(P, L.grid, stream) : launch_tc_d<128, false>(P, L.grid, stream);

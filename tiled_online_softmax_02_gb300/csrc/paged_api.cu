@@ -265,7 +265,8 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   p.causal = causal;
   p.local_window = local_window > 0 ? local_window : 0;
   p.scale = scale;
-  p.softcap = softcap > 0.0f ? softcap : 0.0f;
+  // caps that leave fp32 scores as they are, and caps that leave nothing of them: their factors would pass fp32's range
+  p.softcap = softcap > 0.0f && softcap < 0x1p100f ? std::max(softcap, 0x1p-100f) : 0.0f;
   p.timeout_ns = wait_timeout_ns();
   p.status = status;
   const bool bf16 = dtype == ATTN_BF16;
