@@ -194,3 +194,73 @@ def test_caps_far_below_the_scores(kind, cap):
     x["k_scales"][::3] = 0.0
     x["k_scales"][1::3] = 2.0 ** 30
     _check(w, x, exact=True)
+
+
+# ------------------------------------------------------------------- append
+def _append(slots, N, Hkv=2, D=64, block=16, seed=3):
+    rng = np.random.Generator(np.random.PCG64(seed))
+    T = len(slots)
+    kv = [torch.from_numpy((rng.standard_normal((T, Hkv, D), np.float32)
+                            * np.exp2(rng.integers(-3, 4, (T, 1, 1))).astype(np.float32))).to(torch.bfloat16)
+          for _ in range(2)]
+    caches = [rng.integers(0, 127, (N, Hkv, block, D), dtype=np.uint8) for _ in range(2)]
+    scales = [(2.0 ** rng.integers(-9, 2, (N, Hkv))).astype(np.float32) for _ in range(2)]
+    g = [torch.from_numpy(a).cuda() for a in (*caches, *scales)]
+    attn.attn_cache_append_fp8(kv[0].cuda(), kv[1].cuda(), torch.from_numpy(slots).cuda(), *g)
+    torch.cuda.synchronize()
+    live = np.flatnonzero((slots >= 0) & (slots < N * block))
+    for i in range(2):
+        s = scales[i].astype(np.float64)
+        # the reference walks runs of adjacent tokens: those between them that have no slot stay
+        ref.append(kv[i].double().numpy(), slots, caches[i], s)
+        assert np.array_equal(g[2 + i].double().cpu().numpy(), s)
+        got = g[i].cpu().numpy()
+        assert np.array_equal(np.where(got == 128, 0, got), np.where(caches[i] == 128, 0, caches[i]))
+    assert len(live) > 0
+
+
+@pytest.mark.parametrize("T", [900, 5000, 70001])
+@pytest.mark.parametrize("at", ["first", "last", "spread", "ends"])
+def test_append_over_long_gaps(T, at):
+    """A few tokens of two blocks among many that have no slot: one block's runs lie far apart and are taken in order."""
+    n = 11
+    where = {"first": np.arange(n), "last": T - n + np.arange(n),
+             "spread": np.sort(np.random.default_rng(T).choice(T, n, replace=False)),
+             "ends": np.concatenate([np.arange(5), T - 6 + np.arange(6)])}[at]
+    slots = np.full(T, -1, np.int64)
+    slots[where] = np.concatenate([16 * 3 + 5 + np.arange(6), 16 * 1 + 9 + np.arange(5)])
+    slots[where[3]] = 2 ** 40  # a slot of no block is passed over too
+    _append(slots, 5)
+
+
+def test_append_many_short_runs():
+    """1040 requests, a token or two each: just past the size where a CTA takes more tokens."""
+    rng = np.random.default_rng(2)
+    slots = []
+    for b in rng.permutation(700):
+        off = int(rng.integers(0, 15))
+        slots += [b * 16 + off] + ([b * 16 + off + 1] if rng.random() < 0.5 else [])
+    slots = np.array(slots, np.int64)
+    assert len(slots) > 1024
+    _append(slots, 700)
+
+
+def test_append_does_not_wait_for_padding():
+    """A decode step's 64 tokens in a slot map padded to 65536.  Passing over the tail 32 entries at a time, one load after
+    the other, took 576 us; with 1024 on their way it is 105 us."""
+    T, n, Hkv, D = 65536, 64, 8, 128
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slots[:n] = torch.arange(n, device="cuda") * 64 + 17
+    kv = [torch.randn((T, Hkv, D), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    c = [torch.zeros((n, Hkv, 64, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.ones((n, Hkv), device="cuda") for _ in range(2)]
+    times = []
+    for _ in range(8):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(10):
+            attn.attn_cache_append_fp8(*kv, slots, *c, *s)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 100)
+    assert min(times) < 300.0, times

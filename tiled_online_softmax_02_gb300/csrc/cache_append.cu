@@ -16,12 +16,17 @@
 // runs that begin in its chunk of tokens, for one head of K or of V: short
 // runs (a decode step's) take a warp each, long ones the whole CTA.  The slots
 // that can matter are read once into shared memory, and a thread keeps its
-// first values in registers between finding the maximum and encoding them.
+// first values in registers between finding the maximum and encoding them.  A
+// block whose tokens go on behind that window, past skipped ones, is followed by
+// the whole CTA, 1024 entries of the map at a time.
 //
-// Measured (one GB300, device time): 64 new tokens of 8 kv heads 4.7 us; 16K
-// tokens of 8 kv heads, D = 128, bf16, 24.7 us, 4.1 TB/s (26.9 without the
-// prefetch).  The latter waits for its chain of slots, rows, maximum and stores
-// (leaving out the maximum's or the encoding's arithmetic changes nothing);
+// Measured (one GB300, device time): 64 new tokens of 8 kv heads 5.1 us; 16K
+// tokens of 8 kv heads, D = 128, bf16, 24.8 us, 4.1 TB/s (26.9 without the
+// prefetch; 25.6 with one that does not wait for the slots, and reads the rows of
+// skipped tokens); 64 tokens in a map of 65536 entries 105 us.  The prompts wait
+// for their chain of slots, rows, maximum and stores (leaving out the maximum's or
+// the encoding's arithmetic changes nothing).  Ten CTAs an SM leave 48 registers a
+// thread (80 and six CTAs for f32), of which the long-run path spills 116 bytes (136);
 // 256 threads a CTA (31 us), twice the values in registers (28 us: fewer CTAs
 // fit), several heads a CTA (31 to 48 us), 8 or 12 CTAs an SM instead of 10 (26
 // and 27 us), 32 or 128 tokens a CTA (26 and 29 us) were all slower.
@@ -213,64 +218,117 @@ __device__ __forceinline__ void append_run(const T* x, int64_t stride, uint8_t* 
   if (tid == 0) *scale = s;
 }
 
+// The first token of [from, end) whose slot names a row (back: the last), or -1.  Called by the whole CTA: a thread has
+// eight entries on their way, as a map padded for a captured graph may hold many thousands that name none.
+__device__ __noinline__ int find_slot(const int64_t* map, int64_t num_slots, int from, int end, bool back, uint32_t* red) {
+  constexpr int kDeep = 8;
+  const uint32_t count = (uint32_t)max(end - from, 0);
+  for (uint32_t done = 0; done < count; done += kThreads * kDeep) {
+    int64_t s[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const uint32_t i = done + k * kThreads + threadIdx.x;
+      s[k] = i < count ? __ldg(map + (back ? end - 1 - (int)i : from + (int)i)) : -1;
+    }
+    uint32_t best = 0xffffffffu;
+#pragma unroll
+    for (int k = kDeep - 1; k >= 0; --k)
+      if (s[k] >= 0 && s[k] < num_slots) best = done + k * kThreads + threadIdx.x;
+    if (!__syncthreads_or(best != 0xffffffffu)) continue;
+    best = __reduce_min_sync(0xffffffffu, best);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) best = min(best, red[w]);
+    __syncthreads();
+    return back ? end - 1 - (int)best : from + (int)best;
+  }
+  return -1;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ int64_t window[kWindow];  // slots of tokens first - 1 ..
   __shared__ uint32_t begin[kMaxChunk / 32];  // a bit where a block's tokens begin
   __shared__ uint32_t red[kWarps];
+  __shared__ int unsure, tail;  // a token that may begin a block; where the last block may go on past the window (-1: none)
+  __shared__ int64_t tail_block;
   const int first = blockIdx.x * p.chunk, h = blockIdx.y, which = blockIdx.z;
   const int n = min(p.chunk, p.T - first);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bs = p.block_size, shift = p.block_shift;
   const T* x0 = static_cast<const T*>(which ? p.x[1] : p.x[0]);
   const int64_t stride = which ? p.stride[1] : p.stride[0];
-  // Most rows that this CTA will read are its own tokens': their lines come to L2 while the slots are looked up.
-  if (p.chunk == kMaxChunk) {
-    constexpr int kLines = D * sizeof(T) / 128;
-    for (int i = threadIdx.x; i < n * kLines; i += kThreads) {
-      const T* line = x0 + (int64_t)(first + i / kLines) * stride + h * D + i % kLines * (D / kLines);
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-    }
-  }
+  auto valid = [&](int64_t s) { return s >= 0 && s < p.num_slots; };
+  if (threadIdx.x == 0) unsure = tail = -1;
   const int held = 1 + p.chunk + bs;
+  const int window_end = min(p.T, first + p.chunk + bs);  // the first token past it
   for (int i = threadIdx.x; i < held; i += kThreads) {
     const int t = first + i - 1;
     window[i] = t >= 0 && t < p.T ? __ldg(p.slot_map + t) : -1;
   }
   __syncthreads();
+  // Most rows that this CTA will read are its own tokens': their lines come to L2 while the window is looked at.
+  if (p.chunk == kMaxChunk) {
+    constexpr int kLines = D * sizeof(T) / 128;
+    for (int i = threadIdx.x; i < n * kLines; i += kThreads) {
+      const T* line = x0 + (int64_t)(first + i / kLines) * stride + h * D + i % kLines * (D / kLines);
+      if (valid(window[1 + i / kLines])) asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+    }
+  }
   auto slot_of = [&](int t) -> int64_t {  // -1 past the map
     const int i = t - first + 1;
     return i < held ? window[i] : t < p.T ? __ldg(p.slot_map + t) : -1;
   };
-  auto valid = [&](int64_t s) { return s >= 0 && s < p.num_slots; };
+  bool begins = false;
   for (int i0 = warp * 32; i0 < n; i0 += kThreads) {
     // a token begins its block's tokens unless the nearest token before it
-    // that has a slot is of the same block (that one is almost always the
-    // one before; past skipped tokens the warp looks 32 back at a time)
+    // that has a slot (almost always the one before) is of the same block
     const int i = i0 + lane;
-    const int64_t s = i < n ? window[i + 1] : -1, prev = i < n ? window[i] : -1;
-    int b = valid(s) && !(valid(prev) && prev >> shift == s >> shift);
-    unsigned look = __ballot_sync(0xffffffffu, b && !valid(prev) && first + i > 0);
-    while (look) {
+    const int64_t s = i < n ? window[i + 1] : -1;
+    int64_t prev = i < n ? window[i] : -1;
+    for (unsigned look = __ballot_sync(0xffffffffu, valid(s) && !valid(prev) && first + i > 0); look; look &= look - 1) {
       const int l = __ffs(look) - 1;
-      look &= look - 1;
-      const int64_t mine = window[i0 + l + 1] >> shift;
-      for (int back = first + i0 + l - 1; back >= 0; back -= 32) {
-        const int64_t t = back - lane >= 0 ? __ldg(p.slot_map + back - lane) : -1;
-        const unsigned m = __ballot_sync(0xffffffffu, valid(t));
-        if (m) {
-          if (__shfl_sync(0xffffffffu, t, __ffs(m) - 1) >> shift == mine && lane == l) b = 0;
-          break;
-        }
+      int64_t near = -1;
+      for (int j = i0 + l; j >= 0; j -= 32) {  // 32 of the window's tokens at a time, back from the one before
+        const int64_t y = j >= lane ? window[j - lane] : -1;
+        const unsigned m = __ballot_sync(0xffffffffu, valid(y));
+        if (!m) continue;
+        near = __shfl_sync(0xffffffffu, y, __ffs(m) - 1);
+        break;
       }
+      if (lane == l) prev = near;
     }
+    const bool b = valid(s) && !(valid(prev) && prev >> shift == s >> shift);
+    if (b && !valid(prev) && first > 1) unsure = i;  // only one token has none before it in the window
     const unsigned m = __ballot_sync(0xffffffffu, b);
     if (lane == 0) begin[i0 >> 5] = m;
+    begins |= m != 0u;
   }
-  __syncthreads();
+  if (!__syncthreads_or(begins)) return;
+  const int at = unsure;
+  if (at >= 0) {  // no slot from one token before the chunk to here: the nearest one lies before that
+    const int t = find_slot(p.slot_map, p.num_slots, 0, first - 1, true, red);
+    if (threadIdx.x == 0 && t >= 0 && __ldg(p.slot_map + t) >> shift == window[at + 1] >> shift)
+      begin[at >> 5] &= ~(1u << (at & 31));
+    __syncthreads();
+  }
   uint8_t* cache = which ? p.cache[1] : p.cache[0];
   float* scales = which ? p.scales[1] : p.scales[0];
 
+  // Length of the run from token t with slot s: tokens t + 1 .. whose slots rise by one inside the block, 32 looked at a time.
+  auto run_length = [&](int t, int64_t s, int64_t* next) {
+    const int off = (int)s & (bs - 1);
+    for (int len = 1;;) {
+      const int64_t y = slot_of(t + len + lane);
+      const unsigned m = __ballot_sync(0xffffffffu, off + len + lane < bs && y == s + len + lane);
+      const int more = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+      len += more;
+      if (more == 32) continue;
+      *next = __shfl_sync(0xffffffffu, y, more);
+      return len;
+    }
+  };
   for (int pass = 0; pass < 2; ++pass) {  // blocks with a short first run by warps, then the others by the CTA
     int mine = 0;
     for (int j = 0; j < n; j += 32)
@@ -284,19 +342,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
       bool later = false;
       for (;;) {
         const int off = (int)s & (bs - 1);
-        // length: tokens t + 1 .. whose slots rise by one inside the block, 32 looked at a time
-        int len = 1;
         int64_t next;  // the slot after the run; -1 where it names no row
-        for (;;) {
-          const int64_t y = slot_of(t + len + lane);
-          const unsigned m = __ballot_sync(0xffffffffu, off + len + lane < bs && y == s + len + lane);
-          const int more = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-          len += more;
-          if (more < 32) {
-            next = __shfl_sync(0xffffffffu, y, more);
-            break;
-          }
-        }
+        const int len = run_length(t, s, &next);
         if (!later && (len * (D / 16) <= kWarpPieces) != (pass == 0)) break;
         const T* x = x0 + (int64_t)t * stride + h * D;
         const int64_t tile = blk * p.Hkv + h;
@@ -305,12 +352,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
         else
           append_run<T, D, kThreads>(x, stride, cache + tile * bs * D, scales + tile, off, len, threadIdx.x, red);
         t += len;
-        while (!valid(next) && t < p.T) {  // over skipped tokens
-          const int64_t y = slot_of(t + lane);
+        while (!valid(next) && t < window_end) {  // over skipped tokens
+          const int64_t y = t + lane < window_end ? window[t + lane - first + 1] : -1;
           const unsigned m = __ballot_sync(0xffffffffu, valid(y));
           const int skip = m ? __ffs(m) - 1 : 32;
           t += skip;
           if (m) next = __shfl_sync(0xffffffffu, y, skip);
+        }
+        if (!valid(next) && t < p.T && lane == 0) {  // it may go on behind the window (as no other block here can)
+          tail = t;
+          tail_block = blk;
         }
         if (!valid(next) || next >> shift != blk) break;
         s = next;
@@ -318,6 +369,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
         if (pass == 0) __syncwarp(); else __syncthreads();  // the block's rows and scale are written
       }
     }
+  }
+
+  // the last block's runs behind the window, past any number of skipped tokens
+  if (window_end == p.T || valid(window[held - 1])) return;
+  __syncthreads();
+  const int64_t blk = tail_block;
+  for (int t = tail; t >= 0;) {
+    t = find_slot(p.slot_map, p.num_slots, t, p.T, false, red);
+    if (t < 0) break;
+    const int64_t s = __ldg(p.slot_map + t);
+    if (s >> shift != blk) break;
+    int64_t next;
+    const int len = run_length(t, s, &next);
+    const int64_t tile = blk * p.Hkv + h;
+    append_run<T, D, kThreads>(x0 + (int64_t)t * stride + h * D, stride, cache + tile * bs * D, scales + tile,
+                               (int)s & (bs - 1), len, threadIdx.x, red);
+    t += len;
+    __syncthreads();  // the block's rows and scale are written
   }
 }
 
