@@ -365,7 +365,8 @@ int attn_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, const 
  * a request whose length shrank keeps its blocks.
  * result receives 0, or why the step cannot be done: 1 too few free blocks,
  * 2 a request needs more than max_blocks entries, 3 more new tokens than
- * num_tokens, 4 a negative length, 5 free_count or a table entry out of range.
+ * num_tokens, 4 a negative length (a finished row's past length among them),
+ * 5 free_count, a table entry or a free-list entry to be taken out of range.
  * Then the tables, the free stack and its count are left as they were,
  * q_starts is all 0, total_lengths = past_lengths and every slot is -1: the
  * step's append and attention do nothing.

@@ -264,3 +264,100 @@ def test_append_does_not_wait_for_padding():
         torch.cuda.synchronize()
         times.append(a.elapsed_time(b) * 100)
     assert min(times) < 300.0, times
+
+
+# ------------------------------------------------------------------- assign
+def _assign(past, new, tables, free, count, block, T, finished=None, outputs=()):
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    g = [d(np.array(past, np.int32)), d(np.array(new, np.int32)), d(tables), d(free), d(np.array([count], np.int32))]
+    made = attn.attn_cache_assign(*g, block_size=block, num_tokens=T,
+                                  finished=None if finished is None else d(finished), **dict(outputs))
+    torch.cuda.synchronize()
+    return made, [t.cpu().numpy() for t in (*made, g[2], g[3], g[4])]
+
+
+@pytest.mark.parametrize("entry", [-1, -2 ** 31, 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("B", [3, 200])
+@pytest.mark.parametrize("which", ["top", "deepest"])
+def test_assign_refuses_a_free_list_entry_it_would_take(B, which, entry):
+    """A stack entry that names no block is not handed out: the step is refused, nothing changes."""
+    N = 20 + B
+    entry = N if entry == 20 else entry
+    tables = np.full((B, 3), -1, np.int32)
+    tables[:, 0] = np.arange(B)
+    free = np.full(N, -1, np.int32)
+    free[:20] = B + np.arange(20)
+    past, new = np.full(B, 16), np.zeros(B, np.int64)
+    new[[0, B - 1]] = 17, 3  # two blocks and one: entries 19, 18, 17
+    bad = free.copy()
+    bad[19 if which == "top" else 17] = entry
+    _, got = _assign(past, new, tables, bad, 20, 16, 40)
+    assert got[3][0] == 5
+    assert np.array_equal(got[4], tables) and np.array_equal(got[5], bad) and got[6][0] == 20
+    assert (got[0] == 0).all() and np.array_equal(got[1], past) and (got[2] == -1).all()
+    # an entry below those it takes is another step's
+    bad = free.copy()
+    bad[16] = entry
+    _, got = _assign(past, new, tables, bad, 20, 16, 40)
+    assert got[3][0] == 0 and got[4][0, 1:].tolist() == [B + 19, B + 18] and got[4][B - 1, 1] == B + 17
+
+
+@pytest.mark.parametrize("B,each", [(1, 2000), (200, 60)])
+@pytest.mark.parametrize("where", [0, 700, -1])
+def test_assign_looks_at_all_of_a_long_take(B, each, where):
+    """A step that takes thousands of blocks: a bad entry anywhere among them refuses it, one below them does not."""
+    take = B * each
+    N = take + 5
+    tables = np.full((B, each), -1, np.int32)
+    free = np.random.default_rng(B).permutation(N).astype(np.int32)
+    past, new = np.full(B, 16 * each - 1), np.ones(B, np.int64)
+    at = N - 1 - (where % take)
+    bad = free.copy()
+    bad[at] = -3
+    _, got = _assign(past, new, tables, bad, N, 16, B)
+    assert got[3][0] == 5 and np.array_equal(got[4], tables) and np.array_equal(got[5], bad) and got[6][0] == N
+    bad = free.copy()
+    bad[4] = N
+    _, got = _assign(past, new, tables, bad, N, 16, B)
+    assert got[3][0] == 0 and got[6][0] == 5 and np.array_equal(got[4].reshape(-1), free[:4:-1])
+
+
+def test_assign_takes_returned_blocks_before_a_bad_entry():
+    """Blocks given back by a finished row lie on top of the stack: an entry under them that is not taken is not looked at,
+    one that is taken refuses the step and leaves the finished row its blocks."""
+    tables = np.array([[0, 1, -1], [2, -1, -1]], np.int32)
+    free = np.array([3, 99, -1, -1, -1, -1], np.int32)
+    fin = np.array([True, False])
+    _, got = _assign([32, 16], [5, 1], tables, free, 2, 16, 8, fin)
+    assert got[3][0] == 0 and got[4].tolist() == [[1, -1, -1], [2, 0, -1]] and got[6][0] == 2
+    _, got = _assign([32, 16], [5, 20], tables, free, 2, 16, 40, fin)
+    assert got[3][0] == 5 and got[4].tolist() == tables.tolist() and got[5].tolist() == free.tolist() and got[6][0] == 2
+
+
+def test_assign_into_the_callers_tensors():
+    """q_starts, total_lengths, slot_map and result given by the caller are what the call writes and returns."""
+    rng = np.random.Generator(np.random.PCG64(9))
+    past, new = rng.integers(0, 200, 50).astype(np.int32), rng.integers(0, 40, 50).astype(np.int32)
+    fin = rng.random(50) < 0.3
+    tables = np.full((50, 20), -1, np.int32)
+    free = rng.permutation(900).astype(np.int32)
+    at = 900
+    for b in range(50):
+        for i in range(-(-int(past[b]) // 16)):
+            at -= 1
+            tables[b, i] = free[at]
+    T = int(new.sum()) + 9
+    mine = dict(q_starts=torch.full((51,), 77, dtype=torch.int32, device="cuda"),
+                total_lengths=torch.full((50,), 77, dtype=torch.int32, device="cuda"),
+                slot_map=torch.full((T,), 77, dtype=torch.int64, device="cuda"),
+                result=torch.full((1,), 77, dtype=torch.int32, device="cuda"))
+    made, got = _assign(past, new, tables, free, at, 16, T, fin, mine)
+    for a, b in zip(made, mine.values()):
+        assert a.data_ptr() == b.data_ptr()
+    starts, totals, slots, result, n = ref.assign(past, new, fin, tables, free, at, 16, T)
+    for a, b in zip(got, (starts, totals, slots, np.array([result]), tables, free, np.array([n]))):
+        assert np.array_equal(a, b)
+    for name, wrong in (("q_starts", 50), ("total_lengths", 51), ("slot_map", T - 1), ("result", 2)):
+        with pytest.raises(ValueError, match=name):
+            _assign(past, new, tables, free, at, 16, T, fin,
+                    {name: torch.empty(wrong, dtype=mine[name].dtype, device="cuda")})

@@ -544,8 +544,9 @@ def attn_cache_assign(past_lengths, new_lengths, block_tables, free_blocks, free
     sum of new_lengths.  Returns (q_starts int32 [B + 1], total_lengths int32
     [B], slot_map int64 [num_tokens], result int32 [1]), allocated with torch
     when not given; result is 0, or why the step was not done (1 too few free
-    blocks, 2 a table row too short, 3 too many tokens, 4 a negative length, 5
-    a count or entry out of range), in which case nothing was assigned."""
+    blocks, 2 a table row too short, 3 too many tokens, 4 a negative length, a
+    finished row's too, 5 the count, a table entry or a free-list entry to be
+    taken out of range), in which case nothing was assigned."""
     index = past_lengths.get_device()
     if index < 0 or past_lengths.dim() != 1 or block_tables.dim() != 2 or free_blocks.dim() != 1:
         raise ValueError("attn_cache_assign takes CUDA tensors: lengths [B], block_tables [B, max_blocks], "

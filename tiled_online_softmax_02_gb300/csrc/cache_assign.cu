@@ -22,8 +22,8 @@
 // before any is taken, and every row is complete before a slot is read from
 // it.  The order of every list follows the rows, never the timing.
 //
-// Measured (one GB300, device time): 64 requests, a new token each, 7.5 us on
-// one CTA; 48 requests with up to 2048 new tokens, 65536 slots, 14.5 us on the
+// Measured (one GB300, device time): 64 requests, a new token each, 7.8 us on
+// one CTA; 48 requests with up to 2048 new tokens, 65536 slots, 15.1 us on the
 // cluster.
 #include <cstdint>
 
@@ -40,8 +40,10 @@ constexpr int kClusterCtas = 8;
 struct Sums {  // of a CTA's rows
   int lacks;   // table entries that need a block
   int given;   // blocks of finished rows
-  int flags;   // 1 << AssignResult of every problem met
+  int flags;   // 1 << AssignResult of every problem met, and kListFlag
+  int bad;     // whether a block that they would take is none
 };
+constexpr int kListFlag = 1 << 16;  // an entry near the top of the free stack names no block
 
 __device__ __forceinline__ int peer_i32(const void* ptr, int rank) {
   uint32_t remote;
@@ -116,6 +118,11 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
   __syncthreads();
 
   // ---- what every row of this CTA needs and gives
+  // (The free stack's topmost entries, one a thread, come with them: were one taken that names no block, the step could
+  // not be done.  Which are taken is known only with the sums; where one of these is bad, or more are taken, that is
+  // looked at once more below.)
+  const int top = min(max(count0, 0), p.num_blocks) - 1 - (rank * kThreads + tid);
+  const int top_entry = top >= 0 ? __ldcg(p.free_blocks + top) : 0;
   auto need_of = [&](int b) {
     return ((long long)past[b] + max(__ldg(p.added + b), 0) + p.block_size - 1) >> p.block_shift;
   };
@@ -164,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
     }
     if (lane == 0 && flags) atomicOr(&sums.flags, flags);
   }
+  if (top >= 0 && (top_entry < 0 || top_entry >= p.num_blocks)) atomicOr(&sums.flags, kListFlag);
   __syncthreads();
 
   // ---- offsets within the CTA, and the CTA's sums
@@ -213,6 +221,21 @@ __global__ void __launch_bounds__(kThreads) cache_assign_kernel(const __grid_con
   else if (tokens > p.T) res = kAssignTokens;
   else if ((flags & (1 << kAssignCorrupt)) || count0 < 0 || count1 > p.num_blocks) res = kAssignCorrupt;
   else if (lack_all > count1) res = kAssignNoBlocks;
+  if (res == kAssignOk && ((flags & kListFlag) || lack_all - given_all > ctas * kThreads)) {
+    bool bad = false;  // among the entries that this CTA's rows take; those of finished rows have been looked at
+    for (int n = tid; n < sums.lacks; n += kThreads) {
+      const long long at = count1 - 1 - lack_base - n;
+      const int e = at < count0 ? __ldcg(p.free_blocks + at) : 0;
+      bad |= e < 0 || e >= p.num_blocks;
+    }
+    bad = __syncthreads_or(bad);
+    if (CLUSTER) {
+      if (tid == 0) sums.bad = bad;
+      sync_all();
+      for (int c = 0; c < kClusterCtas; ++c) bad |= peer_i32(&sums.bad, c) != 0;
+    }
+    if (bad) res = kAssignCorrupt;
+  }
   const bool ok = res == kAssignOk;
 
   // ---- row starts and totals; blocks of finished rows go onto the stack

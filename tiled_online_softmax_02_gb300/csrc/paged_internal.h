@@ -25,7 +25,7 @@ enum AssignResult {
   kAssignRowShort = 2,   // a request needs more table entries than a row has
   kAssignTokens = 3,     // more new tokens than the slot map holds
   kAssignLength = 4,     // a negative length
-  kAssignCorrupt = 5     // free_count, a table entry or a free-list entry out of range
+  kAssignCorrupt = 5     // free_count, a table entry or a free-list entry to be taken out of range
 };
 
 constexpr int kAssignMaxRequests = 8192;
