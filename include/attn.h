@@ -443,7 +443,8 @@ int attn_cache_append_fp8(const void *k, const void *v, const int64_t *slot_map,
  *                 writes.  A key's weight times its V scale is held to 11 bits, or to
  *                 2^-24 of the row's largest such product, V scales below 2^-100
  *                 counting as that; the row sum has every key's weight
- *   block_tables  int32 [B, max_blocks].  An entry below a request's length that
+ *   block_tables  int32 [B, max_blocks], max_blocks * block_size at most
+ *                 2^31 - 128 (more: ATTN_ERR_INVALID_ARG).  An entry below a request's length that
  *                 names no block of [0, num_blocks) is not followed: its keys
  *                 count as zeros, and attn_get_device_status then reports
  *                 ATTN_ERR_INVALID_ARG once

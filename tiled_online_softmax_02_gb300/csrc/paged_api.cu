@@ -218,7 +218,7 @@ extern "C" int attn_fwd_paged_fp8(const void* q, const void* k_cache, const void
   if (!mul_ok(num_tokens, Hq, &rows) || rows > INT32_MAX - 1024 || !mul_ok(rows, D, &out_elems))
     return ATTN_ERR_INVALID_ARG;
   if (!mul_ok((int64_t)B * 4, max_blocks, &table_bytes)) return ATTN_ERR_INVALID_ARG;
-  if ((int64_t)max_blocks * block_size > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)max_blocks * block_size > INT32_MAX - 127) return ATTN_ERR_INVALID_ARG;  // rounded up to a tile of 128
   if (num_tokens == 0 || B == 0) return ATTN_OK;  // no row belongs to a request
   if (!q || !out || !q_starts || !total_lengths) return ATTN_ERR_INVALID_ARG;
   if (num_blocks == 0 || !k_cache || !v_cache || !k_scales || !v_scales || (max_blocks > 0 && !block_tables))
