@@ -233,6 +233,23 @@ def test_append_over_long_gaps(T, at):
     _append(slots, 5)
 
 
+@pytest.mark.parametrize("seed", range(40))
+def test_append_random_gaps(seed):
+    """Runs of any length and order, and gaps between and inside them of every length around what a CTA looks at."""
+    rng = np.random.default_rng(seed)
+    block, gaps = int(rng.choice([16, 32, 64, 128])), [0, 0, 0, 1, 3, 28, 31, 33, 40, 64, 67, 129, 193, 300, 1500]
+    slots = [-1] * int(rng.choice(gaps))
+    for b in rng.permutation(30)[:int(rng.integers(1, 30))]:
+        for _ in range(int(rng.integers(1, 4))):
+            a = int(rng.integers(0, block))
+            for s in range(a, int(rng.integers(a, block)) + 1):
+                slots.append(b * block + s)
+                if rng.random() < 0.08:
+                    slots += [-1] * int(rng.choice(gaps[3:]))
+            slots += [-1] * int(rng.choice(gaps))
+    _append(np.array(slots, np.int64), 30, Hkv=1, block=block, seed=seed)
+
+
 def test_append_many_short_runs():
     """1040 requests, a token or two each: just past the size where a CTA takes more tokens."""
     rng = np.random.default_rng(2)

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
         while (!valid(next) && t < window_end) {  // over skipped tokens
           const int64_t y = t + lane < window_end ? window[t + lane - first + 1] : -1;
           const unsigned m = __ballot_sync(0xffffffffu, valid(y));
-          const int skip = m ? __ffs(m) - 1 : 32;
+          const int skip = m ? __ffs(m) - 1 : min(32, window_end - t);
           t += skip;
           if (m) next = __shfl_sync(0xffffffffu, y, skip);
         }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 10) cache_appen
   }
 
   // the last block's runs behind the window, past any number of skipped tokens
-  if (window_end == p.T || valid(window[held - 1])) return;
+  if (window_end == p.T) return;
   __syncthreads();
   const int64_t blk = tail_block;
   for (int t = tail; t >= 0;) {
