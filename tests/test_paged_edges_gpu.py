@@ -351,6 +351,23 @@ def test_assign_takes_returned_blocks_before_a_bad_entry():
     assert got[3][0] == 5 and got[4].tolist() == tables.tolist() and got[5].tolist() == free.tolist() and got[6][0] == 2
 
 
+@pytest.mark.parametrize("B", [2, 300])
+def test_assign_resets_finished_rows_without_blocks(B):
+    """A finished row's entries become -1, whichever negative numbers they were, though it gives no block back."""
+    tables = np.full((B, 4), -1, np.int32)
+    tables[:, 0], tables[:, 3] = -5, -2 ** 31
+    free = np.arange(B, dtype=np.int32)
+    fin = np.arange(B) % 2 == 1
+    _, got = _assign(np.full(B, 9), np.arange(B) < 2, tables, free, B, 16, 2, fin)
+    want = tables.copy()
+    want[fin] = -1
+    taken = np.flatnonzero(~fin | (np.arange(B) < 2))  # every row that goes on lacks its block, so does the one that begins
+    want[taken, 0] = B - 1 - np.arange(len(taken))
+    assert got[3][0] == 0 and np.array_equal(got[4], want) and got[6][0] == B - len(taken)
+    _, got = _assign(np.full(B, 9), np.zeros(B), tables, free, B, 16, 0, np.ones(B, bool))
+    assert got[3][0] == 0 and (got[4] == -1).all() and got[6][0] == B and np.array_equal(got[5], free)
+
+
 def test_assign_into_the_callers_tensors():
     """q_starts, total_lengths, slot_map and result given by the caller are what the call writes and returns."""
     rng = np.random.Generator(np.random.PCG64(9))
