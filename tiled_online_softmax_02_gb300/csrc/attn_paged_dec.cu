@@ -13,7 +13,8 @@
 // pieces hold a bf16 Q exactly and three an f16 Q (down to 2^-23 and 2^-28 of
 // the row's largest element, which a power of two brings into e4m3's range), and
 // three hold a P of 11 bits (it is rounded to f16 first, as packed f16
-// arithmetic splits it in half the instructions), down to 2^-25 of its largest.
+// arithmetic splits it in half the instructions; 16-bit outputs have no more
+// bits, the row sum takes the unrounded weights), down to 2^-25 of its largest.
 //
 // Scales: a key's K scale multiplies its scores (the thread that owns the key
 // holds it).  Its V scale enters the exponent, t = s log2 e + log2 v_scale,
@@ -27,13 +28,14 @@
 // warp 7 the next unit's Q into pieces, and the scales of its tiles.
 //
 // Measured (one GB300, device time with the join): 8 requests of 9K to 32.7K
-// tokens, 8 kv heads, 4 rows each, bf16, D = 128: 58 us, 5.9 TB/s, 87% of a
+// tokens, 8 kv heads, 4 rows each, bf16, D = 128: 58.2 us, 5.9 TB/s, 87% of a
 // copy's rate; 64 requests of 100 to 8000 tokens, 4 kv heads, 8 rows, f16,
-// blocks of 16: 53.5 us, 5.0 TB/s, 73%; one request of 3.5K tokens: 11.3 us,
+// blocks of 16: 54.1 us, 4.9 TB/s, 73%; one request of 3.5K tokens: 11.3 us,
 // which is the way to the first result.  Two CTAs an SM, each with a ring of
 // 80 KB (64 KB at D = 64), keep about 24 MB on their way; a warp's
 // instructions, not registers or shared memory, are what these roles run out
-// of, so loops stay rolled where they can.
+// of, so loops stay rolled where they can.  Units of 16 rows spill about 120
+// bytes a thread at the 128 registers that two CTAs leave.
 #include <algorithm>
 #include <atomic>
 

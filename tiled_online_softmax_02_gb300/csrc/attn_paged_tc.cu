@@ -9,15 +9,19 @@
 //               16-bit Q is two (bf16) or three (f16) e4m3 pieces at one scale,
 //               each accumulated into the same S.  e4m3 runs at twice the
 //               16-bit rate, so bf16's two pieces cost what one 16-bit product
-//               would, and K needs no conversion.
+//               would, f16's three half more, and K needs no conversion.
 //   O += P V    kind::f16: P is f16 in tensor memory, V is widened to f16 by
 //               four warps on its way from one shared buffer to another.
 //               P as e4m3 pieces would cost the softmax warps, which have no
 //               slots to spare, about six instructions a value; widening V
 //               costs other warps half of one.
-// A row of Q carries its own power-of-two scale, the largest that keeps it in
-// e4m3's range, and pieces x0 = e4m3(x), x1 = e4m3(x - x0), ...: what is left
-// is below 2^-18 of the row's largest element.
+// A row of Q carries its own power-of-two scale, which brings its largest element
+// into [128, 256), and pieces x0 = e4m3(x), x1 = e4m3(x - x0), ...  One S takes
+// them all, so they share that scale, and e4m3's smallest step there, 2^-9: what is
+// left is at most 2^-10, 2^-17 of the row's largest element or less.  That holds
+// bf16 elements down to 2^-9 of it exactly and f16 ones down to 2^-6; smaller ones
+// lose low bits, which their share of the score hardly shows.  (The few-rows kernel
+// has a column for each piece, and scales them apart.)
 //
 // Scales are constant over 16 keys or more (the smallest block).  Per group of
 // 16 keys: the largest raw score is found first and scaled once, and
@@ -33,14 +37,14 @@
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
 //
 // Measured (one GB300, device time with the join, bf16, 32 query and 8 kv heads,
-// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 581 us, 1240
-// TFLOP/s, 66% of a 16-bit library product's rate; two whole prompts of 3.5K to
-// 4K tokens 252 us, 937 TFLOP/s.  The tensor pipe is busy half of the first's
+// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 592 us, 1216
+// TFLOP/s, 65% of a 16-bit library product's rate; two whole prompts of 3.5K to
+// 4K tokens 257 us, 919 TFLOP/s.  The tensor pipe is busy half of the first's
 // time: a lane's S, softmax and P V follow one another, as P takes S's place
 // (two of each and two O of 128 columns fill tensor memory), and two lanes do
 // not cover that entirely; P V of a tile's first 64 keys at least runs beside
-// the exponentials of the others.  A lane's tile is 1200 cycles of waiting for S,
-// 700 for the maximum and 1550 for the exponentials.  A unit costs about three
+// the exponentials of the others.  A lane's tile is 1240 cycles of waiting for S,
+// 700 for the maximum, 100 for what follows it and 1600 for the exponentials.  A unit costs about three
 // tiles more than its tiles: 6000 cycles to bring Q, most of them conversions
 // to e4m3 and back, and 4000 to store the rows.
 #include <algorithm>
@@ -59,8 +63,8 @@ constexpr int kVWarp0 = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
 constexpr float kRise = 8.0f;          // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
-// Loops over a tile's four runs of 32 keys.  Two whole prompts: 252 us with these; 258 and 259 with the maximum's
-// loop unrolled 1 and 4 times, 257 with the exponentials' unrolled twice (instruction fetches).
+// Loops over a tile's four runs of 32 keys.  Two whole prompts took 252 us with these when they were chosen; 258 and 259
+// with the maximum's loop unrolled 1 and 4 times, 257 with the exponentials' unrolled twice (instruction fetches).
 constexpr int kMaxUnroll = 2, kExpUnroll = 1;
 
 template <int D, bool BF16>

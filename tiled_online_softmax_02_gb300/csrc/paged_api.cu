@@ -145,17 +145,19 @@ PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_t
   const int group = Hq / Hkv;
   // Rows per (request, kv head) of an even batch; a request with more takes several units.  The few-rows kernel's
   // time a tile grows with the rows it holds, the many-rows kernel's does not.  48 requests of up to 8K tokens, 4 kv
-  // heads, D = 128: 9, 12, 16 rows take 61, 66, 69 us in units of 16 and 89 in the many-rows kernel; 20 and 32 rows
-  // 112 and 120 us as two units of 16 each, 92 there.
+  // heads, D = 128: 9, 12, 16 rows take 64, 70, 74 us in units of 16 and 93 in the many-rows kernel; 20 and 32 rows
+  // 110 and 125 us as two units of 16 each, 94 there.
+  // Lengths are on the device, so the mean is all there is to go by, padding rows in it: 64 single tokens at 4K take 87
+  // us, in a T of 2048 rows 204; 63 of them with one chunk of 2048 332 us, where the two alone take 86 and 116.
   const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
   pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedTcRows;
   int64_t most = (int64_t)sm_count() * (pl.rows == kPagedTcRows ? 1 : kPagedDecCtas);
   const size_t slots = 2 * (size_t)most * pl.rows;  // the choice below needs no more
   // With little to read a call is the way to the first result and the join of the parts, both shorter in units of 8
   // rows, and reading the keys once a unit costs nothing yet.  What there may be to read: the tables' width.
-  // 12 rows, 4 requests of up to 8K tokens: 14.5 us against 18.6; 16 rows, 4 of 100K: 126 against 85.  32 rows,
-  // 8 requests of up to 8K: 28 against 30 (4 of them: 19 against 25); 16 of them: 47 against 41.  128 rows, one
-  // request of 4K, 8 kv heads: 26 against 32; two of them: 38 against 27.
+  // 4 kv heads: 12 rows, 4 requests of up to 8K tokens 14.8 us against 18.8; 16 rows, 4 of 100K 125 against 84.  32
+  // rows, 8 requests of up to 8K 27 against 30 (4 of them 18 against 28); 16 of them 48 against 41.  8 kv heads: 128
+  // rows, one request of 4K 27 against 31; two of them 37 against 26.
   const int64_t eights = B * Hkv * ((rows + 7) / 8), small = (int64_t)1 << 13;  // key tiles
   if (pl.rows == 16 ? eights * max_tiles <= 2 * small
                     : pl.rows == kPagedTcRows && eights <= sm_count() && eights * max_tiles <= small) {

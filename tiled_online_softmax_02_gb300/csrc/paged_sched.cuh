@@ -88,12 +88,12 @@ __device__ __forceinline__ void paged_unit_tiles(const PagedParams& p, PagedUnit
   u.te = hi > lo ? (hi + kPagedKeys - 1) / kPagedKeys : 0;
 }
 
-// What a unit costs besides its tiles, in tiles.
-template <int NR>
+// What a unit costs besides its tiles, in tiles: the many-rows kernel's Q and output rows, about 10000 cycles.  The
+// few-rows kernel's units are given the same.
 constexpr int kOver = 3;
 
 template <int NR>
-__device__ __forceinline__ int paged_cost(const PagedUnit& u) { return max(u.te - u.tb, 1) + kOver<NR>; }
+__device__ __forceinline__ int paged_cost(const PagedUnit& u) { return max(u.te - u.tb, 1) + kOver; }
 
 // Length on the line of one kv head of a request: the sum over its row tiles.
 template <int NR>
@@ -198,7 +198,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
       if (rest < paged_cost<NR>(u)) break;
       rest -= paged_cost<NR>(u);
     }
-    const int off = rest > kOver<NR> ? (int)rest : 0;
+    const int off = rest > kOver ? (int)rest : 0;
     if (end) {
       sh->w1 = at - (rest - off);
     } else {
@@ -240,9 +240,9 @@ struct PagedWalk {
   __device__ __forceinline__ void segment() {
     head = off == 0;
     whole = head && len() == paged_cost<NR>(u);
-    const int before = head ? 0 : off - kOver<NR>;
+    const int before = head ? 0 : off - kOver;
     t0 = u.tb + before;
-    nt = u.te > u.tb ? off + len() - kOver<NR> - before : 0;
+    nt = u.te > u.tb ? off + len() - kOver - before : 0;
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
     left -= len();
