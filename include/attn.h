@@ -469,6 +469,143 @@ int attn_fwd_paged_fp8(const void *q, const void *k_cache, const void *v_cache, 
 /* Workspace bytes attn_fwd_paged_fp8 needs on the current device. */
 size_t attn_paged_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, int D);
 
+/*
+ * The paged 4-bit KV cache: the 8-bit one's blocks, slots and block tables
+ * (attn_cache_assign serves both) with 4.5 bits a value:
+ *   attn_cache_append_fp4  the step's K / V rows into their slots
+ *   attn_cache_read_fp4    rows of slots back out, as f32, f16 or bf16
+ *   attn_fwd_paged_fp4     attention of the step's rows over the cache
+ *
+ * Layout.  The cache (one for K, one for V) is [num_blocks, Hkv, block_size,
+ * D / 2] bytes, D = 64 or 128: byte i of a row holds the e2m1 codes of values
+ * 2 i (low half) and 2 i + 1, with scales [num_blocks, Hkv, block_size, D / 16]
+ * of e4m3, one for every 16 values of a row.  An e2m1 code is a sign and 0,
+ * 1/2, 1, 3/2, 2, 3, 4 or 6.  Head scales, f32 [Hkv], are optional (NULL: 1):
+ *   value = e2m1 * e4m3 * head_scale.
+ * They are positive, finite and the same in every call on a cache; they bring a
+ * head whose values lie outside 2^-6 to 2^11 into the range where e4m3 scales
+ * are exact to 2^-4.
+ */
+
+/*
+ * attn_cache_append_fp4 -- K and V rows into their slots, quantised.
+ *
+ * For 16 values x of a row that share a scale, h the head scale and g the
+ * largest finite |x| among them:
+ *   s    = e4m3(g / (6 h)), to nearest even, at least 2^-9, at most 448
+ *   code = e2m1(x / (s h)), to nearest even, cut at 6 (infinities so)
+ * 6 h, s h and the quotients rounded to f32.  A group with a NaN gets the scale NaN
+ * (0x7f) and codes of zero.  Negative slots and slots of no block are passed over.
+ *
+ * Arguments (device pointers, caller-owned; the caches and scales overlap nothing):
+ *   k, v          [num_tokens, Hkv, D] dtype, 16-byte aligned; token t begins
+ *                 at element t * token_stride (>= Hkv * D, whole 16 bytes)
+ *   slot_map      int64 [num_tokens], in any order.  Two tokens with the same
+ *                 slot leave unspecified contents there
+ *   k_cache, v_cache, k_scales, v_scales   see the layout above, 16-byte aligned
+ *   k_head_scales, v_head_scales           f32 [Hkv] or NULL
+ *   dtype         enum attn_dtype of k and v
+ * One launch on `stream`; allocates and synchronises nothing.
+ */
+int attn_cache_append_fp4(const void *k, const void *v, const int64_t *slot_map, void *k_cache, void *v_cache,
+                          void *k_scales, void *v_scales, const float *k_head_scales, const float *v_head_scales,
+                          int num_tokens, int Hkv, int D, int64_t k_token_stride, int64_t v_token_stride,
+                          int num_blocks, int block_size, int dtype, void *stream);
+
+/*
+ * attn_cache_read_fp4 -- rows of the cache, widened: for prompts whose dense
+ * attention is to see what the cache holds, and for contexts that move.
+ *
+ * Row t of k and v receives the values of slot slot_map[t], rounded to nearest
+ * even; zeros where the slot is negative or of no block.  The same slot may be
+ * read any number of times.
+ *
+ * Arguments (device pointers, caller-owned; k and v overlap nothing):
+ *   k, v          [num_tokens, Hkv, D] dtype, 16-byte aligned: head h of token t
+ *                 at element t * token_stride + h * head_stride, its D values
+ *                 together; strides whole 16 bytes, and such that no two rows
+ *                 overlap: heads inside tokens or tokens inside heads
+ *   the rest      as attn_cache_append_fp4
+ * One launch on `stream`; allocates and synchronises nothing.
+ */
+int attn_cache_read_fp4(const void *k_cache, const void *v_cache, const void *k_scales, const void *v_scales,
+                        const float *k_head_scales, const float *v_head_scales, const int64_t *slot_map, void *k,
+                        void *v, int num_tokens, int Hkv, int D, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, int num_blocks, int block_size, int dtype,
+                        void *stream);
+
+/*
+ * attn_fwd_paged_fp4 -- attention of the step's rows over the 4-bit cache:
+ * attn_fwd_paged_fp8's definition (visibility, soft-cap, rows without keys, rows
+ * of no request, log-sum-exp) over the values that the 4-bit cache holds.
+ *
+ * Slots at or past a request's total length may hold any bits; they never
+ * reach the output.  A NaN scale in a slot below it may reach every row of the
+ * same request and kv head.
+ *
+ * Arguments as attn_fwd_paged_fp8, except:
+ *   k_cache, v_cache, k_scales, v_scales   the 4-bit layout, 16-byte aligned
+ *   k_head_scales, v_head_scales           f32 [Hkv] or NULL
+ *   workspace     at least attn_paged_fp4_workspace_bytes(...) bytes, 16-byte
+ *                 aligned, for partial rows; nothing in it has to start at zero.
+ *                 Calls that share a workspace must not overlap on the GPU.
+ * A key's weight is held to 11 bits, or to 2^-29 of the row's largest; the row
+ * sum has every key's weight.  A block-table entry below a request's length
+ * that names no block is not followed: its keys count as zeros, and
+ * attn_get_device_status then reports ATTN_ERR_INVALID_ARG once.
+ * Enqueues on `stream`; allocates and synchronises nothing, so it may be captured into a CUDA
+ * graph (make one call on the device before capturing).
+ */
+int attn_fwd_paged_fp4(const void *q, const void *k_cache, const void *v_cache, const void *k_scales,
+                       const void *v_scales, const float *k_head_scales, const float *v_head_scales,
+                       const int32_t *block_tables, const int32_t *q_starts, const int32_t *total_lengths, void *out,
+                       float *lse, int num_tokens, int B, int Hq, int Hkv, int D, int64_t q_token_stride,
+                       int num_blocks, int block_size, int max_blocks, int causal, int local_window, float scale,
+                       float softcap, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes attn_fwd_paged_fp4 needs on the current device. */
+size_t attn_paged_fp4_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, int D);
+
+/*
+ * attn_rope -- rotary positions: query and key rows turned by their positions,
+ * before a step's attn_cache_append_* and attn_fwd_paged_*, or on dense rows.
+ *
+ * Of every row the first rotary_dim = R values are R / 2 pairs, pair i being
+ * values (i, i + R / 2), or (2 i, 2 i + 1) when interleaved is 1.  With the
+ * token's position pos and w = pos * inv_freq[i], a pair (a, b) becomes
+ *   scale * (a cos w - b sin w, b cos w + a sin w),
+ * or, when inverse is 1, that with -w: for the same scale the transpose, which
+ * takes gradients of the turned rows to gradients of the rows.  Values from R
+ * on are kept.  Angles are exact to 2^-24 turns at any position; the rotation
+ * is done in f32 and rounded to nearest even.
+ *
+ * Position of token t: positions[t] or, when positions is NULL, that of a paged
+ * step's rows: total_lengths[b] - q_starts[b + 1] + t for the request b with
+ * q_starts[b] <= t < q_starts[b + 1]; rows of no request are left as they
+ * were in the outputs.
+ *
+ * Arguments (device pointers, caller-owned):
+ *   q, k          [num_tokens, Hq or Hk, D] dtype: token t at element
+ *                 t * token_stride (>= heads * D); k unused when Hk is 0
+ *   q_out, k_out  the same shapes and types.  Either the same rows as q (or k),
+ *                 in place, or no byte in common with any input; rows of one
+ *                 stride may lie between each other (slices of a projection)
+ *   inv_freq      f64 [rotary_dim / 2] radians a position
+ *   positions     int32 [num_tokens] or NULL
+ *   q_starts      int32 [B + 1], non-decreasing in [0, num_tokens];
+ *   total_lengths int32 [B]; both NULL when positions is given
+ *   rotary_dim    even, 0 to D
+ *   dtype         enum attn_dtype
+ *   Hq + Hk       up to 65535 (more: ATTN_ERR_UNSUPPORTED)
+ * Any D and alignment; rows that begin on 16 bytes and R in whole 32 bytes are the fast case.
+ * One launch on `stream`; allocates and synchronises nothing.
+ */
+int attn_rope(const void *q, const void *k, void *q_out, void *k_out, const double *inv_freq,
+              const int32_t *positions, const int32_t *q_starts, const int32_t *total_lengths, int num_tokens, int B,
+              int Hq, int Hk, int D, int rotary_dim, int64_t q_token_stride, int64_t k_token_stride,
+              int64_t q_out_token_stride, int64_t k_out_token_stride, int interleaved, int inverse, float scale,
+              int dtype, void *stream);
+
 /* Human-readable name of a status code; never NULL. */
 const char *attn_status_string(int status);
 
@@ -480,8 +617,8 @@ int attn_last_cuda_error(void);
  * attn_get_device_status -- synchronises `stream`, then reports and clears
  * the device-side status word of the current device: ATTN_ERR_TIMEOUT if any
  * kernel of this library gave up on a bounded wait since the last query,
- * else ATTN_ERR_INVALID_ARG if attn_fwd_paged_fp8 met a block-table entry that
- * names no block, else ATTN_OK (or ATTN_ERR_CUDA if the synchronisation failed).
+ * else ATTN_ERR_INVALID_ARG if attn_fwd_paged_fp8 or attn_fwd_paged_fp4 met a
+ * block-table entry that names no block, else ATTN_OK (or ATTN_ERR_CUDA if the synchronisation failed).
  */
 int attn_get_device_status(void *stream);
 

@@ -58,6 +58,12 @@ SIGNATURES = {
     "attn_fwd_paged_fp8": (_i32, [_vp] * 10 + [_i32] * 5 + [ctypes.c_int64] + [_i32] * 5 +
                            [ctypes.c_float, ctypes.c_float, _i32, _vp, ctypes.c_size_t, _vp]),
     "attn_paged_workspace_bytes": (ctypes.c_size_t, [_i32] * 5),
+    "attn_cache_append_fp4": (_i32, [_vp] * 9 + [_i32] * 3 + [ctypes.c_int64] * 2 + [_i32] * 3 + [_vp]),
+    "attn_cache_read_fp4": (_i32, [_vp] * 9 + [_i32] * 3 + [ctypes.c_int64] * 4 + [_i32] * 3 + [_vp]),
+    "attn_fwd_paged_fp4": (_i32, [_vp] * 12 + [_i32] * 5 + [ctypes.c_int64] + [_i32] * 5 +
+                           [ctypes.c_float, ctypes.c_float, _i32, _vp, ctypes.c_size_t, _vp]),
+    "attn_paged_fp4_workspace_bytes": (ctypes.c_size_t, [_i32] * 5),
+    "attn_rope": (_i32, [_vp] * 8 + [_i32] * 6 + [ctypes.c_int64] * 4 + [_i32] * 2 + [ctypes.c_float, _i32, _vp]),
     "attn_status_string": (ctypes.c_char_p, [_i32]),
     "attn_last_cuda_error": (_i32, []),
     "attn_get_device_status": (_i32, [_vp]),
@@ -669,10 +675,275 @@ def attn_paged_workspace_bytes(num_tokens, B, Hq, Hkv, D) -> int:
     return load_library().attn_paged_workspace_bytes(int(num_tokens), int(B), int(Hq), int(Hkv), int(D))
 
 
+# ---------------------------------------------------------------------------
+# The paged 4-bit KV cache, and rotary positions.
+CODE_DTYPES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+GROUP4 = 16  # values that share a scale
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales, v_head_scales, index):
+    """(num_blocks, Hkv, block_size, D, head scales' addresses) of a 4-bit cache, after checking its tensors."""
+    shape, dtype, sdtype = k_cache.shape, k_cache.dtype, k_scales.dtype
+    if len(shape) != 4 or dtype not in CODE_DTYPES or sdtype not in CACHE_DTYPES:
+        raise ValueError("the caches must be [num_blocks, Hkv, block_size, D / 2] of uint8 (or float4_e2m1fn_x2) with "
+                         f"scales of float8_e4m3fn or uint8: got {dtype} {tuple(shape)}, {sdtype}")
+    _need(k_cache, "k_cache", dtype, shape, index)
+    _need(v_cache, "v_cache", dtype, shape, index)
+    groups = (*shape[:3], shape[3] * 2 // GROUP4)
+    _need(k_scales, "k_scales", sdtype, groups, index)
+    _need(v_scales, "v_scales", sdtype, groups, index)
+    heads = []
+    for t, name in ((k_head_scales, "k_head_scales"), (v_head_scales, "v_head_scales")):
+        if t is not None:
+            _need(t, name, _F32, (shape[1],), index)
+        heads.append(None if t is None else t.data_ptr())
+    return shape[0], shape[1], shape[2], shape[3] * 2, heads
+
+
+def attn_cache_append_fp4(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, *, k_head_scales=None,
+                          v_head_scales=None):
+    """New K / V rows into the paged 4-bit cache, as e2m1 with one e4m3 scale
+    for every 16 values of a row (attn_cache_append_fp4 in the C ABI).
+
+    k, v [T, Hkv, D] (one dtype among float32 / float16 / bfloat16; a token's
+    heads contiguous, tokens any stride apart); slot_map int64 [T] (negative =
+    skip; no slot twice); k_cache, v_cache [num_blocks, Hkv, block_size, D / 2]
+    uint8 (or float4_e2m1fn_x2) and k_scales, v_scales [num_blocks, Hkv,
+    block_size, D / 16] float8_e4m3fn (or uint8), updated in place;
+    k_head_scales, v_head_scales float32 [Hkv] or None (1)."""
+    index, dtype = k.get_device(), k.dtype
+    if k.dim() != 3 or index < 0 or v.shape != k.shape or v.get_device() != index:
+        raise ValueError("k, v must be CUDA tensors [T, Hkv, D] of one shape and device")
+    if dtype not in DTYPE_CODES or v.dtype is not dtype:
+        raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
+    T, Hkv, D = k.shape
+    num_blocks, heads, block_size, width, (kh, vh) = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
+                                                                   v_head_scales, index)
+    if heads != Hkv or width != D:
+        raise ValueError(f"shape mismatch: rows of {Hkv} kv heads of {D}, a cache of {heads} of {width}")
+    _need(slot_map, "slot_map", _I64, (T,), index)
+    with _on(index):
+        rc = load_library().attn_cache_append_fp4(
+            k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), kh, vh, T, Hkv, D, _token_stride(k, "k"), _token_stride(v, "v"),
+            num_blocks, block_size, DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_append_fp4")
+
+
+def _row_strides(t, name):
+    """Elements from one token, and from one head, of a [T, H, D] tensor to the next; D must be dense."""
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous, strides {(st, sh, sd)}")
+    return (st if T > 1 else max(H * D, sh * H)), (sh if H > 1 else D)
+
+
+def attn_cache_read_fp4(k_cache, v_cache, k_scales, v_scales, slot_map, *, dtype=torch.bfloat16, k_head_scales=None,
+                        v_head_scales=None, k=None, v=None):
+    """Rows of the paged 4-bit cache, widened (attn_cache_read_fp4 in the C ABI).
+
+    The cache as attn_cache_append_fp4 takes it; slot_map int64 [T].  Returns
+    (k, v), [T, Hkv, D]: row t has the values of slot slot_map[t], zeros where
+    that is negative.  k and v are allocated with torch (of `dtype`: float32,
+    float16 or bfloat16) when not given; given, they share a dtype, their values
+    of a row are contiguous, and tokens and heads may be any strides apart (a
+    transposed [Hkv, T, D], say)."""
+    index = k_cache.get_device()
+    if index < 0 or slot_map.dim() != 1:
+        raise ValueError("attn_cache_read_fp4 takes CUDA tensors: caches [num_blocks, Hkv, block_size, D / 2], slot_map [T]")
+    num_blocks, Hkv, block_size, D, (kh, vh) = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
+                                                             v_head_scales, index)
+    T = slot_map.shape[0]
+    _need(slot_map, "slot_map", _I64, (T,), index)
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    if k is None:
+        k, v = (torch.empty((T, Hkv, D), dtype=dtype, device=k_cache.device) for _ in range(2))
+    elif k.shape != (T, Hkv, D) or v.shape != k.shape or k.get_device() != index or v.get_device() != index:
+        raise ValueError(f"k, v must be [{T}, {Hkv}, {D}] on cuda:{index}")
+    if k.dtype not in DTYPE_CODES or v.dtype is not k.dtype:
+        raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
+    with _on(index):
+        rc = load_library().attn_cache_read_fp4(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kh, vh,
+            slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), T, Hkv, D, *_row_strides(k, "k"), *_row_strides(v, "v"),
+            num_blocks, block_size, DTYPE_CODES[k.dtype], torch._C._cuda_getCurrentRawStream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_read_fp4")
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged4_workspace(num_tokens, B, Hq, Hkv, D, index):
+    with _on(index):
+        return load_library().attn_paged_fp4_workspace_bytes(num_tokens, B, Hq, Hkv, D)
+
+
+def attn_fwd_paged_fp4(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_starts, total_lengths, *,
+                       k_head_scales=None, v_head_scales=None, causal=True, local_window=0, scale=None, softcap=0.0,
+                       out=None, lse=None, workspace=None):
+    """Attention over the paged 4-bit KV cache (attn_fwd_paged_fp4 in the C ABI).
+
+    q [T, Hq, D] float16 or bfloat16, D 64 or 128, the packed rows of all
+    requests; the cache as attn_cache_append_fp4 takes it; the rest as
+    attn_fwd_paged_fp8.  Returns out [T, Hq, D] (allocated with torch when not
+    given; rows of no request are not written)."""
+    index, dtype = q.get_device(), q.dtype
+    if q.dim() != 3 or index < 0 or block_tables.dim() != 2:
+        raise ValueError("attn_fwd_paged_fp4 takes CUDA tensors: q [T, Hq, D], caches "
+                         "[num_blocks, Hkv, block_size, D / 2], block_tables [B, max_blocks]")
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("q must be float16 or bfloat16")
+    shape = q.shape
+    T, Hq, D = shape
+    B, width = block_tables.shape
+    num_blocks, Hkv, block_size, cache_d, (kh, vh) = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
+                                                                   v_head_scales, index)
+    if cache_d != D:
+        raise ValueError(f"shape mismatch: q rows of {D}, cache rows of {cache_d}")
+    _need(block_tables, "block_tables", _I32, (B, width), index)
+    _need(q_starts, "q_starts", _I32, (B + 1,), index)
+    _need(total_lengths, "total_lengths", _I32, (B,), index)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    else:
+        _need(out, "out", dtype, shape, index)
+    if lse is not None:
+        _need(lse, "lse", _F32, (T, Hq), index)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if workspace is None:
+        workspace = _workspace(_paged4_workspace(T, B, Hq, Hkv, D, index), index, stream, q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    with _on(index):
+        rc = load_library().attn_fwd_paged_fp4(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kh, vh,
+            block_tables.data_ptr(), q_starts.data_ptr(), total_lengths.data_ptr(), out.data_ptr(),
+            None if lse is None else lse.data_ptr(), T, B, Hq, Hkv, D, _token_stride(q, "q"), num_blocks, block_size,
+            width, 1 if causal else 0, int(local_window), 1.0 / math.sqrt(D) if scale is None else scale, softcap,
+            DTYPE_CODES[dtype], workspace.data_ptr(), workspace.nbytes, stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_paged_fp4")
+    return out
+
+
+def attn_paged_fp4_workspace_bytes(num_tokens, B, Hq, Hkv, D) -> int:
+    """Workspace bytes attn_fwd_paged_fp4 needs on the current device, for callers that keep their own."""
+    return load_library().attn_paged_fp4_workspace_bytes(int(num_tokens), int(B), int(Hq), int(Hkv), int(D))
+
+
+def attn_rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_length=None, fast_turns=32.0,
+                          slow_turns=1.0, device="cuda"):
+    """Frequencies of attn_rope and the factor for its `scale`: (float64 [rotary_dim / 2] on `device`, float).
+
+    base^(-2 i / rotary_dim) for pair i, and for contexts `factor` times as long
+    as the `original_length` that was trained on, by `scaling`:
+      "linear"  every frequency divided by the factor
+      "base"    the base times factor^(rotary_dim / (rotary_dim - 2)): the slowest pair is
+                stretched by the factor, the fastest kept
+      "parts"   pairs that make `slow_turns` or fewer over original_length positions divided by the
+                factor, those with `fast_turns` or more kept, a ramp over the logarithm of the turns
+                between them; the scale is then 0.1 ln(factor) + 1, else 1
+    """
+    R = int(rotary_dim)
+    if R <= 0 or R % 2 or not base > 0 or not factor > 0:
+        raise ValueError("rotary_dim must be positive and even, base and factor positive")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts': got {scaling!r}")
+    i = torch.arange(0, R, 2, dtype=torch.float64) / R
+    out_scale = 1.0
+    if scaling == "base":
+        if R < 4:
+            raise ValueError("scaling 'base' needs a rotary_dim of 4 or more")
+        base = base * factor ** (R / (R - 2))
+    freq = base ** -i
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        if not original_length or not 0 < slow_turns < fast_turns:
+            raise ValueError("scaling 'parts' needs original_length, and 0 < slow_turns < fast_turns")
+        made = original_length * freq / (2 * math.pi)
+        keep = ((made / slow_turns).log() / math.log(fast_turns / slow_turns)).clamp(0.0, 1.0)
+        freq = freq * (keep + (1 - keep) / factor)
+        out_scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return freq.to(device), out_scale
+
+
+def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=None, layout="half", inverse=False,
+              scale=1.0, q_out=None, k_out=None):
+    """Rotary positions onto query and key rows (attn_rope in the C ABI).
+
+    q [T, Hq, D] and k [T, Hk, D] or None (one dtype among float32 / float16 /
+    bfloat16; a token's heads contiguous, tokens any stride apart); inv_freq
+    float64 [R / 2], the first R <= D values of a row being turned.  The tokens'
+    positions: positions int32 [T], or q_starts int32 [B + 1] and total_lengths
+    int32 [B] of a paged step, whose rows are each request's newest tokens.
+    layout "half" pairs values (i, i + R / 2), "interleaved" (2 i, 2 i + 1).
+    inverse turns back: with the same scale it takes gradients of the turned
+    rows to gradients of q and k.  Returns (q_out, k_out), allocated with torch
+    when not given; q_out=q, k_out=k works in place.  Rows of no request are not
+    written."""
+    index, dtype = q.get_device(), q.dtype
+    if q.dim() != 3 or index < 0:
+        raise ValueError("attn_rope takes CUDA tensors: q [T, Hq, D], k [T, Hk, D] or None")
+    if dtype not in DTYPE_CODES:
+        raise ValueError("q must be float32, float16 or bfloat16")
+    T, Hq, D = q.shape
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 3 else -1
+        if k.shape != (T, Hk, D) or k.dtype is not dtype or k.get_device() != index:
+            raise ValueError(f"k must be [{T}, Hk, {D}] of {dtype} on cuda:{index}: got {k.dtype} {tuple(k.shape)}")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [R / 2]")
+    _need(inv_freq, "inv_freq", torch.float64, inv_freq.shape, index)
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be 'half' or 'interleaved': got {layout!r}")
+    B = 0
+    if positions is not None:
+        if q_starts is not None or total_lengths is not None:
+            raise ValueError("give positions, or q_starts and total_lengths")
+        _need(positions, "positions", _I32, (T,), index)
+    else:
+        if q_starts is None or total_lengths is None or total_lengths.dim() != 1:
+            raise ValueError("give positions, or q_starts and total_lengths")
+        B = total_lengths.shape[0]
+        _need(q_starts, "q_starts", _I32, (B + 1,), index)
+        _need(total_lengths, "total_lengths", _I32, (B,), index)
+
+    def made(t, x, name):
+        if x is None:
+            if t is not None:
+                raise ValueError(f"{name} without its input")
+            return None
+        if t is None:
+            return torch.empty(x.shape, dtype=dtype, device=x.device)
+        if t.shape != x.shape or t.dtype is not dtype or t.get_device() != index:
+            raise ValueError(f"{name} must be {dtype} {tuple(x.shape)} on cuda:{index}: got {t.dtype} {tuple(t.shape)}")
+        return t
+
+    q_out, k_out = made(q_out, q, "q_out"), made(k_out, k, "k_out")
+    with _on(index):
+        rc = load_library().attn_rope(
+            q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+            None if k is None else k_out.data_ptr(), inv_freq.data_ptr(),
+            None if positions is None else positions.data_ptr(), None if q_starts is None else q_starts.data_ptr(),
+            None if total_lengths is None else total_lengths.data_ptr(), T, B, Hq, Hk, D, 2 * inv_freq.shape[0],
+            _token_stride(q, "q"), 0 if k is None else _token_stride(k, "k"), _token_stride(q_out, "q_out"),
+            0 if k is None else _token_stride(k_out, "k_out"), ROPE_LAYOUTS[layout], 1 if inverse else 0, scale,
+            DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope")
+    return q_out, k_out
+
+
 def get_device_status(device=None) -> int:
     """Synchronises the current stream and returns (and clears) the device
     status word: ATTN_OK, ATTN_ERR_TIMEOUT, or ATTN_ERR_INVALID_ARG after an
-    attn_fwd_paged_fp8 whose block tables named no block below a length."""
+    attn_fwd_paged_fp8 or attn_fwd_paged_fp4 whose block tables named no block below a length."""
     dev = device if device is not None else torch.cuda.current_device()
     with torch.cuda.device(dev):
         return load_library().attn_get_device_status(_stream_handle(dev))

@@ -1,0 +1,536 @@
+// attn_paged4_dec.cu -- attention over the paged 4-bit KV cache for few query
+// rows per (request, kv head): decode steps and drafted tokens.
+//
+// Bound: HBM, 4.5 bits a value.  At that rate every clock brings 41 values to
+// an SM, which has 128 lanes of arithmetic for them, so what counts is how few
+// instructions a value costs:
+//   S^T = K Q^T, O^T = V^T P^T   mma m16n8k16 in f16, keys (d for V) in M, the
+//   query rows in N.  Its operands are registers, so the bytes go from shared
+//   memory straight into them: one conversion and one multiplication for two
+//   values.  (On the tcgen05 path the widened values would have to be written
+//   to shared memory and read again: 2 + 2 bytes a value, above what shared
+//   memory moves.)
+//   e2m1 * e4m3 is exact in f16 (6 bits, 2^-10 to 2688).  Q is f16 as it is, or
+//   bf16 times a power of two a row that brings its largest element to 2^14,
+//   which loses nothing above 2^-31 of that.  P is f16: 11 bits, 2^-29 of the
+//   row's largest weight or less.
+// Which value lies at which place of an operand is free as long as both sides
+// agree, so every lane reads whole pieces of a row: 16 bytes of a key's K
+// (values 32 t ..), 8 bytes of a key's V, whose 16 values share a scale.
+// Two keys' V codes are put side by side in a byte before they are widened:
+// four instructions for 16 values.
+//
+// Work sharing as in the 8-bit kernel (paged_sched.cuh); a CTA's eight warps
+// take 32 keys each of two tiles of 128 in turn, with their own maximum, sum and
+// O^T, and meet once a unit.  A ninth warp brings tiles by bulk copies, as a
+// block's rows of a head lie together.
+#include <algorithm>
+#include <atomic>
+
+#include "paged4.cuh"
+#include "paged4_internal.h"
+#include "paged_mma.cuh"
+#include "paged_sched.cuh"
+
+namespace gb300_attn {
+namespace {
+
+constexpr int kWarps = 8;                  // warps that compute
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kSub = 32;                   // keys of a warp in a tile
+constexpr int kTileWarps = kPagedKeys / kSub;
+constexpr float kRise = 8.0f;              // the maximum moves when a key passes it by 2^8
+constexpr float kPLog2 = kPaged4DecLog2;   // P is carried as 2^(t - m + 5) <= 2^13
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int NR = 8 * NT;                      // query rows of a unit
+  static constexpr int kRow = D / 2, kScRow = D / kGroup4;  // bytes of a row, and of its scales
+  static constexpr int kData = kPagedKeys * kRow, kSc = kPagedKeys * kScRow;
+  static constexpr int kStage = 2 * (kData + kSc);       // K, V, K scales, V scales
+  static constexpr int kCtas = NT == 1 ? kPaged4DecCtas : 1;
+  static constexpr int kMerge = kWarps * NR * D * 4, kMl = kWarps * NR * 8;
+  static constexpr int kFixed = kMerge + kMl + 256 + (int)sizeof(PagedShare) + 64;
+  static constexpr int kRoom = (kCtas == 2 ? 113 : 226) * 1024 - kFixed;
+  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+  static constexpr int kOffMerge = kStages * kStage;
+  static constexpr int kOffMl = kOffMerge + kMerge;
+  static constexpr int kOffBar = kOffMl + kMl;
+  static constexpr int kOffShare = kOffBar + 256;
+  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 16;
+  static_assert(kStages >= 3 && kStages * 16 <= 256, "stages");
+};
+
+struct Paged4DecParams {
+  Paged4Params p;
+  float scale_log2;     // scale log2 e
+  float sc_in, sc_out;  // soft-cap: sc_out tanh(sc_in s) in log2 units, s the raw score times its row's factor
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// tanh to 2^-20 of itself: 1 - 2 / (e^2|y| + 1), and below 0.3 the Taylor series (the next term is 2^-24 of y).
+__device__ __forceinline__ float tanh20(float y) {
+  const float a = fabsf(y), z = y * y;
+  const float big = copysignf(1.0f - 2.0f * fast_rcp(fast_exp2(a * 2.8853900817779268f) + 1.0f), y);
+  float s = fmaf(z, 62.0f / 2835.0f, -17.0f / 315.0f);
+  s = fmaf(z, s, 2.0f / 15.0f);
+  s = fmaf(z, s, -1.0f / 3.0f);
+  return a < 0.3f ? fmaf(y * z, s, y) : big;
+}
+
+// ------------------------------------------------------------------- loads
+// One warp: lane 4 i + j copies part j (K, V, K scales, V scales) of block i of a tile.  Blocks past the last key are
+// not read; of an entry that names no block the scales become zeros.
+template <int D, int NT>
+__device__ __forceinline__ void load_role(const Paged4Params& P, uint32_t smem, uint32_t bars, PagedWalk<8 * NT> w, int lane) {
+  using C = Cfg<D, NT>;
+  const PagedParams& p = P.c;
+  const int per = kPagedKeys >> p.block_shift, i = lane >> 2, part = lane & 3;
+  const uint32_t row_bytes = part < 2 ? C::kRow : C::kScRow, bytes = p.block_size * row_bytes;
+  const uint32_t block_bytes = p.block_size * 2 * (C::kRow + C::kScRow);
+  const uint8_t* src = part == 0 ? p.k_cache : part == 1 ? p.v_cache : part == 2 ? P.k_sc : P.v_sc;
+  const uint32_t off = (part == 0 ? 0 : part == 1 ? C::kData : part == 2 ? 2 * C::kData : 2 * C::kData + C::kSc) + i * bytes;
+  int g = 0;
+  bool ok = true;
+  for (; ok && !w.done(); w.next(p)) {
+    const int valid = paged_valid(p, w.u.q);
+    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
+    auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
+      const int64_t n = (int64_t)t * per + i;
+      if (i >= per || n >= ((int64_t)valid + p.block_size - 1) >> p.block_shift) return -1;
+      const int e = __ldg(table + n);
+      return e >= 0 && e < p.num_blocks ? e : -2;
+    };
+    int next = w.nt > 0 ? lookup(w.t0) : -1;
+    for (int n = 0; n < w.nt; ++n, ++g) {
+      const int blk = next;
+      if (n + 1 < w.nt) next = lookup(w.t0 + n + 1);
+      const int st = g % C::kStages;
+      const uint32_t full = bars + st * 16, stage = smem + st * C::kStage;
+      if (g >= C::kStages && !wait_warp(full + 8, ((g / C::kStages) - 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
+      const unsigned there = __ballot_sync(0xffffffffu, blk >= 0 && part == 0);
+      if (blk == -2) {
+        if (part == 0) atomicOr(p.status, kStatusBadBlock);
+        if (part >= 2) {
+          for (uint32_t o = 0; o < bytes; o += 16)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(stage + off + o), "r"(0u) : "memory");
+          fence_proxy_async_smem();  // before a later tile's copies to the same place
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(full, __popc(there) * block_bytes);
+      __syncwarp();
+      if (blk >= 0) bulk_load(stage + off, src + ((int64_t)blk * p.Hkv + w.u.kvh) * bytes, bytes, full);
+    }
+  }
+  // every copy lands before the CTA may exit
+  for (int n = max(0, g - C::kStages); n < g; ++n) wait_warp(bars + (n % C::kStages) * 16, (n / C::kStages) & 1, p.timeout_ns, p.status);
+}
+
+// ----------------------------------------------------------------- compute
+template <int D, int NT, bool BF16, bool SOFTCAP>
+__device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t* smem, uint32_t bars, const PagedShare* share,
+                                             PagedWalk<8 * NT> w, int warp, int lane) {
+  using C = Cfg<D, NT>;
+  const Paged4Params& P = DP.p;
+  const PagedParams& p = P.c;
+  constexpr int KS = D / 16, MT = D / 16, NR = C::NR;
+  const int g = lane >> 2, t = lane & 3;
+  const int half = warp / kTileWarps, sub = warp % kTileWarps;
+  int tile = 0;      // tiles of the line
+  bool dead = false;  // a wait ran out: the units' meetings go on, without their tiles
+  for (; !w.done(); w.next(p)) {
+    const PagedUnit& u = w.u;
+    // ---- this lane's part of Q: row g of every 8, values (D / 4) t ..
+    uint32_t qf[NT][KS][2];
+    float fac[NT][2];  // what brings the raw scores of rows 2 t, 2 t + 1 to log2 units
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = j * 8 + g;
+      uint32_t raw[2 * KS];
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i) raw[i] = 0u;
+      if (r < u.rows) {
+        const int x = u.row0 + r, tok = paged_token(p, x);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (int64_t)(u.q.s0 + tok) * p.q_stride +
+                                                          (int64_t)(u.kvh * p.group + x - tok * p.group) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 v = __ldg(src + i);
+          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+        }
+      }
+      float down = 1.0f;  // 1 / the power of two that row g's Q carries
+      if constexpr (BF16) {
+        uint32_t top2 = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) top2 = __vmaxu2(top2, raw[i] & 0x7fff7fffu);
+        uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // up to [2^14, 2^15); rows of zeros and rows that hold an infinity or NaN stay as they are
+        const int e = top == 0u || top >= 0x7f80u ? 0 : min(max(14 - ((int)(top >> 7) - 127), -120), 120);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xffff0000u) * up);
+          raw[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      const float kh = P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f;
+      down *= (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh;
+      fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+      fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        qf[j][s][0] = raw[2 * s];
+        qf[j][s][1] = raw[2 * s + 1];
+      }
+    }
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[j][i][k] = 0.0f;
+      m[j][0] = m[j][1] = kNone;
+      l[j][0] = l[j][1] = 0.0f;
+    }
+    const int valid = paged_valid(p, u.q);
+    const int full_lo = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).x;
+    const int full_hi = paged_limits(p, u.q, paged_token(p, u.row0)).y;
+    // ---- this warp's keys
+    for (int n = (tile ^ half) & 1; n < w.nt && !dead; n += 2) {
+      const int gt = tile + n, st = gt % C::kStages;
+      if (!wait_warp(bars + st * 16, (gt / C::kStages) & 1, p.timeout_ns, p.status)) { dead = true; break; }
+      const int key0 = (w.t0 + n) * kPagedKeys + sub * kSub;
+      const uint8_t* stage = smem + st * C::kStage;
+      if (key0 < valid) {
+        const uint8_t* kd = stage + sub * kSub * C::kRow;
+        const uint8_t* ksc = stage + 2 * C::kData + sub * kSub * C::kScRow;
+        float s[NT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.0f;
+          uint32_t wd[2][KS / 2], sc[2][2];  // rows g and g + 8: codes, and their scales as pairs
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int row = mt * 16 + x * 8 + g;
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kd + row * C::kRow + t * 16);
+              wd[x][0] = v.x; wd[x][1] = v.y; wd[x][2] = v.z; wd[x][3] = v.w;
+              const uint32_t h = widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ksc + row * C::kScRow + t * 2));
+              sc[x][0] = __byte_perm(h, 0, 0x1010);
+              sc[x][1] = __byte_perm(h, 0, 0x3232);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(kd + row * C::kRow + t * 8);
+              wd[x][0] = v.x; wd[x][1] = v.y;
+              const uint32_t h = widen_e4m3x2(ksc[row * C::kScRow + t]);
+              sc[x][0] = sc[x][1] = __byte_perm(h, 0, 0x1010);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < KS / 2; ++i) {  // eight values a lane: two steps of 16
+            uint32_t a[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              widen8(wd[x][i], a[x][0], a[x][1], a[x][2], a[x][3]);
+              const uint32_t f = sc[x][D == 128 ? i >> 1 : 0];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) a[x][k] = mul_f16x2(a[x][k], f);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              mma16816(s[j][mt], a[0][0], a[1][0], a[0][1], a[1][1], qf[j][2 * i][0], qf[j][2 * i][1]);
+              mma16816(s[j][mt], a[0][2], a[1][2], a[0][3], a[1][3], qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+            }
+          }
+        }
+        // ---- scores in log2 units
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              s[j][mt][k] *= fac[j][k & 1];
+              if constexpr (SOFTCAP) s[j][mt][k] = DP.sc_out * tanh20(s[j][mt][k]);
+            }
+        if (key0 < full_lo || key0 + kSub > full_hi) {  // some key is hidden from some row
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int r = j * 8 + 2 * t + x;
+              const int2 lim = r < u.rows ? paged_limits(p, u.q, paged_token(p, u.row0 + r)) : make_int2(0, 0);
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int key = key0 + mt * 16 + k * 8 + g;
+                  if (key < lim.x || key >= lim.y) s[j][mt][2 * k + x] = -INFINITY;
+                }
+            }
+        }
+        // ---- the running maxima, which all lanes of a row share, move only when a key passes them by far
+        float mx[NT][2];
+        bool rise = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            mx[j][x] = fmaxf(fmaxf(s[j][0][x], s[j][0][x + 2]), fmaxf(s[j][1][x], s[j][1][x + 2]));
+            rise |= mx[j][x] > m[j][x] + kRise;
+          }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float al[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float v = mx[j][x];
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              v = v > m[j][x] + kRise ? v : m[j][x];
+              al[x] = fast_exp2(m[j][x] - v);
+              l[j][x] *= al[x];
+              m[j][x] = v;
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[j][i][k] *= al[k & 1];
+          }
+        }
+        // ---- weights, transposed into the second product's operand
+        uint32_t pf[NT][2][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float off0 = kPLog2 - m[j][0], off1 = kPLog2 - m[j][1];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float a = fast_exp2(s[j][mt][2 * k] + off0), b = fast_exp2(s[j][mt][2 * k + 1] + off1);
+              l[j][0] += a;
+              l[j][1] += b;
+              const __half2 h = __floats2half2_rn(a, b);
+              pf[j][mt][k] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+            }
+        }
+        // ---- O^T += V^T P^T: lane (g, t) has values (D / 8) g .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        const uint8_t* vd = stage + C::kData + sub * kSub * C::kRow;
+        const uint8_t* vsc = stage + 2 * C::kData + C::kSc + sub * kSub * C::kScRow;
+        constexpr int VW = D / 64;  // words of a lane's values of a key
+        const int gs = D == 128 ? g : g >> 1;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          uint32_t wv[4][VW], sb[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = kt * 16 + (x >> 1) * 8 + 2 * t + (x & 1);
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(vd + row * C::kRow + g * 8);
+              wv[x][0] = v.x;
+              wv[x][1] = v.y;
+            } else {
+              wv[x][0] = *reinterpret_cast<const uint32_t*>(vd + row * C::kRow + g * 4);
+            }
+            sb[x] = vsc[row * C::kScRow + gs];
+            if (key0 + row >= valid) sb[x] = 0u;  // slots past the last key may hold NaN scales
+          }
+          const uint32_t s0 = widen_e4m3x2(sb[0] | sb[1] << 8), s1 = widen_e4m3x2(sb[2] | sb[3] << 8);
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            widen8(select_bits(wv[0][i], wv[1][i] << 4, 0x0f0f0f0fu), a0[0], a0[1], a0[2], a0[3]);
+            widen8(select_bits(wv[0][i] >> 4, wv[1][i], 0x0f0f0f0fu), a1[0], a1[1], a1[2], a1[3]);
+            widen8(select_bits(wv[2][i], wv[3][i] << 4, 0x0f0f0f0fu), a2[0], a2[1], a2[2], a2[3]);
+            widen8(select_bits(wv[2][i] >> 4, wv[3][i], 0x0f0f0f0fu), a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              a0[k] = mul_f16x2(a0[k], s0);
+              a1[k] = mul_f16x2(a1[k], s0);
+              a2[k] = mul_f16x2(a2[k], s1);
+              a3[k] = mul_f16x2(a3[k], s1);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma16816(o[j][4 * i + k], a0[k], a1[k], a2[k], a3[k], pf[j][kt][0], pf[j][kt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + st * 16 + 8);
+    }
+    tile += w.nt;
+
+    // ---- the warps meet: rows' maxima, sums and O, joined in the order of the warps
+    float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+    float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float v = l[j][x];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        const int r = j * 8 + 2 * t + x;
+        if (g == 0) ml[warp * NR + r] = make_float2(m[j][x], v);
+        float* dst = merge + (warp * NR + r) * D + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < MT / 2; ++i)
+          *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(o[j][2 * i][x], o[j][2 * i][x + 2], o[j][2 * i + 1][x], o[j][2 * i + 1][x + 2]);
+      }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    const float vh = P.v_heads ? __ldg(P.v_heads + u.kvh) : 1.0f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = j * 8 + warp;
+      constexpr int V = D / 32;
+      float M = kNone, L = 0.0f, acc[V];
+#pragma unroll
+      for (int c = 0; c < kWarps; ++c) M = fmaxf(M, ml[c * NR + r].x);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kWarps; ++c) {
+        const float2 x = ml[c * NR + r];
+        const float wgt = fast_exp2(x.x - M);
+        L = fmaf(wgt, x.y, L);
+        const float* src = merge + (c * NR + r) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          acc[0] = fmaf(wgt, y.x, acc[0]); acc[1] = fmaf(wgt, y.y, acc[1]);
+          acc[2] = fmaf(wgt, y.z, acc[2]); acc[3] = fmaf(wgt, y.w, acc[3]);
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(wgt, y.x, acc[0]); acc[1] = fmaf(wgt, y.y, acc[1]);
+        }
+      }
+      if (r < u.rows) {
+        if (w.whole) {
+          const int x = u.row0 + r, tok = paged_token(p, x);
+          const int64_t row = (int64_t)(u.q.s0 + tok) * p.Hq + u.kvh * p.group + x - tok * p.group;
+          const float inv = L == 0.0f ? 0.0f : vh / L;
+          uint32_t y[V / 2];
+#pragma unroll
+          for (int v = 0; v < V / 2; ++v)
+            y[v] = (uint32_t)to_bits<BF16>(acc[2 * v] * inv) | (uint32_t)to_bits<BF16>(acc[2 * v + 1] * inv) << 16;
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + lane * V;
+          if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+          else *reinterpret_cast<uint32_t*>(dst) = y[0];
+          if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + (__log2f(L) - kPLog2)) * kLn2;
+        } else {
+          const int64_t row = (int64_t)(2 * blockIdx.x + (w.head ? 1 : 0)) * NR + r;
+          float* dst = P.ws_o + row * D + lane * V;
+          if constexpr (V == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * vh, acc[1] * vh, acc[2] * vh, acc[3] * vh);
+          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * vh, acc[1] * vh);
+          if (lane == 0) P.ws_ml[row] = make_float2(M, L * kPagedSumFactor);
+        }
+      }
+    }
+    if (!w.whole && w.head && threadIdx.x == 0) {
+      PagedCut c;
+      c.parts = paged_parts(w, share);
+      c.token0 = u.q.s0;
+      c.head0 = u.kvh * p.group;
+      c.row0 = u.row0;
+      c.rows = u.rows;
+      P.cuts[blockIdx.x] = c;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");  // the rows have been read
+  }
+}
+
+template <int D, int NT, bool BF16, bool SOFTCAP>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_paged4_dec_kernel(const __grid_constant__ Paged4DecParams DP) {
+  using C = Cfg<D, NT>;
+  const PagedParams& p = DP.p.c;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem), bars = base + C::kOffBar;
+  PagedShare* share = reinterpret_cast<PagedShare*>(smem + C::kOffShare);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bars + i * 16, 1);              // full: the loading warp's, and its copies
+      mbar_init(bars + i * 16 + 8, kTileWarps);  // empty
+    }
+    mbar_init_fence();
+    DP.p.cuts[blockIdx.x].parts = 0;
+  }
+  paged_share<8 * NT, kThreads>(p, share);
+  __syncthreads();
+  PagedWalk<8 * NT> w;
+  w.begin(p, share);
+  if (warp == kWarps) load_role<D, NT>(DP.p, base, bars, w, lane);
+  else compute_role<D, NT, BF16, SOFTCAP>(DP, smem, bars, share, w, warp, lane);
+}
+
+template <int D, int NT, bool BF16, bool SOFTCAP>
+cudaError_t launch_k(const Paged4DecParams& DP, int grid, cudaStream_t stream) {
+  auto kernel = attn_paged4_dec_kernel<D, NT, BF16, SOFTCAP>;
+  constexpr int smem = Cfg<D, NT>::kSmem;
+  static std::atomic<bool> ready[128];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128 || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  kernel<<<grid, kThreads, smem, stream>>>(DP);
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_n(const Paged4DecParams& DP, int grid, bool bf16, cudaStream_t stream) {
+  if (DP.p.c.softcap > 0.0f) return bf16 ? launch_k<D, NT, true, true>(DP, grid, stream) : launch_k<D, NT, false, true>(DP, grid, stream);
+  return bf16 ? launch_k<D, NT, true, false>(DP, grid, stream) : launch_k<D, NT, false, false>(DP, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_paged4_dec(const Paged4Params& p, int rows, int grid, bool bf16, cudaStream_t stream) {
+  Paged4DecParams DP{};
+  DP.p = p;
+  DP.scale_log2 = (float)((double)p.c.scale * 1.4426950408889634);
+  if (p.c.softcap > 0.0f) {
+    DP.sc_in = (float)((double)p.c.scale / (double)p.c.softcap);
+    DP.sc_out = (float)((double)p.c.softcap * 1.4426950408889634);
+  }
+  if (p.c.D == 128) return rows == 8 ? launch_n<128, 1>(DP, grid, bf16, stream) : launch_n<128, 2>(DP, grid, bf16, stream);
+  return rows == 8 ? launch_n<64, 1>(DP, grid, bf16, stream) : launch_n<64, 2>(DP, grid, bf16, stream);
+}
+
+}  // namespace gb300_attn

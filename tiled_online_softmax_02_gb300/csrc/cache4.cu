@@ -1,0 +1,221 @@
+// cache4.cu -- rows into the paged 4-bit cache, and back out of it.
+//
+// A group is 16 values of a row, with the kv head's factor h (1 where there is
+// none) and g the largest finite |x|:
+//   s    = e4m3(g / (6 h)), at least 2^-9, at most 448
+//   code = e2m1(x / (s h)), to nearest even, cut at 6
+// both quotients in fp32, which settles e4m3's and e2m1's ties as exact ones
+// would: a quotient next to a border of so few bits is never rounded onto it.
+// A group with a NaN gets the scale NaN and zeros.  value = code * s * h.
+//
+// 16-bit rows under a power-of-two h take x * (1 / (s h)) in place of the
+// quotient (the fp32 division costs twelve instructions a value): the product
+// is off by 2^-23 of itself, so it is brought to the nearest multiple of
+// 2^-16 before the last rounding.  Borders are multiples of 2^-2, which that
+// restores, and any other quotient of an 11-bit x lies 2^-13 or more from one.
+//
+// Bound: HBM for prompts, and for a few tokens the chain of slot, row, group
+// maximum and store.  A thread has one group: its 16 values are two or four
+// wide loads in flight beside the slot's, no thread waits for another, and the
+// 32 lanes of a warp write whole sectors (rows of one head that follow one
+// another in a block).
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "../../include/attn.h"
+#include "paged4.cuh"
+#include "paged4_internal.h"
+
+namespace gb300_attn {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void widen16(const uint4 (&v)[sizeof(T)], float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        x[4 * i + j] = __uint_as_float(w[j]);
+      } else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        x[8 * i + 2 * j] = f.x;
+        x[8 * i + 2 * j + 1] = f.y;
+      } else {
+        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+// The token, head, cache and group of a thread: lanes go over a row's groups, then over tokens.
+template <int D>
+struct Place {
+  static constexpr int kPer = D / kGroup4, kTokens = kThreads / kPer;
+  int t, h, which, part;
+  bool there;
+  __device__ __forceinline__ Place(const Cache4Params& p, int64_t unit) {
+    which = (int)(unit & 1);
+    const int64_t u = unit >> 1;
+    const int64_t tile = u / p.Hkv;
+    h = (int)(u - tile * p.Hkv);
+    const int64_t tok = tile * kTokens + threadIdx.x / kPer;
+    there = tok < p.T;
+    t = there ? (int)tok : 0;
+    part = threadIdx.x % kPer;
+  }
+  // index of the row in the cache; -1: no row
+  __device__ __forceinline__ int64_t row(const Cache4Params& p) const {
+    const int64_t s = __ldg(p.slot_map + t);
+    if (!there || s < 0 || s >= p.num_slots) return -1;
+    return ((s >> p.block_shift) * p.Hkv + h) * p.block_size + (s & (p.block_size - 1));
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ Cache4Params p, int64_t units) {
+  using P = Place<D>;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const P at(p, unit);
+    const T* src = static_cast<const T*>(at.which ? p.x[1] : p.x[0]) +
+                   (int64_t)at.t * (at.which ? p.stride[1] : p.stride[0]) + at.h * D + at.part * kGroup4;
+    uint4 v[sizeof(T)];
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    const float* heads = at.which ? p.heads[1] : p.heads[0];
+    const float hs = heads ? __ldg(heads + at.h) : 1.0f;
+    const int64_t row = at.row(p);
+    if (row < 0) continue;
+    float x[16];
+    widen16<T>(v, x);
+    // magnitudes order as their bits; not finite from 0x7f800000 on
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    bool nan = false;
+    if (top >= 0x7f800000u) {  // infinities set no scale
+      nan = top > 0x7f800000u;
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
+        top = a < 0x7f800000u ? max(top, a) : top;
+      }
+    }
+    uint32_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f * hs), __NV_SATFINITE, __NV_E4M3);
+    sb = max(sb & 0x7fu, 1u);
+    const float unit_v = e4m3_value(sb) * hs;
+    uint32_t w[2] = {0u, 0u};
+    const uint32_t hb = __float_as_uint(hs);
+    if (!nan) {
+      if (sizeof(T) == 2 && (hb & 0x7fffffu) == 0u && hb >= (27u << 23) && hb <= (227u << 23)) {
+        const float r = __fdiv_rn(1.0f, unit_v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t sign = __float_as_uint(x[i]) & 0x80000000u;
+          const float c = __uint_as_float(sign | 0x43400000u);  // 192 with x's sign: steps of 2^-16
+          x[i] = __uint_as_float(__float_as_uint(__fsub_rn(__fmaf_rn(x[i], r, c), c)) | sign);  // zeros keep it too
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], unit_v);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_E2M1, cudaRoundNearest) << (8 * (i & 3));
+    } else {
+      sb = 0x7fu;
+    }
+    uint8_t* cache = at.which ? p.cache[1] : p.cache[0];
+    uint8_t* scales = at.which ? p.scales[1] : p.scales[0];
+    *reinterpret_cast<uint2*>(cache + row * (D / 2) + at.part * 8) = make_uint2(w[0], w[1]);
+    scales[row * (D / kGroup4) + at.part] = (uint8_t)sb;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ Cache4Params p, int64_t units) {
+  using P = Place<D>;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const P at(p, unit);
+    if (!at.there) continue;
+    const int64_t row = at.row(p);
+    const float* heads = at.which ? p.heads[1] : p.heads[0];
+    const float hs = heads ? __ldg(heads + at.h) : 1.0f;
+    uint2 code = make_uint2(0u, 0u);
+    float s = 0.0f;
+    if (row >= 0) {
+      const uint8_t* cache = at.which ? p.cache[1] : p.cache[0];
+      const uint8_t* scales = at.which ? p.scales[1] : p.scales[0];
+      code = __ldg(reinterpret_cast<const uint2*>(cache + row * (D / 2) + at.part * 8));
+      s = e4m3_value(__ldg(scales + row * (D / kGroup4) + at.part));
+    }
+    uint32_t h[8];
+    widen8(code.x, h[0], h[1], h[2], h[3]);
+    widen8(code.y, h[4], h[5], h[6], h[7]);
+    T* dst = static_cast<T*>(at.which ? p.x[1] : p.x[0]) + (int64_t)at.t * (at.which ? p.stride[1] : p.stride[0]) +
+             (int64_t)at.h * (at.which ? p.head_stride[1] : p.head_stride[0]) + at.part * kGroup4;
+    uint32_t o[4 * sizeof(T)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      f.x = f.x * s * hs;  // code * s is exact
+      f.y = f.y * s * hs;
+      if constexpr (sizeof(T) == 4) {
+        o[2 * i] = __float_as_uint(f.x);
+        o[2 * i + 1] = __float_as_uint(f.y);
+      } else if constexpr (std::is_same<T, __half>::value) {
+        const __half2 y = __floats2half2_rn(f.x, f.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+      } else {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i)
+      reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(const Cache4Params& p, bool read, cudaStream_t stream) {
+  const int64_t units = ((int64_t)p.T + Place<D>::kTokens - 1) / Place<D>::kTokens * p.Hkv * 2;
+  const unsigned grid = (unsigned)std::min<int64_t>(units, 1 << 30);
+  if (read) cache4_read_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, units);
+  else cache4_append_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, units);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_d(const Cache4Params& p, bool read, cudaStream_t stream) {
+  return p.D == 128 ? launch<T, 128>(p, read, stream) : launch<T, 64>(p, read, stream);
+}
+
+cudaError_t launch_t(const Cache4Params& p, int dtype, bool read, cudaStream_t stream) {
+  if (dtype == ATTN_BF16) return launch_d<__nv_bfloat16>(p, read, stream);
+  if (dtype == ATTN_F16) return launch_d<__half>(p, read, stream);
+  return launch_d<float>(p, read, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache4_append(const Cache4Params& p, int dtype, cudaStream_t stream) {
+  return launch_t(p, dtype, false, stream);
+}
+
+cudaError_t launch_cache4_read(const Cache4Params& p, int dtype, cudaStream_t stream) {
+  return launch_t(p, dtype, true, stream);
+}
+
+}  // namespace gb300_attn

@@ -119,10 +119,8 @@ extern "C" int attn_cache_append_fp8(const void* k, const void* v, const int64_t
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
-namespace {
-
 // SMs of the current device, looked up once for each.
-int sm_count() {
+int gb300_attn::paged_sm_count() {
   static std::atomic<int> cache[128];
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return sms;
@@ -132,6 +130,8 @@ int sm_count() {
   cache[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
+
+namespace {
 
 // How a call of attn_fwd_paged_fp8 runs: rows of a unit, CTAs, and the parts of the workspace.
 struct PagedPlan {
@@ -151,7 +151,7 @@ PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_t
   // us, in a T of 2048 rows 204; 63 of them with one chunk of 2048 332 us, where the two alone take 86 and 116.
   const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
   pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedTcRows;
-  int64_t most = (int64_t)sm_count() * (pl.rows == kPagedTcRows ? 1 : kPagedDecCtas);
+  int64_t most = (int64_t)paged_sm_count() * (pl.rows == kPagedTcRows ? 1 : kPagedDecCtas);
   const size_t slots = 2 * (size_t)most * pl.rows;  // the choice below needs no more
   // With little to read a call is the way to the first result and the join of the parts, both shorter in units of 8
   // rows, and reading the keys once a unit costs nothing yet.  What there may be to read: the tables' width.
@@ -160,16 +160,16 @@ PagedPlan paged_plan(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_t
   // rows, one request of 4K 27 against 31; two of them 37 against 26.
   const int64_t eights = B * Hkv * ((rows + 7) / 8), small = (int64_t)1 << 13;  // key tiles
   if (pl.rows == 16 ? eights * max_tiles <= 2 * small
-                    : pl.rows == kPagedTcRows && eights <= sm_count() && eights * max_tiles <= small) {
+                    : pl.rows == kPagedTcRows && eights <= paged_sm_count() && eights * max_tiles <= small) {
     pl.rows = 8;
-    most = (int64_t)sm_count() * kPagedDecCtas;
+    most = (int64_t)paged_sm_count() * kPagedDecCtas;
   }
   // no more CTAs than there can be tiles
   const int64_t units = (T * group / pl.rows + B) * Hkv;
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
   pl.ml_at = slots * D * 4;
   pl.cuts_at = pl.ml_at + slots * 8;
-  pl.bytes = pl.cuts_at + (size_t)sm_count() * kPagedDecCtas * sizeof(PagedCut);
+  pl.bytes = pl.cuts_at + (size_t)paged_sm_count() * kPagedDecCtas * sizeof(PagedCut);
   return pl;
 }
 

@@ -77,6 +77,7 @@ struct PagedParams {
   int* status;
 };
 
+int paged_sm_count();  // SMs of the current device
 cudaError_t launch_cache_assign(const AssignParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const AppendParams& p, int dtype, cudaStream_t stream);
 
