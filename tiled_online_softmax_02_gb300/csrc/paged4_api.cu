@@ -216,7 +216,7 @@ Plan4 plan4(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
   if (T <= 0 || B <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0) return pl;
   const int group = Hq / Hkv, sms = paged_sm_count();
   const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;  // per (request, kv head) of an even batch
-  pl.rows = rows <= 8 ? 8 : 16;
+  pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedTcRows;
   const int64_t most = (int64_t)sms * (pl.rows == 8 ? kPaged4DecCtas : 1);
   const int64_t units = (T * group / pl.rows + B) * Hkv;  // no more CTAs than there can be tiles
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
@@ -312,7 +312,8 @@ extern "C" int attn_fwd_paged_fp4(const void* q, const void* k_cache, const void
   P.cuts = reinterpret_cast<PagedCut*>(static_cast<char*>(workspace) + plan.cuts_at);
   const bool bf16 = dtype == ATTN_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_attn_paged4_dec(P, plan.rows, plan.grid, bf16, st);
+  cudaError_t e = plan.rows == kPagedTcRows ? launch_attn_paged4_tc(P, plan.grid, bf16, st)
+                                            : launch_attn_paged4_dec(P, plan.rows, plan.grid, bf16, st);
   if (e == cudaSuccess && max_tiles > 1) {
     PagedLaunch L{};
     L.c = p;
@@ -321,7 +322,7 @@ extern "C" int attn_fwd_paged_fp4(const void* q, const void* k_cache, const void
     L.ws_o = P.ws_o;
     L.ws_ml = P.ws_ml;
     L.cuts = P.cuts;
-    L.ml_log2 = kPaged4DecLog2 - kPagedSumLog2;
+    L.ml_log2 = (plan.rows == kPagedTcRows ? kPagedTcLog2 : kPaged4DecLog2) - kPagedSumLog2;
     e = launch_attn_paged_join(L, bf16, st);
   }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);

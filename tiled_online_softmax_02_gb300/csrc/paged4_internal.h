@@ -54,11 +54,11 @@ struct Paged4Params {
 
 constexpr int kPaged4DecCtas = 2;        // CTAs of the few-rows kernel on an SM, in units of 8 rows
 constexpr float kPaged4DecLog2 = 5.0f;   // log2 of the factor that P carries
-constexpr int kPaged4MaxDecRows = 16;
 
 cudaError_t launch_cache4_append(const Cache4Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_cache4_read(const Cache4Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, bool interleaved, int dtype, cudaStream_t stream);
-cudaError_t launch_attn_paged4_dec(const Paged4Params& p, int rows, int grid, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn_paged4_dec(const Paged4Params& p, int rows, int grid, bool bf16, cudaStream_t stream);  // rows 8 or 16
+cudaError_t launch_attn_paged4_tc(const Paged4Params& p, int grid, bool bf16, cudaStream_t stream);  // rows kPagedTcRows
 
 }  // namespace gb300_attn
