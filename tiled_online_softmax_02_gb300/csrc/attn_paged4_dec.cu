@@ -20,10 +20,10 @@
 // Two keys' V codes are put side by side in a byte before they are widened:
 // four instructions for 16 values.
 //
-// Work sharing as in the 8-bit kernel (paged_sched.cuh); a CTA's eight warps
-// take 32 keys each of two tiles of 128 in turn, with their own maximum, sum and
-// O^T, and meet once a unit.  A ninth warp brings tiles by bulk copies, as a
-// block's rows of a head lie together.
+// Work sharing as in the 8-bit kernel (paged_sched.cuh); a CTA's warps take 32
+// keys each in turn, with their own maximum, sum and O^T, and meet once a unit.
+// Every warp brings its own keys by 16-byte asynchronous copies, two sub-tiles
+// ahead, across units too: no warp waits for another between two meetings.
 #include <algorithm>
 #include <atomic>
 
@@ -35,30 +35,24 @@
 namespace gb300_attn {
 namespace {
 
-constexpr int kWarps = 8;                  // warps that compute
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kSub = 32;                   // keys of a warp in a tile
-constexpr int kTileWarps = kPagedKeys / kSub;
+constexpr int kSub = 32;                   // keys a warp takes at a time
 constexpr float kRise = 8.0f;              // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPaged4DecLog2;   // P is carried as 2^(t - m + 5) <= 2^13
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int NR = 8 * NT;                      // query rows of a unit
-  static constexpr int kRow = D / 2, kScRow = D / kGroup4;  // bytes of a row, and of its scales
-  static constexpr int kData = kPagedKeys * kRow, kSc = kPagedKeys * kScRow;
-  static constexpr int kStage = 2 * (kData + kSc);       // K, V, K scales, V scales
+  static constexpr int kWarps = 8, kThreads = 32 * kWarps;
   static constexpr int kCtas = NT == 1 ? kPaged4DecCtas : 1;
-  static constexpr int kMerge = kWarps * NR * D * 4, kMl = kWarps * NR * 8;
-  static constexpr int kFixed = kMerge + kMl + 256 + (int)sizeof(PagedShare) + 64;
-  static constexpr int kRoom = (kCtas == 2 ? 113 : 226) * 1024 - kFixed;
-  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
-  static constexpr int kOffMerge = kStages * kStage;
-  static constexpr int kOffMl = kOffMerge + kMerge;
-  static constexpr int kOffBar = kOffMl + kMl;
-  static constexpr int kOffShare = kOffBar + 256;
-  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 16;
-  static_assert(kStages >= 3 && kStages * 16 <= 256, "stages");
+  static constexpr int kStages = NT == 1 ? 2 : 4;
+  static constexpr int kRow = D / 2, kScRow = D / kGroup4;  // bytes of a row, and of its scales
+  static constexpr int kData = kSub * kRow, kSc = kSub * kScRow;
+  static constexpr int kStage = 2 * (kData + kSc);       // K, V, K scales, V scales
+  static constexpr int kOffMerge = kWarps * kStages * kStage;
+  static constexpr int kOffMl = kOffMerge + kWarps * NR * D * 4;
+  static constexpr int kOffShare = kOffMl + kWarps * NR * 8;
+  static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare);
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 232448, "shared memory");
 };
 
 struct Paged4DecParams {
@@ -82,11 +76,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // tanh to 2^-20 of itself: 1 - 2 / (e^2|y| + 1), and below 0.3 the Taylor series (the next term is 2^-24 of y).
 __device__ __forceinline__ float tanh20(float y) {
@@ -99,67 +95,93 @@ __device__ __forceinline__ float tanh20(float y) {
 }
 
 // ------------------------------------------------------------------- loads
-// One warp: lane 4 i + j copies part j (K, V, K scales, V scales) of block i of a tile.  Blocks past the last key are
-// not read; of an entry that names no block the scales become zeros.
+// A warp's sub-tiles of a unit's segment: first, first + kWarps, ... below end (in sub-tiles of the request's keys).
+struct Subs {
+  int first, count;
+};
+
+template <int NT, int W>
+__device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 * NT>& w, int warp) {
+  const PagedUnit& u = w.u;
+  const int lo = paged_limits(p, u.q, paged_token(p, u.row0)).x, hi = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).y;
+  const int a = max(w.t0 * (kPagedKeys / kSub), lo / kSub) + warp;
+  const int e = min((w.t0 + w.nt) * (kPagedKeys / kSub), (int)(((int64_t)hi + kSub - 1) / kSub));
+  return Subs{a, w.nt > 0 && a < e ? (e - a + W - 1) / W : 0};
+}
+
+// The block-table entry of this lane's half of a sub-tile (lanes 0-15: its first 16 keys): -1 past the last key, -2 names
+// no block.
+__device__ __forceinline__ int entry_of(const PagedParams& p, const int32_t* table, int valid, int sub, int lane) {
+  const int64_t key = (int64_t)sub * kSub + (lane & 16);
+  if (key >= valid) return -1;
+  const int e = __ldg(table + (key >> p.block_shift));
+  return e >= 0 && e < p.num_blocks ? e : -2;
+}
+
+// Copies a sub-tile into a stage: codes and scales as they lie, zeros for what has no block.
 template <int D, int NT>
-__device__ __forceinline__ void load_role(const Paged4Params& P, uint32_t smem, uint32_t bars, PagedWalk<8 * NT> w, int lane) {
+__device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, int kvh, int sub, int entry, int lane) {
   using C = Cfg<D, NT>;
   const PagedParams& p = P.c;
-  const int per = kPagedKeys >> p.block_shift, i = lane >> 2, part = lane & 3;
-  const uint32_t row_bytes = part < 2 ? C::kRow : C::kScRow, bytes = p.block_size * row_bytes;
-  const uint32_t block_bytes = p.block_size * 2 * (C::kRow + C::kScRow);
-  const uint8_t* src = part == 0 ? p.k_cache : part == 1 ? p.v_cache : part == 2 ? P.k_sc : P.v_sc;
-  const uint32_t off = (part == 0 ? 0 : part == 1 ? C::kData : part == 2 ? 2 * C::kData : 2 * C::kData + C::kSc) + i * bytes;
-  int g = 0;
-  bool ok = true;
-  for (; ok && !w.done(); w.next(p)) {
-    const int valid = paged_valid(p, w.u.q);
-    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
-    auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
-      const int64_t n = (int64_t)t * per + i;
-      if (i >= per || n >= ((int64_t)valid + p.block_size - 1) >> p.block_shift) return -1;
-      const int e = __ldg(table + n);
-      return e >= 0 && e < p.num_blocks ? e : -2;
-    };
-    int next = w.nt > 0 ? lookup(w.t0) : -1;
-    for (int n = 0; n < w.nt; ++n, ++g) {
-      const int blk = next;
-      if (n + 1 < w.nt) next = lookup(w.t0 + n + 1);
-      const int st = g % C::kStages;
-      const uint32_t full = bars + st * 16, stage = smem + st * C::kStage;
-      if (g >= C::kStages && !wait_warp(full + 8, ((g / C::kStages) - 1) & 1, p.timeout_ns, p.status)) { ok = false; break; }
-      const unsigned there = __ballot_sync(0xffffffffu, blk >= 0 && part == 0);
-      if (blk == -2) {
-        if (part == 0) atomicOr(p.status, kStatusBadBlock);
-        if (part >= 2) {
-          for (uint32_t o = 0; o < bytes; o += 16)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(stage + off + o), "r"(0u) : "memory");
-          fence_proxy_async_smem();  // before a later tile's copies to the same place
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(full, __popc(there) * block_bytes);
-      __syncwarp();
-      if (blk >= 0) bulk_load(stage + off, src + ((int64_t)blk * p.Hkv + w.u.kvh) * bytes, bytes, full);
-    }
+  if (entry == -2 && (lane & 15) == 0) atomicOr(p.status, kStatusBadBlock);
+  const bool split = p.block_size < kSub;  // two blocks of 16
+  const int within = split ? 0 : (sub * kSub) & (p.block_size - 1);
+  int64_t row[2];  // of the cache, of the sub-tile's first key as each half sees it
+  bool there[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = __shfl_sync(0xffffffffu, entry, 16 * h);
+    there[h] = e >= 0;
+    row[h] = ((int64_t)max(e, 0) * p.Hkv + kvh) * p.block_size + within - (split ? 16 * h : 0);
   }
-  // every copy lands before the CTA may exit
-  for (int n = max(0, g - C::kStages); n < g; ++n) wait_warp(bars + (n % C::kStages) * 16, (n / C::kStages) & 1, p.timeout_ns, p.status);
+  // a block past the last key may follow one that is there in the same block of 32 or more: same rows either way
+  constexpr int kN = C::kData / 512;  // pieces of 16 bytes a lane takes of K, and of V
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    const int h = j / (kN / 2), at = j * 512 + lane * 16;
+    const int64_t off = row[h] * C::kRow + at;
+    copy16(stage + at, p.k_cache + (there[h] ? off : 0), there[h]);
+    copy16(stage + C::kData + at, p.v_cache + (there[h] ? off : 0), there[h]);
+  }
+  constexpr int kL = C::kSc / 16;  // lanes for K's scales, and for V's
+  if (lane < 2 * kL) {
+    const int l = lane & (kL - 1);
+    const int h = l / (kL / 2);
+    const bool ok = h ? there[1] : there[0];
+    const int64_t off = (h ? row[1] : row[0]) * C::kScRow + l * 16;
+    copy16(stage + 2 * C::kData + lane * 16, (lane < kL ? P.k_sc : P.v_sc) + (ok ? off : 0), ok);
+  }
 }
 
 // ----------------------------------------------------------------- compute
 template <int D, int NT, bool BF16, bool SOFTCAP>
-__device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t* smem, uint32_t bars, const PagedShare* share,
+__device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t* smem, const PagedShare* share,
                                              PagedWalk<8 * NT> w, int warp, int lane) {
   using C = Cfg<D, NT>;
   const Paged4Params& P = DP.p;
   const PagedParams& p = P.c;
-  constexpr int KS = D / 16, MT = D / 16, NR = C::NR;
+  constexpr int KS = D / 16, MT = D / 16, NR = C::NR, S = C::kStages, W = C::kWarps;
   const int g = lane >> 2, t = lane & 3;
-  const int half = warp / kTileWarps, sub = warp % kTileWarps;
-  int tile = 0;      // tiles of the line
-  bool dead = false;  // a wait ran out: the units' meetings go on, without their tiles
-  for (; !w.done(); w.next(p)) {
+  uint8_t* ring = smem + warp * (S * C::kStage);
+  const uint32_t ring_s = smem_u32(ring);
+  Subs subs;
+  int entry;  // of the sub-tile that is loaded next
+  auto prefetch = [&]() {  // the first sub-tiles of the walk's unit
+    subs = subs_of<NT, W>(p, w, warp);
+    const int valid = paged_valid(p, w.u.q);
+    const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
+    int first[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) first[s] = s < subs.count ? entry_of(p, table, valid, subs.first + s * W, lane) : -1;
+    entry = S < subs.count ? entry_of(p, table, valid, subs.first + S * W, lane) : -1;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, first[s], lane);
+      copies_commit();
+    }
+  };
+  if (!w.done()) prefetch();
+  while (!w.done()) {
     const PagedUnit& u = w.u;
     // ---- this lane's part of Q: row g of every 8, values (D / 4) t ..
     uint32_t qf[NT][KS][2];
@@ -222,14 +244,15 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
     const int full_lo = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).x;
     const int full_hi = paged_limits(p, u.q, paged_token(p, u.row0)).y;
     // ---- this warp's keys
-    for (int n = (tile ^ half) & 1; n < w.nt && !dead; n += 2) {
-      const int gt = tile + n, st = gt % C::kStages;
-      if (!wait_warp(bars + st * 16, (gt / C::kStages) & 1, p.timeout_ns, p.status)) { dead = true; break; }
-      const int key0 = (w.t0 + n) * kPagedKeys + sub * kSub;
-      const uint8_t* stage = smem + st * C::kStage;
-      if (key0 < valid) {
-        const uint8_t* kd = stage + sub * kSub * C::kRow;
-        const uint8_t* ksc = stage + 2 * C::kData + sub * kSub * C::kScRow;
+    const int32_t* table = p.tables + (int64_t)u.b * p.width;
+    for (int n = 0; n < subs.count; ++n) {
+      copies_wait<S - 1>();
+      __syncwarp();
+      const int key0 = (subs.first + n * W) * kSub;
+      const uint8_t* stage = ring + n % S * C::kStage;
+      {
+        const uint8_t* kd = stage;
+        const uint8_t* ksc = stage + 2 * C::kData;
         float s[NT][2][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -345,8 +368,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
             }
         }
         // ---- O^T += V^T P^T: lane (g, t) has values (D / 8) g .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        const uint8_t* vd = stage + C::kData + sub * kSub * C::kRow;
-        const uint8_t* vsc = stage + 2 * C::kData + C::kSc + sub * kSub * C::kScRow;
+        const uint8_t* vd = stage + C::kData;
+        const uint8_t* vsc = stage + 2 * C::kData + C::kSc;
         constexpr int VW = D / 64;  // words of a lane's values of a key
         const int gs = D == 128 ? g : g >> 1;
 #pragma unroll
@@ -387,14 +410,34 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + st * 16 + 8);
+      __syncwarp();  // the stage has been read
+      if (n + S < subs.count) {
+        const int next = subs.first + (n + S) * W;
+        load_sub<D, NT>(P, ring_s + n % S * C::kStage, u.kvh, next, entry, lane);
+        if (n + S + 1 < subs.count) entry = entry_of(p, table, valid, next + W, lane);
+      }
+      copies_commit();
     }
-    tile += w.nt;
+
+    // ---- the unit's rows, once the next unit's first keys are on their way
+    const int s0 = u.q.s0, head0 = u.kvh * p.group, kvh = u.kvh, row0 = u.row0, rows = u.rows;
+    const bool whole = w.whole, head = w.head;
+    if (!whole && head && threadIdx.x == 0) {
+      PagedCut c;
+      c.parts = paged_parts(w, share);
+      c.token0 = s0;
+      c.head0 = head0;
+      c.row0 = row0;
+      c.rows = rows;
+      P.cuts[blockIdx.x] = c;
+    }
+    w.next(p);
+    if (!w.done()) prefetch();
 
     // ---- the warps meet: rows' maxima, sums and O, joined in the order of the warps
     float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
     float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+    asm volatile("bar.sync 2, %0;" ::"n"(C::kThreads) : "memory");  // the last unit's have been read
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -410,19 +453,18 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         for (int i = 0; i < MT / 2; ++i)
           *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(o[j][2 * i][x], o[j][2 * i][x + 2], o[j][2 * i + 1][x], o[j][2 * i + 1][x + 2]);
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-    const float vh = P.v_heads ? __ldg(P.v_heads + u.kvh) : 1.0f;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int r = j * 8 + warp;
+    asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory");
+    const float vh = P.v_heads ? __ldg(P.v_heads + kvh) : 1.0f;
+#pragma unroll 1
+    for (int r = warp; r < rows; r += W) {
       constexpr int V = D / 32;
       float M = kNone, L = 0.0f, acc[V];
 #pragma unroll
-      for (int c = 0; c < kWarps; ++c) M = fmaxf(M, ml[c * NR + r].x);
+      for (int c = 0; c < W; ++c) M = fmaxf(M, ml[c * NR + r].x);
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < kWarps; ++c) {
+      for (int c = 0; c < W; ++c) {
         const float2 x = ml[c * NR + r];
         const float wgt = fast_exp2(x.x - M);
         L = fmaf(wgt, x.y, L);
@@ -436,64 +478,45 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
           acc[0] = fmaf(wgt, y.x, acc[0]); acc[1] = fmaf(wgt, y.y, acc[1]);
         }
       }
-      if (r < u.rows) {
-        if (w.whole) {
-          const int x = u.row0 + r, tok = paged_token(p, x);
-          const int64_t row = (int64_t)(u.q.s0 + tok) * p.Hq + u.kvh * p.group + x - tok * p.group;
-          const float inv = L == 0.0f ? 0.0f : vh / L;
-          uint32_t y[V / 2];
+      if (whole) {
+        const int x = row0 + r, tok = paged_token(p, x);
+        const int64_t row = (int64_t)(s0 + tok) * p.Hq + head0 + x - tok * p.group;
+        const float inv = L == 0.0f ? 0.0f : vh / L;
+        uint32_t y[V / 2];
 #pragma unroll
-          for (int v = 0; v < V / 2; ++v)
-            y[v] = (uint32_t)to_bits<BF16>(acc[2 * v] * inv) | (uint32_t)to_bits<BF16>(acc[2 * v + 1] * inv) << 16;
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + lane * V;
-          if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-          else *reinterpret_cast<uint32_t*>(dst) = y[0];
-          if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + (__log2f(L) - kPLog2)) * kLn2;
-        } else {
-          const int64_t row = (int64_t)(2 * blockIdx.x + (w.head ? 1 : 0)) * NR + r;
-          float* dst = P.ws_o + row * D + lane * V;
-          if constexpr (V == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * vh, acc[1] * vh, acc[2] * vh, acc[3] * vh);
-          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * vh, acc[1] * vh);
-          if (lane == 0) P.ws_ml[row] = make_float2(M, L * kPagedSumFactor);
-        }
+        for (int v = 0; v < V / 2; ++v)
+          y[v] = (uint32_t)to_bits<BF16>(acc[2 * v] * inv) | (uint32_t)to_bits<BF16>(acc[2 * v + 1] * inv) << 16;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + lane * V;
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = y[0];
+        if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + (__log2f(L) - kPLog2)) * kLn2;
+      } else {
+        const int64_t row = (int64_t)(2 * blockIdx.x + (head ? 1 : 0)) * NR + r;
+        float* dst = P.ws_o + row * D + lane * V;
+        if constexpr (V == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * vh, acc[1] * vh, acc[2] * vh, acc[3] * vh);
+        else *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * vh, acc[1] * vh);
+        if (lane == 0) P.ws_ml[row] = make_float2(M, L * kPagedSumFactor);
       }
     }
-    if (!w.whole && w.head && threadIdx.x == 0) {
-      PagedCut c;
-      c.parts = paged_parts(w, share);
-      c.token0 = u.q.s0;
-      c.head0 = u.kvh * p.group;
-      c.row0 = u.row0;
-      c.rows = u.rows;
-      P.cuts[blockIdx.x] = c;
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");  // the rows have been read
   }
+  copies_wait<0>();
 }
 
 template <int D, int NT, bool BF16, bool SOFTCAP>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_paged4_dec_kernel(const __grid_constant__ Paged4DecParams DP) {
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
+    attn_paged4_dec_kernel(const __grid_constant__ Paged4DecParams DP) {
   using C = Cfg<D, NT>;
   const PagedParams& p = DP.p.c;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem), bars = base + C::kOffBar;
   PagedShare* share = reinterpret_cast<PagedShare*>(smem + C::kOffShare);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bars + i * 16, 1);              // full: the loading warp's, and its copies
-      mbar_init(bars + i * 16 + 8, kTileWarps);  // empty
-    }
-    mbar_init_fence();
-    DP.p.cuts[blockIdx.x].parts = 0;
-  }
-  paged_share<8 * NT, kThreads>(p, share);
+  if (threadIdx.x == 0) DP.p.cuts[blockIdx.x].parts = 0;
+  paged_share<8 * NT, C::kThreads>(p, share);
   __syncthreads();
   PagedWalk<8 * NT> w;
   w.begin(p, share);
-  if (warp == kWarps) load_role<D, NT>(DP.p, base, bars, w, lane);
-  else compute_role<D, NT, BF16, SOFTCAP>(DP, smem, bars, share, w, warp, lane);
+  compute_role<D, NT, BF16, SOFTCAP>(DP, smem, share, w, warp, lane);
 }
 
 template <int D, int NT, bool BF16, bool SOFTCAP>
@@ -509,7 +532,7 @@ cudaError_t launch_k(const Paged4DecParams& DP, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev].store(true, std::memory_order_relaxed);
   }
-  kernel<<<grid, kThreads, smem, stream>>>(DP);
+  kernel<<<grid, Cfg<D, NT>::kThreads, smem, stream>>>(DP);
   return cudaGetLastError();
 }
 
