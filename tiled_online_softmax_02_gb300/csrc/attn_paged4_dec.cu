@@ -26,6 +26,7 @@
 // ahead, across units too: no warp waits for another between two meetings.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "paged4.cuh"
 #include "paged4_internal.h"
@@ -44,21 +45,23 @@ struct Cfg {
   static constexpr int NR = 8 * NT;                      // query rows of a unit
   static constexpr int kWarps = 8, kThreads = 32 * kWarps;
   static constexpr int kCtas = NT == 1 ? kPaged4DecCtas : 1;
-  static constexpr int kStages = NT == 1 ? 2 : 4;
+  static constexpr int kStages = NT == 1 ? 2 : 4;        // sub-tiles in a warp's ring
+  static constexpr int kLeft = NT == 1 ? 1 : 0;          // its last stages, which take the warp's O when a unit ends (0: a buffer apart)
   static constexpr int kRow = D / 2, kScRow = D / kGroup4;  // bytes of a row, and of its scales
   static constexpr int kData = kSub * kRow, kSc = kSub * kScRow;
   static constexpr int kStage = 2 * (kData + kSc);       // K, V, K scales, V scales
-  static constexpr int kOffMerge = kWarps * kStages * kStage;
-  static constexpr int kOffMl = kOffMerge + kWarps * NR * D * 4;
+  static constexpr int kOffMerge = kWarps * kStages * kStage, kOwn = NR * D * 4;
+  static constexpr int kOffMl = kOffMerge + (kLeft ? 0 : kWarps * kOwn);
   static constexpr int kOffShare = kOffMl + kWarps * NR * 8;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare);
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 232448, "shared memory");
+  static_assert((kLeft == 0 || kOwn <= kLeft * kStage) && kLeft < kStages && kStage % 16 == 0, "a warp's O");
 };
 
 struct Paged4DecParams {
   Paged4Params p;
-  float scale_log2;     // scale log2 e
-  float sc_in, sc_out;  // soft-cap: sc_out tanh(sc_in s) in log2 units, s the raw score times its row's factor
+  float scale_log2;     // |scale| log2 e
+  float sc_in, sc_out;  // soft-cap: sc_out tanh(sc_in s) in log2 units
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -124,32 +127,34 @@ __device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, 
   using C = Cfg<D, NT>;
   const PagedParams& p = P.c;
   if (entry == -2 && (lane & 15) == 0) atomicOr(p.status, kStatusBadBlock);
-  const bool split = p.block_size < kSub;  // two blocks of 16
-  const int within = split ? 0 : (sub * kSub) & (p.block_size - 1);
-  int64_t row[2];  // of the cache, of the sub-tile's first key as each half sees it
-  bool there[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int e = __shfl_sync(0xffffffffu, entry, 16 * h);
-    there[h] = e >= 0;
-    row[h] = ((int64_t)max(e, 0) * p.Hkv + kvh) * p.block_size + within - (split ? 16 * h : 0);
+  // rows of the cache, of the sub-tile's first key as each half of it sees them
+  const int e0 = __shfl_sync(0xffffffffu, entry, 0);
+  const bool there0 = e0 >= 0;
+  bool there1 = there0;
+  int64_t row0 = ((int64_t)max(e0, 0) * p.Hkv + kvh) * p.block_size, row1;
+  if (p.block_size < kSub) {  // two blocks of 16
+    const int e1 = __shfl_sync(0xffffffffu, entry, 16);
+    there1 = e1 >= 0;
+    row1 = there1 ? ((int64_t)e1 * p.Hkv + kvh) * 16 - 16 : -16;
+  } else {
+    row0 += there0 ? (sub * kSub) & (p.block_size - 1) : 0;
+    row1 = row0;
   }
-  // a block past the last key may follow one that is there in the same block of 32 or more: same rows either way
   constexpr int kN = C::kData / 512;  // pieces of 16 bytes a lane takes of K, and of V
+  const int at = lane * 16;
+  const int64_t off0 = row0 * C::kRow + at, off1 = row1 * C::kRow + at;
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    const int h = j / (kN / 2), at = j * 512 + lane * 16;
-    const int64_t off = row[h] * C::kRow + at;
-    copy16(stage + at, p.k_cache + (there[h] ? off : 0), there[h]);
-    copy16(stage + C::kData + at, p.v_cache + (there[h] ? off : 0), there[h]);
+    const int64_t off = (j < kN / 2 ? off0 : off1) + j * 512;
+    const bool there = j < kN / 2 ? there0 : there1;
+    copy16(stage + j * 512 + at, p.k_cache + off, there);
+    copy16(stage + C::kData + j * 512 + at, p.v_cache + off, there);
   }
   constexpr int kL = C::kSc / 16;  // lanes for K's scales, and for V's
   if (lane < 2 * kL) {
     const int l = lane & (kL - 1);
-    const int h = l / (kL / 2);
-    const bool ok = h ? there[1] : there[0];
-    const int64_t off = (h ? row[1] : row[0]) * C::kScRow + l * 16;
-    copy16(stage + 2 * C::kData + lane * 16, (lane < kL ? P.k_sc : P.v_sc) + (ok ? off : 0), ok);
+    const bool second = l >= kL / 2;
+    copy16(stage + 2 * C::kData + at, (lane < kL ? P.k_sc : P.v_sc) + (second ? row1 : row0) * C::kScRow + l * 16, second ? there1 : there0);
   }
 }
 
@@ -160,27 +165,40 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
   using C = Cfg<D, NT>;
   const Paged4Params& P = DP.p;
   const PagedParams& p = P.c;
-  constexpr int KS = D / 16, MT = D / 16, NR = C::NR, S = C::kStages, W = C::kWarps;
+  constexpr int KS = D / 16, MT = D / 16, NR = C::NR, S = C::kStages, E = S - C::kLeft, W = C::kWarps;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * (S * C::kStage);
   const uint32_t ring_s = smem_u32(ring);
+  const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;  // of the scale, into Q: larger raw scores are larger scores
   Subs subs;
-  int entry;  // of the sub-tile that is loaded next
+  int entry, entry_rest[C::kLeft + 1];  // of the sub-tile that is loaded next, and of those for the last stages
   auto prefetch = [&]() {  // the first sub-tiles of the walk's unit
     subs = subs_of<NT, W>(p, w, warp);
     const int valid = paged_valid(p, w.u.q);
     const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
-    int first[S];
+    int first[S + 1];
 #pragma unroll
-    for (int s = 0; s < S; ++s) first[s] = s < subs.count ? entry_of(p, table, valid, subs.first + s * W, lane) : -1;
-    entry = S < subs.count ? entry_of(p, table, valid, subs.first + S * W, lane) : -1;
+    for (int s = 0; s <= S; ++s) first[s] = s < subs.count ? entry_of(p, table, valid, subs.first + s * W, lane) : -1;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < E; ++s) {
       if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, first[s], lane);
       copies_commit();
     }
+#pragma unroll
+    for (int s = E; s < S; ++s) entry_rest[s - E] = first[s];
+    entry = first[S];
   };
-  if (!w.done()) prefetch();
+  auto prefetch_rest = [&]() {
+#pragma unroll
+    for (int s = E; s < S; ++s) {
+      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, entry_rest[s - E], lane);
+      copies_commit();
+    }
+  };
+  if (!w.done()) {
+    prefetch();
+    prefetch_rest();
+  }
   while (!w.done()) {
     const PagedUnit& u = w.u;
     // ---- this lane's part of Q: row g of every 8, values (D / 4) t ..
@@ -199,7 +217,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) {
           const uint4 v = __ldg(src + i);
-          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+          raw[4 * i] = v.x ^ sign; raw[4 * i + 1] = v.y ^ sign; raw[4 * i + 2] = v.z ^ sign; raw[4 * i + 3] = v.w ^ sign;
         }
       }
       float down = 1.0f;  // 1 / the power of two that row g's Q carries
@@ -221,7 +239,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         }
       }
       const float kh = P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f;
-      down *= (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh;
+      down = fmaxf(down * (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh, 1.2e-38f);  // positive: -inf stays -inf
       fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * t);
       fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
@@ -230,7 +248,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         qf[j][s][1] = raw[2 * s + 1];
       }
     }
-    float o[NT][MT][4], m[NT][2], l[NT][2];
+    float o[NT][MT][4], m[NT][2];
+    uint64_t l2[NT];  // the rows' sums, a pair
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -238,18 +257,20 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[j][i][k] = 0.0f;
       m[j][0] = m[j][1] = kNone;
-      l[j][0] = l[j][1] = 0.0f;
+      l2[j] = 0ull;
     }
     const int valid = paged_valid(p, u.q);
     const int full_lo = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).x;
     const int full_hi = paged_limits(p, u.q, paged_token(p, u.row0)).y;
     // ---- this warp's keys
     const int32_t* table = p.tables + (int64_t)u.b * p.width;
+    int at = 0;  // n % S
     for (int n = 0; n < subs.count; ++n) {
+      const int key0 = (subs.first + n * W) * kSub;
+      uint32_t pf[NT][2][2];
       copies_wait<S - 1>();
       __syncwarp();
-      const int key0 = (subs.first + n * W) * kSub;
-      const uint8_t* stage = ring + n % S * C::kStage;
+      const uint8_t* stage = ring + at * C::kStage;
       {
         const uint8_t* kd = stage;
         const uint8_t* ksc = stage + 2 * C::kData;
@@ -260,21 +281,19 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.0f;
-          uint32_t wd[2][KS / 2], sc[2][2];  // rows g and g + 8: codes, and their scales as pairs
+          uint32_t wd[2][KS / 2];  // rows g and g + 8: codes, and their scales
+          __half2 sc[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = mt * 16 + x * 8 + g;
             if constexpr (D == 128) {
               const uint4 v = *reinterpret_cast<const uint4*>(kd + row * C::kRow + t * 16);
               wd[x][0] = v.x; wd[x][1] = v.y; wd[x][2] = v.z; wd[x][3] = v.w;
-              const uint32_t h = widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ksc + row * C::kScRow + t * 2));
-              sc[x][0] = __byte_perm(h, 0, 0x1010);
-              sc[x][1] = __byte_perm(h, 0, 0x3232);
+              sc[x] = as_half2(widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ksc + row * C::kScRow + t * 2)));
             } else {
               const uint2 v = *reinterpret_cast<const uint2*>(kd + row * C::kRow + t * 8);
               wd[x][0] = v.x; wd[x][1] = v.y;
-              const uint32_t h = widen_e4m3x2(ksc[row * C::kScRow + t]);
-              sc[x][0] = sc[x][1] = __byte_perm(h, 0, 0x1010);
+              sc[x] = as_half2(widen_e4m3x2(ksc[row * C::kScRow + t]));
             }
           }
 #pragma unroll
@@ -283,9 +302,9 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               widen8(wd[x][i], a[x][0], a[x][1], a[x][2], a[x][3]);
-              const uint32_t f = sc[x][D == 128 ? i >> 1 : 0];
+              const __half2 f = D == 128 && i >= KS / 4 ? __high2half2(sc[x]) : __low2half2(sc[x]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) a[x][k] = mul_f16x2(a[x][k], f);
+              for (int k = 0; k < 4; ++k) a[x][k] = as_bits(__hmul2(as_half2(a[x][k]), f));
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -294,16 +313,14 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
             }
           }
         }
-        // ---- scores in log2 units
+        if constexpr (SOFTCAP) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              s[j][mt][k] *= fac[j][k & 1];
-              if constexpr (SOFTCAP) s[j][mt][k] = DP.sc_out * tanh20(s[j][mt][k]);
-            }
+              for (int k = 0; k < 4; ++k) s[j][mt][k] = tanh20(s[j][mt][k] * fac[j][k & 1]);
+        }
         if (key0 < full_lo || key0 + kSub > full_hi) {  // some key is hidden from some row
 #pragma unroll
           for (int j = 0; j < NT; ++j)
@@ -327,7 +344,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            mx[j][x] = fmaxf(fmaxf(s[j][0][x], s[j][0][x + 2]), fmaxf(s[j][1][x], s[j][1][x + 2]));
+            mx[j][x] = fmaxf(fmax3(s[j][0][x], s[j][0][x + 2], s[j][1][x]), s[j][1][x + 2]) * (SOFTCAP ? DP.sc_out : fac[j][x]);
             rise |= mx[j][x] > m[j][x] + kRise;
           }
         if (__any_sync(0xffffffffu, rise)) {
@@ -342,9 +359,9 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
               v = v > m[j][x] + kRise ? v : m[j][x];
               al[x] = fast_exp2(m[j][x] - v);
-              l[j][x] *= al[x];
               m[j][x] = v;
             }
+            l2[j] = fmul2(l2[j], f2(al[0], al[1]));
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -352,19 +369,20 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
           }
         }
         // ---- weights, transposed into the second product's operand
-        uint32_t pf[NT][2][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const float off0 = kPLog2 - m[j][0], off1 = kPLog2 - m[j][1];
+          const uint64_t mul = SOFTCAP ? f2(DP.sc_out, DP.sc_out) : f2(fac[j][0], fac[j][1]);
+          const uint64_t off = f2(kPLog2 - m[j][0], kPLog2 - m[j][1]);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float a = fast_exp2(s[j][mt][2 * k] + off0), b = fast_exp2(s[j][mt][2 * k + 1] + off1);
-              l[j][0] += a;
-              l[j][1] += b;
-              const __half2 h = __floats2half2_rn(a, b);
-              pf[j][mt][k] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+              float a, b;
+              f2_split(ffma2(f2(s[j][mt][2 * k], s[j][mt][2 * k + 1]), mul, off), a, b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              l2[j] = fadd2(l2[j], f2(a, b));
+              pf[j][mt][k] = transpose8x8(as_bits(__floats2half2_rn(a, b)));
             }
         }
         // ---- O^T += V^T P^T: lane (g, t) has values (D / 8) g .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -386,7 +404,11 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
               wv[x][0] = *reinterpret_cast<const uint32_t*>(vd + row * C::kRow + g * 4);
             }
             sb[x] = vsc[row * C::kScRow + gs];
-            if (key0 + row >= valid) sb[x] = 0u;  // slots past the last key may hold NaN scales
+          }
+          if (key0 + kSub > valid) {  // slots past the last key may hold NaN scales
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (key0 + kt * 16 + (x >> 1) * 8 + 2 * t + (x & 1) >= valid) sb[x] = 0u;
           }
           const uint32_t s0 = widen_e4m3x2(sb[0] | sb[1] << 8), s1 = widen_e4m3x2(sb[2] | sb[3] << 8);
 #pragma unroll
@@ -413,10 +435,11 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
       __syncwarp();  // the stage has been read
       if (n + S < subs.count) {
         const int next = subs.first + (n + S) * W;
-        load_sub<D, NT>(P, ring_s + n % S * C::kStage, u.kvh, next, entry, lane);
+        load_sub<D, NT>(P, ring_s + at * C::kStage, u.kvh, next, entry, lane);
         if (n + S + 1 < subs.count) entry = entry_of(p, table, valid, next + W, lane);
       }
       copies_commit();
+      at = at + 1 == S ? 0 : at + 1;
     }
 
     // ---- the unit's rows, once the next unit's first keys are on their way
@@ -435,29 +458,31 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
     if (!w.done()) prefetch();
 
     // ---- the warps meet: rows' maxima, sums and O, joined in the order of the warps
-    float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+    auto left = [&](int c) { return reinterpret_cast<float*>(smem + (C::kLeft ? (c * S + E) * C::kStage : C::kOffMerge + c * C::kOwn)); };
     float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
-    asm volatile("bar.sync 2, %0;" ::"n"(C::kThreads) : "memory");  // the last unit's have been read
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      float l[2];
+      f2_split(l2[j], l[0], l[1]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float v = l[j][x];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 4);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 8);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 16);
         const int r = j * 8 + 2 * t + x;
-        if (g == 0) ml[warp * NR + r] = make_float2(m[j][x], v);
-        float* dst = merge + (warp * NR + r) * D + g * (D / 8);
+        if (g == 0) ml[warp * NR + r] = make_float2(m[j][x], l[x]);
+        float* dst = left(warp) + r * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < MT / 2; ++i)
           *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(o[j][2 * i][x], o[j][2 * i][x + 2], o[j][2 * i + 1][x], o[j][2 * i + 1][x + 2]);
       }
+    }
     asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory");
     const float vh = P.v_heads ? __ldg(P.v_heads + kvh) : 1.0f;
 #pragma unroll 1
     for (int r = warp; r < rows; r += W) {
       constexpr int V = D / 32;
+      const int d = lane * V;
       float M = kNone, L = 0.0f, acc[V];
 #pragma unroll
       for (int c = 0; c < W; ++c) M = fmaxf(M, ml[c * NR + r].x);
@@ -465,38 +490,39 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
       for (int v = 0; v < V; ++v) acc[v] = 0.0f;
 #pragma unroll
       for (int c = 0; c < W; ++c) {
-        const float2 x = ml[c * NR + r];
-        const float wgt = fast_exp2(x.x - M);
-        L = fmaf(wgt, x.y, L);
-        const float* src = merge + (c * NR + r) * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src);
-          acc[0] = fmaf(wgt, y.x, acc[0]); acc[1] = fmaf(wgt, y.y, acc[1]);
-          acc[2] = fmaf(wgt, y.z, acc[2]); acc[3] = fmaf(wgt, y.w, acc[3]);
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          acc[0] = fmaf(wgt, y.x, acc[0]); acc[1] = fmaf(wgt, y.y, acc[1]);
-        }
+        const float2 y = ml[c * NR + r];
+        const float wgt = fast_exp2(y.x - M);
+        L = fmaf(wgt, y.y, L);
+        const float* src = left(c) + r * D + d;
+        float y4[4];
+        if constexpr (V == 4) *reinterpret_cast<float4*>(y4) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(y4) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(wgt, y4[v], acc[v]);
       }
       if (whole) {
         const int x = row0 + r, tok = paged_token(p, x);
         const int64_t row = (int64_t)(s0 + tok) * p.Hq + head0 + x - tok * p.group;
         const float inv = L == 0.0f ? 0.0f : vh / L;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + d;
         uint32_t y[V / 2];
 #pragma unroll
         for (int v = 0; v < V / 2; ++v)
           y[v] = (uint32_t)to_bits<BF16>(acc[2 * v] * inv) | (uint32_t)to_bits<BF16>(acc[2 * v + 1] * inv) << 16;
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + lane * V;
         if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
         else *reinterpret_cast<uint32_t*>(dst) = y[0];
-        if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + (__log2f(L) - kPLog2)) * kLn2;
+        if (p.lse != nullptr && d == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + (__log2f(L) - kPLog2)) * kLn2;
       } else {
         const int64_t row = (int64_t)(2 * blockIdx.x + (head ? 1 : 0)) * NR + r;
-        float* dst = P.ws_o + row * D + lane * V;
+        float* dst = P.ws_o + row * D + d;
         if constexpr (V == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * vh, acc[1] * vh, acc[2] * vh, acc[3] * vh);
         else *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * vh, acc[1] * vh);
-        if (lane == 0) P.ws_ml[row] = make_float2(M, L * kPagedSumFactor);
+        if (d == 0) P.ws_ml[row] = make_float2(M, L * kPagedSumFactor);
       }
+    }
+    if (!w.done()) {
+      asm volatile("bar.sync 2, %0;" ::"n"(C::kThreads) : "memory");  // the rows have been read
+      prefetch_rest();
     }
   }
   copies_wait<0>();
@@ -547,9 +573,9 @@ cudaError_t launch_n(const Paged4DecParams& DP, int grid, bool bf16, cudaStream_
 cudaError_t launch_attn_paged4_dec(const Paged4Params& p, int rows, int grid, bool bf16, cudaStream_t stream) {
   Paged4DecParams DP{};
   DP.p = p;
-  DP.scale_log2 = (float)((double)p.c.scale * 1.4426950408889634);
+  DP.scale_log2 = (float)(fabs((double)p.c.scale) * 1.4426950408889634);  // the sign goes into Q
   if (p.c.softcap > 0.0f) {
-    DP.sc_in = (float)((double)p.c.scale / (double)p.c.softcap);
+    DP.sc_in = (float)(fabs((double)p.c.scale) / (double)p.c.softcap);
     DP.sc_out = (float)((double)p.c.softcap * 1.4426950408889634);
   }
   if (p.c.D == 128) return rows == 8 ? launch_n<128, 1>(DP, grid, bf16, stream) : launch_n<128, 2>(DP, grid, bf16, stream);
