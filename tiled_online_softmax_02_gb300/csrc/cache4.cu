@@ -15,10 +15,10 @@
 // restores, and any other quotient of an 11-bit x lies 2^-13 or more from one.
 //
 // Bound: HBM for prompts, and for a few tokens the chain of slot, row, group
-// maximum and store.  A thread has one group: its 16 values are two or four
-// wide loads in flight beside the slot's, no thread waits for another, and the
-// 32 lanes of a warp write whole sectors (rows of one head that follow one
-// another in a block).
+// maximum and store.  A thread has one group of K and the same one of V: their
+// values are wide loads in flight beside the slot's, no thread waits for another,
+// and the 32 lanes of a warp write whole sectors (rows of one head that follow
+// one another in a block).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -58,17 +58,15 @@ __device__ __forceinline__ void widen16(const uint4 (&v)[sizeof(T)], float (&x)[
   }
 }
 
-// The token, head, cache and group of a thread: lanes go over a row's groups, then over tokens.
+// The token, head and group of a thread: lanes go over a row's groups, then over tokens.
 template <int D>
 struct Place {
   static constexpr int kPer = D / kGroup4, kTokens = kThreads / kPer;
-  int t, h, which, part;
+  int t, h, part;
   bool there;
   __device__ __forceinline__ Place(const Cache4Params& p, int64_t unit) {
-    which = (int)(unit & 1);
-    const int64_t u = unit >> 1;
-    const int64_t tile = u / p.Hkv;
-    h = (int)(u - tile * p.Hkv);
+    const int64_t tile = unit / p.Hkv;
+    h = (int)(unit - tile * p.Hkv);
     const int64_t tok = tile * kTokens + threadIdx.x / kPer;
     there = tok < p.T;
     t = there ? (int)tok : 0;
@@ -82,64 +80,73 @@ struct Place {
   }
 };
 
+// 16 values as codes and the byte of their scale.
+template <typename T>
+__device__ __forceinline__ uint2 quantise(const uint4 (&v)[sizeof(T)], float hs, uint32_t& sb) {
+  float x[16];
+  widen16<T>(v, x);
+  // magnitudes order as their bits; not finite from 0x7f800000 on
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  if (top >= 0x7f800000u) {  // infinities set no scale
+    if (top > 0x7f800000u) {
+      sb = 0x7fu;
+      return make_uint2(0u, 0u);
+    }
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
+      top = a < 0x7f800000u ? max(top, a) : top;
+    }
+  }
+  sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f * hs), __NV_SATFINITE, __NV_E4M3);
+  sb = max(sb & 0x7fu, 1u);
+  const float unit = e4m3_value(sb) * hs;
+  const uint32_t hb = __float_as_uint(hs);
+  if (sizeof(T) == 2 && (hb & 0x7fffffu) == 0u && hb >= (27u << 23) && hb <= (227u << 23)) {
+    const float r = __fdiv_rn(1.0f, unit);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t sign = __float_as_uint(x[i]) & 0x80000000u;
+      const float c = __uint_as_float(sign | 0x43400000u);  // 192 with x's sign: steps of 2^-16
+      x[i] = __uint_as_float(__float_as_uint(__fsub_rn(__fmaf_rn(x[i], r, c), c)) | sign);  // zeros keep it too
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], unit);
+  }
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_E2M1, cudaRoundNearest) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ Cache4Params p, int64_t units) {
   using P = Place<D>;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const P at(p, unit);
-    const T* src = static_cast<const T*>(at.which ? p.x[1] : p.x[0]) +
-                   (int64_t)at.t * (at.which ? p.stride[1] : p.stride[0]) + at.h * D + at.part * kGroup4;
-    uint4 v[sizeof(T)];
+    uint4 v[2][sizeof(T)];
+    float hs[2];
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-    const float* heads = at.which ? p.heads[1] : p.heads[0];
-    const float hs = heads ? __ldg(heads + at.h) : 1.0f;
+    for (int k = 0; k < 2; ++k) {
+      const T* src = static_cast<const T*>(p.x[k]) + (int64_t)at.t * p.stride[k] + at.h * D + at.part * kGroup4;
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i) v[k][i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      hs[k] = p.heads[k] ? __ldg(p.heads[k] + at.h) : 1.0f;
+    }
     const int64_t row = at.row(p);
     if (row < 0) continue;
-    float x[16];
-    widen16<T>(v, x);
-    // magnitudes order as their bits; not finite from 0x7f800000 on
-    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-    bool nan = false;
-    if (top >= 0x7f800000u) {  // infinities set no scale
-      nan = top > 0x7f800000u;
-      top = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
-        top = a < 0x7f800000u ? max(top, a) : top;
-      }
+    for (int k = 0; k < 2; ++k) {
+      uint32_t sb;
+      const uint2 w = quantise<T>(v[k], hs[k], sb);
+      *reinterpret_cast<uint2*>(p.cache[k] + row * (D / 2) + at.part * 8) = w;
+      p.scales[k][row * (D / kGroup4) + at.part] = (uint8_t)sb;
     }
-    uint32_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f * hs), __NV_SATFINITE, __NV_E4M3);
-    sb = max(sb & 0x7fu, 1u);
-    const float unit_v = e4m3_value(sb) * hs;
-    uint32_t w[2] = {0u, 0u};
-    const uint32_t hb = __float_as_uint(hs);
-    if (!nan) {
-      if (sizeof(T) == 2 && (hb & 0x7fffffu) == 0u && hb >= (27u << 23) && hb <= (227u << 23)) {
-        const float r = __fdiv_rn(1.0f, unit_v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t sign = __float_as_uint(x[i]) & 0x80000000u;
-          const float c = __uint_as_float(sign | 0x43400000u);  // 192 with x's sign: steps of 2^-16
-          x[i] = __uint_as_float(__float_as_uint(__fsub_rn(__fmaf_rn(x[i], r, c), c)) | sign);  // zeros keep it too
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], unit_v);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_E2M1, cudaRoundNearest) << (8 * (i & 3));
-    } else {
-      sb = 0x7fu;
-    }
-    uint8_t* cache = at.which ? p.cache[1] : p.cache[0];
-    uint8_t* scales = at.which ? p.scales[1] : p.scales[0];
-    *reinterpret_cast<uint2*>(cache + row * (D / 2) + at.part * 8) = make_uint2(w[0], w[1]);
-    scales[row * (D / kGroup4) + at.part] = (uint8_t)sb;
   }
 }
 
@@ -150,47 +157,51 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
     const P at(p, unit);
     if (!at.there) continue;
     const int64_t row = at.row(p);
-    const float* heads = at.which ? p.heads[1] : p.heads[0];
-    const float hs = heads ? __ldg(heads + at.h) : 1.0f;
-    uint2 code = make_uint2(0u, 0u);
-    float s = 0.0f;
-    if (row >= 0) {
-      const uint8_t* cache = at.which ? p.cache[1] : p.cache[0];
-      const uint8_t* scales = at.which ? p.scales[1] : p.scales[0];
-      code = __ldg(reinterpret_cast<const uint2*>(cache + row * (D / 2) + at.part * 8));
-      s = e4m3_value(__ldg(scales + row * (D / kGroup4) + at.part));
-    }
-    uint32_t h[8];
-    widen8(code.x, h[0], h[1], h[2], h[3]);
-    widen8(code.y, h[4], h[5], h[6], h[7]);
-    T* dst = static_cast<T*>(at.which ? p.x[1] : p.x[0]) + (int64_t)at.t * (at.which ? p.stride[1] : p.stride[0]) +
-             (int64_t)at.h * (at.which ? p.head_stride[1] : p.head_stride[0]) + at.part * kGroup4;
-    uint32_t o[4 * sizeof(T)];
+    uint2 code[2];
+    uint32_t sb[2] = {0u, 0u};
+    float hs[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      f.x = f.x * s * hs;  // code * s is exact
-      f.y = f.y * s * hs;
-      if constexpr (sizeof(T) == 4) {
-        o[2 * i] = __float_as_uint(f.x);
-        o[2 * i + 1] = __float_as_uint(f.y);
-      } else if constexpr (std::is_same<T, __half>::value) {
-        const __half2 y = __floats2half2_rn(f.x, f.y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&y);
-      } else {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+    for (int k = 0; k < 2; ++k) {
+      code[k] = make_uint2(0u, 0u);
+      hs[k] = p.heads[k] ? __ldg(p.heads[k] + at.h) : 1.0f;
+      if (row >= 0) {
+        code[k] = __ldg(reinterpret_cast<const uint2*>(p.cache[k] + row * (D / 2) + at.part * 8));
+        sb[k] = __ldg(p.scales[k] + row * (D / kGroup4) + at.part);
       }
     }
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i)
-      reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    for (int k = 0; k < 2; ++k) {
+      const float s = e4m3_value(sb[k]);
+      uint32_t h[8];
+      widen8(code[k].x, h[0], h[1], h[2], h[3]);
+      widen8(code[k].y, h[4], h[5], h[6], h[7]);
+      T* dst = static_cast<T*>(p.x[k]) + (int64_t)at.t * p.stride[k] + (int64_t)at.h * p.head_stride[k] + at.part * kGroup4;
+      uint32_t o[4 * sizeof(T)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 f = __half22float2(as_half2(h[i]));
+        f.x = f.x * s * hs[k];  // code * s is exact
+        f.y = f.y * s * hs[k];
+        if constexpr (sizeof(T) == 4) {
+          o[2 * i] = __float_as_uint(f.x);
+          o[2 * i + 1] = __float_as_uint(f.y);
+        } else if constexpr (std::is_same<T, __half>::value) {
+          o[i] = as_bits(__floats2half2_rn(f.x, f.y));
+        } else {
+          const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
+          o[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i)
+        reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
   }
 }
 
 template <typename T, int D>
 cudaError_t launch(const Cache4Params& p, bool read, cudaStream_t stream) {
-  const int64_t units = ((int64_t)p.T + Place<D>::kTokens - 1) / Place<D>::kTokens * p.Hkv * 2;
+  const int64_t units = ((int64_t)p.T + Place<D>::kTokens - 1) / Place<D>::kTokens * p.Hkv;
   const unsigned grid = (unsigned)std::min<int64_t>(units, 1 << 30);
   if (read) cache4_read_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, units);
   else cache4_append_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, units);

@@ -11,9 +11,10 @@
 // of which the upper 32 bits go to sincospi.  Rotation in fp32, rounded once.
 //
 // Bound: HBM, each value read and written once.  A warp has a token: its lanes
-// hold the sine and cosine of 8 pairs each (4 in f32) and go over the heads, so
-// that their 30 instructions a pair are paid once a token and 4 lanes, not once
-// a head.  With few tokens a token's heads are spread over more warps.
+// share out the sines and cosines of the token's pairs, through shared memory,
+// and go over its heads, 16-byte pieces of 8 pairs (4 in f32) each, so that the
+// 60 instructions of a pair's angle are paid once a token, not once a head.
+// With few tokens a token's heads are spread over more warps.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -28,6 +29,7 @@ namespace gb300_attn {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kPairs = 256;  // pairs whose sines and cosines a warp holds at a time
 
 // Turns a position of radians a position, modulo 1, times 2^64.
 __device__ __forceinline__ uint64_t turns(double radians) {
@@ -81,11 +83,14 @@ template <typename T, int VP, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int row_lanes, int heads_each,
                                                         int parts) {
   using V = Vec<T, VP>;
-  const int lane = threadIdx.x & 31;
+  __shared__ __align__(16) float cs[kThreads / 32][2][kPairs];  // cosines and sines of a warp's pairs
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), all = (int64_t)p.T * parts;
-  const int half = p.rotary / 2, nvec = half / VP;
+  const int half = p.rotary / 2;
   const int sub = lane / row_lanes, i0 = lane - sub * row_lanes, subs = 32 / row_lanes;
-  for (int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < all; item += warps) {
+  float* cw = cs[warp][0];
+  float* nw = cs[warp][1];
+  for (int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + warp; item < all; item += warps) {
     const int t = (int)(item / parts);
     const int h0 = (int)(item - (int64_t)t * parts) * heads_each, h1 = min(h0 + heads_each, p.H[0] + p.H[1]);
     int64_t pos;
@@ -96,49 +101,77 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       if (b >= p.B || t < __ldg(p.q_starts)) continue;  // rows of no request
       pos = (int64_t)__ldg(p.totals + b) - __ldg(p.q_starts + b + 1) + t;
     }
-    for (int i = i0; i < nvec; i += row_lanes) {
-      float c[VP], n[VP];
-#pragma unroll
-      for (int k = 0; k < VP; ++k) {
-        const uint64_t turn = (uint64_t)pos * turns(__ldg(p.freq + i * VP + k));
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &n[k], &c[k]);
-        c[k] *= p.scale;
-        n[k] *= p.inverse ? -p.scale : p.scale;
+    // head h of q and k together lies at in(h) + h D
+    const int hq = p.H[0];
+    const T* in0 = static_cast<const T*>(p.in[0]) + (int64_t)t * p.in_stride[0];
+    const T* in1 = static_cast<const T*>(p.in[1]) + (int64_t)t * p.in_stride[1] - (int64_t)hq * p.D;
+    T* out0 = static_cast<T*>(p.out[0]) + (int64_t)t * p.out_stride[0];
+    T* out1 = static_cast<T*>(p.out[1]) + (int64_t)t * p.out_stride[1] - (int64_t)hq * p.D;
+    auto in = [&](int h) { return (h >= hq ? in1 : in0) + (int64_t)h * p.D; };
+    auto out = [&](int h) { return (h >= hq ? out1 : out0) + (int64_t)h * p.D; };
+    for (int pair0 = 0; pair0 < half; pair0 += kPairs) {
+      const int pairs = min(kPairs, half - pair0);
+      __syncwarp();  // the last ones have been read
+      for (int i = lane; i < pairs; i += 32) {
+        const uint64_t turn = (uint64_t)pos * turns(__ldg(p.freq + pair0 + i));
+        float c, n;
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &n, &c);
+        cw[i] = c * p.scale;
+        nw[i] = n * (p.inverse ? -p.scale : p.scale);
       }
-#pragma unroll 2
-      for (int h = h0 + sub; h < h1; h += subs) {
-        const bool isk = h >= p.H[0];
-        const int hh = isk ? h - p.H[0] : h;
-        const T* src = static_cast<const T*>(isk ? p.in[1] : p.in[0]) + (int64_t)t * (isk ? p.in_stride[1] : p.in_stride[0]) +
-                       (int64_t)hh * p.D;
-        T* dst = static_cast<T*>(isk ? p.out[1] : p.out[0]) + (int64_t)t * (isk ? p.out_stride[1] : p.out_stride[0]) +
-                 (int64_t)hh * p.D;
-        const int at = INTER ? 2 * i * VP : i * VP, to = INTER ? at + VP : at + half;
-        V u = *reinterpret_cast<const V*>(src + at), v = *reinterpret_cast<const V*>(src + to);
+      __syncwarp();
+      for (int i = i0; i * VP < pairs; i += row_lanes) {
+        float c[VP], n[VP];
 #pragma unroll
         for (int k = 0; k < VP; ++k) {
-          T& a = INTER && VP > 1 ? (2 * k < VP ? u.x[(2 * k) % VP] : v.x[(2 * k) % VP]) : u.x[k];
-          T& b = INTER && VP > 1 ? (2 * k < VP ? u.x[(2 * k + 1) % VP] : v.x[(2 * k + 1) % VP]) : v.x[k];
-          const float x = to_f(a), y = to_f(b);
-          a = from_f<T>(x * c[k] - y * n[k]);
-          b = from_f<T>(y * c[k] + x * n[k]);
+          c[k] = cw[i * VP + k];
+          n[k] = nw[i * VP + k];
         }
-        *reinterpret_cast<V*>(dst + at) = u;
-        *reinterpret_cast<V*>(dst + to) = v;
+        const int at = INTER ? 2 * (pair0 + i * VP) : pair0 + i * VP, to = INTER ? at + VP : at + half;
+#pragma unroll 4
+        for (int h = h0 + sub; h < h1; h += subs) {
+          const T* src = in(h);
+          T* dst = out(h);
+          V u = *reinterpret_cast<const V*>(src + at), v = *reinterpret_cast<const V*>(src + to);
+#pragma unroll
+          for (int k = 0; k < VP; ++k) {
+            T& a = INTER && VP > 1 ? (2 * k < VP ? u.x[(2 * k) % VP] : v.x[(2 * k) % VP]) : u.x[k];
+            T& b = INTER && VP > 1 ? (2 * k < VP ? u.x[(2 * k + 1) % VP] : v.x[(2 * k + 1) % VP]) : v.x[k];
+            const float x = to_f(a), y = to_f(b);
+            a = from_f<T>(x * c[k] - y * n[k]);
+            b = from_f<T>(y * c[k] + x * n[k]);
+          }
+          *reinterpret_cast<V*>(dst + at) = u;
+          *reinterpret_cast<V*>(dst + to) = v;
+        }
       }
     }
-    // what is not turned
+    // what is not turned: lanes over the pieces of all heads
     const int rest = (p.D - p.rotary) / VP;
     if (rest == 0 || (p.in_place[0] && p.in_place[1])) continue;
-    for (int h = h0; h < h1; ++h) {
-      const bool isk = h >= p.H[0];
-      if (isk ? p.in_place[1] : p.in_place[0]) continue;
-      const int hh = isk ? h - p.H[0] : h;
-      const T* src = static_cast<const T*>(isk ? p.in[1] : p.in[0]) + (int64_t)t * (isk ? p.in_stride[1] : p.in_stride[0]) +
-                     (int64_t)hh * p.D + p.rotary;
-      T* dst = static_cast<T*>(isk ? p.out[1] : p.out[0]) + (int64_t)t * (isk ? p.out_stride[1] : p.out_stride[0]) +
-               (int64_t)hh * p.D + p.rotary;
-      for (int i = lane; i < rest; i += 32) reinterpret_cast<V*>(dst)[i] = reinterpret_cast<const V*>(src)[i];
+    int h = h0, i = lane;
+    while (i >= rest && h < h1) {
+      i -= rest;
+      ++h;
+    }
+    while (h < h1) {
+      V x[4];
+      int hs[4], is[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        hs[k] = h;
+        is[k] = i;
+        if (h < h1) x[k] = reinterpret_cast<const V*>(in(h) + p.rotary)[i];
+        i += 32;
+        while (i >= rest && h < h1) {
+          i -= rest;
+          ++h;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (hs[k] < h1 && !(hs[k] >= hq ? p.in_place[1] : p.in_place[0]))
+          reinterpret_cast<V*>(out(hs[k]) + p.rotary)[is[k]] = x[k];
     }
   }
 }
