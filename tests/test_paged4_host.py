@@ -168,18 +168,25 @@ def test_reference_encodes_by_hand():
     assert held[32:35].tolist() == [6.0, 6.0, 0.0] and np.isnan(held[48:]).all()
 
 
-def test_a_product_snapped_to_16_bits_rounds_as_the_quotient():
-    """16-bit rows take x times the f32 inverse of the scale, brought to a multiple of 2^-16, for the quotient: the
-    codes are the same for every scale and every 16-bit x (here: all that lie next to a border, and many others)."""
+def test_two_products_round_as_the_quotient():
+    """The codes of x rh + x rl, 1 / s as the sum of rh, rounded down, and rl, are those of x / s: for every scale, and
+    every 16- and 32-bit x next to a border between codes, and many others."""
     f = np.float32
-    scales = ref.E4M3[1:127]
     rng = np.random.Generator(np.random.PCG64(3))
-    for t in (torch.bfloat16, torch.float16):
-        for s in scales:
-            near = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * s
-            x = torch.from_numpy(np.concatenate([near, rng.uniform(0, 8 * s, 300)])).to(t)
-            bits = x.view(torch.int16)
-            x = torch.cat([x, (bits - 1).view(t), (bits + 1).view(t)]).double().numpy()
-            product = (x.astype(f) * (f(1) / f(s))).astype(f)
-            snapped = ((product + f(192)).astype(f) - f(192)).astype(f)
-            assert np.array_equal(ref.encode_e2m1(snapped.astype(np.float64)), ref.encode_e2m1(x / s)), (t, s)
+    for s in ref.E4M3[1:127]:
+        rh = f(1 / s)
+        if float(rh) > 1 / s:
+            rh = np.nextafter(rh, f(0))
+        rl = max(f(f(1 - float(rh) * s) * rh), f(rh * f(2.0 ** -60)))  # 1 - rh s is exact in 64 bits, as in the one rounding of an fma
+        assert abs((float(rh) + float(rl)) * s - 1) < 2.0 ** -45
+        near = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * s
+        x = []
+        for t in (torch.bfloat16, torch.float16, torch.float32):
+            y = torch.from_numpy(np.concatenate([near, rng.uniform(0, 8 * s, 200)])).to(t)
+            bits = y.view(torch.int32 if t == torch.float32 else torch.int16)
+            x += [(bits + i).view(t).double().numpy() for i in range(-2, 3)]
+        x = np.concatenate(x)
+        small = (x.astype(f) * rl).astype(f).astype(np.float64)
+        # x rh is exact in 64 bits; the sum is rounded to 64 bits before 32, 2^-29 units of the last place apart
+        q = (x * float(rh) + small).astype(f).astype(np.float64)
+        assert np.array_equal(ref.encode_e2m1(q), ref.encode_e2m1(x / s)), s

@@ -8,11 +8,12 @@
 // would: a quotient next to a border of so few bits is never rounded onto it.
 // A group with a NaN gets the scale NaN and zeros.  value = code * s * h.
 //
-// 16-bit rows under a power-of-two h take x * (1 / (s h)) in place of the
-// quotient (the fp32 division costs twelve instructions a value): the product
-// is off by 2^-23 of itself, so it is brought to the nearest multiple of
-// 2^-16 before the last rounding.  Borders are multiples of 2^-2, which that
-// restores, and any other quotient of an 11-bit x lies 2^-13 or more from one.
+// Under a power-of-two h (1 among them) the quotient x / (s h) is x rh + x rl,
+// the inverse of s h as a sum of two: rh rounded down and what is left of it, so
+// that the sum is off by 2^-46 of itself and its rounding is the quotient's
+// wherever that lies next to a border (the nearest quotients are 0.53 units of
+// the last place from one).  rl is kept above 0, for infinities and zeros.  Two
+// instructions a value; the fp32 division costs twelve.
 //
 // Bound: HBM for prompts, and for a few tokens the chain of slot, row, group
 // maximum and store.  A thread has one group of K and the same one of V: their
@@ -23,7 +24,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -35,7 +35,7 @@
 namespace gb300_attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 
 template <typename T>
 __device__ __forceinline__ void widen16(const uint4 (&v)[sizeof(T)], float (&x)[16]) {
@@ -80,20 +80,25 @@ struct Place {
   }
 };
 
-// 16 values as codes and the byte of their scale.
+// The largest finite |x| of 16 values, as fp32 bits; 0x7fc00000 where one is NaN.
 template <typename T>
-__device__ __forceinline__ uint2 quantise(const uint4 (&v)[sizeof(T)], float hs, uint32_t& sb) {
-  float x[16];
-  widen16<T>(v, x);
-  // magnitudes order as their bits; not finite from 0x7f800000 on
-  uint32_t top = 0;
+__device__ __forceinline__ uint32_t largest(const uint4 (&v)[sizeof(T)], const float (&x)[16]) {
+  uint32_t top = 0;  // magnitudes order as their bits; not finite from 0x7f800000 on
+  if constexpr (sizeof(T) == 2) {  // 16-bit ones two at a time
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 2; ++i)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                               __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+    const uint32_t t = max(m & 0xffffu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value) top = __float_as_uint(__half2float(__ushort_as_half((unsigned short)t)));
+    else top = t << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  }
   if (top >= 0x7f800000u) {  // infinities set no scale
-    if (top > 0x7f800000u) {
-      sb = 0x7fu;
-      return make_uint2(0u, 0u);
-    }
+    if (top > 0x7f800000u) return 0x7fc00000u;
     top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -101,27 +106,44 @@ __device__ __forceinline__ uint2 quantise(const uint4 (&v)[sizeof(T)], float hs,
       top = a < 0x7f800000u ? max(top, a) : top;
     }
   }
+  return top;
+}
+
+// Eight values as codes, in order.
+__device__ __forceinline__ uint32_t narrow8(const float* x) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return w;
+}
+
+// 16 values as codes and the byte of their scale.
+template <typename T>
+__device__ __forceinline__ uint2 quantise(const uint4 (&v)[sizeof(T)], float hs, uint32_t& sb) {
+  float x[16];
+  widen16<T>(v, x);
+  const uint32_t top = largest<T>(v, x);
+  if (top == 0x7fc00000u) {
+    sb = 0x7fu;
+    return make_uint2(0u, 0u);
+  }
   sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f * hs), __NV_SATFINITE, __NV_E4M3);
   sb = max(sb & 0x7fu, 1u);
   const float unit = e4m3_value(sb) * hs;
   const uint32_t hb = __float_as_uint(hs);
-  if (sizeof(T) == 2 && (hb & 0x7fffffu) == 0u && hb >= (27u << 23) && hb <= (227u << 23)) {
-    const float r = __fdiv_rn(1.0f, unit);
+  if ((hb & 0x7fffffu) == 0u && hb >= (67u << 23) && hb <= (187u << 23)) {  // 2^-60 to 2^60: all of this in range
+    const float rh = __frcp_rd(unit), rl = fmaxf(__fmaf_rn(-rh, unit, 1.0f) * rh, rh * 0x1p-60f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t sign = __float_as_uint(x[i]) & 0x80000000u;
-      const float c = __uint_as_float(sign | 0x43400000u);  // 192 with x's sign: steps of 2^-16
-      x[i] = __uint_as_float(__float_as_uint(__fsub_rn(__fmaf_rn(x[i], r, c), c)) | sign);  // zeros keep it too
-    }
+    for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(x[i], rh, __fmul_rn(x[i], rl));
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], unit);
   }
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_E2M1, cudaRoundNearest) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+  return make_uint2(narrow8(x), narrow8(x + 8));
 }
 
 template <typename T, int D>
