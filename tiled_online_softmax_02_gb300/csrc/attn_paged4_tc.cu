@@ -22,6 +22,7 @@
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "paged4.cuh"
 #include "paged4_internal.h"
@@ -35,8 +36,8 @@ constexpr int BM = 128, BN = kPagedKeys;
 constexpr int kRows = kPagedTcRows;    // rows of a unit: two lanes of 128
 constexpr int kThreads = 512;
 constexpr int kWidenWarp0 = 8, kWidenWarps = 4, kLoadWarp = 12, kMmaWarp = 13;
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kWidenRegs = 72, kRestRegs = 56;
-static_assert(2 * kSoftmaxRegs + kWidenRegs + kRestRegs <= 4 * kLaunchRegs, "the warpgroups' registers are those of the launch");
+constexpr bool kHalves = true;
+constexpr int kMaxUnroll = 2, kExpUnroll = 1;
 constexpr float kRise = 8.0f;          // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
@@ -55,8 +56,8 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kSK * kTile;
   static constexpr int kOffP = kOffV + kSV * kTile;
   static constexpr int kOffBar = kOffP + kSP * kPacked;
-  // p_full, p_empty [kSP], k_full, k_empty [kSK], v_full, v_empty [kSV], q_full, s_full, w_full, o_final [2], drain
-  static constexpr int kBars = 2 * (kSP + kSK + kSV) + 9;
+  // p_full, p_empty [kSP], k_full, k_empty [kSK], v_full, v_empty [kSV], q_full, s_full, w_half, w_full, o_final [2], drain
+  static constexpr int kBars = 2 * (kSP + kSK + kSV) + 11;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;
@@ -87,9 +88,10 @@ struct Lay {
   __device__ uint32_t rest(int i) const { return bar(2 * (C::kSP + C::kSK + C::kSV) + i); }
   __device__ uint32_t q_full(int t) const { return rest(t); }
   __device__ uint32_t s_full(int t) const { return rest(2 + t); }
-  __device__ uint32_t w_full(int t) const { return rest(4 + t); }  // P, the weights
-  __device__ uint32_t o_final(int t) const { return rest(6 + t); }
-  __device__ uint32_t drain() const { return rest(8); }
+  __device__ uint32_t w_half(int t) const { return rest(4 + t); }  // P, the weights, of a tile's first 64 keys
+  __device__ uint32_t w_full(int t) const { return rest(6 + t); }  // all of them
+  __device__ uint32_t o_final(int t) const { return rest(8 + t); }
+  __device__ uint32_t drain() const { return rest(10); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
@@ -188,7 +190,7 @@ __device__ __forceinline__ void widen_role(const Paged4Params& P, const Lay<D>& 
         if (g >= kS && !wait_warp(which ? sm.v_empty(to) : sm.k_empty(to), ((g / kS) - 1) & 1, p.timeout_ns, p.status)) return;
         const uint8_t* src = sm.packed_ptr(st);
         uint8_t* dst = (which ? sm.v_ptr(to) : sm.k_ptr(to)) + (part >> 1) * C::kSub;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < BN / kStep / kWidenWarps; ++i) {
           const int row = (i * kWidenWarps + warp) * kStep + r0;
           const uint4 v = *reinterpret_cast<const uint4*>(src + row * C::kRow + part * 16);
@@ -239,13 +241,12 @@ __device__ __forceinline__ void mma_role(const Paged4Params& P, const Lay<D>& sm
     }
     tc_commit_elect(sm.s_full(t));
   };
-  auto issue_pv = [&](int t, int vs, bool first) {
+  auto issue_pv = [&](int t, int vs, int half, bool first) {  // keys 64 half .. of the tile
     const uint64_t b = make_sdesc_sw128(sm.v_tile(vs), C::kSub, 1024);
     const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
-#pragma unroll
-    for (int k = 0; k < BN / 16; k += 4)
-      mma_ts4_elect(d, a + k * 8, b + (uint32_t)(k * 128), a + (k + 1) * 8, b + (uint32_t)((k + 1) * 128), a + (k + 2) * 8,
-                    b + (uint32_t)((k + 2) * 128), a + (k + 3) * 8, b + (uint32_t)((k + 3) * 128), kIdO, first && k == 0 ? 0u : 1u);
+    const int k = 4 * half;
+    mma_ts4_elect(d, a + k * 8, b + (uint32_t)(k * 128), a + (k + 1) * 8, b + (uint32_t)((k + 1) * 128), a + (k + 2) * 8,
+                  b + (uint32_t)((k + 2) * 128), a + (k + 3) * 8, b + (uint32_t)((k + 3) * 128), kIdO, first ? 0u : 1u);
   };
   for (; ok && !w.done(); w.next(p)) {
     if (w.nt == 0) continue;  // no S, and no Q was brought
@@ -256,9 +257,15 @@ __device__ __forceinline__ void mma_role(const Paged4Params& P, const Lay<D>& sm
       if (n >= 1 && !wait_warp(sm.v_full(sv), ((g + n - 1) / C::kSV) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         if (n >= 1) {
+          if (kHalves) {
+            if (!wait_warp(sm.w_half(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv(t, sv, 0, n == 1);
+          }
           if (!wait_warp(sm.w_full(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
-          issue_pv(t, sv, n == 1);
+          if (!kHalves) issue_pv(t, sv, 0, n == 1);
+          issue_pv(t, sv, 1, false);
           if (n == w.nt) tc_commit_elect(sm.o_final(t));
           ++pc[t];
         }
@@ -315,7 +322,8 @@ __device__ __forceinline__ float bring_q(const Paged4Params& P, const Lay<D>& sm
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
-  if constexpr (!BF16) return 1.0f;
+  const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;  // of the scale: larger raw scores are larger scores
+  if (!BF16 && sign == 0u) return 1.0f;
   const int r = row0 + lane;
   uint8_t* mine = sm.q_ptr(t) + r * 128;
   uint32_t top2 = 0;
@@ -333,7 +341,11 @@ __device__ __forceinline__ float bring_q(const Paged4Params& P, const Lay<D>& sm
   for (int i = 0; i < kVec; ++i) {
     uint4* at = reinterpret_cast<uint4*>(mine + (i >> 3) * C::kSub + (((i & 7) ^ (r & 7)) << 4));
     const uint4 v = *at;
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t x[4] = {v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
+    if constexpr (!BF16) {
+      *at = make_uint4(x[0], x[1], x[2], x[3]);
+      continue;
+    }
     uint32_t y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -342,7 +354,7 @@ __device__ __forceinline__ float bring_q(const Paged4Params& P, const Lay<D>& sm
     }
     *at = make_uint4(y[0], y[1], y[2], y[3]);
   }
-  return __uint_as_float((uint32_t)(127 - e) << 23);
+  return BF16 ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
 }
 
 // 32 bytes of a row, which lies apart from other threads' rows: one store of
@@ -356,18 +368,6 @@ __device__ __forceinline__ void store_32b(void* ptr, const uint32_t* v, bool ali
     reinterpret_cast<uint4*>(ptr)[0] = make_uint4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<uint4*>(ptr)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
-}
-
-// The largest of 128 values, in eight chains of three-input maxima.
-__device__ __forceinline__ float max128(const float (&x)[BN]) {
-  float m[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m[k] = fmaxf(x[k], x[k + 8]);
-#pragma unroll
-  for (int i = 16; i < BN; i += 16)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m[k] = fmax3(m[k], x[i + k], x[i + 8 + k]);
-  return fmaxf(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], fmax3(m[5], m[6], m[7])));
 }
 
 template <int D, bool BF16, bool SOFTCAP>
@@ -448,9 +448,9 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
     const int last = min(x0 + BM, u.row0 + u.rows) - 1;
     const int2 lim = mine ? paged_limits(p, u.q, paged_token(p, x0 + row)) : make_int2(0, 0);
     const int full_lo = paged_limits(p, u.q, paged_token(p, last)).x, full_hi = paged_limits(p, u.q, paged_token(p, x0)).y;
-    const float raw = qs * (P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2);
-    // what brings x, the raw score or its tanh, to log2 units: positive, so that -inf stays -inf
-    const float xs = SOFTCAP ? TP.sc_out : fmaxf(fabsf(raw), 1.2e-38f);
+    // positive, so that -inf stays -inf
+    const float raw = fmaxf(qs * (P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2), 1.2e-38f);
+    const float xs = SOFTCAP ? TP.sc_out : raw;  // brings x, the raw score or its tanh, to log2 units
     vh = P.v_heads ? __ldg(P.v_heads + u.kvh) : 1.0f;
     m_run = kNone;
     l_run = 0.0f;
@@ -458,64 +458,44 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
       const int key0 = (t0 + n) * BN;
       if (!wait_warp(sm.s_full(t), sc & 1, p.timeout_ns, p.status)) return;
       tc_fence_after();
-      float x[BN];
-      {
-        uint32_t sr[4][32];
+      if (key0 < full_lo || key0 + BN > full_hi) {  // some key is hidden from some row: -inf over its score
+        const int lo = min(max(lim.x - key0, 0), BN), span = max(min(max(lim.y - key0, 0), BN) - lo, 0);
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t x[32];
+          tmem_ld32(s_addr + ch * 32, x);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(s_addr + k * 32, sr[k]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[k * 32 + i] = __uint_as_float(sr[k][i]);
-      }
-      if constexpr (SOFTCAP) {
-        const uint64_t in2 = f2(raw, raw);
-#pragma unroll
-        for (int i = 0; i < BN; i += 2) {
-          float a, b;
-          f2_split(fmul2(f2(x[i], x[i + 1]), in2), a, b);
-          x[i] = fast_tanh(a);
-          x[i + 1] = fast_tanh(b);
+          for (int i = 0; i < 32; ++i) x[i] = (uint32_t)(ch * 32 + i - lo) < (uint32_t)span ? x[i] : 0xff800000u;
+          tmem_st32(s_addr + ch * 32, x);
         }
-      } else if (raw < 0.0f) {
-#pragma unroll
-        for (int i = 0; i < BN; ++i) x[i] = -x[i];
+        tmem_wait_st();
       }
-      if (key0 < full_lo || key0 + BN > full_hi) {  // some key is hidden from some row
-        const int lo = min(max(lim.x - key0, 0), BN);
-        const uint32_t span = (uint32_t)max(min(max(lim.y - key0, 0), BN) - lo, 0);
+      // tanh(scale s / c) of a raw score; hidden ones stay -inf
+      auto capped = [&](float x) {
+        if constexpr (SOFTCAP) return x == -INFINITY ? x : fast_tanh(x * raw);
+        else return x;
+      };
+      float m_tile = -INFINITY;
+#pragma unroll kMaxUnroll
+      for (int ch = 0; ch < 4; ++ch) {
+        float x[32];
+        tmem_ld32(s_addr + ch * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+        tmem_wait_ld();
+        float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
 #pragma unroll
-        for (int i = 0; i < BN; ++i) x[i] = (uint32_t)(i - lo) < span ? x[i] : -INFINITY;
+        for (int k = 4; k < 32; k += 4) {
+          a = fmax3(a, x[k], x[k + 1]);
+          b = fmax3(b, x[k + 2], x[k + 3]);
+        }
+        m_tile = fmax3(m_tile, a, b);
       }
-      const float m_tile = max128(x) * xs;
+      m_tile = capped(m_tile) * xs;
       const bool rise = m_tile > m_run + kRise;
       const float m_new = rise ? m_tile : m_run;
-      const float alpha = fast_exp2(m_run - m_new);
-      m_run = m_new;
-      l_run *= alpha;
-      const float off = kPLog2 - m_run;
-      const uint64_t mul = f2(xs, xs), add = f2(off, off);
-      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a, b;
-          f2_split(ffma2(f2(x[ch * 32 + 2 * i], x[ch * 32 + 2 * i + 1]), mul, add), a, b);
-          a = fast_exp2(a);
-          b = fast_exp2(b);
-          acc[i & 3] = fadd2(acc[i & 3], f2(a, b));
-          const __half2 hh = __floats2half2_rn(a, b);
-          pk[i] = *reinterpret_cast<const uint32_t*>(&hh);
-        }
-        tmem_st16(s_addr + ch * 16, pk);
-      }
-      float sa, sb;
-      f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), sa, sb);
-      l_run += sa + sb;
       if (n > 0 && __any_sync(0xffffffffu, rise)) {  // O holds every earlier tile
+        const float alpha = fast_exp2(m_run - m_new);
+        l_run *= alpha;
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
@@ -526,6 +506,36 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
           tmem_st32(o_addr + k * 32, o);
         }
       }
+      m_run = m_new;
+      const float off = kPLog2 - m_run;
+      const uint64_t mul = f2(xs, xs), add = f2(off, off);
+      uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll kExpUnroll
+      for (int ch = 0; ch < 4; ++ch) {
+        float x[32];
+        tmem_ld32(s_addr + ch * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+        tmem_wait_ld();
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float a, b;
+          f2_split(ffma2(f2(capped(x[2 * i]), capped(x[2 * i + 1])), mul, add), a, b);
+          a = fast_exp2(a);
+          b = fast_exp2(b);
+          acc[i & 1] = fadd2(acc[i & 1], f2(a, b));
+          pk[i] = as_bits(__floats2half2_rn(a, b));
+        }
+        tmem_st16(s_addr + ch * 16, pk);  // over columns of S that have been read
+        if (kHalves && ch == 1) {  // P V of the first 64 keys runs during the others' exponentials
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sm.w_half(t));
+        }
+      }
+      float sa, sb;
+      f2_split(fadd2(acc[0], acc[1]), sa, sb);
+      l_run += sa + sb;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -577,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
     for (int t = 0; t < 2; ++t) {
       mbar_init(sm.q_full(t), 4);
       mbar_init(sm.s_full(t), 1);
+      mbar_init(sm.w_half(t), 4);
       mbar_init(sm.w_full(t), 4);
       mbar_init(sm.o_final(t), 1);
     }
@@ -596,13 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
   Walk w;
   w.begin(p, sm.share());
   if (warp < kWidenWarp0) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     softmax_role<D, BF16, SOFTCAP>(TP, sm, w, tmem, warp, lane);
   } else if (warp < kLoadWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
     widen_role<D>(TP.p, sm, w, warp - kWidenWarp0, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == kLoadWarp) load_role<D>(TP.p, sm, w, lane);
     else if (warp == kMmaWarp) mma_role<D>(TP.p, sm, w, tmem, lane);
   }
@@ -623,11 +631,6 @@ cudaError_t launch_tc(const Paged4TcParams& TP, int grid, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 128 || !ready[dev].load(std::memory_order_relaxed)) {
-    // the registers that the warpgroups share out are the launch's: with fewer the softmax warps would wait for ever
-    cudaFuncAttributes a{};
-    e = cudaFuncGetAttributes(&a, kernel);
-    if (e != cudaSuccess) return e;
-    if (a.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev].store(true, std::memory_order_relaxed);
@@ -647,9 +650,9 @@ cudaError_t launch_attn_paged4_tc(const Paged4Params& p, int grid, bool bf16, cu
   Paged4TcParams TP{};
   TP.p = p;
   TP.aligned32 = ((reinterpret_cast<uintptr_t>(p.c.out) | reinterpret_cast<uintptr_t>(p.ws_o)) & 31) == 0;
-  TP.scale_log2 = (float)((double)p.c.scale * 1.4426950408889634);
+  TP.scale_log2 = (float)(fabs((double)p.c.scale) * 1.4426950408889634);  // the sign goes into Q
   if (p.c.softcap > 0.0f) {
-    TP.sc_in = (float)((double)p.c.scale / (double)p.c.softcap);
+    TP.sc_in = (float)(fabs((double)p.c.scale) / (double)p.c.softcap);
     TP.sc_out = (float)((double)p.c.softcap * 1.4426950408889634);
   }
   if (p.c.D == 128) return bf16 ? launch_tc_d<128, true>(TP, grid, stream) : launch_tc_d<128, false>(TP, grid, stream);
