@@ -683,22 +683,33 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 
 def _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales, v_head_scales, index):
-    """(num_blocks, Hkv, block_size, D, head scales' addresses) of a 4-bit cache, after checking its tensors."""
+    """(num_blocks, Hkv, block_size, D, addresses of the head scales) of a 4-bit cache, after checking its tensors."""
     shape, dtype, sdtype = k_cache.shape, k_cache.dtype, k_scales.dtype
     if len(shape) != 4 or dtype not in CODE_DTYPES or sdtype not in CACHE_DTYPES:
         raise ValueError("the caches must be [num_blocks, Hkv, block_size, D / 2] of uint8 (or float4_e2m1fn_x2) with "
                          f"scales of float8_e4m3fn or uint8: got {dtype} {tuple(shape)}, {sdtype}")
+    num_blocks, Hkv, block_size, half = shape
     _need(k_cache, "k_cache", dtype, shape, index)
     _need(v_cache, "v_cache", dtype, shape, index)
-    groups = (*shape[:3], shape[3] * 2 // GROUP4)
+    groups = (num_blocks, Hkv, block_size, half * 2 // GROUP4)
     _need(k_scales, "k_scales", sdtype, groups, index)
     _need(v_scales, "v_scales", sdtype, groups, index)
-    heads = []
-    for t, name in ((k_head_scales, "k_head_scales"), (v_head_scales, "v_head_scales")):
-        if t is not None:
-            _need(t, name, _F32, (shape[1],), index)
-        heads.append(None if t is None else t.data_ptr())
-    return shape[0], shape[1], shape[2], shape[3] * 2, heads
+    kh = vh = None
+    if k_head_scales is not None:
+        _need(k_head_scales, "k_head_scales", _F32, (Hkv,), index)
+        kh = k_head_scales.data_ptr()
+    if v_head_scales is not None:
+        _need(v_head_scales, "v_head_scales", _F32, (Hkv,), index)
+        vh = v_head_scales.data_ptr()
+    return num_blocks, Hkv, block_size, half * 2, kh, vh
+
+
+def _on_device(index, call, *args):
+    """call(*args) with device `index` current: almost always it is already."""
+    if index == torch._C._cuda_getDevice():
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
 
 
 def attn_cache_append_fp4(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, *, k_head_scales=None,
@@ -718,16 +729,15 @@ def attn_cache_append_fp4(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, 
     if dtype not in DTYPE_CODES or v.dtype is not dtype:
         raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
     T, Hkv, D = k.shape
-    num_blocks, heads, block_size, width, (kh, vh) = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
-                                                                   v_head_scales, index)
+    num_blocks, heads, block_size, width, kh, vh = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
+                                                                 v_head_scales, index)
     if heads != Hkv or width != D:
         raise ValueError(f"shape mismatch: rows of {Hkv} kv heads of {D}, a cache of {heads} of {width}")
     _need(slot_map, "slot_map", _I64, (T,), index)
-    with _on(index):
-        rc = load_library().attn_cache_append_fp4(
-            k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), kh, vh, T, Hkv, D, _token_stride(k, "k"), _token_stride(v, "v"),
-            num_blocks, block_size, DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
+    rc = _on_device(
+        index, load_library().attn_cache_append_fp4, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kh, vh, T, Hkv, D, _token_stride(k, "k"),
+        _token_stride(v, "v"), num_blocks, block_size, DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_append_fp4")
 
@@ -754,23 +764,29 @@ def attn_cache_read_fp4(k_cache, v_cache, k_scales, v_scales, slot_map, *, dtype
     index = k_cache.get_device()
     if index < 0 or slot_map.dim() != 1:
         raise ValueError("attn_cache_read_fp4 takes CUDA tensors: caches [num_blocks, Hkv, block_size, D / 2], slot_map [T]")
-    num_blocks, Hkv, block_size, D, (kh, vh) = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
-                                                             v_head_scales, index)
+    num_blocks, Hkv, block_size, D, kh, vh = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
+                                                           v_head_scales, index)
     T = slot_map.shape[0]
     _need(slot_map, "slot_map", _I64, (T,), index)
     if (k is None) != (v is None):
         raise ValueError("give both k and v, or neither")
     if k is None:
-        k, v = (torch.empty((T, Hkv, D), dtype=dtype, device=k_cache.device) for _ in range(2))
-    elif k.shape != (T, Hkv, D) or v.shape != k.shape or k.get_device() != index or v.get_device() != index:
-        raise ValueError(f"k, v must be [{T}, {Hkv}, {D}] on cuda:{index}")
-    if k.dtype not in DTYPE_CODES or v.dtype is not k.dtype:
-        raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
-    with _on(index):
-        rc = load_library().attn_cache_read_fp4(
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kh, vh,
-            slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), T, Hkv, D, *_row_strides(k, "k"), *_row_strides(v, "v"),
-            num_blocks, block_size, DTYPE_CODES[k.dtype], torch._C._cuda_getCurrentRawStream(index))
+        if dtype not in DTYPE_CODES:
+            raise ValueError("dtype must be float32, float16 or bfloat16")
+        k = torch.empty((T, Hkv, D), dtype=dtype, device=k_cache.device)
+        v = torch.empty_like(k)
+        strides = (Hkv * D, D, Hkv * D, D)
+    else:
+        dtype = k.dtype
+        if k.shape != (T, Hkv, D) or v.shape != k.shape or k.get_device() != index or v.get_device() != index:
+            raise ValueError(f"k, v must be [{T}, {Hkv}, {D}] on cuda:{index}")
+        if dtype not in DTYPE_CODES or v.dtype is not dtype:
+            raise ValueError("k and v must share one dtype among float32 / float16 / bfloat16")
+        strides = (*_row_strides(k, "k"), *_row_strides(v, "v"))
+    rc = _on_device(
+        index, load_library().attn_cache_read_fp4, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), kh, vh, slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), T, Hkv, D, *strides, num_blocks,
+        block_size, DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_read_fp4")
     return k, v
@@ -800,8 +816,8 @@ def attn_fwd_paged_fp4(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_
     shape = q.shape
     T, Hq, D = shape
     B, width = block_tables.shape
-    num_blocks, Hkv, block_size, cache_d, (kh, vh) = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
-                                                                   v_head_scales, index)
+    num_blocks, Hkv, block_size, cache_d, kh, vh = _cache4_shape(k_cache, v_cache, k_scales, v_scales, k_head_scales,
+                                                                 v_head_scales, index)
     if cache_d != D:
         raise ValueError(f"shape mismatch: q rows of {D}, cache rows of {cache_d}")
     _need(block_tables, "block_tables", _I32, (B, width), index)
@@ -818,13 +834,13 @@ def attn_fwd_paged_fp4(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_
         workspace = _workspace(_paged4_workspace(T, B, Hq, Hkv, D, index), index, stream, q.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-    with _on(index):
-        rc = load_library().attn_fwd_paged_fp4(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kh, vh,
-            block_tables.data_ptr(), q_starts.data_ptr(), total_lengths.data_ptr(), out.data_ptr(),
-            None if lse is None else lse.data_ptr(), T, B, Hq, Hkv, D, _token_stride(q, "q"), num_blocks, block_size,
-            width, 1 if causal else 0, int(local_window), 1.0 / math.sqrt(D) if scale is None else scale, softcap,
-            DTYPE_CODES[dtype], workspace.data_ptr(), workspace.nbytes, stream)
+    rc = _on_device(
+        index, load_library().attn_fwd_paged_fp4, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), kh, vh, block_tables.data_ptr(), q_starts.data_ptr(),
+        total_lengths.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), T, B, Hq, Hkv, D,
+        _token_stride(q, "q"), num_blocks, block_size, width, 1 if causal else 0, int(local_window),
+        1.0 / math.sqrt(D) if scale is None else scale, softcap, DTYPE_CODES[dtype], workspace.data_ptr(),
+        workspace.nbytes, stream)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_paged_fp4")
     return out
@@ -886,55 +902,61 @@ def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=No
     rows to gradients of q and k.  Returns (q_out, k_out), allocated with torch
     when not given; q_out=q, k_out=k works in place.  Rows of no request are not
     written."""
-    index, dtype = q.get_device(), q.dtype
-    if q.dim() != 3 or index < 0:
+    index, dtype, shape = q.get_device(), q.dtype, q.shape
+    if len(shape) != 3 or index < 0:
         raise ValueError("attn_rope takes CUDA tensors: q [T, Hq, D], k [T, Hk, D] or None")
     if dtype not in DTYPE_CODES:
         raise ValueError("q must be float32, float16 or bfloat16")
-    T, Hq, D = q.shape
-    Hk = 0
-    if k is not None:
-        Hk = k.shape[1] if k.dim() == 3 else -1
-        if k.shape != (T, Hk, D) or k.dtype is not dtype or k.get_device() != index:
-            raise ValueError(f"k must be [{T}, Hk, {D}] of {dtype} on cuda:{index}: got {k.dtype} {tuple(k.shape)}")
+    T, Hq, D = shape
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [R / 2]")
-    _need(inv_freq, "inv_freq", torch.float64, inv_freq.shape, index)
-    if layout not in ROPE_LAYOUTS:
+    pairs = inv_freq.shape[0]
+    _need(inv_freq, "inv_freq", torch.float64, (pairs,), index)
+    inter = ROPE_LAYOUTS.get(layout)
+    if inter is None:
         raise ValueError(f"layout must be 'half' or 'interleaved': got {layout!r}")
-    B = 0
+    B, at = 0, (None, None, None)
     if positions is not None:
         if q_starts is not None or total_lengths is not None:
             raise ValueError("give positions, or q_starts and total_lengths")
         _need(positions, "positions", _I32, (T,), index)
+        at = (positions.data_ptr(), None, None)
     else:
         if q_starts is None or total_lengths is None or total_lengths.dim() != 1:
             raise ValueError("give positions, or q_starts and total_lengths")
         B = total_lengths.shape[0]
         _need(q_starts, "q_starts", _I32, (B + 1,), index)
         _need(total_lengths, "total_lengths", _I32, (B,), index)
+        at = (None, q_starts.data_ptr(), total_lengths.data_ptr())
 
-    def made(t, x, name):
-        if x is None:
-            if t is not None:
-                raise ValueError(f"{name} without its input")
-            return None
-        if t is None:
-            return torch.empty(x.shape, dtype=dtype, device=x.device)
-        if t.shape != x.shape or t.dtype is not dtype or t.get_device() != index:
-            raise ValueError(f"{name} must be {dtype} {tuple(x.shape)} on cuda:{index}: got {t.dtype} {tuple(t.shape)}")
-        return t
+    def given(t, shape, name):
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{index}: got {t.dtype} {tuple(t.shape)}")
+        return _token_stride(t, name)
 
-    q_out, k_out = made(q_out, q, "q_out"), made(k_out, k, "k_out")
-    with _on(index):
-        rc = load_library().attn_rope(
-            q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-            None if k is None else k_out.data_ptr(), inv_freq.data_ptr(),
-            None if positions is None else positions.data_ptr(), None if q_starts is None else q_starts.data_ptr(),
-            None if total_lengths is None else total_lengths.data_ptr(), T, B, Hq, Hk, D, 2 * inv_freq.shape[0],
-            _token_stride(q, "q"), 0 if k is None else _token_stride(k, "k"), _token_stride(q_out, "q_out"),
-            0 if k is None else _token_stride(k_out, "k_out"), ROPE_LAYOUTS[layout], 1 if inverse else 0, scale,
-            DTYPE_CODES[dtype], torch._C._cuda_getCurrentRawStream(index))
+    qs = _token_stride(q, "q")
+    if q_out is None:
+        q_out, qos = torch.empty(shape, dtype=dtype, device=q.device), Hq * D
+    else:
+        qos = given(q_out, shape, "q_out")
+    Hk = ks = kos = 0
+    k_ptr = k_out_ptr = None
+    if k is not None:
+        k_shape = k.shape
+        if len(k_shape) != 3 or k_shape[0] != T or k_shape[2] != D:
+            raise ValueError(f"k must be [{T}, Hk, {D}]: got {tuple(k_shape)}")
+        Hk, ks, k_ptr = k_shape[1], given(k, k_shape, "k"), k.data_ptr()
+        if k_out is None:
+            k_out, kos = torch.empty(k_shape, dtype=dtype, device=q.device), Hk * D
+        else:
+            kos = given(k_out, k_shape, "k_out")
+        k_out_ptr = k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rc = _on_device(
+        index, load_library().attn_rope, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, inv_freq.data_ptr(), *at, T, B,
+        Hq, Hk, D, 2 * pairs, qs, ks, qos, kos, inter, 1 if inverse else 0, scale, DTYPE_CODES[dtype],
+        torch._C._cuda_getCurrentRawStream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope")
     return q_out, k_out

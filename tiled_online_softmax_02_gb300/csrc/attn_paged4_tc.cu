@@ -15,11 +15,11 @@
 //
 // One CTA an SM walks its share of the line of key tiles (paged_sched.cuh).
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two lanes, thread =
-// row, the row's 128 scores in registers, which the other warps give up
-// (setmaxnreg); they also bring the next unit's Q before they store the last
-// one's rows.  Warps 8-11 widen; warp 12 loads (bulk copies: a block's rows of a
-// head lie together), 13 issues MMAs.
-// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each.
+// row; they also bring the next unit's Q before they store the last one's rows.
+// Warps 8-11 widen; warp 12 loads (bulk copies: a block's rows of a head lie
+// together), 13 issues MMAs.
+// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
+//
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -36,11 +36,13 @@ constexpr int BM = 128, BN = kPagedKeys;
 constexpr int kRows = kPagedTcRows;    // rows of a unit: two lanes of 128
 constexpr int kThreads = 512;
 constexpr int kWidenWarp0 = 8, kWidenWarps = 4, kLoadWarp = 12, kMmaWarp = 13;
-constexpr bool kHalves = true;
-constexpr int kMaxUnroll = 2, kExpUnroll = 1;
 constexpr float kRise = 8.0f;          // the maximum moves when a key passes it by 2^8
 constexpr float kPLog2 = kPagedTcLog2;  // P is carried as 2^(t - m + 7) <= 2^15
 constexpr uint32_t kColO = 256;
+// Loops over a tile's four runs of 32 keys.  Their code is what counts: long chunks take 555 us with these, 567 with the
+// maximum's loop unrolled once, 577 four times, 602 with the row's scores in registers and no loops, 572 with the next
+// run's scores on their way during this one's exponentials.
+constexpr int kMaxUnroll = 2, kExpUnroll = 1;
 
 template <int D>
 struct Cfg {
@@ -56,8 +58,8 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kSK * kTile;
   static constexpr int kOffP = kOffV + kSV * kTile;
   static constexpr int kOffBar = kOffP + kSP * kPacked;
-  // p_full, p_empty [kSP], k_full, k_empty [kSK], v_full, v_empty [kSV], q_full, s_full, w_half, w_full, o_final [2], drain
-  static constexpr int kBars = 2 * (kSP + kSK + kSV) + 11;
+  // p_full, p_empty [kSP], k_full, k_empty [kSK], v_full, v_empty [kSV], q_full, s_full, w_full, o_final [2], drain
+  static constexpr int kBars = 2 * (kSP + kSK + kSV) + 9;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffShare = (kOffSlot + 16 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShare + (int)sizeof(PagedShare) + 1024;
@@ -88,10 +90,9 @@ struct Lay {
   __device__ uint32_t rest(int i) const { return bar(2 * (C::kSP + C::kSK + C::kSV) + i); }
   __device__ uint32_t q_full(int t) const { return rest(t); }
   __device__ uint32_t s_full(int t) const { return rest(2 + t); }
-  __device__ uint32_t w_half(int t) const { return rest(4 + t); }  // P, the weights, of a tile's first 64 keys
-  __device__ uint32_t w_full(int t) const { return rest(6 + t); }  // all of them
-  __device__ uint32_t o_final(int t) const { return rest(8 + t); }
-  __device__ uint32_t drain() const { return rest(10); }
+  __device__ uint32_t w_full(int t) const { return rest(4 + t); }  // P, the weights
+  __device__ uint32_t o_final(int t) const { return rest(6 + t); }
+  __device__ uint32_t drain() const { return rest(8); }
   __device__ uint32_t* slot() const { return reinterpret_cast<uint32_t*>(base + C::kOffSlot); }
   __device__ PagedShare* share() const { return reinterpret_cast<PagedShare*>(base + C::kOffShare); }
 };
@@ -241,12 +242,13 @@ __device__ __forceinline__ void mma_role(const Paged4Params& P, const Lay<D>& sm
     }
     tc_commit_elect(sm.s_full(t));
   };
-  auto issue_pv = [&](int t, int vs, int half, bool first) {  // keys 64 half .. of the tile
+  auto issue_pv = [&](int t, int vs, bool first) {
     const uint64_t b = make_sdesc_sw128(sm.v_tile(vs), C::kSub, 1024);
     const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
-    const int k = 4 * half;
-    mma_ts4_elect(d, a + k * 8, b + (uint32_t)(k * 128), a + (k + 1) * 8, b + (uint32_t)((k + 1) * 128), a + (k + 2) * 8,
-                  b + (uint32_t)((k + 2) * 128), a + (k + 3) * 8, b + (uint32_t)((k + 3) * 128), kIdO, first ? 0u : 1u);
+#pragma unroll
+    for (int k = 0; k < BN / 16; k += 4)
+      mma_ts4_elect(d, a + k * 8, b + (uint32_t)(k * 128), a + (k + 1) * 8, b + (uint32_t)((k + 1) * 128), a + (k + 2) * 8,
+                    b + (uint32_t)((k + 2) * 128), a + (k + 3) * 8, b + (uint32_t)((k + 3) * 128), kIdO, first && k == 0 ? 0u : 1u);
   };
   for (; ok && !w.done(); w.next(p)) {
     if (w.nt == 0) continue;  // no S, and no Q was brought
@@ -257,15 +259,9 @@ __device__ __forceinline__ void mma_role(const Paged4Params& P, const Lay<D>& sm
       if (n >= 1 && !wait_warp(sm.v_full(sv), ((g + n - 1) / C::kSV) & 1, p.timeout_ns, p.status)) { ok = false; break; }
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         if (n >= 1) {
-          if (kHalves) {
-            if (!wait_warp(sm.w_half(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv(t, sv, 0, n == 1);
-          }
           if (!wait_warp(sm.w_full(t), pc[t] & 1, p.timeout_ns, p.status)) { ok = false; break; }
           tc_fence_after();
-          if (!kHalves) issue_pv(t, sv, 0, n == 1);
-          issue_pv(t, sv, 1, false);
+          issue_pv(t, sv, n == 1);
           if (n == w.nt) tc_commit_elect(sm.o_final(t));
           ++pc[t];
         }
@@ -342,16 +338,10 @@ __device__ __forceinline__ float bring_q(const Paged4Params& P, const Lay<D>& sm
     uint4* at = reinterpret_cast<uint4*>(mine + (i >> 3) * C::kSub + (((i & 7) ^ (r & 7)) << 4));
     const uint4 v = *at;
     const uint32_t x[4] = {v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
-    if constexpr (!BF16) {
-      *at = make_uint4(x[0], x[1], x[2], x[3]);
-      continue;
-    }
     uint32_t y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __half2 h = __floats2half2_rn(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
-      y[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+    for (int k = 0; k < 4; ++k)
+      y[k] = BF16 ? as_bits(__floats2half2_rn(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up)) : x[k];
     *at = make_uint4(y[0], y[1], y[2], y[3]);
   }
   return BF16 ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
@@ -526,12 +516,6 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
           pk[i] = as_bits(__floats2half2_rn(a, b));
         }
         tmem_st16(s_addr + ch * 16, pk);  // over columns of S that have been read
-        if (kHalves && ch == 1) {  // P V of the first 64 keys runs during the others' exponentials
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sm.w_half(t));
-        }
       }
       float sa, sb;
       f2_split(fadd2(acc[0], acc[1]), sa, sb);
@@ -587,7 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
     for (int t = 0; t < 2; ++t) {
       mbar_init(sm.q_full(t), 4);
       mbar_init(sm.s_full(t), 1);
-      mbar_init(sm.w_half(t), 4);
       mbar_init(sm.w_full(t), 4);
       mbar_init(sm.o_final(t), 1);
     }
