@@ -82,6 +82,7 @@ class Problem:
     heads: bool = False     # head scales, no powers of two
     spread: bool = False    # group scales over all that e4m3 holds
     strided: bool = False
+    wide: bool = False      # block tables as for contexts of a million tokens: calls with many rows go to their kernel
     sink: float = 0.0       # > 0: key 0 of every request points along every query, its V row is small
     seed: int = 5
 
@@ -95,7 +96,7 @@ def make(w: Problem) -> dict:
     rng = np.random.Generator(np.random.PCG64(w.seed))
     B, T = len(w.new), sum(w.new) + w.pad
     held = [-(-max(t, 0) // w.block) for t in w.total]
-    width, N = max(held + [1]) + 1, sum(held) + 2
+    width, N = max(held + [1]) + 1 + (2 ** 20 // w.block if w.wide else 0), sum(held) + 2
     pool = rng.permutation(N)
     tables = rng.choice(np.array([-1, -7, N, N + 5, 2 ** 31 - 1]), size=(B, width)).astype(np.int64)
     at = 0

@@ -182,6 +182,12 @@ def test_decode_heads(Hq, Hkv, dtype, D):
     check(Problem(new=(1, 1, 1), total=(300, 77, 1), Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, block=32))
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("Hq,Hkv,block", [(4, 4, 16), (15, 3, 32), (40, 2, 128), (12, 1, 64)])
+def test_many_rows_heads(Hq, Hkv, block, dtype, D):
+    check(Problem(new=(80, 1, 200), total=(300, 77, 200), Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, block=block, wide=True))
+
+
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
 @pytest.mark.parametrize("total", [(1,), (127, 128, 129), (255, 256, 257, 15, 16, 17), (33, 2000)])
 def test_decode_lengths(total, block):
@@ -206,21 +212,21 @@ FEATURES = {
 
 
 @pytest.mark.parametrize("feature", list(FEATURES))
-@pytest.mark.parametrize("shape", list(SHAPES))
-def test_shapes_and_features(shape, feature):
-    check(Problem(**{**SHAPES[shape], **FEATURES[feature]}))
+@pytest.mark.parametrize("shape,wide", [(s, w) for s in SHAPES for w in (False, True) if not w or sum(SHAPES[s]["new"]) > 20])
+def test_shapes_and_features(shape, wide, feature):
+    check(Problem(**{**SHAPES[shape], **FEATURES[feature]}, wide=wide))
 
 
 @pytest.mark.parametrize("new", [1, 3, 60, 200])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_one_key_far_above_the_others(new, dtype):
-    check(Problem(new=(new,), total=(900,), dtype=dtype, sink=40.0, Hq=4, Hkv=1))
+    check(Problem(new=(new,), total=(900,), dtype=dtype, sink=40.0, Hq=4, Hkv=1, wide=new == 200))
 
 
 @pytest.mark.parametrize("new", [(2, 1), (150, 40)])
 def test_growing_maximum(new):
     """Keys ever larger: every tile moves the running maximum."""
-    w = Problem(new=new, total=(1100, 700), Hq=4, Hkv=1, dtype="f16")
+    w = Problem(new=new, total=(1100, 700), Hq=4, Hkv=1, dtype="f16", wide=True)
     x = ref.make(w)
     x["q"] = x["q"].abs()
     x["k_cache"] &= 0x77  # positive
@@ -244,7 +250,7 @@ def test_8192_requests():
 
 @pytest.mark.parametrize("new", [(1, 1), (70, 3)])
 def test_tables_that_name_no_block_are_reported(new):
-    w = Problem(new=new, total=(300, 200), block=32)
+    w = Problem(new=new, total=(300, 200), block=32, wide=True)
     x = ref.make(w)
     x["tables"][0, 1] = -1
     x["tables"][1, 3] = x["k_cache"].shape[0]
@@ -262,7 +268,7 @@ def test_tables_that_name_no_block_are_reported(new):
 
 @pytest.mark.parametrize("new", [(1, 1, 1), (200, 1, 33)])
 def test_repeats_and_streams_give_the_same_bits(new):
-    w = Problem(new=new, total=(2000, 300, 1000), Hq=8, Hkv=2)
+    w = Problem(new=new, total=(2000, 300, 1000), Hq=8, Hkv=2, wide=True)
     x = ref.make(w)
     out, lse = _run(w, x)
     for _ in range(3):
@@ -278,7 +284,7 @@ def test_repeats_and_streams_give_the_same_bits(new):
 @pytest.mark.parametrize("new", [(2, 1), (80, 40)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_rows_of_very_different_size_and_rows_not_finite(new, dtype):
-    w = Problem(new=new, total=(400, 300), dtype=dtype, Hq=8, Hkv=2)
+    w = Problem(new=new, total=(400, 300), dtype=dtype, Hq=8, Hkv=2, wide=True)
     x = ref.make(w)
     e = torch.linspace(-100, 3, w.Hq) if dtype == "bf16" else torch.linspace(-12, 5, w.Hq)
     x["q"] = (x["q"].double() * 2.0 ** e.double()[None, :, None]).to(x["q"].dtype)
@@ -296,7 +302,7 @@ def test_rows_of_very_different_size_and_rows_not_finite(new, dtype):
 @pytest.mark.parametrize("cap", [2.0, 50.0, 3e4, 1e30])
 @pytest.mark.parametrize("new", [(2, 1), (150, 40)])
 def test_soft_caps(cap, new):
-    check(Problem(new=new, total=(500, 300), softcap=cap, q_std=20.0 if cap < 100 else 2.0))
+    check(Problem(new=new, total=(500, 300), softcap=cap, q_std=20.0 if cap < 100 else 2.0, wide=True))
 
 
 def test_caller_workspace_and_float_views():
@@ -450,7 +456,7 @@ def test_prompt_read_back_for_dense_attention():
 @pytest.mark.parametrize("new", [(1, 2, 1), (150, 1, 20)])
 def test_blocks_past_four_gigabytes(new):
     """A cache whose blocks lie past 2^32 bytes: its first and last blocks are used."""
-    w = Problem(new=new, total=(300, 90, 130), block=128, Hq=8, Hkv=8)
+    w = Problem(new=new, total=(300, 90, 130), block=128, Hq=8, Hkv=8, wide=True)
     x = ref.make(w)
     per = w.Hkv * w.block * w.D // 2
     N = (5 << 30) // per

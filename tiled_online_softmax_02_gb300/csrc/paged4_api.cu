@@ -211,19 +211,36 @@ struct Plan4 {
   size_t ml_at, cuts_at, bytes;
 };
 
+// `max_tiles`: key tiles that a unit may see, as far as the host knows; the workspace does not depend on it.
 Plan4 plan4(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
   Plan4 pl{};
   if (T <= 0 || B <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0) return pl;
   const int group = Hq / Hkv, sms = paged_sm_count();
-  const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;  // per (request, kv head) of an even batch
+  // Rows per (request, kv head) of an even batch; a request with more takes several units.  The lengths are on the device,
+  // so the mean is all there is to go by.  48 requests of up to 8K tokens, 4 kv heads, D = 128, in units of 8 and of 16
+  // rows: 12 rows 59 and 58 us, 16 rows 57 and 54, 24 rows 77 and 88.
+  const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
   pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedTcRows;
-  const int64_t most = (int64_t)sms * (pl.rows == 8 ? kPaged4DecCtas : 1);
+  int64_t most = (int64_t)sms * (pl.rows == 8 ? kPaged4DecCtas : 1);
+  const size_t slots = 2 * (size_t)most * pl.rows;  // the choice below needs no more
+  const size_t cuts = (size_t)sms * kPaged4DecCtas;
+  if (pl.rows == kPagedTcRows) {
+    // More rows: the few-rows kernel's time goes with its units of 8 rows, 273 of their tiles a microsecond, the
+    // many-rows kernel's with those of 256, 77 tiles, and 15 us more for its first result and the join of what one unit's
+    // tiles leave on many SMs.  What there may be to read: the tables' width, or the window.  4 kv heads: 24 rows, 48
+    // requests of up to 8K 77 us against 85, 32 rows 98 against 85; 8 requests, 32 rows 31 against 32, 64 rows 51 against
+    // 33; one of 4K, 64 rows 14 against 30, 128 rows 19 against 31, 512 rows 48 against 33.
+    const int64_t heads = B * Hkv, few = heads * ((rows + 7) / 8) * max_tiles, many = heads * ((rows + kPagedTcRows - 1) / kPagedTcRows) * max_tiles;
+    if (few / 273 < 15 + many / 77) {
+      pl.rows = 8;
+      most = (int64_t)sms * kPaged4DecCtas;
+    }
+  }
   const int64_t units = (T * group / pl.rows + B) * Hkv;  // no more CTAs than there can be tiles
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
-  const size_t slots = 2 * (size_t)most * pl.rows;
   pl.ml_at = slots * D * 4;
   pl.cuts_at = pl.ml_at + slots * 8;
-  pl.bytes = pl.cuts_at + (size_t)most * sizeof(PagedCut);
+  pl.bytes = pl.cuts_at + cuts * sizeof(PagedCut);
   return pl;
 }
 
@@ -306,7 +323,9 @@ extern "C" int attn_fwd_paged_fp4(const void* q, const void* k_cache, const void
   p.timeout_ns = wait_timeout_ns();
   p.status = status;
   const int64_t max_tiles = std::max<int64_t>(1, ((int64_t)max_blocks * block_size + 127) / 128);
-  const Plan4 plan = plan4(T, B, Hq, Hkv, D, max_tiles);
+  // tiles that a unit of an even batch can see
+  const int64_t seen = p.local_window > 0 ? std::min(max_tiles, (p.local_window + T / B) / 128 + 2) : max_tiles;
+  const Plan4 plan = plan4(T, B, Hq, Hkv, D, seen);
   P.ws_o = static_cast<float*>(workspace);
   P.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ml_at);
   P.cuts = reinterpret_cast<PagedCut*>(static_cast<char*>(workspace) + plan.cuts_at);
