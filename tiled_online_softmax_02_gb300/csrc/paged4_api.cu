@@ -342,7 +342,10 @@ extern "C" int attn_fwd_paged_fp4(const void* q, const void* k_cache, const void
     L.ws_ml = P.ws_ml;
     L.cuts = P.cuts;
     L.ml_log2 = (plan.rows == kPagedTcRows ? kPagedTcLog2 : kPaged4DecLog2) - kPagedSumLog2;
-    e = launch_attn_paged_join(L, bf16, st);
+    // Parts a unit, about: CTAs over units.  64 requests (three) take 43.0 us with a CTA a row and 40.3 with one a unit, one
+    // request of 4K (39) 10.1 and 11.7, 4 of 16 rows (ten) 15.5 and 17.8.
+    const int64_t parts = plan.grid / ((int64_t)B * Hkv * std::max<int64_t>(1, (T / B * p.group + plan.rows - 1) / plan.rows)) + 1;
+    e = plan.rows == kPagedTcRows || parts > 8 ? launch_attn_paged_join(L, bf16, st) : launch_attn_paged4_join(L, bf16, st);
   }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

@@ -61,4 +61,6 @@ cudaError_t launch_rope(const RopeParams& p, bool interleaved, int dtype, cudaSt
 cudaError_t launch_attn_paged4_dec(const Paged4Params& p, int rows, int grid, bool bf16, cudaStream_t stream);  // rows 8 or 16
 cudaError_t launch_attn_paged4_tc(const Paged4Params& p, int grid, bool bf16, cudaStream_t stream);  // rows kPagedTcRows
 
+cudaError_t launch_attn_paged4_join(const PagedLaunch& L, bool bf16, cudaStream_t stream);  // rows 8 or 16, few parts a unit
+
 }  // namespace gb300_attn
