@@ -79,9 +79,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
 
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+// 16 bytes to shared memory: `bytes` of them copied, the others zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -121,9 +121,11 @@ __device__ __forceinline__ int entry_of(const PagedParams& p, const int32_t* tab
   return e >= 0 && e < p.num_blocks ? e : -2;
 }
 
-// Copies a sub-tile into a stage: codes and scales as they lie, zeros for what has no block.
+// Copies a sub-tile into a stage: codes and scales as they lie, zeros for what has no block, and for the scales of keys past
+// the last (their slots may hold NaN, and a weight of 0 times that is not 0).
 template <int D, int NT>
-__device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, int kvh, int sub, int entry, int lane) {
+__device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, int kvh, int sub, int entry, int valid,
+                                         int lane) {
   using C = Cfg<D, NT>;
   const PagedParams& p = P.c;
   if (entry == -2 && (lane & 15) == 0) atomicOr(p.status, kStatusBadBlock);
@@ -146,15 +148,17 @@ __device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, 
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
     const int64_t off = (j < kN / 2 ? off0 : off1) + j * 512;
-    const bool there = j < kN / 2 ? there0 : there1;
-    copy16(stage + j * 512 + at, p.k_cache + off, there);
-    copy16(stage + C::kData + j * 512 + at, p.v_cache + off, there);
+    const int bytes = (j < kN / 2 ? there0 : there1) ? 16 : 0;
+    copy16(stage + j * 512 + at, p.k_cache + off, bytes);
+    copy16(stage + C::kData + j * 512 + at, p.v_cache + off, bytes);
   }
   constexpr int kL = C::kSc / 16;  // lanes for K's scales, and for V's
   if (lane < 2 * kL) {
     const int l = lane & (kL - 1);
     const bool second = l >= kL / 2;
-    copy16(stage + 2 * C::kData + at, (lane < kL ? P.k_sc : P.v_sc) + (second ? row1 : row0) * C::kScRow + l * 16, second ? there1 : there0);
+    const int bytes = min(max(valid - sub * kSub, 0), kSub) * C::kScRow - l * 16;
+    copy16(stage + 2 * C::kData + at, (lane < kL ? P.k_sc : P.v_sc) + (second ? row1 : row0) * C::kScRow + l * 16,
+           (second ? there1 : there0) ? min(max(bytes, 0), 16) : 0);
   }
 }
 
@@ -181,7 +185,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
     for (int s = 0; s <= S; ++s) first[s] = s < subs.count ? entry_of(p, table, valid, subs.first + s * W, lane) : -1;
 #pragma unroll
     for (int s = 0; s < E; ++s) {
-      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, first[s], lane);
+      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, first[s], valid, lane);
       copies_commit();
     }
 #pragma unroll
@@ -191,7 +195,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
   auto prefetch_rest = [&]() {
 #pragma unroll
     for (int s = E; s < S; ++s) {
-      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, entry_rest[s - E], lane);
+      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, entry_rest[s - E],
+                                                paged_valid(p, w.u.q), lane);
       copies_commit();
     }
   };
@@ -405,11 +410,6 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
             }
             sb[x] = vsc[row * C::kScRow + gs];
           }
-          if (key0 + kSub > valid) {  // slots past the last key may hold NaN scales
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (key0 + kt * 16 + (x >> 1) * 8 + 2 * t + (x & 1) >= valid) sb[x] = 0u;
-          }
           const uint32_t s0 = widen_e4m3x2(sb[0] | sb[1] << 8), s1 = widen_e4m3x2(sb[2] | sb[3] << 8);
 #pragma unroll
           for (int i = 0; i < VW; ++i) {
@@ -435,7 +435,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
       __syncwarp();  // the stage has been read
       if (n + S < subs.count) {
         const int next = subs.first + (n + S) * W;
-        load_sub<D, NT>(P, ring_s + at * C::kStage, u.kvh, next, entry, lane);
+        load_sub<D, NT>(P, ring_s + at * C::kStage, u.kvh, next, entry, valid, lane);
         if (n + S + 1 < subs.count) entry = entry_of(p, table, valid, next + W, lane);
       }
       copies_commit();
