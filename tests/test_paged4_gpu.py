@@ -342,6 +342,74 @@ def test_refusals_of_the_binding():
     assert e.value.status == attn.ATTN_ERR_INVALID_ARG
 
 
+class _Ordinary:
+    """The extension module, which must take the calls made through it."""
+
+    def __init__(self, calls):
+        self.calls, self.taken = calls, 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            made = getattr(self.calls, name)(*args)
+            self.taken += made is not None
+            return made
+        return call
+
+
+class _Nothing:
+    """An extension module that takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+@pytest.mark.parametrize("heads", [False, True])
+def test_both_ways_of_marshalling(monkeypatch, heads):
+    """Calls through the extension module and those that Python marshals: the same results and the same errors."""
+    from tiled_online_softmax_02_gb300 import _binding
+    w = Problem(new=(3, 4), total=(90, 40), heads=heads, window=30, softcap=20.0, strided=True)
+    g = {n: gpu(t) for n, t in ref.make(w).items()}
+    h = dict(k_head_scales=g["k_heads"], v_head_scales=g["v_heads"])
+    freq = attn.attn_rope_frequencies(64)[0]
+    slots = torch.tensor([5, 900000, 7, -1, 3, 66, 68], device="cuda")
+    wide = torch.zeros((10, 12, 128), dtype=torch.bfloat16, device="cuda")
+    wide[:, :8] = g["q"]
+
+    def everything():
+        made = []
+        cache = [g[n].clone() for n in ("k_cache", "v_cache", "k_scales", "v_scales")]
+        made += attn.attn_rope(wide[:, :8], wide[:, 8:10], freq, positions=torch.arange(10, dtype=torch.int32, device="cuda"), scale=1.5)
+        made += attn.attn_rope(g["q"], None, freq, q_starts=g["starts"], total_lengths=g["totals"], inverse=True, layout="interleaved",
+                               q_out=torch.zeros_like(g["q"]))[:1]
+        attn.attn_cache_append_fp4(wide[:7, :2], wide[:7, 2:4], slots, *cache, **h)
+        made += cache
+        made += attn.attn_cache_read_fp4(*cache, slots, dtype=torch.float16, **h)
+        made.append(attn.attn_fwd_paged_fp4(wide[:, :8], *cache, g["tables"], g["starts"], g["totals"], local_window=w.window,
+                                            softcap=w.softcap, scale=0.1, out=torch.full_like(g["q"], 7.0), **h))
+        made.append(attn.attn_fwd_paged_fp4(g["q"], *cache, g["tables"], g["starts"], g["totals"], causal=False, **h)[:7])
+        errors = []
+        for bad in (lambda: attn.attn_fwd_paged_fp4(g["q"], *cache, g["tables"], g["starts"], g["totals"], scale=float("nan")),
+                    lambda: attn.attn_rope(g["q"], None, freq, positions=g["totals"]),
+                    lambda: attn.attn_rope(g["q"], None, torch.cat([freq] * 3), positions=torch.zeros(10, dtype=torch.int32, device="cuda")),
+                    lambda: attn.attn_cache_read_fp4(*cache, slots.int()),
+                    lambda: attn.attn_cache_append_fp4(wide[:7, :2], wide[:7, 2:4], slots[:3], *cache)):
+            with pytest.raises((ValueError, attn.AttnError)) as e:
+                bad()
+            errors.append(str(e.value))
+        torch.cuda.synchronize()
+        return made, errors
+
+    ordinary = _Ordinary(_binding._calls)
+    monkeypatch.setattr(_binding, "_calls", ordinary)
+    a, ae = everything()
+    assert ordinary.taken == 8  # six results, and two statuses of the C ABI
+    monkeypatch.setattr(_binding, "_calls", _Nothing())
+    b, be = everything()
+    assert ae == be and len(a) == len(b)
+    for x, y in zip(a, b):
+        assert x.dtype == y.dtype and torch.equal(x, y)
+
+
 # ---------------------------------------------------------- a serving step
 class Batch:
     """A batch's state on the GPU, and in plain numpy beside it."""

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
@@ -74,6 +76,7 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_calls = None  # the extension module of csrc/calls.cpp, bound to _lib
 _host_copies = threading.local()  # (h2d, d2h) bytes of this thread's last host-tensor call
 
 
@@ -105,8 +108,23 @@ def load_library():
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+            _load_calls(lib)
             _lib = lib
         return _lib
+
+
+def _load_calls(lib):
+    """Load the extension module that marshals calls on ordinary tensors, for the functions of `lib`."""
+    global _calls
+    if not os.path.exists(_build.CALLS):
+        raise RuntimeError(f"extension module {_build.CALLS} is missing: build it first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS)
+    calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    calls.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "attn_cache_append_fp4", "attn_cache_read_fp4", "attn_fwd_paged_fp4", "attn_paged_fp4_workspace_bytes",
+        "attn_rope")))
+    _calls = calls
 
 
 def status_string(status: int) -> str:
@@ -676,7 +694,8 @@ def attn_paged_workspace_bytes(num_tokens, B, Hq, Hkv, D) -> int:
 
 
 # ---------------------------------------------------------------------------
-# The paged 4-bit KV cache, and rotary positions.
+# The paged 4-bit KV cache, and rotary positions.  Calls on ordinary arguments go through the extension module
+# (csrc/calls.cpp), which returns None where something is out of the ordinary: the code here then looks at each argument.
 CODE_DTYPES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
 GROUP4 = 16  # values that share a scale
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -723,6 +742,13 @@ def attn_cache_append_fp4(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, 
     uint8 (or float4_e2m1fn_x2) and k_scales, v_scales [num_blocks, Hkv,
     block_size, D / 16] float8_e4m3fn (or uint8), updated in place;
     k_head_scales, v_head_scales float32 [Hkv] or None (1)."""
+    if _lib is None:
+        load_library()
+    rc = _calls.append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, k_head_scales, v_head_scales)
+    if rc is not None:
+        if rc != ATTN_OK:
+            raise AttnError(rc, "attn_cache_append_fp4")
+        return
     index, dtype = k.get_device(), k.dtype
     if k.dim() != 3 or index < 0 or v.shape != k.shape or v.get_device() != index:
         raise ValueError("k, v must be CUDA tensors [T, Hkv, D] of one shape and device")
@@ -761,6 +787,14 @@ def attn_cache_read_fp4(k_cache, v_cache, k_scales, v_scales, slot_map, *, dtype
     float16 or bfloat16) when not given; given, they share a dtype, their values
     of a row are contiguous, and tokens and heads may be any strides apart (a
     transposed [Hkv, T, D], say)."""
+    if _lib is None:
+        load_library()
+    if k is None and v is None:
+        made = _calls.read(k_cache, v_cache, k_scales, v_scales, slot_map, dtype, k_head_scales, v_head_scales)
+        if made is not None:
+            if type(made) is int:
+                raise AttnError(made, "attn_cache_read_fp4")
+            return made
     index = k_cache.get_device()
     if index < 0 or slot_map.dim() != 1:
         raise ValueError("attn_cache_read_fp4 takes CUDA tensors: caches [num_blocks, Hkv, block_size, D / 2], slot_map [T]")
@@ -807,6 +841,15 @@ def attn_fwd_paged_fp4(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_
     requests; the cache as attn_cache_append_fp4 takes it; the rest as
     attn_fwd_paged_fp8.  Returns out [T, Hq, D] (allocated with torch when not
     given; rows of no request are not written)."""
+    if _lib is None:
+        load_library()
+    if lse is None and workspace is None:
+        made = _calls.attend(q, k_cache, v_cache, k_scales, v_scales, block_tables, q_starts, total_lengths,
+                             k_head_scales, v_head_scales, causal, local_window, scale, softcap, out)
+        if made is not None:
+            if type(made) is int:
+                raise AttnError(made, "attn_fwd_paged_fp4")
+            return made
     index, dtype = q.get_device(), q.dtype
     if q.dim() != 3 or index < 0 or block_tables.dim() != 2:
         raise ValueError("attn_fwd_paged_fp4 takes CUDA tensors: q [T, Hq, D], caches "
@@ -902,6 +945,15 @@ def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=No
     rows to gradients of q and k.  Returns (q_out, k_out), allocated with torch
     when not given; q_out=q, k_out=k works in place.  Rows of no request are not
     written."""
+    if _lib is None:
+        load_library()
+    inter = ROPE_LAYOUTS.get(layout)
+    if inter is not None:
+        made = _calls.rope(q, k, inv_freq, positions, q_starts, total_lengths, inter, inverse, scale, q_out, k_out)
+        if made is not None:
+            if type(made) is int:
+                raise AttnError(made, "attn_rope")
+            return made
     index, dtype, shape = q.get_device(), q.dtype, q.shape
     if len(shape) != 3 or index < 0:
         raise ValueError("attn_rope takes CUDA tensors: q [T, Hq, D], k [T, Hk, D] or None")
@@ -912,7 +964,6 @@ def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=No
         raise ValueError("inv_freq must be [R / 2]")
     pairs = inv_freq.shape[0]
     _need(inv_freq, "inv_freq", torch.float64, (pairs,), index)
-    inter = ROPE_LAYOUTS.get(layout)
     if inter is None:
         raise ValueError(f"layout must be 'half' or 'interleaved': got {layout!r}")
     B, at = 0, (None, None, None)

@@ -1,7 +1,9 @@
 """Builds libattn.so (the CUDA library behind include/attn.h) in-tree with nvcc
 for sm_103a.  Translation units compile in parallel; the link uses the static
 CUDA runtime, so the library loads on machines without a GPU driver (its
-entry points then report ATTN_ERR_CUDA on the first CUDA call)."""
+entry points then report ATTN_ERR_CUDA on the first CUDA call).  Beside it,
+with g++ and torch's headers, the extension module that marshals the 4-bit
+cache's and the rotary positions' calls (csrc/calls.cpp)."""
 from __future__ import annotations
 
 import glob
@@ -9,12 +11,16 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn.so")
+CALLS = os.path.join(PKG, f"_calls-{torch.__version__}.so")  # by torch's version: it uses torch's C++ interface
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"]
@@ -36,15 +42,27 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _start_calls(out: str):
+    """g++ on csrc/calls.cpp, as a running process that writes the extension module to `out`."""
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in include), os.path.join(CSRC, "calls.cpp"), "-o", out, f"-L{os.path.join(base, 'lib')}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ...] = (),
@@ -59,6 +77,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
     objdir = BUILD if out_path is None else os.path.join(BUILD, "variant_" + os.path.basename(lib))
     os.makedirs(objdir, exist_ok=True)
     procs = []
+    if out_path is None:
+        made = CALLS + f".tmp{os.getpid()}"
+        procs.append((os.path.join(CSRC, "calls.cpp"), None, _start_calls(made)))
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), *extra_flags, "-c", src,
@@ -74,11 +95,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
             sys.stdout.write(out)
         if pr.returncode != 0:
             failed.append(src)
-        objs.append(obj)
+        if obj is not None:
+            objs.append(obj)
     if failed:
         raise RuntimeError(f"nvcc failed for {failed}")
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", *ARCH, "-o", tmp, *objs], check=True)
+    if out_path is None:
+        os.replace(made, CALLS)
     os.replace(tmp, lib)
     return lib
 
