@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   PagedShare* share = reinterpret_cast<PagedShare*>(smem + C::kOffShare);
+  after_earlier_kernels();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) DP.p.cuts[blockIdx.x].parts = 0;
   paged_share<8 * NT, C::kThreads>(p, share);
@@ -574,8 +575,7 @@ cudaError_t launch_k(const Paged4DecParams& DP, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev].store(true, std::memory_order_relaxed);
   }
-  kernel<<<grid, Cfg<D, NT>::kThreads, smem, stream>>>(DP);
-  return cudaGetLastError();
+  return launch_early(kernel, (unsigned)grid, Cfg<D, NT>::kThreads, smem, stream, DP);
 }
 
 template <int D, int NT>

@@ -565,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
   sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   sm.s = smem_u32(sm.base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  after_earlier_kernels();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSP; ++i) {
@@ -629,8 +630,7 @@ cudaError_t launch_tc(const Paged4TcParams& TP, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev].store(true, std::memory_order_relaxed);
   }
-  kernel<<<grid, kThreads, smem, stream>>>(TP);
-  return cudaGetLastError();
+  return launch_early(kernel, (unsigned)grid, kThreads, smem, stream, TP);
 }
 
 template <int D, bool BF16>

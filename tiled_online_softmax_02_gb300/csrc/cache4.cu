@@ -153,6 +153,7 @@ __device__ __forceinline__ uint2 quantise(const uint4 (&v)[sizeof(T)], float hs,
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ Cache4Params p, int64_t units) {
+  after_earlier_kernels();
   using P = Place<D>;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const P at(p, unit);
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ Cache4Params p, int64_t units) {
+  after_earlier_kernels();
   using P = Place<D>;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const P at(p, unit);
@@ -230,9 +232,7 @@ template <typename T, int D>
 cudaError_t launch(const Cache4Params& p, bool read, cudaStream_t stream) {
   const int64_t units = ((int64_t)p.T + Place<D>::kTokens - 1) / Place<D>::kTokens * p.Hkv;
   const unsigned grid = (unsigned)std::min<int64_t>(units, 1 << 30);
-  if (read) cache4_read_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, units);
-  else cache4_append_kernel<T, D><<<grid, kThreads, 0, stream>>>(p, units);
-  return cudaGetLastError();
+  return launch_early(read ? cache4_read_kernel<T, D> : cache4_append_kernel<T, D>, grid, kThreads, 0, stream, p, units);
 }
 
 template <typename T>

@@ -1,4 +1,5 @@
-// paged4.cuh -- device helpers of the 4-bit cache: e2m1 and e4m3 widened.
+// paged4.cuh -- device helpers of the 4-bit cache: e2m1 and e4m3 widened; the
+// wait for earlier kernels.
 #pragma once
 
 #include <cstdint>
@@ -7,6 +8,9 @@
 
 namespace gb300_attn {
 namespace {
+
+// What launch_early asks of a kernel, before anything else.
+__device__ __forceinline__ void after_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Eight e2m1 codes as f16 pairs, in order.
 __device__ __forceinline__ void widen8(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {

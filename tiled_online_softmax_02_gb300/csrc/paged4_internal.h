@@ -55,6 +55,23 @@ struct Paged4Params {
 constexpr int kPaged4DecCtas = 2;        // CTAs of the few-rows kernel on an SM, in units of 8 rows
 constexpr float kPaged4DecLog2 = 5.0f;   // log2 of the factor that P carries
 
+// A launch that may begin while the kernel before it on the stream drains: every kernel launched so waits for all of that
+// one (after_earlier_kernels) before it reads or writes anything.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_early(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 cudaError_t launch_cache4_append(const Cache4Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_cache4_read(const Cache4Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, bool interleaved, int dtype, cudaStream_t stream);

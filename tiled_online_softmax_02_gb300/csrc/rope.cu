@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "../../include/attn.h"
+#include "paged4.cuh"
 #include "paged4_internal.h"
 
 namespace gb300_attn {
@@ -156,6 +157,7 @@ __device__ __forceinline__ void turn_pairs(Vec<T, VP>& u, Vec<T, VP>& v, const f
 template <typename T, int VP, bool INTER>
 __global__ void __launch_bounds__(kThreads, 32) rope_kernel(const __grid_constant__ RopeParams p, int row_lanes, int rest_lanes,
                                                            int heads_each, int parts) {
+  after_earlier_kernels();
   using V = Vec<T, VP>;
   __shared__ __align__(16) float cs[kThreads / 32][2][kPairs];  // cosines and sines of a warp's pairs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -257,9 +259,8 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
     heads_each = std::max(subs, (heads_each + 1) / 2);
   const int parts = (H + heads_each - 1) / heads_each;
   const int64_t blocks = ((int64_t)p.T * parts + kThreads / 32 - 1) / (kThreads / 32);
-  rope_kernel<T, VP, INTER><<<(unsigned)std::min<int64_t>(blocks, 1 << 30), kThreads, 0, stream>>>(
-      p, row_lanes, rest_lanes, heads_each, parts);
-  return cudaGetLastError();
+  return launch_early(rope_kernel<T, VP, INTER>, (unsigned)std::min<int64_t>(blocks, 1 << 30), kThreads, 0, stream, p, row_lanes,
+                      rest_lanes, heads_each, parts);
 }
 
 template <typename T>
