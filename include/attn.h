@@ -550,7 +550,8 @@ int attn_cache_read_fp4(const void *k_cache, const void *v_cache, const void *k_
  *                 aligned, for partial rows; nothing in it has to start at zero.
  *                 Calls that share a workspace must not overlap on the GPU.
  * A key's weight is held to 11 bits, or to 2^-29 of the row's largest; the row
- * sum has every key's weight.  A block-table entry below a request's length
+ * sum has every key's weight.  A row whose largest score is below -6e29 counts as
+ * one without keys.  A block-table entry below a request's length
  * that names no block is not followed: its keys count as zeros, and
  * attn_get_device_status then reports ATTN_ERR_INVALID_ARG once.
  * Enqueues on `stream`; allocates and synchronises nothing, so it may be captured into a CUDA
@@ -590,7 +591,7 @@ size_t attn_paged_fp4_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, in
  *   q_out, k_out  the same shapes and types.  Either the same rows as q (or k),
  *                 in place, or no byte in common with any input; rows of one
  *                 stride may lie between each other (slices of a projection)
- *   inv_freq      f64 [rotary_dim / 2] radians a position
+ *   inv_freq      f64 [rotary_dim / 2] radians a position, finite
  *   positions     int32 [num_tokens] or NULL
  *   q_starts      int32 [B + 1], non-decreasing in [0, num_tokens];
  *   total_lengths int32 [B]; both NULL when positions is given

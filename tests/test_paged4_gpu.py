@@ -305,6 +305,53 @@ def test_soft_caps(cap, new):
     check(Problem(new=new, total=(500, 300), softcap=cap, q_std=20.0 if cap < 100 else 2.0, wide=True))
 
 
+@pytest.mark.parametrize("new", [(2, 1), (150, 40)])
+def test_caps_and_scales_at_their_ends(new):
+    """Factors that pass fp32's range, either way: scores of zero stay zero, the others go to the cap's two ends or to zero."""
+    w = Problem(new=new, total=(300, 200), wide=True, dtype="f16")
+    x = ref.make(w)
+    x["q"][:, 0] = 0.0
+    for scale, cap in ((1e30, 1e-25), (1e-30, 1e30), (3e38, 1e-38)):
+        out, lse = _run(w.replace(scale=scale, softcap=cap), x)
+        assert bool(out[:sum(new)].isfinite().all()) and bool(lse[:sum(new)].isfinite().all())
+        # caps of nothing leave every key its share, as does a scale of nothing
+        want, _, tol, _ = ref.attend(w.replace(scale=0.0), x)
+        rows = slice(0, sum(new))
+        assert (np.abs(out.double().cpu().numpy()[rows] - want[rows]) <= 2 * tol[rows]).all()
+
+
+@pytest.mark.parametrize("new", [(3, 4), (200, 100)])
+def test_tables_without_blocks(new):
+    w = Problem(new=new, total=(900, 400))
+    x = ref.make(w)
+    x["tables"] = x["tables"][:, :0].contiguous()
+    out, lse = _run(w, x)
+    n = sum(new)
+    assert bool((out[:n] == 0).all()) and bool((lse[:n] == -np.inf).all()) and bool((out[n:] == 7).all())
+    assert attn.get_device_status() == attn.ATTN_OK
+
+
+def test_calls_without_rows():
+    w = Problem(new=(3, 4), total=(90, 40))
+    g = {n: gpu(t) for n, t in ref.make(w).items()}
+    cache = [g[n] for n in ("k_cache", "v_cache", "k_scales", "v_scales")]
+    before = [c.clone() for c in cache]
+    none = torch.zeros(0, dtype=torch.int64, device="cuda")
+    rows = torch.zeros((0, 2, 128), device="cuda")
+    attn.attn_cache_append_fp4(rows, rows, none, *cache)
+    assert [t.shape for t in attn.attn_cache_read_fp4(*cache, none)] == [(0, 2, 128)] * 2
+    assert attn.attn_fwd_paged_fp4(g["q"][:0], *cache, g["tables"], g["starts"], g["totals"]).shape == (0, 8, 128)
+    out = torch.full_like(g["q"], 7.0)
+    empty = (g["tables"][:0], g["starts"][:1], g["totals"][:0])
+    assert bool((attn.attn_fwd_paged_fp4(g["q"], *cache, *empty, out=out) == 7).all())
+    freq = attn.attn_rope_frequencies(128)[0]
+    assert attn.attn_rope(g["q"][:0], rows.bfloat16(), freq, positions=none.int())[0].shape == (0, 8, 128)
+    assert bool((attn.attn_rope(g["q"], None, freq, q_starts=empty[1], total_lengths=empty[2], q_out=out)[0] == 7).all())
+    torch.cuda.synchronize()
+    for a, b in zip(before, cache):
+        assert torch.equal(a, b)
+
+
 def test_caller_workspace_and_float_views():
     w = Problem(new=(3, 4), total=(900, 40))
     x = ref.make(w)

@@ -260,7 +260,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         }
       }
       const float kh = P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f;
-      down = fmaxf(down * (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh, 1.2e-38f);  // positive: -inf stays -inf
+      // positive, so that -inf stays -inf, and finite, so that 0 stays 0
+      down = fminf(fmaxf(down * (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh, 1.2e-38f), 3e38f);
       fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * t);
       fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
@@ -589,9 +590,9 @@ cudaError_t launch_n(const Paged4DecParams& DP, int grid, bool bf16, cudaStream_
 cudaError_t launch_attn_paged4_dec(const Paged4Params& p, int rows, int grid, bool bf16, cudaStream_t stream) {
   Paged4DecParams DP{};
   DP.p = p;
-  DP.scale_log2 = (float)(fabs((double)p.c.scale) * 1.4426950408889634);  // the sign goes into Q
+  DP.scale_log2 = (float)std::min(3e38, fabs((double)p.c.scale) * 1.4426950408889634);  // the sign goes into Q
   if (p.c.softcap > 0.0f) {
-    DP.sc_in = (float)(fabs((double)p.c.scale) / (double)p.c.softcap);
+    DP.sc_in = (float)std::min(3e38, fabs((double)p.c.scale) / (double)p.c.softcap);
     DP.sc_out = (float)((double)p.c.softcap * 1.4426950408889634);
   }
   if (p.c.D == 128) return rows == 8 ? launch_n<128, 1>(DP, grid, bf16, stream) : launch_n<128, 2>(DP, grid, bf16, stream);

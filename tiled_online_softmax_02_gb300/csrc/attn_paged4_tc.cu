@@ -21,7 +21,7 @@
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
 //
 // Measured (one GB300, device time with the join, bf16, 32 query and 8 kv heads,
-// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 564 us, 1276
+// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 561 us, 1284
 // TFLOP/s, 67% of a 16-bit library product's rate (the 8-bit kernel 591 us); two
 // whole prompts of 3.5K to 4K tokens 244 us, 966 TFLOP/s (257).  The tensor pipe is
 // busy 56% of the first's time: a lane's S, softmax and P V follow one another, as
@@ -449,8 +449,8 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
     const int last = min(x0 + BM, u.row0 + u.rows) - 1;
     const int2 lim = mine ? paged_limits(p, u.q, paged_token(p, x0 + row)) : make_int2(0, 0);
     const int full_lo = paged_limits(p, u.q, paged_token(p, last)).x, full_hi = paged_limits(p, u.q, paged_token(p, x0)).y;
-    // positive, so that -inf stays -inf
-    const float raw = fmaxf(qs * (P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2), 1.2e-38f);
+    // positive, so that -inf stays -inf, and finite, so that 0 stays 0
+    const float raw = fminf(fmaxf(qs * (P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2), 1.2e-38f), 3e38f);
     const float xs = SOFTCAP ? TP.sc_out : raw;  // brings x, the raw score or its tanh, to log2 units
     vh = P.v_heads ? __ldg(P.v_heads + u.kvh) : 1.0f;
     m_run = kNone;
@@ -644,9 +644,9 @@ cudaError_t launch_attn_paged4_tc(const Paged4Params& p, int grid, bool bf16, cu
   Paged4TcParams TP{};
   TP.p = p;
   TP.aligned32 = ((reinterpret_cast<uintptr_t>(p.c.out) | reinterpret_cast<uintptr_t>(p.ws_o)) & 31) == 0;
-  TP.scale_log2 = (float)(fabs((double)p.c.scale) * 1.4426950408889634);  // the sign goes into Q
+  TP.scale_log2 = (float)std::min(3e38, fabs((double)p.c.scale) * 1.4426950408889634);  // the sign goes into Q
   if (p.c.softcap > 0.0f) {
-    TP.sc_in = (float)(fabs((double)p.c.scale) / (double)p.c.softcap);
+    TP.sc_in = (float)std::min(3e38, fabs((double)p.c.scale) / (double)p.c.softcap);
     TP.sc_out = (float)((double)p.c.softcap * 1.4426950408889634);
   }
   if (p.c.D == 128) return bf16 ? launch_tc_d<128, true>(TP, grid, stream) : launch_tc_d<128, false>(TP, grid, stream);
