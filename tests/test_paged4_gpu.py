@@ -217,6 +217,22 @@ def test_shapes_and_features(shape, wide, feature):
     check(Problem(**{**SHAPES[shape], **FEATURES[feature]}, wide=wide))
 
 
+@pytest.mark.parametrize("feature", [dict(window=50), dict(window=1), dict(window=200, dtype="f16", heads=True),
+                                     dict(window=33, causal=False), dict(window=300, D=64, softcap=5.0)], ids=str)
+def test_windows_of_many_rows(feature):
+    """Windows shorten what there may be to read, so it takes this many requests to fill the kernel for many rows."""
+    new = tuple(100 + 37 * b % 56 for b in range(30))
+    total = tuple(n + (0, 1, 90, 513)[b % 4] for b, n in enumerate(new))
+    check(Problem(new=new, total=total, Hq=16, Hkv=8, **feature))
+
+
+@pytest.mark.parametrize("new", [(5, 5, 7), (12, 1, 11), (3, 4, 5, 2)])
+@pytest.mark.parametrize("feature", ["plain", "window", "d64_bf16", "d64", "odd_group"])
+def test_units_of_8_and_of_16_rows(new, feature):
+    """A mean of 23, 32 and 14 rows and a group that is no divisor of a unit; every request takes its own number of units."""
+    check(Problem(**{**dict(new=new, total=tuple(300 * b + n for b, n in enumerate(new)), Hq=8, Hkv=2), **FEATURES[feature]}))
+
+
 @pytest.mark.parametrize("new", [1, 3, 60, 200])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_one_key_far_above_the_others(new, dtype):

@@ -27,9 +27,9 @@
 // another between two meetings, and nothing waits on a barrier in memory.
 //
 // Measured (one GB300, device time with the join, D = 128): 8 requests of 9K to
-// 33K tokens, 32 query and 8 kv heads, bf16, 44.4 us, 4.3 TB/s, 64% of a copy's
+// 33K tokens, 32 query and 8 kv heads, bf16, 42.6 us, 4.5 TB/s, 67% of a copy's
 // rate (the 8-bit kernel 58); 64 requests of up to 8K, 4 kv heads, f16, blocks of
-// 16 slots, 40.4 us (54); one request of 3.5K 10.1 us (11.4).  About 9 us of each
+// 16 slots, 39.2 us (54); one request of 3.5K 9.9 us (11.4).  About 8 us of each
 // are the launch, the shares, the first keys and the join.  32 keys cost 540
 // instructions: 128 conversions and 128 multiplications, on two pipes that take
 // one every other cycle, 32 products, which with those alone take 138 cycles
@@ -191,61 +191,62 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
   const uint32_t ring_s = smem_u32(ring);
   const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u;  // of the scale, into Q: larger raw scores are larger scores
   Subs subs;
-  int entry, entry_rest[C::kLeft + 1];  // of the sub-tile that is loaded next, and of those for the last stages
-  auto prefetch = [&]() {  // the first sub-tiles of the walk's unit
+  int first[S + 1];  // entries of the unit's first sub-tiles
+  int entry;         // and of the one that is loaded next
+  uint32_t raw[NT][2 * KS];  // this lane's part of Q: row g of every 8, values (D / 4) t ..
+  // What a unit begins with, in the order in which it waits for memory: which blocks hold its first keys, its Q, the keys
+  // themselves, all but those whose place still holds the last unit's O.
+  auto look_up = [&]() {
     subs = subs_of<NT, W>(p, w, warp);
     const int valid = paged_valid(p, w.u.q);
     const int32_t* table = p.tables + (int64_t)w.u.b * p.width;
-    int first[S + 1];
 #pragma unroll
     for (int s = 0; s <= S; ++s) first[s] = s < subs.count ? entry_of(p, table, valid, subs.first + s * W, lane) : -1;
-#pragma unroll
-    for (int s = 0; s < E; ++s) {
-      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, first[s], valid, lane);
-      copies_commit();
-    }
-#pragma unroll
-    for (int s = E; s < S; ++s) entry_rest[s - E] = first[s];
-    entry = first[S];
   };
-  auto prefetch_rest = [&]() {
+  auto load_q = [&]() {
 #pragma unroll
-    for (int s = E; s < S; ++s) {
-      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, entry_rest[s - E],
-                                                paged_valid(p, w.u.q), lane);
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i) raw[j][i] = 0u;
+      if (j * 8 + g < w.u.rows) {
+        const int x = w.u.row0 + j * 8 + g, tok = paged_token(p, x);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (int64_t)(w.u.q.s0 + tok) * p.q_stride +
+                                                          (int64_t)(w.u.kvh * p.group + x - tok * p.group) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 v = __ldg(src + i);
+          raw[j][4 * i] = v.x; raw[j][4 * i + 1] = v.y; raw[j][4 * i + 2] = v.z; raw[j][4 * i + 3] = v.w;
+        }
+      }
+    }
+  };
+  auto load_keys = [&](int from, int to) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (s < from || s >= to) continue;
+      if (s < subs.count) load_sub<D, NT>(P, ring_s + s * C::kStage, w.u.kvh, subs.first + s * W, first[s], paged_valid(p, w.u.q), lane);
       copies_commit();
     }
   };
   if (!w.done()) {
-    prefetch();
-    prefetch_rest();
+    look_up();
+    load_q();
+    load_keys(0, S);
   }
   while (!w.done()) {
     const PagedUnit& u = w.u;
-    // ---- this lane's part of Q: row g of every 8, values (D / 4) t ..
+    entry = first[S];
     uint32_t qf[NT][KS][2];
     float fac[NT][2];  // what brings the raw scores of rows 2 t, 2 t + 1 to log2 units
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int r = j * 8 + g;
-      uint32_t raw[2 * KS];
 #pragma unroll
-      for (int i = 0; i < 2 * KS; ++i) raw[i] = 0u;
-      if (r < u.rows) {
-        const int x = u.row0 + r, tok = paged_token(p, x);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (int64_t)(u.q.s0 + tok) * p.q_stride +
-                                                          (int64_t)(u.kvh * p.group + x - tok * p.group) * D + t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i) {
-          const uint4 v = __ldg(src + i);
-          raw[4 * i] = v.x ^ sign; raw[4 * i + 1] = v.y ^ sign; raw[4 * i + 2] = v.z ^ sign; raw[4 * i + 3] = v.w ^ sign;
-        }
-      }
+      for (int i = 0; i < 2 * KS; ++i) raw[j][i] ^= sign;
       float down = 1.0f;  // 1 / the power of two that row g's Q carries
       if constexpr (BF16) {
         uint32_t top2 = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * KS; ++i) top2 = __vmaxu2(top2, raw[i] & 0x7fff7fffu);
+        for (int i = 0; i < 2 * KS; ++i) top2 = __vmaxu2(top2, raw[j][i] & 0x7fff7fffu);
         uint32_t top = max(top2 & 0xffffu, top2 >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -254,10 +255,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-        for (int i = 0; i < 2 * KS; ++i) {
-          const __half2 h = __floats2half2_rn(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xffff0000u) * up);
-          raw[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        for (int i = 0; i < 2 * KS; ++i)
+          raw[j][i] = as_bits(__floats2half2_rn(__uint_as_float(raw[j][i] << 16) * up, __uint_as_float(raw[j][i] & 0xffff0000u) * up));
       }
       const float kh = P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f;
       // positive, so that -inf stays -inf, and finite, so that 0 stays 0
@@ -266,8 +265,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
       fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        qf[j][s][0] = raw[2 * s];
-        qf[j][s][1] = raw[2 * s + 1];
+        qf[j][s][0] = raw[j][2 * s];
+        qf[j][s][1] = raw[j][2 * s + 1];
       }
     }
     float o[NT][MT][4], m[NT][2];
@@ -459,7 +458,8 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
       at = at + 1 == S ? 0 : at + 1;
     }
 
-    // ---- the unit's rows, once the next unit's first keys are on their way
+    // ---- the unit's rows: the warps leave their maxima, sums and O, and the next unit's Q and first keys are on their way
+    // while they meet.  A row's 16-byte pieces lie in an order that keeps eight writing lanes out of each other's banks.
     const int s0 = u.q.s0, head0 = u.kvh * p.group, kvh = u.kvh, row0 = u.row0, rows = u.rows;
     const bool whole = w.whole, head = w.head;
     if (!whole && head && threadIdx.x == 0) {
@@ -472,10 +472,9 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
       P.cuts[blockIdx.x] = c;
     }
     w.next(p);
-    if (!w.done()) prefetch();
-
-    // ---- the warps meet: rows' maxima, sums and O, joined in the order of the warps
+    if (!w.done()) look_up();
     auto left = [&](int c) { return reinterpret_cast<float*>(smem + (C::kLeft ? (c * S + E) * C::kStage : C::kOffMerge + c * C::kOwn)); };
+    auto turn = [](int r) { return D == 128 ? (r >> 1) & 3 : ((r >> 1) & 1) | ((r >> 2) & 1) << 2; };
     float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -487,13 +486,20 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 8);
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 16);
         const int r = j * 8 + 2 * t + x;
+        if (r >= rows) continue;
         if (g == 0) ml[warp * NR + r] = make_float2(m[j][x], l[x]);
-        float* dst = left(warp) + r * D + g * (D / 8);
+        float4* dst = reinterpret_cast<float4*>(left(warp) + r * D);
 #pragma unroll
         for (int i = 0; i < MT / 2; ++i)
-          *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(o[j][2 * i][x], o[j][2 * i][x + 2], o[j][2 * i + 1][x], o[j][2 * i + 1][x + 2]);
+          dst[(g * (D / 32) + i) ^ turn(r)] = make_float4(o[j][2 * i][x], o[j][2 * i][x + 2], o[j][2 * i + 1][x], o[j][2 * i + 1][x + 2]);
       }
     }
+    if (!w.done()) {
+      load_q();
+      load_keys(0, E);
+    }
+
+    // ---- the warps meet: rows' maxima, sums and O, joined in the order of the warps
     asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory");
     const float vh = P.v_heads ? __ldg(P.v_heads + kvh) : 1.0f;
 #pragma unroll 1
@@ -510,7 +516,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         const float2 y = ml[c * NR + r];
         const float wgt = fast_exp2(y.x - M);
         L = fmaf(wgt, y.y, L);
-        const float* src = left(c) + r * D + d;
+        const float* src = left(c) + r * D + ((d >> 2) ^ turn(r)) * 4 + (d & 3);
         float y4[4];
         if constexpr (V == 4) *reinterpret_cast<float4*>(y4) = *reinterpret_cast<const float4*>(src);
         else *reinterpret_cast<float2*>(y4) = *reinterpret_cast<const float2*>(src);
@@ -539,7 +545,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
     }
     if (!w.done()) {
       asm volatile("bar.sync 2, %0;" ::"n"(C::kThreads) : "memory");  // the rows have been read
-      prefetch_rest();
+      load_keys(E, S);
     }
   }
   copies_wait<0>();

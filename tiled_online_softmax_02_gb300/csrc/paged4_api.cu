@@ -217,25 +217,22 @@ Plan4 plan4(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
   if (T <= 0 || B <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0) return pl;
   const int group = Hq / Hkv, sms = paged_sm_count();
   // Rows per (request, kv head) of an even batch; a request with more takes several units.  The lengths are on the device,
-  // so the mean is all there is to go by.  48 requests of up to 8K tokens, 4 kv heads, D = 128, in units of 8 and of 16
-  // rows: 12 rows 59 and 58 us, 16 rows 57 and 54, 24 rows 77 and 88.
-  const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group;
-  pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedTcRows;
-  int64_t most = (int64_t)sms * (pl.rows == 8 ? kPaged4DecCtas : 1);
-  const size_t slots = 2 * (size_t)most * pl.rows;  // the choice below needs no more
+  // so the mean is all there is to go by.  A unit of 16 rows costs 1.5 times one of 8.  48 requests of up to 8K tokens, 4 kv
+  // heads, D = 128, in units of 8 and of 16 rows: 12 rows 53 and 48 us, 16 rows 49 and 44, 24 rows 69 and 74, 32 rows 89 and
+  // 77; 4 requests, 16 rows 14.1 and 13.7.
+  const int64_t rows = std::max<int64_t>(1, (T + B / 2) / B) * group, eights = (rows + 7) / 8;
+  pl.rows = eights == 1 || eights == 3 ? 8 : 16;
+  const size_t slots = 2 * (size_t)sms * (rows <= 16 ? 16 : kPagedTcRows);  // the choice below needs no more
   const size_t cuts = (size_t)sms * kPaged4DecCtas;
-  if (pl.rows == kPagedTcRows) {
-    // More rows: the few-rows kernel's time goes with its units of 8 rows, 273 of their tiles a microsecond, the
-    // many-rows kernel's with those of 256, 77 tiles, and 15 us more for its first result and the join of what one unit's
-    // tiles leave on many SMs.  What there may be to read: the tables' width, or the window.  4 kv heads: 24 rows, 48
-    // requests of up to 8K 77 us against 85, 32 rows 98 against 85; 8 requests, 32 rows 31 against 32, 64 rows 51 against
-    // 33; one of 4K, 64 rows 14 against 30, 128 rows 19 against 31, 512 rows 48 against 33.
-    const int64_t heads = B * Hkv, few = heads * ((rows + 7) / 8) * max_tiles, many = heads * ((rows + kPagedTcRows - 1) / kPagedTcRows) * max_tiles;
-    if (few / 273 < 15 + many / 77) {
-      pl.rows = 8;
-      most = (int64_t)sms * kPaged4DecCtas;
-    }
-  }
+  // The few-rows kernel takes 300 tiles a microsecond in units of 8 rows, 200 in units of 16, the many-rows kernel 100 of its
+  // 256 rows, and 13 us more for its first result and the join of what one unit's tiles leave on many SMs.  Of the tiles that
+  // there may be to read (the tables' width, or the window) 0.7 are taken to be there.  Few and many: 4 kv heads, 48 requests
+  // of up to 8K, 24 rows 69 and 85 us, 32 rows 77 and 86; 8 requests, 32 rows 25 and 32, 64 rows 40 and 33; one of 4K, 64 rows
+  // 13 and 30, 128 rows 17 and 31, 512 rows 35 and 33; 8 kv heads, 4 requests of 32K, 32 rows 85 and 102.  D = 64: the same
+  // order but for the 64 rows, 31 and 29.
+  auto tiles = [&](int unit) { return B * Hkv * ((rows + unit - 1) / unit) * max_tiles; };
+  if (rows > 16 && tiles(pl.rows) / (pl.rows == 8 ? 430 : 286) >= 13 + tiles(kPagedTcRows) / 143) pl.rows = kPagedTcRows;
+  const int64_t most = (int64_t)sms * (pl.rows == 8 ? kPaged4DecCtas : 1);
   const int64_t units = (T * group / pl.rows + B) * Hkv;  // no more CTAs than there can be tiles
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);
   pl.ml_at = slots * D * 4;
@@ -342,8 +339,8 @@ extern "C" int attn_fwd_paged_fp4(const void* q, const void* k_cache, const void
     L.ws_ml = P.ws_ml;
     L.cuts = P.cuts;
     L.ml_log2 = (plan.rows == kPagedTcRows ? kPagedTcLog2 : kPaged4DecLog2) - kPagedSumLog2;
-    // Parts a unit, about: CTAs over units.  64 requests (three) take 43.0 us with a CTA a row and 40.3 with one a unit, one
-    // request of 4K (39) 10.1 and 11.7, 4 of 16 rows (ten) 15.5 and 17.8.
+    // Parts a unit, about: CTAs over units.  64 requests (three) take 41.8 us with a CTA a row and 39.4 with one a unit, one
+    // request of 4K (39) 9.8 and 11.3, 4 of 16 rows (ten) 13.8 and 15.9.
     const int64_t parts = plan.grid / ((int64_t)B * Hkv * std::max<int64_t>(1, (T / B * p.group + plan.rows - 1) / plan.rows)) + 1;
     e = plan.rows == kPagedTcRows || parts > 8 ? launch_attn_paged_join(L, bf16, st) : launch_attn_paged4_join(L, bf16, st);
   }
