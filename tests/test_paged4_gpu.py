@@ -233,6 +233,15 @@ def test_units_of_8_and_of_16_rows(new, feature):
     check(Problem(**{**dict(new=new, total=tuple(300 * b + n for b, n in enumerate(new)), Hq=8, Hkv=2), **FEATURES[feature]}))
 
 
+@pytest.mark.parametrize("new,Hq", [((300,) + (1,) * 100, 8), ((1,) * 40 + (500,) + (0,) * 9 + (1,) * 50 + (90,), 2),
+                                    ((1,) * 150 + (400, 300) + (1,) * 148, 8), ((0,) * 33 + (350,), 6)],
+                         ids=["first", "one_head_a_group", "300_requests", "alone"])
+def test_prompts_among_single_tokens(new, Hq):
+    """Requests of many units beside requests of one, in the kernel for few rows: 300 are more than a CTA has threads."""
+    total = tuple(n + 7 * (b % 40) for b, n in enumerate(new))
+    check(Problem(new=new, total=total, Hq=Hq, Hkv=2, D=64, block=32))
+
+
 @pytest.mark.parametrize("new", [1, 3, 60, 200])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_one_key_far_above_the_others(new, dtype):

@@ -551,7 +551,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
   copies_wait<0>();
 }
 
-template <int D, int NT, bool BF16, bool SOFTCAP>
+template <int D, int NT, bool BF16, bool SOFTCAP, bool LONG>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
     attn_paged4_dec_kernel(const __grid_constant__ Paged4DecParams DP) {
   using C = Cfg<D, NT>;
@@ -562,16 +562,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
   after_earlier_kernels();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) DP.p.cuts[blockIdx.x].parts = 0;
-  paged_share<8 * NT, C::kThreads>(p, share);
+  if constexpr (LONG) paged_share_long<8 * NT, C::kThreads>(p, share);
+  else paged_share<8 * NT, C::kThreads>(p, share);
   __syncthreads();
   PagedWalk<8 * NT> w;
   w.begin(p, share);
   compute_role<D, NT, BF16, SOFTCAP>(DP, smem, share, w, warp, lane);
 }
 
-template <int D, int NT, bool BF16, bool SOFTCAP>
+template <int D, int NT, bool BF16, bool SOFTCAP, bool LONG>
 cudaError_t launch_k(const Paged4DecParams& DP, int grid, cudaStream_t stream) {
-  auto kernel = attn_paged4_dec_kernel<D, NT, BF16, SOFTCAP>;
+  auto kernel = attn_paged4_dec_kernel<D, NT, BF16, SOFTCAP, LONG>;
   constexpr int smem = Cfg<D, NT>::kSmem;
   static std::atomic<bool> ready[128];
   int dev = 0;
@@ -585,10 +586,16 @@ cudaError_t launch_k(const Paged4DecParams& DP, int grid, cudaStream_t stream) {
   return launch_early(kernel, (unsigned)grid, Cfg<D, NT>::kThreads, smem, stream, DP);
 }
 
+template <int D, int NT, bool BF16, bool SOFTCAP>
+cudaError_t launch_l(const Paged4DecParams& DP, int grid, cudaStream_t stream) {
+  return paged_may_be_long<8 * NT>(DP.p.c) ? launch_k<D, NT, BF16, SOFTCAP, true>(DP, grid, stream)
+                                           : launch_k<D, NT, BF16, SOFTCAP, false>(DP, grid, stream);
+}
+
 template <int D, int NT>
 cudaError_t launch_n(const Paged4DecParams& DP, int grid, bool bf16, cudaStream_t stream) {
-  if (DP.p.c.softcap > 0.0f) return bf16 ? launch_k<D, NT, true, true>(DP, grid, stream) : launch_k<D, NT, false, true>(DP, grid, stream);
-  return bf16 ? launch_k<D, NT, true, false>(DP, grid, stream) : launch_k<D, NT, false, false>(DP, grid, stream);
+  if (DP.p.c.softcap > 0.0f) return bf16 ? launch_l<D, NT, true, true>(DP, grid, stream) : launch_l<D, NT, false, true>(DP, grid, stream);
+  return bf16 ? launch_l<D, NT, true, false>(DP, grid, stream) : launch_l<D, NT, false, false>(DP, grid, stream);
 }
 
 }  // namespace

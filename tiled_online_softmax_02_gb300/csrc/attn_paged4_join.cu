@@ -6,7 +6,7 @@
 // Bound: latency.  A CTA has a unit, a row's parts are shared out to as many of
 // its eight warps as there are to a row, and each has four parts in flight.  (A
 // CTA a row, as that kernel has them for the many parts of few units, is eight
-// times the CTAs, most of them without a row: 64 requests of 4 kv heads take 43.0 us with it, 40.3 with this.)
+// times the CTAs, most of them without a row: 64 requests of 4 kv heads take 41.8 us with it, 39.4 with this.)
 // A programmatic dependent of the attention kernel: it may be scheduled while
 // that one drains, and waits for all of it before it reads.
 #include "paged4_internal.h"

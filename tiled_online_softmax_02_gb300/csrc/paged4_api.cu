@@ -225,13 +225,18 @@ Plan4 plan4(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
   const size_t slots = 2 * (size_t)sms * (rows <= 16 ? 16 : kPagedTcRows);  // the choice below needs no more
   const size_t cuts = (size_t)sms * kPaged4DecCtas;
   // The few-rows kernel takes 300 tiles a microsecond in units of 8 rows, 200 in units of 16, the many-rows kernel 100 of its
-  // 256 rows, and 13 us more for its first result and the join of what one unit's tiles leave on many SMs.  Of the tiles that
-  // there may be to read (the tables' width, or the window) 0.7 are taken to be there.  Few and many: 4 kv heads, 48 requests
-  // of up to 8K, 24 rows 69 and 85 us, 32 rows 77 and 86; 8 requests, 32 rows 25 and 32, 64 rows 40 and 33; one of 4K, 64 rows
-  // 13 and 30, 128 rows 17 and 31, 512 rows 35 and 33; 8 kv heads, 4 requests of 32K, 32 rows 85 and 102.  D = 64: the same
-  // order but for the 64 rows, 31 and 29.
-  auto tiles = [&](int unit) { return B * Hkv * ((rows + unit - 1) / unit) * max_tiles; };
-  if (rows > 16 && tiles(pl.rows) / (pl.rows == 8 ? 430 : 286) >= 13 + tiles(kPagedTcRows) / 143) pl.rows = kPagedTcRows;
+  // 256 rows; a unit costs some tiles more; and what one unit's tiles leave on many SMs takes the latter up to 13 us to join.
+  // Of the tiles that there may be to read (the tables' width, or the window) 0.7 are taken to be there.  Few and many: 4 kv
+  // heads, 48 requests of up to 8K, 24 rows 69 and 85 us, 32 rows 77 and 86; 8 requests, 32 rows 25 and 32, 64 rows 40 and
+  // 33; one of 4K, 64 rows 13 and 30, 128 rows 17 and 31, 512 rows 35 and 33; 8 kv heads, 4 requests of 32K, 32 rows 85 and
+  // 102, 200 tokens over 800 34 and 25; prompts of 4 kv heads: one of 500 tokens 26 and 22, 4 of 120 19 and 11.  D = 64: the
+  // same order.
+  auto time = [&](int unit, int64_t over, int64_t rate) {
+    return (double)(B * Hkv * ((rows + unit - 1) / unit)) * (0.7 * max_tiles + over) / rate;
+  };
+  const double few = pl.rows == 8 ? time(8, 2, 300) : time(16, 4, 200);
+  const double many = time(kPagedTcRows, 3, 100) + std::min<int64_t>(13, 3 + 3 * max_tiles);
+  if (rows > 16 && few >= many) pl.rows = kPagedTcRows;
   const int64_t most = (int64_t)sms * (pl.rows == 8 ? kPaged4DecCtas : 1);
   const int64_t units = (T * group / pl.rows + B) * Hkv;  // no more CTAs than there can be tiles
   pl.grid = (int)(units >= most || units * max_tiles >= most ? most : units * max_tiles);

@@ -95,17 +95,57 @@ constexpr int kOver = 3;
 template <int NR>
 __device__ __forceinline__ int paged_cost(const PagedUnit& u) { return max(u.te - u.tb, 1) + kOver; }
 
-// Length on the line of one kv head of a request: the sum over its row tiles.
+// Length on the line of one kv head of a request: the sum over its row tiles; or over first, first + step, ... of them.
 template <int NR>
-__device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedReq& q) {
+__device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedReq& q, int first = 0, int step = 1) {
   PagedUnit u;
   u.q = q;
   const int rows = u.q.n * p.group;
   long long c = 0;
 #pragma unroll 1
-  for (u.rt = 0; u.rt * NR < rows; ++u.rt) {
+  for (u.rt = first; u.rt * NR < rows; u.rt += step) {
     paged_unit_tiles<NR>(p, u);
     c += paged_cost<NR>(u);
+  }
+  return c;
+}
+
+// Where a call may have requests of many row tiles, a warp takes those of more than kLongReq together.  (One prompt of 500
+// tokens in 125 row tiles of 16: 44 us a call, 18 of them in one lane's loops; two of 4K in tiles of 256 243 us, 236.)  Single
+// tokens would pay 0.2 to 0.7 us for it, so the rows beyond one token a request tell, and the code stands apart: a function
+// that the many-rows kernel calls, a kernel of its own for few rows (which lose 2% to the mere call).  The kernels over the
+// 8-bit cache do without: the call costs the one for many rows 3%.
+constexpr int kLongReq = 8;
+
+template <int NR>
+__host__ __device__ inline bool paged_may_be_long(const PagedParams& p) {
+  return (long long)(p.T - p.B) * p.group > 4 * kLongReq * NR;
+}
+
+template <int NR>
+__device__ __forceinline__ int paged_row_tiles(const PagedParams& p, const PagedReq& q) {
+  return (int)((q.n * (uint32_t)p.group + NR - 1) / NR);
+}
+
+// paged_head_cost of every lane's own request, called by the whole warp: the lanes take the long ones one after the other
+// where that is shorter than a lane's own way through the longest.
+template <int NR>
+__device__ __forceinline__ long long paged_head_costs(const PagedParams& p, const PagedReq& q, int lane) {
+  const int tiles = paged_row_tiles<NR>(p, q);
+  uint32_t longs = __ballot_sync(0xffffffffu, tiles > kLongReq);
+  if (longs != 0 && __reduce_max_sync(0xffffffffu, (uint32_t)tiles) <= (uint32_t)(kLongReq * __popc(longs))) longs = 0;
+  long long c = (longs >> lane & 1) != 0 ? 0 : paged_head_cost<NR>(p, q);
+  __syncwarp();
+  for (; longs != 0; longs &= longs - 1) {
+    const int src = __ffs(longs) - 1;
+    PagedReq r;
+    r.s0 = 0;
+    r.n = __shfl_sync(0xffffffffu, q.n, src);
+    r.total = __shfl_sync(0xffffffffu, q.total, src);
+    long long v = paged_head_cost<NR>(p, r, lane, 32);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == src) c = v;
   }
   return c;
 }
@@ -127,6 +167,148 @@ struct PagedShare {
 
 __device__ __forceinline__ long long paged_cut(long long per, long long more, int c) {
   return per * c + min((long long)c, more);
+}
+
+// paged_share, below, for such calls.
+template <int NR, int NT>
+__device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int apart = 0;  // few requests are 2^apart threads apart, so that every warp has some
+  while (apart < 5 && p.B <= NT >> (apart + 1)) ++apart;
+  const int n = (p.B + NT - 1) / NT;  // requests of a thread
+  const int b0 = (tid & ((1 << apart) - 1)) == 0 ? min((tid >> apart) * n, p.B) : p.B, b1 = min(b0 + n, p.B);
+  PagedReq q{0, 0, 0};
+  long long c = 0, mine = 0;  // of the thread's last request; of all of them
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const bool there = b0 + i < b1;
+    if (there) q = paged_req(p, b0 + i);
+    __syncwarp();
+    const long long x = paged_head_costs<NR>(p, there ? q : PagedReq{0, 0, 0}, lane);
+    if (there) c = x;
+    mine += x * p.Hkv;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sh->warp_sum[warp] = inc;
+  __syncthreads();
+  long long total = 0, before = inc - mine;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += sh->warp_sum[w];
+    total += sh->warp_sum[w];
+  }
+  const int ctas = (int)min((long long)gridDim.x, total);
+  const bool in = (int)blockIdx.x < ctas;
+  long long per = 0, more = 0, w0 = 0, w1 = 0;
+  if (in) {
+    per = paged_div(total, ctas);
+    more = total - per * ctas;
+    w0 = paged_cut(per, more, blockIdx.x);
+    w1 = paged_cut(per, more, blockIdx.x + 1);
+  }
+  if (tid == 0) {
+    sh->per = per;
+    sh->more = more;
+    sh->ctas = ctas;
+    if (!in) sh->w0 = 0;
+    if (!in || w1 == total) sh->w1 = w1;
+  }
+  // the thread whose requests hold a border finds its unit, with its warp's help where the request is long
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {
+    const long long at = end ? w1 : w0;
+    const bool here = in && at >= before && at < before + mine;
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;  // one thread of the CTA at most
+    if (src < 0) continue;
+    long long rest = at - before;
+    PagedUnit u;
+    u.b = b1 - 1;
+    u.q = q;
+    u.kvh = u.rt = 0;
+    if (n > 1) {  // not the thread's only request
+      bool found = false;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        PagedReq r{0, 0, 0};
+        if (here && !found && b0 + i < b1) r = paged_req(p, b0 + i);
+        __syncwarp();
+        const long long x = paged_head_costs<NR>(p, r, lane);
+        if (!here || found) continue;
+        if (rest < x * p.Hkv) {
+          found = true;
+          u.b = b0 + i;
+          u.q = r;
+          c = x;
+        } else {
+          rest -= x * p.Hkv;
+        }
+      }
+    }
+    if (here) {
+      u.kvh = (int)paged_div(rest, c);
+      rest -= c * u.kvh;
+    }
+    __syncwarp();
+    if (__shfl_sync(0xffffffffu, paged_row_tiles<NR>(p, u.q), src) > kLongReq) {  // 32 row tiles at a time
+      PagedUnit y;
+      y.q.s0 = 0;
+      y.q.n = __shfl_sync(0xffffffffu, u.q.n, src);
+      y.q.total = __shfl_sync(0xffffffffu, u.q.total, src);
+      long long to_go = __shfl_sync(0xffffffffu, rest, src);
+      const int tiles = paged_row_tiles<NR>(p, y.q);
+#pragma unroll 1
+      for (int rt0 = 0; rt0 < tiles; rt0 += 32) {
+        y.rt = rt0 + lane;
+        int cost = 0;
+        if (y.rt < tiles) {
+          paged_unit_tiles<NR>(p, y);
+          cost = paged_cost<NR>(y);
+        }
+        long long upto = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, to_go < upto);
+        if (past != 0) {
+          const int first = __ffs(past) - 1;
+          const long long begun = __shfl_sync(0xffffffffu, to_go - (upto - cost), first);
+          if (here) {
+            rest = begun;
+            u.rt = rt0 + first;
+          }
+          break;
+        }
+        to_go -= __shfl_sync(0xffffffffu, upto, 31);
+      }
+    } else if (here) {
+#pragma unroll 1
+      for (u.rt = 0;; ++u.rt) {
+        paged_unit_tiles<NR>(p, u);
+        if (rest < paged_cost<NR>(u)) break;
+        rest -= paged_cost<NR>(u);
+      }
+    }
+    __syncwarp();
+    if (!here) continue;
+    const int off = rest > kOver ? (int)rest : 0;
+    if (end) {
+      sh->w1 = at - (rest - off);
+    } else {
+      sh->w0 = at - (rest - off);
+      sh->b = u.b;
+      sh->kvh = u.kvh;
+      sh->rt = u.rt;
+      sh->off = off;
+      sh->q = u.q;
+    }
+  }
 }
 
 // Called by every thread of the CTA (NT threads) before a __syncthreads().
