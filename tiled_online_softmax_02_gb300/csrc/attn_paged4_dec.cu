@@ -29,7 +29,7 @@
 // Measured (one GB300, device time with the join, D = 128): 8 requests of 9K to
 // 33K tokens, 32 query and 8 kv heads, bf16, 42.6 us, 4.5 TB/s, 67% of a copy's
 // rate (the 8-bit kernel 58); 64 requests of up to 8K, 4 kv heads, f16, blocks of
-// 16 slots, 39.2 us (54); one request of 3.5K 9.9 us (11.4).  About 8 us of each
+// 16 slots, 39.2 us (54); one request of 3.5K 8.9 us (11.4).  About 8 us of each
 // are the launch, the shares, the first keys and the join.  32 keys cost 540
 // instructions: 128 conversions and 128 multiplications, on two pipes that take
 // one every other cycle, 32 products, which with those alone take 138 cycles
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
   after_earlier_kernels();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) DP.p.cuts[blockIdx.x].parts = 0;
-  if constexpr (LONG) paged_share_long<8 * NT, C::kThreads>(p, share);
-  else paged_share<8 * NT, C::kThreads>(p, share);
+  if constexpr (LONG) paged_share_long<8 * NT, C::kThreads, kPaged4Piece>(p, share);
+  else paged_share<8 * NT, C::kThreads, kPaged4Piece>(p, share);
   __syncthreads();
   PagedWalk<8 * NT> w;
   w.begin(p, share);

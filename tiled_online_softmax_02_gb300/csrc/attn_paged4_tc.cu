@@ -594,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
     tmem_alloc(smem_u32(sm.slot()), 512);
     tmem_relinquish();
   }
-  if (paged_may_be_long<kRows>(p)) paged_share_long<kRows, kThreads>(p, sm.share());
-  else paged_share<kRows, kThreads>(p, sm.share());
+  if (paged_may_be_long<kRows>(p)) paged_share_long<kRows, kThreads, kPaged4Piece>(p, sm.share());
+  else paged_share<kRows, kThreads, kPaged4Piece>(p, sm.share());
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

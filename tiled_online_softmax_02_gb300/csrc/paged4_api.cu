@@ -228,7 +228,7 @@ Plan4 plan4(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_tiles) {
   // 256 rows; a unit costs some tiles more; and what one unit's tiles leave on many SMs takes the latter up to 13 us to join.
   // Of the tiles that there may be to read (the tables' width, or the window) 0.7 are taken to be there.  Few and many: 4 kv
   // heads, 48 requests of up to 8K, 24 rows 69 and 85 us, 32 rows 77 and 86; 8 requests, 32 rows 25 and 32, 64 rows 40 and
-  // 33; one of 4K, 64 rows 13 and 30, 128 rows 17 and 31, 512 rows 35 and 33; 8 kv heads, 4 requests of 32K, 32 rows 85 and
+  // 33; one of 4K, 64 rows 13 and 30, 128 rows 17 and 31, 512 rows 35 and 28; 8 kv heads, 4 requests of 32K, 32 rows 85 and
   // 102, 200 tokens over 800 34 and 25; prompts of 4 kv heads: one of 500 tokens 26 and 22, 4 of 120 19 and 11.  D = 64: the
   // same order.
   auto time = [&](int unit, int64_t over, int64_t rate) {
@@ -345,7 +345,7 @@ extern "C" int attn_fwd_paged_fp4(const void* q, const void* k_cache, const void
     L.cuts = P.cuts;
     L.ml_log2 = (plan.rows == kPagedTcRows ? kPagedTcLog2 : kPaged4DecLog2) - kPagedSumLog2;
     // Parts a unit, about: CTAs over units.  64 requests (three) take 41.8 us with a CTA a row and 39.4 with one a unit, one
-    // request of 4K (39) 9.8 and 11.3, 4 of 16 rows (ten) 13.8 and 15.9.
+    // request of 4K (39) 8.9 and 9.3, 4 of 16 rows (ten) 13.8 and 15.9.
     const int64_t parts = plan.grid / ((int64_t)B * Hkv * std::max<int64_t>(1, (T / B * p.group + plan.rows - 1) / plan.rows)) + 1;
     e = plan.rows == kPagedTcRows || parts > 8 ? launch_attn_paged_join(L, bf16, st) : launch_attn_paged4_join(L, bf16, st);
   }

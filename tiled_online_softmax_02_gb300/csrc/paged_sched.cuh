@@ -170,7 +170,7 @@ __device__ __forceinline__ long long paged_cut(long long per, long long more, in
 }
 
 // paged_share, below, for such calls.
-template <int NR, int NT>
+template <int NR, int NT, int kPiece = 1>
 __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int apart = 0;  // few requests are 2^apart threads apart, so that every warp has some
@@ -202,7 +202,7 @@ __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* 
     if (w < warp) before += sh->warp_sum[w];
     total += sh->warp_sum[w];
   }
-  const int ctas = (int)min((long long)gridDim.x, total);
+  const int ctas = (int)min((long long)gridDim.x, (total + kPiece - 1) / kPiece);
   const bool in = (int)blockIdx.x < ctas;
   long long per = 0, more = 0, w0 = 0, w1 = 0;
   if (in) {
@@ -311,8 +311,9 @@ __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* 
   }
 }
 
-// Called by every thread of the CTA (NT threads) before a __syncthreads().
-template <int NR, int NT>
+// Called by every thread of the CTA (NT threads) before a __syncthreads().  Where there is too little for every CTA of the
+// grid, those that work have kPiece tiles or more.
+template <int NR, int NT, int kPiece = 1>
 __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (p.B + NT - 1) / NT;  // requests of a thread
@@ -339,7 +340,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
     if (w < warp) before += sh->warp_sum[w];
     total += sh->warp_sum[w];
   }
-  const int ctas = (int)min((long long)gridDim.x, total);
+  const int ctas = (int)min((long long)gridDim.x, (total + kPiece - 1) / kPiece);
   const bool in = (int)blockIdx.x < ctas;
   long long per = 0, more = 0, w0 = 0, w1 = 0;
   if (in) {
