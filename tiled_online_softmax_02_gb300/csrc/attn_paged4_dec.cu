@@ -120,7 +120,7 @@ struct Subs {
 };
 
 template <int NT, int W>
-__device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 * NT>& w, int warp) {
+__device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 * NT, true>& w, int warp) {
   const PagedUnit& u = w.u;
   const int lo = paged_limits(p, u.q, paged_token(p, u.row0)).x, hi = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).y;
   const int a = max(w.t0 * (kPagedKeys / kSub), lo / kSub) + warp;
@@ -133,7 +133,7 @@ __device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 
 __device__ __forceinline__ int entry_of(const PagedParams& p, const int32_t* table, int valid, int sub, int lane) {
   const int64_t key = (int64_t)sub * kSub + (lane & 16);
   if (key >= valid) return -1;
-  const int e = __ldg(table + (key >> p.block_shift));
+  const int e = table[key >> p.block_shift];
   return e >= 0 && e < p.num_blocks ? e : -2;
 }
 
@@ -181,7 +181,7 @@ __device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, 
 // ----------------------------------------------------------------- compute
 template <int D, int NT, bool BF16, bool SOFTCAP>
 __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t* smem, const PagedShare* share,
-                                             PagedWalk<8 * NT> w, int warp, int lane) {
+                                             PagedWalk<8 * NT, true> w, int warp, int lane) {
   using C = Cfg<D, NT>;
   const Paged4Params& P = DP.p;
   const PagedParams& p = P.c;
@@ -214,7 +214,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
                                                           (int64_t)(w.u.kvh * p.group + x - tok * p.group) * D + t * (D / 4));
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) {
-          const uint4 v = __ldg(src + i);
+          const uint4 v = src[i];
           raw[j][4 * i] = v.x; raw[j][4 * i + 1] = v.y; raw[j][4 * i + 2] = v.z; raw[j][4 * i + 3] = v.w;
         }
       }
@@ -258,7 +258,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
         for (int i = 0; i < 2 * KS; ++i)
           raw[j][i] = as_bits(__floats2half2_rn(__uint_as_float(raw[j][i] << 16) * up, __uint_as_float(raw[j][i] & 0xffff0000u) * up));
       }
-      const float kh = P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f;
+      const float kh = P.k_heads ? P.k_heads[u.kvh] : 1.0f;
       // positive, so that -inf stays -inf, and finite, so that 0 stays 0
       down = fminf(fmaxf(down * (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh, 1.2e-38f), 3e38f);
       fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * t);
@@ -501,7 +501,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
 
     // ---- the warps meet: rows' maxima, sums and O, joined in the order of the warps
     asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory");
-    const float vh = P.v_heads ? __ldg(P.v_heads + kvh) : 1.0f;
+    const float vh = P.v_heads ? P.v_heads[kvh] : 1.0f;
 #pragma unroll 1
     for (int r = warp; r < rows; r += W) {
       constexpr int V = D / 32;
@@ -563,9 +563,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) DP.p.cuts[blockIdx.x].parts = 0;
   if constexpr (LONG) paged_share_long<8 * NT, C::kThreads, kPaged4Piece>(p, share);
-  else paged_share<8 * NT, C::kThreads, kPaged4Piece>(p, share);
+  else paged_share<8 * NT, C::kThreads, kPaged4Piece, true>(p, share);
   __syncthreads();
-  PagedWalk<8 * NT> w;
+  PagedWalk<8 * NT, true> w;
   w.begin(p, share);
   compute_role<D, NT, BF16, SOFTCAP>(DP, smem, share, w, warp, lane);
 }

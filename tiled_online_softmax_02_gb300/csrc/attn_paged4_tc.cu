@@ -115,7 +115,7 @@ struct Paged4TcParams {
   float sc_in, sc_out; // soft-cap, from and to log2 units: sc_out tanh(sc_in s)
 };
 
-using Walk = PagedWalk<kRows>;
+using Walk = PagedWalk<kRows, true>;
 
 // Whether lane t of a unit has rows.
 __device__ __forceinline__ bool lane_on(const PagedUnit& u, int t) { return t == 0 || u.rows > BM; }
@@ -145,7 +145,7 @@ __device__ __forceinline__ void load_role(const Paged4Params& P, const Lay<D>& s
     auto lookup = [&](int t) {  // -1: past the last key; -2: names no block
       const int64_t n = (int64_t)t * per + i;
       if (i >= per || n >= ((int64_t)valid + p.block_size - 1) >> p.block_shift) return -1;
-      const int e = __ldg(table + n);
+      const int e = table[n];
       return e >= 0 && e < p.num_blocks ? e : -2;
     };
     int next = w.nt > 0 ? lookup(w.t0) : -1;
@@ -450,9 +450,9 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
     const int2 lim = mine ? paged_limits(p, u.q, paged_token(p, x0 + row)) : make_int2(0, 0);
     const int full_lo = paged_limits(p, u.q, paged_token(p, last)).x, full_hi = paged_limits(p, u.q, paged_token(p, x0)).y;
     // positive, so that -inf stays -inf, and finite, so that 0 stays 0
-    const float raw = fminf(fmaxf(qs * (P.k_heads ? __ldg(P.k_heads + u.kvh) : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2), 1.2e-38f), 3e38f);
+    const float raw = fminf(fmaxf(qs * (P.k_heads ? P.k_heads[u.kvh] : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2), 1.2e-38f), 3e38f);
     const float xs = SOFTCAP ? TP.sc_out : raw;  // brings x, the raw score or its tanh, to log2 units
-    vh = P.v_heads ? __ldg(P.v_heads + u.kvh) : 1.0f;
+    vh = P.v_heads ? P.v_heads[u.kvh] : 1.0f;
     m_run = kNone;
     l_run = 0.0f;
     for (int n = 0; n < nt; ++n, ++sc) {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
     tmem_relinquish();
   }
   if (paged_may_be_long<kRows>(p)) paged_share_long<kRows, kThreads, kPaged4Piece>(p, sm.share());
-  else paged_share<kRows, kThreads, kPaged4Piece>(p, sm.share());
+  else paged_share<kRows, kThreads, kPaged4Piece, true>(p, sm.share());
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -58,7 +58,7 @@ __device__ __forceinline__ int find_request(const int32_t* q_starts, int B, int 
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + (lane + 1) * step - 1;  // last entry of lane's part
-    const bool past = i >= hi || __ldg(q_starts + i + 1) > t;
+    const bool past = i >= hi || q_starts[i + 1] > t;
     const unsigned m = __ballot_sync(0xffffffffu, past);
     if (m == 0) return hi;
     const int part = __ffs(m) - 1;
@@ -171,11 +171,11 @@ __global__ void __launch_bounds__(kThreads, 32) rope_kernel(const __grid_constan
     const int h0 = (int)(item - (int64_t)t * parts) * heads_each, h1 = min(h0 + heads_each, p.H[0] + p.H[1]);
     int64_t pos;
     if (p.positions) {
-      pos = __ldg(p.positions + t);
+      pos = p.positions[t];
     } else {
       const int b = find_request(p.q_starts, p.B, t, lane);
-      if (b >= p.B || t < __ldg(p.q_starts)) continue;  // rows of no request
-      pos = (int64_t)__ldg(p.totals + b) - __ldg(p.q_starts + b + 1) + t;
+      if (b >= p.B || t < p.q_starts[0]) continue;  // rows of no request
+      pos = (int64_t)p.totals[b] - p.q_starts[b + 1] + t;
     }
     // head h of q and k together lies at in(h) + h D
     const int hq = p.H[0];
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 32) rope_kernel(const __grid_constan
       const int pairs = min(kPairs, half - pair0);
       __syncwarp();  // the last ones have been read
       for (int i = lane; i < pairs; i += 32) {
-        const uint64_t turn = (uint64_t)pos * turns(__ldg(p.freq + pair0 + i));
+        const uint64_t turn = (uint64_t)pos * turns(p.freq[pair0 + i]);
         float c, n;
         sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &n, &c);
         cw[i] = c * p.scale;
