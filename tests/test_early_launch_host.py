@@ -48,3 +48,11 @@ def test_every_kernel_waits(name):
     assert kernels
     for body in kernels:
         assert re.search(r"after_earlier_kernels\(\);|griddepcontrol\.wait", body), body[:200]
+
+
+@pytest.mark.parametrize("name", ["attn_paged4_tc.cu", "attn_paged_tc.cu", "attn_paged_dec.cu"])
+def test_later_kernels_come_in_once_tensor_memory_is_held(name):
+    """A CTA whose columns a later kernel had taken would wait for that one, which waits for this grid."""
+    text = code(name)
+    alloc, sync = text.index("tmem_alloc("), text.index("__syncthreads();", text.index("tmem_alloc("))
+    assert text.count("launch_dependents") == 1 and alloc < sync < text.index("launch_dependents")

@@ -566,7 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
   sm.s = smem_u32(sm.base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   after_earlier_kernels();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSP; ++i) {
       mbar_init(sm.p_full(i), 1);
@@ -599,6 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The joining kernel may be scheduled; it waits.  Where no join follows this may let in any kernel, one with tensor memory
+  // of its own among them, so this CTA has its columns by now.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.slot());
   Walk w;
   w.begin(p, sm.share());

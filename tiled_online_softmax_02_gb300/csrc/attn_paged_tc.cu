@@ -726,7 +726,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   sm.s = smem_u32(sm.base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSK; ++i) {
       mbar_init(sm.k_full(i), 2);  // the TMA's, and the scale warp's
@@ -764,6 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The joining kernel may be scheduled; it waits.  Where no join follows this may let in any kernel, one with tensor memory
+  // of its own among them, so this CTA has its columns by now.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.slot());
   Walk w;
   w.begin(p, sm.share());
