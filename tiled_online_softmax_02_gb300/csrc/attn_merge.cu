@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 
 #include "attn_internal.h"
+#include "device_common.cuh"
 
 namespace gb300_attn {
 namespace {
@@ -34,8 +35,8 @@ __global__ void attn_merge_kernel(const MergeParams p) {
   const int64_t plane = rows * p.D;  // floats per split in ws_o
   for (int64_t row = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5); row < rows;
        row += (int64_t)gridDim.x * warps) {  // (b * Hq + h) * Sq + qi
-    const float l0 = lane < p.num_splits ? __ldg(p.ws_lse + lane * rows + row) : -INFINITY;
-    const float l1 = lane + 32 < p.num_splits ? __ldg(p.ws_lse + (lane + 32) * rows + row) : -INFINITY;
+    const float l0 = lane < p.num_splits ? load_written(p.ws_lse + lane * rows + row) : -INFINITY;
+    const float l1 = lane + 32 < p.num_splits ? load_written(p.ws_lse + (lane + 32) * rows + row) : -INFINITY;
     float m = fmaxf(l0, l1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -53,10 +54,10 @@ __global__ void attn_merge_kernel(const MergeParams p) {
       const float w = __shfl_sync(0xffffffffu, sp < 32 ? w0 : w1, sp & 31);
       float o[VEC];
       if constexpr (VEC == 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(src + sp * plane));
+        const float4 x = load_written(reinterpret_cast<const float4*>(src + sp * plane));
         o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
       } else {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(src + sp * plane));
+        const float2 x = load_written(reinterpret_cast<const float2*>(src + sp * plane));
         o[0] = x.x; o[1] = x.y;
       }
       const bool live = w != 0.f;
