@@ -31,15 +31,15 @@ def test_no_read_only_loads(name):
 
 
 def test_no_read_only_loads_in_the_shares():
-    """The lengths' reader chooses by the kernel, and such kernels ask for the ordinary load.  (The 8-bit kernels' scales,
+    """The lengths' reader chooses by the kernel, and such kernels ask for another load.  (The 8-bit kernels' scales,
     behind the walk, are theirs alone.)"""
     text = code("paged_sched.cuh")
     text = text[:text.index("struct ScaleFeed")]
-    chosen = "if constexpr (EARLY) return *x;\n  else return __ldg(x);"
+    chosen = "if constexpr (LOAD == kReadOnly) return __ldg(x);"
     assert text.count(chosen) == 1 and not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", text.replace(chosen, ""))
     for name in EARLY[2:4]:
-        made = re.findall(r"(?:PagedWalk|paged_share)<[^;(]*?>(?=[ (;])", code(name))
-        assert len(made) >= 2 and all(m.endswith(", true>") for m in made), made
+        made = re.findall(r"(?:PagedWalk|paged_share|paged_share_long)<[^;(]*?>(?=[ (;])", code(name))
+        assert len(made) >= 3 and all(re.search(r", (kWritten|kOrdinary)>$", m) for m in made), made
 
 
 @pytest.mark.parametrize("name", EARLY)

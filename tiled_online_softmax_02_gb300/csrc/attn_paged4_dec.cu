@@ -120,7 +120,7 @@ struct Subs {
 };
 
 template <int NT, int W>
-__device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 * NT, true>& w, int warp) {
+__device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 * NT, kWritten>& w, int warp) {
   const PagedUnit& u = w.u;
   const int lo = paged_limits(p, u.q, paged_token(p, u.row0)).x, hi = paged_limits(p, u.q, paged_token(p, u.row0 + u.rows - 1)).y;
   const int a = max(w.t0 * (kPagedKeys / kSub), lo / kSub) + warp;
@@ -133,7 +133,7 @@ __device__ __forceinline__ Subs subs_of(const PagedParams& p, const PagedWalk<8 
 __device__ __forceinline__ int entry_of(const PagedParams& p, const int32_t* table, int valid, int sub, int lane) {
   const int64_t key = (int64_t)sub * kSub + (lane & 16);
   if (key >= valid) return -1;
-  const int e = table[key >> p.block_shift];
+  const int e = load_written(table + (key >> p.block_shift));
   return e >= 0 && e < p.num_blocks ? e : -2;
 }
 
@@ -181,7 +181,7 @@ __device__ __forceinline__ void load_sub(const Paged4Params& P, uint32_t stage, 
 // ----------------------------------------------------------------- compute
 template <int D, int NT, bool BF16, bool SOFTCAP>
 __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t* smem, const PagedShare* share,
-                                             PagedWalk<8 * NT, true> w, int warp, int lane) {
+                                             PagedWalk<8 * NT, kWritten> w, int warp, int lane) {
   using C = Cfg<D, NT>;
   const Paged4Params& P = DP.p;
   const PagedParams& p = P.c;
@@ -214,7 +214,7 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
                                                           (int64_t)(w.u.kvh * p.group + x - tok * p.group) * D + t * (D / 4));
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) {
-          const uint4 v = src[i];
+          const uint4 v = load_written(src + i);
           raw[j][4 * i] = v.x; raw[j][4 * i + 1] = v.y; raw[j][4 * i + 2] = v.z; raw[j][4 * i + 3] = v.w;
         }
       }
@@ -562,10 +562,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
   after_earlier_kernels();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be scheduled; it waits
   if (threadIdx.x == 0) DP.p.cuts[blockIdx.x].parts = 0;
-  if constexpr (LONG) paged_share_long<8 * NT, C::kThreads, kPaged4Piece>(p, share);
-  else paged_share<8 * NT, C::kThreads, kPaged4Piece, true>(p, share);
+  if constexpr (LONG) paged_share_long<8 * NT, C::kThreads, kPaged4Piece, kWritten>(p, share);
+  else paged_share<8 * NT, C::kThreads, kPaged4Piece, kWritten>(p, share);
   __syncthreads();
-  PagedWalk<8 * NT, true> w;
+  PagedWalk<8 * NT, kWritten> w;
   w.begin(p, share);
   compute_role<D, NT, BF16, SOFTCAP>(DP, smem, share, w, warp, lane);
 }

@@ -115,7 +115,7 @@ struct Paged4TcParams {
   float sc_in, sc_out; // soft-cap, from and to log2 units: sc_out tanh(sc_in s)
 };
 
-using Walk = PagedWalk<kRows, true>;
+using Walk = PagedWalk<kRows, kOrdinary>;
 
 // Whether lane t of a unit has rows.
 __device__ __forceinline__ bool lane_on(const PagedUnit& u, int t) { return t == 0 || u.rows > BM; }
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged4_tc_kernel(const __gri
     tmem_alloc(smem_u32(sm.slot()), 512);
     tmem_relinquish();
   }
-  if (paged_may_be_long<kRows>(p)) paged_share_long<kRows, kThreads, kPaged4Piece>(p, sm.share());
-  else paged_share<kRows, kThreads, kPaged4Piece, true>(p, sm.share());
+  if (paged_may_be_long<kRows>(p)) paged_share_long<kRows, kThreads, kPaged4Piece, kOrdinary>(p, sm.share());
+  else paged_share<kRows, kThreads, kPaged4Piece, kOrdinary>(p, sm.share());
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "../../include/attn.h"
+#include "device_common.cuh"
 #include "paged4.cuh"
 #include "paged4_internal.h"
 
@@ -79,7 +80,7 @@ struct Place {
   }
   // index of the row in the cache; -1: no row
   __device__ __forceinline__ int64_t row(const Cache4Params& p) const {
-    const int64_t s = p.slot_map[t];
+    const int64_t s = load_written(p.slot_map + t);
     if (!there || s < 0 || s >= p.num_slots) return -1;
     return ((s >> p.block_shift) * p.Hkv + h) * p.block_size + (s & (p.block_size - 1));
   }
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
     for (int k = 0; k < 2; ++k) {
       const T* src = static_cast<const T*>(p.x[k]) + (int64_t)at.t * p.stride[k] + at.h * D + at.part * kGroup4;
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T); ++i) v[k][i] = reinterpret_cast<const uint4*>(src)[i];
-      hs[k] = p.heads[k] ? p.heads[k][at.h] : 1.0f;
+      for (int i = 0; i < (int)sizeof(T); ++i) v[k][i] = load_written(reinterpret_cast<const uint4*>(src) + i);
+      hs[k] = p.heads[k] ? load_written(p.heads[k] + at.h) : 1.0f;
     }
     const int64_t row = at.row(p);
     if (row < 0) continue;
@@ -192,9 +193,9 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       code[k] = make_uint2(0u, 0u);
-      hs[k] = p.heads[k] ? p.heads[k][at.h] : 1.0f;
+      hs[k] = p.heads[k] ? load_written(p.heads[k] + at.h) : 1.0f;
       if (row >= 0) {
-        code[k] = *reinterpret_cast<const uint2*>(p.cache[k] + row * (D / 2) + at.part * 8);
+        code[k] = load_written(reinterpret_cast<const uint2*>(p.cache[k] + row * (D / 2) + at.part * 8));
         sb[k] = p.scales[k][row * (D / kGroup4) + at.part];
       }
     }

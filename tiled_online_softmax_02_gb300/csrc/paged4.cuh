@@ -10,7 +10,7 @@ namespace gb300_attn {
 namespace {
 
 // What launch_early asks of a kernel, before anything else.  What earlier kernels may have written is loaded after it, and
-// by ordinary loads: the read-only path (__ldg) is for memory that nobody writes while the kernel lives, and this one may
+// by ordinary loads or load_written: the read-only path (__ldg) is for memory that nobody writes while the kernel lives, and this one may
 // already live while those still write.
 __device__ __forceinline__ void after_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -49,20 +49,25 @@ struct PagedReq {
   int total;   // cached tokens, these rows' among them (at least 0: below it nothing is visible either)
 };
 
-// EARLY: for kernels that may begin while earlier ones still write the lengths, which rules out the read-only path (see
-// after_earlier_kernels).  The 8-bit kernels, launched in order, keep it: without it they lose 1 to 2.5%.
-template <bool EARLY>
+// How the lengths are read.  A kernel that may begin while earlier ones still write them has to keep off the read-only path
+// (see after_earlier_kernels): the few-rows kernel over the 4-bit cache by load_written (8 long requests 42.1 us, by ordinary
+// loads 42.6), the many-rows one by ordinary loads (long chunks 557 us, by load_written 563).  The 8-bit kernels, launched
+// in order, lose 1 to 2.5% off it.
+enum PagedLoad { kReadOnly, kOrdinary, kWritten };
+
+template <PagedLoad LOAD>
 __device__ __forceinline__ int paged_length(const int32_t* x) {
-  if constexpr (EARLY) return *x;
-  else return __ldg(x);
+  if constexpr (LOAD == kReadOnly) return __ldg(x);
+  else if constexpr (LOAD == kWritten) return load_written(x);
+  else return *x;
 }
 
-template <bool EARLY>
+template <PagedLoad LOAD>
 __device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int b) {
   PagedReq r;
-  r.s0 = min(max(paged_length<EARLY>(p.q_starts + b), 0), p.T);
-  r.n = min(max(paged_length<EARLY>(p.q_starts + b + 1), r.s0), p.T) - r.s0;
-  r.total = max(paged_length<EARLY>(p.totals + b), 0);
+  r.s0 = min(max(paged_length<LOAD>(p.q_starts + b), 0), p.T);
+  r.n = min(max(paged_length<LOAD>(p.q_starts + b + 1), r.s0), p.T) - r.s0;
+  r.total = max(paged_length<LOAD>(p.totals + b), 0);
   return r;
 }
 
@@ -178,8 +183,8 @@ __device__ __forceinline__ long long paged_cut(long long per, long long more, in
   return per * c + min((long long)c, more);
 }
 
-// paged_share, below, for such calls (EARLY).
-template <int NR, int NT, int kPiece = 1>
+// paged_share, below, for such calls.
+template <int NR, int NT, int kPiece, PagedLoad LOAD>
 __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int apart = 0;  // few requests are 2^apart threads apart, so that every warp has some
@@ -191,7 +196,7 @@ __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* 
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const bool there = b0 + i < b1;
-    if (there) q = paged_req<true>(p, b0 + i);
+    if (there) q = paged_req<LOAD>(p, b0 + i);
     __syncwarp();
     const long long x = paged_head_costs<NR>(p, there ? q : PagedReq{0, 0, 0}, lane);
     if (there) c = x;
@@ -244,7 +249,7 @@ __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* 
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         PagedReq r{0, 0, 0};
-        if (here && !found && b0 + i < b1) r = paged_req<true>(p, b0 + i);
+        if (here && !found && b0 + i < b1) r = paged_req<LOAD>(p, b0 + i);
         __syncwarp();
         const long long x = paged_head_costs<NR>(p, r, lane);
         if (!here || found) continue;
@@ -322,7 +327,7 @@ __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* 
 
 // Called by every thread of the CTA (NT threads) before a __syncthreads().  Where there is too little for every CTA of the
 // grid, those that work have kPiece tiles or more.
-template <int NR, int NT, int kPiece = 1, bool EARLY = false>
+template <int NR, int NT, int kPiece = 1, PagedLoad LOAD = kReadOnly>
 __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (p.B + NT - 1) / NT;  // requests of a thread
@@ -331,7 +336,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
   long long c = 0, mine = 0;  // of the thread's last request; of all of them
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    q = paged_req<EARLY>(p, b);
+    q = paged_req<LOAD>(p, b);
     c = paged_head_cost<NR>(p, q);
     mine += c * p.Hkv;
   }
@@ -376,7 +381,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
     u.q = q;
     if (n > 1) {  // not the thread's only request
       for (u.b = b0;; ++u.b) {
-        u.q = paged_req<EARLY>(p, u.b);
+        u.q = paged_req<LOAD>(p, u.b);
         c = paged_head_cost<NR>(p, u.q);
         if (rest < c * p.Hkv) break;
         rest -= c * p.Hkv;
@@ -405,7 +410,7 @@ __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh
 }
 
 // Walks a CTA's piece, segment by segment: a unit's tiles [t0, t0 + nt).
-template <int NR, bool EARLY = false>
+template <int NR, PagedLoad LOAD = kReadOnly>
 struct PagedWalk {
   PagedUnit u;
   PagedReq ahead;        // of request u.b + 1, read a unit or more before it is needed
@@ -422,7 +427,7 @@ struct PagedWalk {
     u.kvh = s->kvh;
     u.rt = s->rt;
     u.q = s->q;
-    ahead = paged_req<EARLY>(p, min(u.b + 1, p.B - 1));
+    ahead = paged_req<LOAD>(p, min(u.b + 1, p.B - 1));
     paged_unit_tiles<NR>(p, u);
     off = s->off;
     segment();
@@ -448,7 +453,7 @@ struct PagedWalk {
         do {  // the piece goes on, so some later request has rows
           ++u.b;
           u.q = ahead;
-          ahead = paged_req<EARLY>(p, min(u.b + 1, p.B - 1));
+          ahead = paged_req<LOAD>(p, min(u.b + 1, p.B - 1));
         } while (u.q.n == 0);
       }
     }
@@ -458,8 +463,8 @@ struct PagedWalk {
 };
 
 // CTAs from this one on that hold a part of the walk's unit.
-template <int NR, bool EARLY>
-__device__ __forceinline__ int paged_parts(const PagedWalk<NR, EARLY>& w, const PagedShare* s) {
+template <int NR, PagedLoad LOAD>
+__device__ __forceinline__ int paged_parts(const PagedWalk<NR, LOAD>& w, const PagedShare* s) {
   const long long last = s->w1 - w.left - w.off + paged_cost<NR>(w.u) - 1;
   int c = blockIdx.x;
   while (c + 1 < s->ctas && paged_cut(s->per, s->more, c + 1) <= last) ++c;
