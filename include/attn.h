@@ -549,8 +549,9 @@ int attn_cache_read_fp4(const void *k_cache, const void *v_cache, const void *k_
  *   workspace     at least attn_paged_fp4_workspace_bytes(...) bytes, 16-byte
  *                 aligned, for partial rows; nothing in it has to start at zero.
  *                 Calls that share a workspace must not overlap on the GPU.
- * A key's weight is held to 11 bits, or to 2^-29 of the row's largest; the row
- * sum has every key's weight.  A row whose largest score is below -6e29 counts as
+ * A key's weight is held to 11 bits of what its score gives, or to 2^-29 of the row's
+ * largest; the row sum has every key's weight.  Under a soft-cap the score is held to 2^-16
+ * of itself, which at a capped score of 50 is a weight to 2^-10, at 1000 one to 2%.  A row whose largest score is below -6e29 counts as
  * one without keys.  A block-table entry below a request's length
  * that names no block is not followed: its keys count as zeros, and
  * attn_get_device_status then reports ATTN_ERR_INVALID_ARG once.

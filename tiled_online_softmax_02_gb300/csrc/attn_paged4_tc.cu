@@ -472,7 +472,10 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
         }
         tmem_wait_st();
       }
-      // tanh(scale s / c) of a raw score; hidden ones stay -inf
+      // tanh(scale s / c) of a raw score; hidden ones stay -inf.  The hardware tanh: over all fp32 arguments it is off by
+      // 2^-16.46 of the value at most, and by 2^-16.93, measured on the GB300 (its specification allows 2^-11), which is what
+      // the call promises of capped scores, 2^-16.  With the few-rows kernel's, to 2^-20, the same two long chunks under a
+      // cap take 1251 us in place of 844, two values at a time and without a branch.
       auto capped = [&](float x) {
         if constexpr (SOFTCAP) return x == -INFINITY ? x : fast_tanh(x * raw);
         else return x;
