@@ -92,3 +92,16 @@ def test_capped_scores(new, dtype, D, cap, std):
     x["q"] = torch.zeros_like(x["q"]).scatter(2, one, x["q"].gather(2, one))
     x["q"].clamp_(-6e4, 6e4)  # finite in f16
     check(w, x, 2.0 ** (-16 if sum(new) > 100 else -19))
+
+
+@pytest.mark.parametrize("cap", [2.0 ** 60, 2.0 ** 99])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [(2, 1), (150, 40)], ids=["few", "many"])
+def test_large_caps_over_heads_of_small_keys(new, dtype, cap):
+    """The factor from raw scores to the cap's argument lies below fp32's normal range: the scores are next to nothing, and
+    every key has its share."""
+    w = Problem(new=new, total=(400, 300), Hq=4, Hkv=1, D=64, dtype=dtype, softcap=cap, wide=True)
+    x = ref.make(w)
+    x["k_heads"] = torch.tensor([2.0 ** -60])
+    x["q"] *= 8
+    check(w, x, 2.0 ** -16)

@@ -259,8 +259,9 @@ __device__ __forceinline__ void compute_role(const Paged4DecParams& DP, uint8_t*
           raw[j][i] = as_bits(__floats2half2_rn(__uint_as_float(raw[j][i] << 16) * up, __uint_as_float(raw[j][i] & 0xffff0000u) * up));
       }
       const float kh = P.k_heads ? P.k_heads[u.kvh] : 1.0f;
-      // positive, so that -inf stays -inf, and finite, so that 0 stays 0
-      down = fminf(fmaxf(down * (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh, 1.2e-38f), 3e38f);
+      // positive, so that -inf stays -inf, and finite, so that 0 stays 0.  Under a soft-cap hidden keys do not go through it, and
+      // it may be next to nothing: a large cap brings its share back.
+      down = fminf(fmaxf(down * (SOFTCAP ? DP.sc_in : DP.scale_log2) * kh, SOFTCAP ? 0.0f : 1.2e-38f), 3e38f);
       fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * t);
       fac[j][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
