@@ -15,6 +15,7 @@ import importlib.util
 import math
 import os
 import threading
+import warnings
 
 import torch
 
@@ -113,14 +114,29 @@ def load_library():
         return _lib
 
 
+class _NoCalls:
+    """In place of the extension module where there is none: takes no call, so Python marshals them all."""
+
+    @staticmethod
+    def append(*args):
+        return None
+
+    read = attend = rope = append
+
+
 def _load_calls(lib):
-    """Load the extension module that marshals calls on ordinary tensors, for the functions of `lib`."""
+    """Load the extension module that marshals calls on ordinary tensors, for the functions of `lib`.  It saves time and
+    does nothing else, so a library without it (one that GB300_ATTN_LIBRARY names in a tree that was not built, a tree
+    built under another torch) is whole."""
     global _calls
-    if not os.path.exists(_build.CALLS):
-        raise RuntimeError(f"extension module {_build.CALLS} is missing: build it first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')")
-    loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS)
-    calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS)
+        calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    except ImportError as e:
+        warnings.warn(f"no extension module {_build.CALLS} ({e}): calls over the 4-bit cache and attn_rope are marshalled in "
+                      "Python, 5 to 10 us longer each", RuntimeWarning, stacklevel=4)
+        _calls = _NoCalls
+        return
     calls.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
         "attn_cache_append_fp4", "attn_cache_read_fp4", "attn_fwd_paged_fp4", "attn_paged_fp4_workspace_bytes",
         "attn_rope")))

@@ -3,7 +3,9 @@ for sm_103a.  Translation units compile in parallel; the link uses the static
 CUDA runtime, so the library loads on machines without a GPU driver (its
 entry points then report ATTN_ERR_CUDA on the first CUDA call).  Beside it,
 with g++ and torch's headers, the extension module that marshals the 4-bit
-cache's and the rotary positions' calls (csrc/calls.cpp)."""
+cache's and the rotary positions' calls (csrc/calls.cpp).  Nothing depends on
+that module but the time those calls take: where it cannot be built, the build
+says so and the library is there all the same."""
 from __future__ import annotations
 
 import glob
@@ -12,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 import torch
 
@@ -41,16 +44,22 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+def _newer(made: str, inputs: list[str]) -> bool:
+    """Whether `made` is there and no older than its inputs."""
+    return os.path.exists(made) and all(os.path.getmtime(f) <= os.path.getmtime(made) for f in inputs)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+
+
+def _calls_up_to_date() -> bool:
+    return _newer(CALLS, [os.path.join(CSRC, "calls.cpp"), *glob.glob(os.path.join(INCLUDE, "*.h")), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _library_up_to_date() and _calls_up_to_date()
 
 
 def _start_calls(out: str):
@@ -71,15 +80,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
     ``extra_flags`` / ``out_path`` build a variant next to (not over) the
     default library, e.g. with a different -D setting."""
     lib = out_path or LIB
-    if not force and not extra_flags and out_path is None and up_to_date():
-        return LIB
+    calls = None  # the running compiler of the extension module
+    if out_path is None and (force or not _calls_up_to_date()):
+        made = CALLS + f".tmp{os.getpid()}"
+        try:
+            calls = _start_calls(made)
+        except (OSError, RuntimeError) as e:  # no g++, no toolkit
+            _without_calls(str(e))
+    try:
+        if force or extra_flags or out_path is not None or not _library_up_to_date():
+            _build_library(lib, extra_flags, out_path, verbose)
+    finally:
+        if calls is not None:
+            out, _ = calls.communicate()
+            if calls.returncode != 0:
+                _without_calls(out)
+            else:
+                if out and verbose:
+                    sys.stdout.write(out)
+                os.replace(made, CALLS)
+    return lib
+
+
+def _without_calls(why: str):
+    """Says that there is no extension module; one of other sources does not stay."""
+    if os.path.exists(CALLS):
+        os.remove(CALLS)
+    warnings.warn(f"{CALLS} was not built: the calls it would marshal go through Python, 5 to 10 us longer each\n{why}",
+                  RuntimeWarning, stacklevel=3)
+
+
+def _build_library(lib: str, extra_flags: tuple[str, ...], out_path: str | None, verbose: bool):
     nvcc = _nvcc()
     objdir = BUILD if out_path is None else os.path.join(BUILD, "variant_" + os.path.basename(lib))
     os.makedirs(objdir, exist_ok=True)
     procs = []
-    if out_path is None:
-        made = CALLS + f".tmp{os.getpid()}"
-        procs.append((os.path.join(CSRC, "calls.cpp"), None, _start_calls(made)))
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), *extra_flags, "-c", src,
@@ -95,16 +130,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
             sys.stdout.write(out)
         if pr.returncode != 0:
             failed.append(src)
-        if obj is not None:
-            objs.append(obj)
+        objs.append(obj)
     if failed:
         raise RuntimeError(f"nvcc failed for {failed}")
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", *ARCH, "-o", tmp, *objs], check=True)
-    if out_path is None:
-        os.replace(made, CALLS)
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
