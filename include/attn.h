@@ -578,8 +578,8 @@ size_t attn_paged_fp4_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, in
  *   scale * (a cos w - b sin w, b cos w + a sin w),
  * or, when inverse is 1, that with -w: for the same scale the transpose, which
  * takes gradients of the turned rows to gradients of the rows.  Values from R
- * on are kept.  Angles are exact to 2^-24 turns at any position; the rotation
- * is done in f32 and rounded to nearest even.
+ * on are kept.  Angles are exact to 2^-24 turns at any position, for frequencies
+ * below 2^62 in size; the rotation is done in f32 and rounded to nearest even.
  *
  * Position of token t: positions[t] or, when positions is NULL, that of a paged
  * step's rows: total_lengths[b] - q_starts[b + 1] + t for the request b with

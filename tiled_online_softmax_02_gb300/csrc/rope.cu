@@ -6,9 +6,10 @@
 //
 // Angles: position * frequency in fp32 would be off by 2^-24 of itself, whole
 // turns for far positions.  A frequency becomes turns a position as a 64-bit
-// binary fraction (53 bits of it times 1 / (2 pi)); its product with the
-// position, modulo 2^64, is the angle modulo a turn to position * 2^-62 turns,
-// of which the upper 32 bits go to sincospi.  Rotation in fp32, rounded once.
+// binary fraction (53 bits of it times 1 / (2 pi), 64 or 128 bits of that); its
+// product with the position, modulo 2^64, is the angle modulo a turn to position
+// * 2^-58 turns, of which the upper 32 bits go to sincospi.  Rotation in fp32,
+// rounded once.
 //
 // Bound: HBM, each value read and written once.  A warp has a token: its lanes
 // share out the sines and cosines of the token's pairs, through shared memory,
@@ -39,14 +40,20 @@ constexpr int kThreads = 32;  // a warp a CTA: with four, 31.1 us in place of 29
 constexpr int kBatch = 2;   // rows of a lane in flight
 constexpr int kPairs = 256;  // pairs whose sines and cosines a warp holds at a time
 
-// Turns a position of radians a position, modulo 1, times 2^64.
+// Turns a position of radians a position, modulo 1, times 2^64: off by 2^6 at most for radians below 2^62 in size, so that
+// a position's angle is off by 2^-27 turns, less than its rounding.
 __device__ __forceinline__ uint64_t turns(double radians) {
   const uint64_t bits = (uint64_t)__double_as_longlong(radians);
   const int e = (int)((bits >> 52) & 2047) - 1023;
   const uint64_t m = (bits << 11) | (1ull << 63);              // radians = m 2^(e - 63)
-  const uint64_t hi = __umul64hi(m, 0x28be60db9391054bull);    // 2^64 / (2 pi): turns = hi 2^(e - 63)
+  uint64_t hi = __umul64hi(m, 0x28be60db9391054bull);          // 2^64 / (2 pi): turns = hi 2^(e - 63)
   const int up = e + 1;                                        // times 2^64
-  uint64_t f = up >= 64 ? 0 : up >= 0 ? hi << up : up > -64 ? hi >> -up : 0;
+  uint64_t f = up >= 0 ? hi << (up & 63) : up > -64 ? hi >> -up : 0;
+  if (up > 6) {  // the shift brings in bits below hi's: 64 more of 1 / (2 pi)
+    const uint64_t below = __umul64hi(m, 0x7f09d5f47d4d3770ull), lo = m * 0x28be60db9391054aull + below;
+    hi = __umul64hi(m, 0x28be60db9391054aull) + (lo < below ? 1 : 0);
+    f = up < 64 ? hi << up | lo >> (64 - up) : up < 128 ? lo << (up - 64) : 0;
+  }
   if (e == -1023) f = 0;  // zero, or too small to turn anything
   return (bits >> 63) ? 0 - f : f;
 }
