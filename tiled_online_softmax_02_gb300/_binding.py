@@ -947,6 +947,27 @@ def attn_rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0,
     return freq.to(device), out_scale
 
 
+class _Rope(torch.autograd.Function):
+    """attn_rope of tensors that require gradients.  The map is linear, and its inverse with the same factor is its
+    transpose, so the backward pass is this function again.  clear: rows of no request are zeros, as their gradients are."""
+
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, positions, q_starts, total_lengths, layout, inverse, scale, clear):
+        ctx.save_for_backward(inv_freq, positions, q_starts, total_lengths)
+        ctx.how = layout, inverse, scale
+        out = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) if clear and x is not None else None for x in (q, k)]
+        return attn_rope(q, k, inv_freq, positions=positions, q_starts=q_starts, total_lengths=total_lengths, layout=layout,
+                         inverse=inverse, scale=scale, q_out=out[0], k_out=out[1])
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        inv_freq, positions, q_starts, total_lengths = ctx.saved_tensors
+        layout, inverse, scale = ctx.how
+        dq, dk = _Rope.apply(dq.contiguous(), None if dk is None else dk.contiguous(), inv_freq, positions, q_starts, total_lengths,
+                             layout, not inverse, scale, positions is None)
+        return dq, dk, None, None, None, None, None, None, None, None
+
+
 def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=None, layout="half", inverse=False,
               scale=1.0, q_out=None, k_out=None):
     """Rotary positions onto query and key rows (attn_rope in the C ABI).
@@ -960,7 +981,8 @@ def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=No
     inverse turns back: with the same scale it takes gradients of the turned
     rows to gradients of q and k.  Returns (q_out, k_out), allocated with torch
     when not given; q_out=q, k_out=k works in place.  Rows of no request are not
-    written."""
+    written.  Gradients flow through the returned rows to q and k; where either
+    requires them, q_out and k_out cannot be given."""
     if _lib is None:
         load_library()
     inter = ROPE_LAYOUTS.get(layout)
@@ -970,6 +992,11 @@ def attn_rope(q, k, inv_freq, *, positions=None, q_starts=None, total_lengths=No
             if type(made) is int:
                 raise AttnError(made, "attn_rope")
             return made
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q or k requires gradients, which do not pass through q_out and k_out: leave these out, or call "
+                             "under torch.no_grad()")
+        return _Rope.apply(q, k, inv_freq, positions, q_starts, total_lengths, layout, bool(inverse), float(scale), False)
     index, dtype, shape = q.get_device(), q.dtype, q.shape
     if len(shape) != 3 or index < 0:
         raise ValueError("attn_rope takes CUDA tensors: q [T, Hq, D], k [T, Hk, D] or None")

@@ -13,6 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -244,6 +245,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) try {
     if (!x[i] || !x[i]->is_cuda() || x[i]->get_device() != index || x[i]->dim() != 3 || x[i]->size(0) != T || x[i]->size(2) != D ||
         x[i]->scalar_type() != type || !token_stride(*x[i], &in[i]))
       Py_RETURN_NONE;
+    if (c10::GradMode::is_enabled() && x[i]->requires_grad()) Py_RETURN_NONE;  // recorded by the Python code
     H[i] = x[i]->size(1);
     if (!no_out[i] && (!given[i] || !given[i]->is_cuda() || given[i]->get_device() != index || given[i]->sizes() != x[i]->sizes() ||
                        given[i]->scalar_type() != type || !token_stride(*given[i], &to[i])))
