@@ -524,7 +524,10 @@ int attn_cache_append_fp4(const void *k, const void *v, const int64_t *slot_map,
  *   k, v          [num_tokens, Hkv, D] dtype, 16-byte aligned: head h of token t
  *                 at element t * token_stride + h * head_stride, its D values
  *                 together; strides whole 16 bytes, and such that no two rows
- *                 overlap: heads inside tokens or tokens inside heads
+ *                 overlap: heads inside tokens or tokens inside heads.  With the
+ *                 same strides k and v may lie between each other (side by side
+ *                 in a head, a token or a buffer); with others their extents may
+ *                 not meet
  *   the rest      as attn_cache_append_fp4
  * One launch on `stream`; allocates and synchronises nothing.
  */

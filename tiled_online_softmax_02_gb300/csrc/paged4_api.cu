@@ -18,22 +18,35 @@ namespace {
 
 int block_shift(int bs) { return bs == 16 ? 4 : bs == 32 ? 5 : bs == 64 ? 6 : bs == 128 ? 7 : -1; }
 
-// `n` pieces of `width` bytes, `stride` bytes from one to the next, `outer` times, `outer_stride` apart.
+// Pieces of `width` bytes: `inner` of them `inner_stride` apart, that `n` times, `stride` apart.  Neither strides nor pieces
+// overlap within a set.
 struct Rows {
   const void* p;
-  int64_t n, width, stride;
+  int64_t n, width, stride, inner = 1, inner_stride = 0;
 };
 
-int64_t span(const Rows& r) { return r.n <= 0 || r.width <= 0 ? 0 : (r.n - 1) * r.stride + r.width; }
+int64_t span(const Rows& r) {
+  return r.n <= 0 || r.width <= 0 ? 0 : (r.n - 1) * r.stride + (r.inner - 1) * r.inner_stride + r.width;
+}
 
-// Whether two sets of pieces share a byte.  Sets of one stride may lie between each other (slices of a fused
-// projection); others may not even have spans in common.
+// Whether two sets of pieces share a byte.  Sets of the same strides may lie between each other (slices of a fused
+// projection, K and V of a head side by side); others may not even have spans in common.
 bool share(const Rows& a, const Rows& b) {
   if (!overlaps(a.p, span(a), b.p, span(b))) return false;
-  if (a.stride != b.stride || a.stride <= 0) return true;
-  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % a.stride;
-  if (d < 0) d += a.stride;
-  return d < a.width || d + b.width > a.stride;
+  const bool once = a.n <= 1 && b.n <= 1;
+  if ((!once && (a.stride != b.stride || a.stride <= 0)) || a.inner != b.inner || a.inner_stride != b.inner_stride) return true;
+  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  if (!once && (d %= a.stride) < 0) d += a.stride;
+  // pieces of b lie d + j inner_stride from pieces of a, |j| < inner, and that a stride lower
+  for (int low = 0; low < (once ? 1 : 2); ++low) {
+    const int64_t x = d - (low ? a.stride : 0);
+    const int64_t near = a.inner > 1 ? -x / a.inner_stride : 0;
+    for (int64_t j = std::max(near - 1, 1 - a.inner); j <= std::min(near + 1, a.inner - 1); ++j) {
+      const int64_t at = x + j * a.inner_stride;
+      if (at > -b.width && at < a.width) return true;
+    }
+  }
+  return false;
 }
 
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.stride == b.stride && a.n == b.n && a.width == b.width; }
@@ -85,7 +98,8 @@ int cache4_check(Cache4Params& p, void* k, void* v, const int64_t* slot_map, voi
     row += D;
     if (T > 0 && (!stride_ok(n_in > 1 ? n_in : 0, inner, D) || !stride_ok(n_out > 1 ? n_out : 0, outer, row)))
       return ATTN_ERR_INVALID_ARG;
-    x[i] = Rows{i ? v : k, n_out, row * esize, outer * esize};
+    x[i] = n_in > 1 ? Rows{i ? v : k, n_out, D * esize, outer * esize, n_in, inner * esize}
+                    : Rows{i ? v : k, n_out, D * esize, outer * esize};
   }
   if (T == 0) return 0;
   if (!k || !v || !slot_map) return ATTN_ERR_INVALID_ARG;
