@@ -1,6 +1,6 @@
-"""Rows that lie between each other in one buffer: which calls attn_cache_read_fp4
-refuses (no GPU needed: the calls that pass this check are refused by a later one,
-for blocks of 8 slots, before any CUDA call)."""
+"""Rows that lie between each other in one buffer: which calls attn_cache_read_fp4 and
+attn_rope refuse (no GPU needed: the calls that pass this check are refused by a
+later one, for blocks of 8 slots or a misaligned argument, before any CUDA call)."""
 import numpy as np
 import pytest
 
@@ -20,6 +20,13 @@ def lib():
 def read(lib, T, H, D, k, v, ks, vs):
     """ks, vs: (token stride, head stride) in elements of bf16."""
     return lib.attn_cache_read_fp4(A[3], A[4], A[5], A[6], None, None, A[2], k, v, T, H, D, *ks, *vs, 100, 8, attn.ATTN_BF16, None)
+
+
+def rope(lib, **kw):
+    a = dict(q=A[0], k=A[1], qo=A[2], ko=A[3], freq=A[4] + 4, pos=A[7], starts=None, totals=None, T=10, B=0, Hq=4, Hk=2,
+             D=64, R=64, qst=256, kst=128, qost=256, kost=128, inter=0, inverse=0, scale=1.0, dtype=attn.ATTN_BF16)
+    a.update(kw)
+    return lib.attn_rope(*a.values(), None)
 
 
 @pytest.mark.parametrize("T,H,D", [(7, 3, 64), (1, 3, 64), (7, 1, 128), (1, 1, 64)])
@@ -60,3 +67,11 @@ def test_all_that_meet_are_refused_and_no_others(lib):
         assert got == want, (T, H, D, strides, step)
         seen[want] += 1
     assert min(seen.values()) > 500, seen
+
+
+def test_a_single_token_in_place(lib):
+    """The token stride of one token says nothing."""
+    assert rope(lib, T=1, qo=A[0], qost=999, ko=A[1], kost=128) == PASSES
+    assert rope(lib, T=1, qo=A[0] + 128, qost=999) == CLASH
+    assert rope(lib, T=2, qo=A[0], qost=999) == CLASH
+    assert rope(lib, qo=A[0], ko=A[1]) == PASSES

@@ -49,7 +49,10 @@ bool share(const Rows& a, const Rows& b) {
   return false;
 }
 
-bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.stride == b.stride && a.n == b.n && a.width == b.width; }
+// One-level sets that are the same rows (of a single one the stride says nothing).
+bool same(const Rows& a, const Rows& b) {
+  return a.p == b.p && a.n == b.n && a.width == b.width && (a.n <= 1 || a.stride == b.stride);
+}
 
 Rows flat(const void* p, int64_t bytes) { return Rows{p, p && bytes > 0 ? 1 : 0, bytes, bytes}; }
 
