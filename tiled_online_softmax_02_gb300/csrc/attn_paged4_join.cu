@@ -63,8 +63,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged4_join_kernel(const Pag
       }
       M = Mn;
     }
-    if (share > 1) {  // the row's warps meet at the first of them
-      if (r0 > 0) __syncthreads();  // what lay here has been read
+    if (share > 1) {  // the row's warps meet at the first of them (all rows are there in one pass of the loop)
 #pragma unroll
       for (int v = 0; v < V; ++v) sum_o[warp][lane * V + v] = acc[v];
       if (lane == 0) sum_ml[warp] = make_float2(M, L);
