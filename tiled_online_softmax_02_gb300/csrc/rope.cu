@@ -260,9 +260,10 @@ template <typename T, int VP, bool INTER>
 cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
   const int row_lanes = lanes_for(p.rotary / 2 / VP), rest_lanes = lanes_for((p.D - p.rotary) / VP);
   const int H = p.H[0] + p.H[1], subs = 32 / row_lanes;
+  const int64_t sms = paged_sm_count();
   int heads_each = H;
   // few tokens: more warps a token, down to one head a lane
-  while (heads_each > subs && (int64_t)p.T * ((H + heads_each - 1) / heads_each) < 152 * 16)
+  while (heads_each > subs && (int64_t)p.T * ((H + heads_each - 1) / heads_each) < sms * 16)
     heads_each = std::max(subs, (heads_each + 1) / 2);
   const int parts = (H + heads_each - 1) / heads_each;
   const int64_t blocks = ((int64_t)p.T * parts + kThreads / 32 - 1) / (kThreads / 32);
