@@ -482,9 +482,9 @@ size_t attn_paged_workspace_bytes(int num_tokens, int B, int Hq, int Hkv, int D)
  * of e4m3, one for every 16 values of a row.  An e2m1 code is a sign and 0,
  * 1/2, 1, 3/2, 2, 3, 4 or 6.  Head scales, f32 [Hkv], are optional (NULL: 1):
  *   value = e2m1 * e4m3 * head_scale.
- * They are positive, finite and the same in every call on a cache; they bring a
- * head whose values lie outside 2^-6 to 2^11 into the range where e4m3 scales
- * are exact to 2^-4.
+ * They lie between 2^-60 and 2^60 and are the same in every call on a cache; they
+ * bring a head whose values lie outside 2^-6 to 2^11 into the range where e4m3
+ * scales are exact to 2^-4.
  */
 
 /*
@@ -517,7 +517,8 @@ int attn_cache_append_fp4(const void *k, const void *v, const int64_t *slot_map,
  * attention is to see what the cache holds, and for contexts that move.
  *
  * Row t of k and v receives the values of slot slot_map[t], rounded to nearest
- * even; zeros where the slot is negative or of no block.  The same slot may be
+ * even (where there is a head scale, its product to f32 first); zeros where the
+ * slot is negative or of no block.  The same slot may be
  * read any number of times.
  *
  * Arguments (device pointers, caller-owned; k and v overlap nothing):

@@ -757,7 +757,7 @@ def attn_cache_append_fp4(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, 
     skip; no slot twice); k_cache, v_cache [num_blocks, Hkv, block_size, D / 2]
     uint8 (or float4_e2m1fn_x2) and k_scales, v_scales [num_blocks, Hkv,
     block_size, D / 16] float8_e4m3fn (or uint8), updated in place;
-    k_head_scales, v_head_scales float32 [Hkv] or None (1)."""
+    k_head_scales, v_head_scales float32 [Hkv], 2^-60 to 2^60, or None (1)."""
     if _lib is None:
         load_library()
     rc = _calls.append(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, k_head_scales, v_head_scales)
