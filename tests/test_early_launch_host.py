@@ -9,7 +9,7 @@ from tiled_online_softmax_02_gb300 import build
 
 # files whose kernels are all launched so, one with such a kernel and a fill, and the headers that those share with others
 EARLY = ["cache4.cu", "rope.cu", "attn_paged4_dec.cu", "attn_paged4_tc.cu", "attn_paged4_join.cu", "attn_paged_join.cu"]
-SHARED = ["attn_merge.cu", "paged4.cuh", "paged_join.cuh", "paged_mma.cuh"]
+SHARED = ["attn_merge.cu", "early_load.cuh", "paged4.cuh", "paged_join.cuh", "paged_mma.cuh"]
 
 
 def code(name):

@@ -11,7 +11,7 @@
 #include <cuda_fp16.h>
 
 #include "attn_internal.h"
-#include "device_common.cuh"
+#include "early_load.cuh"
 
 namespace gb300_attn {
 namespace {

@@ -34,7 +34,7 @@
 #include <algorithm>
 
 #include "../../include/attn.h"
-#include "device_common.cuh"
+#include "early_load.cuh"
 #include "paged4.cuh"
 #include "paged4_internal.h"
 

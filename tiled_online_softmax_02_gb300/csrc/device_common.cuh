@@ -223,21 +223,6 @@ __device__ __forceinline__ uint4 ld_nc_hint(const void* ptr, uint64_t policy) {
                : "l"(ptr), "l"(policy));
   return v;
 }
-// A load of what an earlier kernel wrote, in a kernel launched while that one still runs (after griddepcontrol.wait): the
-// read-only path (__ldg) is for memory that nobody writes while a kernel lives.  Volatile, so that it stays behind the
-// wait; without a clobber, so that loads of a loop still go out together (by plain ones a merge of 4K keys in 16 ranges
-// takes 0.9 us longer).
-template <typename T>
-__device__ __forceinline__ T load_written(const T* p) {
-  static_assert(sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "one load");
-  uint32_t w[sizeof(T) / 4];
-  if constexpr (sizeof(T) == 4) asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-  else if constexpr (sizeof(T) == 8) asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  else asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-  T x;
-  __builtin_memcpy(&x, w, sizeof(T));
-  return x;
-}
 __device__ __forceinline__ void st_hint(void* ptr, uint4 v, uint64_t policy) {
   asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(ptr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w), "l"(policy)

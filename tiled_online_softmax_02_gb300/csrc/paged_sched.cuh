@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "early_load.cuh"
 #include "paged_internal.h"
 
 namespace gb300_attn {
