@@ -1,15 +1,14 @@
 // attn_paged4_dec.cu -- attention over the paged 4-bit KV cache for few query
 // rows per (request, kv head): decode steps and drafted tokens.
 //
-// Bound: HBM, 4.5 bits a value.  At that rate every clock brings 41 values to
-// an SM, which has 128 lanes of arithmetic for them, so what counts is how few
-// instructions a value costs:
+// Floor: HBM, 4.5 bits a value.  At that rate every clock brings 41 values to
+// an SM, which has 128 lanes of arithmetic for them, so instructions a value count:
 //   S^T = K Q^T, O^T = V^T P^T   mma m16n8k16 in f16, keys (d for V) in M, the
 //   query rows in N.  Its operands are registers, so the bytes go from shared
 //   memory straight into them: one conversion and one multiplication for two
-//   values.  (On the tcgen05 path the widened values would have to be written
-//   to shared memory and read again: 2 + 2 bytes a value, above what shared
-//   memory moves.)
+//   values.  (On the tcgen05 path widened values would have to be written to
+//   shared memory and read again: 2 + 2 bytes a value, above what shared memory
+//   moves.  Products on K as it lies, with block scales, were not tried.)
 //   e2m1 * e4m3 is exact in f16 (6 bits, 2^-10 to 2688).  Q is f16 as it is, or
 //   bf16 times a power of two a row that brings its largest element to 2^14,
 //   which loses nothing above 2^-31 of that.  P is f16: 11 bits, 2^-29 of the
@@ -27,9 +26,9 @@
 // another between two meetings, and nothing waits on a barrier in memory.
 //
 // Measured (one GB300, device time with the join, D = 128): 8 requests of 9K to
-// 33K tokens, 32 query and 8 kv heads, bf16, 42.6 us, 4.5 TB/s, 67% of a copy's
+// 33K tokens, 32 query and 8 kv heads, bf16, 42.5 us, 4.5 TB/s, 67% of a copy's
 // rate (the 8-bit kernel 58); 64 requests of up to 8K, 4 kv heads, f16, blocks of
-// 16 slots, 39.2 us (54); one request of 3.5K 8.9 us (11.4).  About 8 us of each
+// 16 slots, 39.1 us (54); one request of 3.5K 9.0 us (11.4).  About 8 us of each
 // are the launch, the shares, the first keys and the join.  32 keys cost 540
 // instructions: 128 conversions and 128 multiplications, on two pipes that take
 // one every other cycle, 32 products, which with those alone take 138 cycles
@@ -40,6 +39,10 @@
 // K and V in stages apart (49), three stages (46.1), the next sub-tile's first
 // product beside this one's second (46.1), V's rows in an order without bank
 // conflicts (46.4 against 45.8).  Two accumulators for S: no change.
+// No unit is full in that case: 2.4 of 4 issue slots a cycle, ALU 48%, DRAM 58%,
+// tensor 21%.  16 warps an SM is what 128 registers allow (bf16 spills 24 bytes, 48
+// under a soft-cap), so the rest of the time is latency that four warps a scheduler
+// leave open.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -21,10 +21,10 @@
 // Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; P over its S.
 //
 // Measured (one GB300, device time with the join, bf16, 32 query and 8 kv heads,
-// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 556 us, 1294
-// TFLOP/s, 68% of a 16-bit library product's rate (the 8-bit kernel 591 us); two
+// D = 128): chunks of about 1.8K tokens at 9K to 14K of context 557 us, 1292
+// TFLOP/s, 67% of a 16-bit library product's rate (the 8-bit kernel 591 us); two
 // whole prompts of 3.5K to 4K tokens 236 us, 1003 TFLOP/s (257).  The tensor pipe is
-// busy 56% of the first's time: a lane's S, softmax and P V follow one another, as
+// busy 54% of the first's time: a lane's S, softmax and P V follow one another, as
 // P takes S's place, and two lanes do not cover that.  Without the widening's
 // arithmetic it takes 492 us: its stores, 64 KB a tile, share the memory with the
 // products' operands, 192 KB, and its instructions the issue slots.

@@ -10,8 +10,8 @@ namespace gb300_attn {
 namespace {
 
 // What launch_early asks of a kernel, before anything else.  What earlier kernels may have written is loaded after it, and
-// by ordinary loads or load_written: the read-only path (__ldg) is for memory that nobody writes while the kernel lives, and this one may
-// already live while those still write.
+// by ordinary loads or load_written: the read-only path (__ldg) is for memory that nobody writes while the kernel lives, and
+// this one may already live while those still write.
 __device__ __forceinline__ void after_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Eight e2m1 codes as f16 pairs, in order.

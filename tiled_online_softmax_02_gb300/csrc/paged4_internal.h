@@ -53,8 +53,9 @@ struct Paged4Params {
 };
 
 constexpr int kPaged4DecCtas = 2;        // CTAs of the few-rows kernel on an SM, in units of 8 rows
-// Tiles of a CTA's piece, at least: the few-rows kernel's eight warps have 256 keys between them in the time of 32, and every
-// part of a unit is one more to join.  One request of 3.5K in pieces of 1, 2, 3, 4 tiles 9.8, 8.9, 9.2 and 9.4 us; 512 rows over
+// Length of a CTA's piece of the work line, at least, in tiles (and in the kOver that a unit's head takes of the line, so the
+// pieces of short units may hold one tile or none): the few-rows kernel's eight warps have 256 keys between them in the time of
+// 32, and every part of a unit is one more to join.  One request of 3.5K in pieces of 1, 2, 3, 4 tiles 9.8, 8.9, 9.2 and 9.4 us; 512 rows over
 // 4K, 4 kv heads, in the many-rows kernel 33, 28, 26 and 26; a prompt of 500 tokens there 21.3, 21.2, 22.4 and 22.1.
 constexpr int kPaged4Piece = 2;
 constexpr float kPaged4DecLog2 = 5.0f;   // log2 of the factor that P carries

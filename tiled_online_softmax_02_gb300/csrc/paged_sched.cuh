@@ -104,7 +104,7 @@ __device__ __forceinline__ void paged_unit_tiles(const PagedParams& p, PagedUnit
 }
 
 // What a unit costs besides its tiles, in tiles: the many-rows kernel's Q and output rows, about 10000 cycles.  The
-// few-rows kernel's units are given the same.
+// few-rows kernel's units are given the same (not measured apart; the choice between the kernels counts 2 or 4 for them).
 constexpr int kOver = 3;
 
 template <int NR>
@@ -327,7 +327,7 @@ __device__ __noinline__ void paged_share_long(const PagedParams& p, PagedShare* 
 }
 
 // Called by every thread of the CTA (NT threads) before a __syncthreads().  Where there is too little for every CTA of the
-// grid, those that work have kPiece tiles or more.
+// grid, those that work have pieces kPiece long or more.
 template <int NR, int NT, int kPiece = 1, PagedLoad LOAD = kReadOnly>
 __device__ __forceinline__ void paged_share(const PagedParams& p, PagedShare* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
