@@ -63,7 +63,7 @@ def test_gradients(dtype, layout, inverse, Hk, R):
     want = formula(x[:, :Hq + Hk], pos.cpu(), freq.cpu(), layout, inverse, scale)
     d = torch.cat([y.double().cpu() for y in dy], 1)
     (want * d).sum().backward()
-    close(torch.cat([y for y in made if y is not None], 1), want, 2 * float(x.abs().max()), dtype)
+    close(torch.cat([y for y in made if y is not None], 1), want, 2 * float(x.detach().abs().max()), dtype)
     close(rows.grad, x.grad, 2 * float(d.abs().max()), dtype)
 
 
@@ -96,6 +96,25 @@ def test_rows_of_no_request_have_no_gradient():
     for x in (q, k):
         assert bool((x.grad[0] == 0).all()) and bool((x.grad[7:] == 0).all())
         assert torch.equal(x.grad[1:7], want[1:, :x.shape[1]])
+
+
+def test_the_next_step_before_the_backward_pass():
+    """A paged step's lengths, written anew in place by the next step: the gradient is that of the step's own positions."""
+    T, D, block = 6, 64, 16
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    tables, free, count = torch.full((2, 8), -1, dtype=torch.int32, device="cuda"), torch.arange(16, dtype=torch.int32, device="cuda"), i32(16)
+    starts, total = i32(0, 0, 0), i32(0, 0)
+    assign = lambda past, new: attn.attn_cache_assign(past, new, tables, free, count, block_size=block, num_tokens=T,  # noqa: E731
+                                                      q_starts=starts, total_lengths=total)
+    freq, _ = attn.attn_rope_frequencies(D)
+    q = torch.randn((T, 2, D), device="cuda", requires_grad=True)
+    assign(i32(20, 7), i32(4, 2))
+    y = attn.attn_rope(q, None, freq, q_starts=starts, total_lengths=total)[0]
+    assign(total.clone(), i32(1, 5))
+    y.sum().backward()
+    assert starts.tolist() == [0, 1, 6]
+    want, _ = attn.attn_rope(torch.ones_like(q), None, freq, positions=i32(20, 21, 22, 23, 7, 8), inverse=True)
+    assert torch.equal(q.grad, want)
 
 
 def test_one_output_used_and_second_derivatives():

@@ -953,6 +953,9 @@ class _Rope(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, inv_freq, positions, q_starts, total_lengths, layout, inverse, scale, clear):
+        if positions is None and q_starts is not None and total_lengths is not None:
+            # attn_cache_assign may write the next step's there before the backward pass, which autograd would not see
+            q_starts, total_lengths = q_starts.clone(), total_lengths.clone()
         ctx.save_for_backward(inv_freq, positions, q_starts, total_lengths)
         ctx.how = layout, inverse, scale
         out = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) if clear and x is not None else None for x in (q, k)]
