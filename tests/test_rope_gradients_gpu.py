@@ -129,7 +129,7 @@ def test_one_output_used_and_second_derivatives():
     dx, = torch.autograd.grad(y, q, dy, create_graph=True)
     back, = torch.autograd.grad((dx ** 2).sum() / 2, dy)
     # two rotations, each off by 2^-20 of values up to 2 |dy|
-    assert float((back - dy).abs().max()) <= 2 * 2.0 ** -19 * float(dy.abs().max())
+    assert float((back - dy).detach().abs().max()) <= 2 * 2.0 ** -19 * float(dy.detach().abs().max())
 
 
 def test_only_k_requires_gradients_and_given_outputs():

@@ -28,7 +28,7 @@
 // Measured (one GB300, device time with the join, D = 128): 8 requests of 9K to
 // 33K tokens, 32 query and 8 kv heads, bf16, 42.5 us, 4.5 TB/s, 67% of a copy's
 // rate (the 8-bit kernel 58); 64 requests of up to 8K, 4 kv heads, f16, blocks of
-// 16 slots, 39.1 us (54); one request of 3.5K 9.0 us (11.4).  About 8 us of each
+// 16 slots, 39.1 us (54); one request of 3.5K 9.0 us (11.6).  About 8 us of each
 // are the launch, the shares, the first keys and the join.  32 keys cost 540
 // instructions: 128 conversions and 128 multiplications, on two pipes that take
 // one every other cycle, 32 products, which with those alone take 138 cycles

@@ -451,7 +451,8 @@ __device__ __forceinline__ void softmax_role(const Paged4TcParams& TP, const Lay
     const int full_lo = paged_limits(p, u.q, paged_token(p, last)).x, full_hi = paged_limits(p, u.q, paged_token(p, x0)).y;
     // positive, so that -inf stays -inf, and finite, so that 0 stays 0.  Under a soft-cap hidden keys do not go through it, and
     // it may be next to nothing: a large cap brings its share back.
-    const float raw = fminf(fmaxf(qs * (P.k_heads ? P.k_heads[u.kvh] : 1.0f) * (SOFTCAP ? TP.sc_in : TP.scale_log2), SOFTCAP ? 0.0f : 1.2e-38f), 3e38f);
+    const float kh = P.k_heads ? P.k_heads[u.kvh] : 1.0f;
+    const float raw = fminf(fmaxf(qs * kh * (SOFTCAP ? TP.sc_in : TP.scale_log2), SOFTCAP ? 0.0f : 1.2e-38f), 3e38f);
     const float xs = SOFTCAP ? TP.sc_out : raw;  // brings x, the raw score or its tanh, to log2 units
     vh = P.v_heads ? P.v_heads[u.kvh] : 1.0f;
     m_run = kNone;
